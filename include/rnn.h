@@ -453,6 +453,117 @@ rnn_status rnn_nn_argmax_noalloc(const void *Q, int64_t nq, const void *X, int64
 rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Attention over the tokens of the network that emits the descriptors.
+ *
+ * The maps D1, D2 are the output of an encoder and of decoders whose layers
+ * attend over image tokens, and the multi-view forms keep earlier frames'
+ * tokens in a memory that later frames look at (cv-learn.com "MASt3R" note,
+ * section "Method and architecture"; deep-paper.org MUSt3R summary, memory and
+ * causal mode).  These entry points are that step's counterparts of
+ * rnn_nn_argmax: rows of Q K^T reduced by a softmax and a weighted sum instead
+ * of a maximum, without the score matrix in device memory.
+ *
+ * Conventions beside those at the top of this file:
+ *   - Rows of a head are d contiguous fp16 or bf16 channels; strides are in
+ *     elements, at least d and multiples of 8 (a dimension of size 1 may have
+ *     any stride).  d is a multiple of 8.
+ *   - Hq query heads share Hkv key heads in order: query head h reads key head
+ *     h / (Hq / Hkv).  Hq is a multiple of Hkv.
+ *   - Sequences are packed one behind the other: sequence b has the tokens
+ *     cu[b] .. cu[b+1]-1, with cu an int32 array of B + 1 values that do not
+ *     fall, in device memory.  Lengths may be 0.  Rows before cu[0] and
+ *     from cu[B] on are not touched.
+ *   - A row that sees no key gets zeros, and -infinity as its log-sum.
+ *   - Queries, and the keys and values of a sequence, must be finite.  What
+ *     lies outside the sequences may hold anything.
+ *   - Softmax statistics and sums are fp32; each product's probabilities are
+ *     rounded to the 16-bit type once, outputs once.
+ */
+#define RNN_ATTN_MAX_DIM 128
+#define RNN_ATTN_MAX_HEADS 1024
+
+/* [tokens][heads][d] */
+typedef struct rnn_rows {
+  void *data;
+  int64_t token_stride, head_stride;
+} rnn_rows;
+
+/* [pages][page_size][heads][d], in any order of the first three dimensions */
+typedef struct rnn_pages {
+  void *data;
+  int64_t page_stride, token_stride, head_stride;
+} rnn_pages;
+
+/*
+ * Append the T packed new tokens' keys and values to a paged cache, rotating
+ * keys and queries by their positions.
+ *
+ *   q            [T][Hq][d], rotated into q_out (which may be q itself);
+ *                Hq = 0: no queries (q and q_out are ignored).
+ *   k, v         [T][Hkv][d]; k_out.data may be NULL, else it gets the rotated
+ *                keys packed as k is (for rnn_attn_prompt), and may be k.
+ *   page_table   [B][max_pages] int32, rows table_stride apart: the pages of
+ *                each sequence.  Token t of sequence b is number
+ *                start[b] + t - cu[b] of it and goes to row (number %
+ *                page_size) of page page_table[b][number / page_size].  A
+ *                number below 0 or beyond the table, or a page outside
+ *                [0, num_pages), is not stored (its query and packed key are
+ *                still rotated).  The rows that one call writes must be
+ *                distinct.
+ *   positions    [T][axes] int32, rows position_stride apart, or NULL with one
+ *                axis: the tokens' numbers.
+ *   inv_freq     [pairs] double: pair i turns by position * inv_freq[i]
+ *                radians.  The first 2 * pairs * axes <= d channels are
+ *                rotated, 2 * pairs of them for each of the 1 or 2 axes (row
+ *                and column of an image patch); the rest pass through.
+ *                pairs = axes = 0: no rotation.
+ *   paired       0: channels i and pairs + i of an axis form a pair; else
+ *                channels 2i and 2i + 1.
+ * d <= 256.  No workspace: nothing waits on the device.
+ */
+rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, int Hkv, int d,
+                         rnn_dtype dtype, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
+                         int page_size, const int32_t *page_table, int64_t table_stride,
+                         int max_pages, const int32_t *start, const int32_t *cu, int B,
+                         const int32_t *positions, int64_t position_stride,
+                         const double *inv_freq, int pairs, int axes, int paired, rnn_rows q_out,
+                         rnn_rows k_out, rnn_stream_t stream);
+
+/*
+ * Attention of packed sequences: q [Tq][Hq][d] of sequences cu_q over k, v
+ * [Tk][Hkv][d] of sequences cu_k (both B + 1 values).
+ *   causal   nonzero: row i of nq sees the keys t <= i + nk - nq, so the last
+ *            query sees the last key (nk > nq: the keys in front are earlier
+ *            tokens; nk < nq: the first rows see nothing).  0: all nk keys.
+ *   scale    > 0, multiplies the scores.
+ *   out      [Tq][Hq][d].
+ *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
+ * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded: see
+ * rnn_workspace_status.
+ */
+size_t rnn_attn_prompt_workspace_size(void);
+rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64_t Tk, int Hq,
+                           int Hkv, int d, rnn_dtype dtype, const int32_t *cu_q,
+                           const int32_t *cu_k, int B, int causal, float scale, rnn_rows out,
+                           float *lse, void *workspace, size_t ws_bytes, rnn_stream_t stream);
+
+/*
+ * Attention of one new token of each of B sequences over a paged cache:
+ * q, out [B][Hq][d] (the sequence in the place of the token), lse [B][Hq] or
+ * NULL.  lens [B] int32: tokens of each sequence in the cache, the new one's
+ * included (values below 0 count as 0, values beyond max_pages * page_size as
+ * that).  Keys whose page is outside [0, num_pages) count as absent; rows of
+ * a page behind the last key may hold anything.
+ * d <= RNN_ATTN_MAX_DIM.
+ */
+size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
+rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
+                           int page_size, const int32_t *page_table, int64_t table_stride,
+                           int max_pages, const int32_t *lens, int B, int Hq, int Hkv, int d,
+                           rnn_dtype dtype, float scale, rnn_rows out, float *lse,
+                           void *workspace, size_t ws_bytes, rnn_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics for benchmarking (no effect on results).
  *
  * rnn_launch_count: number of kernels this library has launched in this
@@ -476,8 +587,8 @@ void rnn_set_kernel_timer(void *const *start_events, void *const *stop_events, i
 /*
  * Failure-detection test hook (no use in production).  While `on` is
  * nonzero, every launch of the fused similarity+argmax kernel loads no
- * candidate tile, so the bounded wait of its MMA warps on the first tile runs
- * out after `wait_limit_ns` (0: the default of 1 s); the kernel then stops
+ * candidate tile (and one of rnn_attn_prompt no tile at all), so the bounded
+ * wait of its MMA warps on the first tile runs out after `wait_limit_ns` (0: the default of 1 s); the kernel then stops
  * all its warps, frees tensor memory and returns, and the call's workspace
  * status reads RNN_ETIMEOUT (rnn_workspace_status).  Results of those calls
  * are undefined but every index written is in range.  Nothing faults, traps

@@ -27,6 +27,10 @@ contiguous fp16/bf16 CUDA tensors; pixel index ``p = y*W + x``.
 * ``pts_nn`` / ``pts_mnn`` / ``pts_frm_match``: the same operations on 3-D
   points (fp32 ``[..., 3]``), where MASt3R's NN function is the exact nearest
   point in Euclidean distance (a K-d tree query in its reference code).
+* ``kv_append`` / ``attn_prompt`` / ``attn_decode``: the attention steps of the
+  network in front of the matching (image tokens, and the memory of earlier
+  frames): softmax-weighted sums over the rows of Q K^T instead of their
+  argmax, for packed sequences and over a paged cache.
 
 Results stay on the device; pair lists come back as ``(pairs, count)`` with
 ``pairs`` a ``[cap, 2]`` int32 buffer and ``count`` a device int32 tensor;
@@ -47,7 +51,8 @@ __all__ = [
     "nn_argmax", "mnn_exhaustive", "frm_match", "frm_match_batched", "frm_num_seeds",
     "frm_max_pairs", "workspace_status", "trim", "MNNResult", "FRMResult", "RNNError",
     "RNNLibraryError", "FRMPlan", "frm_match_ex", "frm_refine", "pts_nn", "pts_mnn",
-    "pts_frm_match", "c2f_match", "C2FResult", "mnn_mutual", "FRMGraph",
+    "pts_frm_match", "c2f_match", "C2FResult", "mnn_mutual", "FRMGraph", "kv_append",
+    "attn_prompt", "attn_decode",
 ]
 
 _DT = {torch.float16: _lib.RNN_F16, torch.bfloat16: _lib.RNN_BF16}
@@ -592,3 +597,6 @@ def c2f_match(C1: torch.Tensor, C2: torch.Tensor, F1: torch.Tensor, F2: torch.Te
         out.pairs.data_ptr(), cap, out.count.data_ptr(), out.crops.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _stream(F1)), "rnn_c2f_match")
     return out
+
+
+from .attn import attn_decode, attn_prompt, kv_append  # noqa: E402

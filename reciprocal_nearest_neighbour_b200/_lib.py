@@ -51,6 +51,11 @@ EXPORTS = (
     "rnn_frm_graph_create",
     "rnn_frm_graph_launch",
     "rnn_frm_graph_destroy",
+    "rnn_kv_append",
+    "rnn_attn_prompt_workspace_size",
+    "rnn_attn_prompt",
+    "rnn_attn_decode_workspace_size",
+    "rnn_attn_decode",
 )
 
 STATUS = {
@@ -62,6 +67,20 @@ RNN_DOT, RNN_L2 = 0, 1
 METRICS = {"dot": RNN_DOT, "l2": RNN_L2}
 RNN_MAX_BATCH = 1024
 RNN_NN_NOALLOC_MAX_QUERIES = 65536
+RNN_ATTN_MAX_DIM = 128
+RNN_ATTN_MAX_HEADS = 1024
+
+
+class Rows(ctypes.Structure):
+    """``rnn_rows``: [tokens][heads][d] with strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Pages(ctypes.Structure):
+    """``rnn_pages``: [pages][page_size][heads][d] with strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class RNNLibraryError(RuntimeError):
@@ -137,6 +156,14 @@ def load():
                                      ctypes.c_float, P, I64, P, P, P, P, SZ, P]),
         "rnn_frm_graph_launch": (I, [P, P]),
         "rnn_frm_graph_destroy": (None, [P]),
+        "rnn_kv_append": (I, [Rows, Rows, Rows, I64, I, I, I, I, Pages, Pages, I64, I, P, I64, I,
+                              P, P, I, P, I64, P, I, I, I, Rows, Rows, P]),
+        "rnn_attn_prompt_workspace_size": (SZ, []),
+        "rnn_attn_prompt": (I, [Rows, Rows, Rows, I64, I64, I, I, I, I, P, P, I, I,
+                                ctypes.c_float, Rows, P, P, SZ, P]),
+        "rnn_attn_decode_workspace_size": (SZ, [I, I, I, I]),
+        "rnn_attn_decode": (I, [Rows, Pages, Pages, I64, I, P, I64, I, P, I, I, I, I, I,
+                                ctypes.c_float, Rows, P, P, SZ, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

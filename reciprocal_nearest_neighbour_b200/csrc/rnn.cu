@@ -63,6 +63,7 @@ struct DeviceInfo {
   bool sm100 = false;
   bool smem_set = false;
   bool op_smem_set = false;  // one-pass exhaustive-set kernels
+  bool attn_smem_set = false;
 };
 
 static std::mutex g_mu;
@@ -1461,6 +1462,10 @@ __global__ void frm_emit_kernel(FrmState st, int32_t* pairs, int64_t cap, int32_
 #include "points.cuh"
 // coarse-to-fine kernels (they use block_exclusive_scan)
 #include "c2f.cuh"
+
+#include "attn_decode.cuh"
+#include "attn_prompt.cuh"
+#include "kv_append.cuh"
 
 namespace rnn {
 
@@ -2959,3 +2964,357 @@ extern "C" rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return RNN_ECUDA;
   return err ? RNN_ETIMEOUT : RNN_OK;
 }
+
+// ================================================= attention over a model's tokens
+// Strides of a dimension of size 1 are never used; a valid one stands in.
+static int64_t stride_or(int64_t size, int64_t stride, int64_t other) {
+  return size > 1 ? stride : other;
+}
+// rows of d contiguous 16-bit channels, every one 16-byte aligned, none overlapping
+static rnn_status check_rows(rnn_rows* r, int64_t tokens, int heads, int d) {
+  if (tokens > 0 && !r->data) return RNN_EINVAL;
+  r->head_stride = stride_or(heads, r->head_stride, d);
+  r->token_stride = stride_or(tokens, r->token_stride, static_cast<int64_t>(d) * heads);
+  if (r->head_stride < d || r->token_stride < d) return RNN_EINVAL;
+  if (!aligned16(r->data) || r->head_stride % 8 || r->token_stride % 8) return RNN_EALIGN;
+  return RNN_OK;
+}
+static rnn_status check_pages(rnn_pages* c, int64_t num_pages, int page_size, int heads, int d) {
+  if (!c->data) return RNN_EINVAL;
+  c->head_stride = stride_or(heads, c->head_stride, d);
+  c->token_stride = stride_or(page_size, c->token_stride, d);
+  c->page_stride = stride_or(num_pages, c->page_stride, d);
+  if (c->head_stride < d || c->token_stride < d || c->page_stride < d) return RNN_EINVAL;
+  if (!aligned16(c->data) || c->head_stride % 8 || c->token_stride % 8 || c->page_stride % 8)
+    return RNN_EALIGN;
+  return RNN_OK;
+}
+static rnn_status check_heads(int Hq, int Hkv, int d, int d_max, rnn_dtype dtype) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || !valid_dtype(dtype)) return RNN_EINVAL;
+  if (d % 8) return RNN_EALIGN;
+  return d > d_max || Hq > RNN_ATTN_MAX_HEADS ? RNN_EUNSUPPORTED : RNN_OK;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static rnn_status attn_setup(DeviceInfo* di) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (di->attn_smem_set) return RNN_OK;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const int d64 = static_cast<int>(DecShape<64>::kSmem), d128 = static_cast<int>(DecShape<128>::kSmem);
+  const int p64 = static_cast<int>(AttnShape<64>::kSmem), p128 = static_cast<int>(AttnShape<128>::kSmem);
+  if (cudaFuncSetAttribute(attn_decode_kernel<true, 64>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 64>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<true, 128>, attr, d128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 128>, attr, d128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 64>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 64>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 128>, attr, p128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 128>, attr, p128) != cudaSuccess)
+    return RNN_ECUDA;
+  di->attn_smem_set = true;
+  return RNN_OK;
+}
+
+// [tokens][heads][d] rows in boxes of 64 channels x 1 head x 128 tokens.
+static rnn_status make_rows_map(CUtensorMap* m, const rnn_rows& r, int64_t tokens, int heads, int d) {
+  auto fn = encode_fn();
+  if (!fn) return RNN_ECUDA;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(r.head_stride) * 2,
+                           static_cast<cuuint64_t>(r.token_stride) * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult c = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, r.data, dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return c == CUDA_SUCCESS ? RNN_OK : RNN_ECUDA;
+}
+
+extern "C" {
+
+size_t rnn_attn_prompt_workspace_size(void) { return kAlign; }
+
+rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64_t Tk, int Hq,
+                           int Hkv, int d, rnn_dtype dtype, const int32_t* cu_q,
+                           const int32_t* cu_k, int B, int causal, float scale, rnn_rows out,
+                           float* lse, void* workspace, size_t ws_bytes, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_attn_prompt");
+  if (Tq < 0 || Tk < 0 || Tq > INT32_MAX || Tk > INT32_MAX || B < 0) return RNN_EINVAL;
+  rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
+  if (r != RNN_OK) return r;
+  if (!(scale > 0.f) || !(scale < 3e38f)) return RNN_EINVAL;
+  if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return RNN_EINVAL;
+  if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
+      (r = check_rows(&v, Tk, Hkv, d)) != RNN_OK || (r = check_rows(&out, Tq, Hq, d)) != RNN_OK)
+    return r;
+  if (!workspace || !aligned256(workspace) || ws_bytes < rnn_attn_prompt_workspace_size())
+    return RNN_EWORKSPACE;
+  PromptParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.group = Hq / Hkv;
+  p.pair_heads = p.group % 2 == 0;
+  p.head_units = p.pair_heads ? Hq / 2 : Hq;
+  // every sequence may end in a partial tile
+  const int64_t units = (Tq / (p.pair_heads ? kAttnM : 2 * kAttnM) + B) * p.head_units;
+  if (units > INT32_MAX) return RNN_EUNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK || (r = attn_setup(di)) != RNN_OK) return r;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* err = static_cast<int*>(workspace);
+  if (Tq == 0 || B == 0) {
+    zero_words_kernel<<<1, 32, 0, s>>>(err, 1);
+    return launched();
+  }
+  CUtensorMap mq, mk, mv;
+  if ((r = make_rows_map(&mq, q, Tq, Hq, d)) != RNN_OK) return r;
+  if (Tk > 0) {
+    if ((r = make_rows_map(&mk, k, Tk, Hkv, d)) != RNN_OK ||
+        (r = make_rows_map(&mv, v, Tk, Hkv, d)) != RNN_OK)
+      return r;
+  } else {
+    mk = mv = mq;  // no key is loaded
+  }
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.out = static_cast<uint16_t*>(out.data);
+  p.lse = lse;
+  p.o_ts = out.token_stride;
+  p.o_hs = out.head_stride;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.B = B;
+  p.Hq = Hq;
+  p.d = d;
+  p.causal = causal != 0;
+  p.scale = scale;
+  p.c = scale * 1.44269504f;
+  p.idesc_s = make_idesc(dtype, kAttnN);
+  p.idesc_o = make_idesc(dtype, (d + 15) / 16 * 16) | (1u << 16);  // B with its channels contiguous
+  p.err = err;
+  p.stall_loads = g_stall_loads.load(std::memory_order_relaxed);
+  p.wait_limit_ns = p.stall_loads ? g_stall_limit_ns.load(std::memory_order_relaxed)
+                                  : kWaitLimitNs;
+  const dim3 grid(static_cast<unsigned>(units)), block(kAttnThreads);
+  const bool bf = dtype == RNN_BF16;
+  if (d <= 64) {
+    const size_t sm = AttnShape<64>::kSmem;
+    if (bf) attn_prompt_kernel<true, 64><<<grid, block, sm, s>>>(p, mq, mk, mv);
+    else attn_prompt_kernel<false, 64><<<grid, block, sm, s>>>(p, mq, mk, mv);
+  } else {
+    const size_t sm = AttnShape<128>::kSmem;
+    if (bf) attn_prompt_kernel<true, 128><<<grid, block, sm, s>>>(p, mq, mk, mv);
+    else attn_prompt_kernel<false, 128><<<grid, block, sm, s>>>(p, mq, mk, mv);
+  }
+  return launched();
+}
+
+// Grid of the decode kernel: two CTAs per SM, or one per tile when there are fewer.
+constexpr int kDecMaxGrid = 2 * 160;
+struct DecWs {
+  int* err;
+  float* part;
+  float2* ml;
+  int2* span;
+};
+static size_t dec_layout(void* ws, int64_t B, int Hkv, int group, int d, DecWs* w) {
+  Carve c(ws);
+  w->err = c.take<int>(64);
+  const int64_t dp = d <= 64 ? 64 : 128;
+  w->span = c.take<int2>(B * Hkv * ((group + kDecRows - 1) / kDecRows));
+  w->ml = c.take<float2>(int64_t{kDecMaxGrid} * 2 * kDecRows);
+  w->part = c.take<float>(int64_t{kDecMaxGrid} * 2 * kDecRows * dp);
+  return c.off;
+}
+
+size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
+  if (B < 0 || check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, RNN_F16) != RNN_OK) return 0;
+  DecWs w;
+  return dec_layout(nullptr, B, Hkv, Hq / Hkv, d, &w);
+}
+
+rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
+                           int page_size, const int32_t* page_table, int64_t table_stride,
+                           int max_pages, const int32_t* lens, int B, int Hq, int Hkv, int d,
+                           rnn_dtype dtype, float scale, rnn_rows out, float* lse,
+                           void* workspace, size_t ws_bytes, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_attn_decode");
+  if (B < 0 || num_pages < 1 || num_pages > INT32_MAX || page_size < 1 || max_pages < 1 ||
+      table_stride < 0)
+    return RNN_EINVAL;
+  rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
+  if (r != RNN_OK) return r;
+  if (!(scale > 0.f) || !(scale < 3e38f)) return RNN_EINVAL;
+  if ((B > 0 && (!page_table || !lens)) || !aligned4(page_table) || !aligned4(lens) || !aligned4(lse))
+    return RNN_EINVAL;
+  if ((r = check_rows(&q, B, Hq, d)) != RNN_OK || (r = check_rows(&out, B, Hq, d)) != RNN_OK ||
+      (r = check_pages(&k_cache, num_pages, page_size, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&v_cache, num_pages, page_size, Hkv, d)) != RNN_OK)
+    return r;
+  if (static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
+  if (!workspace || !aligned256(workspace) ||
+      ws_bytes < rnn_attn_decode_workspace_size(B, Hq, Hkv, d))
+    return RNN_EWORKSPACE;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK || (r = attn_setup(di)) != RNN_OK) return r;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0) return RNN_OK;
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  DecWs w;
+  dec_layout(workspace, B, Hkv, Hq / Hkv, d, &w);
+  p.q = static_cast<const uint16_t*>(q.data);
+  p.kc = static_cast<const uint16_t*>(k_cache.data);
+  p.vc = static_cast<const uint16_t*>(v_cache.data);
+  p.out = static_cast<uint16_t*>(out.data);
+  p.lse = lse;
+  p.q_bs = q.token_stride;
+  p.q_hs = q.head_stride;
+  p.o_bs = out.token_stride;
+  p.o_hs = out.head_stride;
+  p.k_ps = k_cache.page_stride;
+  p.k_ts = k_cache.token_stride;
+  p.k_hs = k_cache.head_stride;
+  p.v_ps = v_cache.page_stride;
+  p.v_ts = v_cache.token_stride;
+  p.v_hs = v_cache.head_stride;
+  p.table = page_table;
+  p.lens = lens;
+  p.table_bs = table_stride;
+  p.num_pages = num_pages;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.hblocks = (p.group + kDecRows - 1) / kDecRows;
+  p.d = d;
+  p.max_pages = max_pages;
+  p.page = make_fastdiv(page_size);
+  p.scale = scale;
+  p.c = scale * 1.44269504f;
+  p.part = w.part;
+  p.part_ml = w.ml;
+  p.span = w.span;
+  p.err = w.err;
+  const int64_t room = static_cast<int64_t>(max_pages) * page_size;
+  const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
+  const int64_t tiles = (keys + kDecTile - 1) / kDecTile * B * Hkv * p.hblocks;
+  const int most = std::min(2 * di->sms, kDecMaxGrid);
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(kDecWarps * 32);
+  const dim3 jgrid(static_cast<unsigned>(B) * Hq);
+  const bool bf = dtype == RNN_BF16;
+  if (d <= 64) {
+    const size_t sm = DecShape<64>::kSmem;
+    if (bf) attn_decode_kernel<true, 64><<<grid, block, sm, s>>>(p);
+    else attn_decode_kernel<false, 64><<<grid, block, sm, s>>>(p);
+  } else {
+    const size_t sm = DecShape<128>::kSmem;
+    if (bf) attn_decode_kernel<true, 128><<<grid, block, sm, s>>>(p);
+    else attn_decode_kernel<false, 128><<<grid, block, sm, s>>>(p);
+  }
+  if ((r = launched()) != RNN_OK) return r;
+  if (d <= 64) {
+    if (bf) launch_k(attn_decode_join_kernel<true, 64>, jgrid, dim3(128), 0, s, true, p);
+    else launch_k(attn_decode_join_kernel<false, 64>, jgrid, dim3(128), 0, s, true, p);
+  } else {
+    if (bf) launch_k(attn_decode_join_kernel<true, 128>, jgrid, dim3(128), 0, s, true, p);
+    else launch_k(attn_decode_join_kernel<false, 128>, jgrid, dim3(128), 0, s, true, p);
+  }
+  return launched();
+}
+
+}  // extern "C"
+
+template <bool kBf16>
+static void kv_append_launch(const AppendParams& p, int vec, dim3 grid, size_t smem, cudaStream_t s) {
+  if (vec == 8) kv_append_kernel<kBf16, 8><<<grid, kAppThreads, smem, s>>>(p);
+  else if (vec == 4) kv_append_kernel<kBf16, 4><<<grid, kAppThreads, smem, s>>>(p);
+  else if (vec == 2) kv_append_kernel<kBf16, 2><<<grid, kAppThreads, smem, s>>>(p);
+  else kv_append_kernel<kBf16, 1><<<grid, kAppThreads, smem, s>>>(p);
+}
+
+extern "C" {
+
+rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, int Hkv, int d,
+                         rnn_dtype dtype, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
+                         int page_size, const int32_t* page_table, int64_t table_stride,
+                         int max_pages, const int32_t* start, const int32_t* cu, int B,
+                         const int32_t* positions, int64_t position_stride,
+                         const double* inv_freq, int pairs, int axes, int paired, rnn_rows q_out,
+                         rnn_rows k_out, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_kv_append");
+  if (T < 0 || T > INT32_MAX || B < 0 || B == INT32_MAX || Hq < 0 || Hkv < 1 || num_pages < 1 ||
+      num_pages > INT32_MAX || page_size < 1 || max_pages < 1 || table_stride < 0 || d < 1 ||
+      !valid_dtype(dtype))
+    return RNN_EINVAL;
+  if (d % 8) return RNN_EALIGN;
+  if (d > 256 || Hq > RNN_ATTN_MAX_HEADS || Hkv > RNN_ATTN_MAX_HEADS) return RNN_EUNSUPPORTED;
+  if (pairs < 0 || axes < 0 || axes > 2 || (pairs == 0) != (axes == 0) || 2 * pairs * axes > d ||
+      (pairs > 0 && !inv_freq) || (axes == 2 && !positions) ||
+      (positions && T > 1 && position_stride < axes))
+    return RNN_EINVAL;
+  if ((B > 0 && (!page_table || !start || !cu)) || !aligned4(page_table) || !aligned4(start) || !aligned4(cu) ||
+      !aligned4(positions) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+    return RNN_EINVAL;
+  rnn_status r;
+  if ((r = check_rows(&k, T, Hkv, d)) != RNN_OK || (r = check_rows(&v, T, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&k_cache, num_pages, page_size, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&v_cache, num_pages, page_size, Hkv, d)) != RNN_OK)
+    return r;
+  if (Hq > 0 && ((r = check_rows(&q, T, Hq, d)) != RNN_OK ||
+                 (r = check_rows(&q_out, T, Hq, d)) != RNN_OK))
+    return r;
+  if (k_out.data && (r = check_rows(&k_out, T, Hkv, d)) != RNN_OK) return r;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK) return r;
+  if (T == 0 || B == 0) return RNN_OK;
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q.data);
+  p.k = static_cast<const uint16_t*>(k.data);
+  p.v = static_cast<const uint16_t*>(v.data);
+  p.q_out = static_cast<uint16_t*>(q_out.data);
+  p.k_out = static_cast<uint16_t*>(k_out.data);
+  p.kc = static_cast<uint16_t*>(k_cache.data);
+  p.vc = static_cast<uint16_t*>(v_cache.data);
+  p.q_ts = q.token_stride, p.q_hs = q.head_stride;
+  p.k_ts = k.token_stride, p.k_hs = k.head_stride;
+  p.v_ts = v.token_stride, p.v_hs = v.head_stride;
+  p.qo_ts = q_out.token_stride, p.qo_hs = q_out.head_stride;
+  p.ko_ts = k_out.token_stride, p.ko_hs = k_out.head_stride;
+  p.kc_ps = k_cache.page_stride, p.kc_ts = k_cache.token_stride, p.kc_hs = k_cache.head_stride;
+  p.vc_ps = v_cache.page_stride, p.vc_ts = v_cache.token_stride, p.vc_hs = v_cache.head_stride;
+  p.table = page_table;
+  p.start = start;
+  p.cu = cu;
+  p.positions = positions;
+  p.table_bs = table_stride;
+  p.pos_ts = position_stride;
+  p.num_pages = num_pages;
+  p.inv_freq = inv_freq;
+  p.T = static_cast<int>(T);
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  p.pairs = pairs;
+  p.axes = axes;
+  p.paired = paired != 0;
+  const int vec = pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
+  const int row_units = (axes * pairs + d - 2 * axes * pairs) / vec;
+  // one token a block until the blocks fill the GPU several times over
+  p.tokens = static_cast<int>(std::min<int64_t>(kAppMaxTokens, std::max<int64_t>(1, T / (16 * di->sms))));
+  p.by_unit = make_fastdiv(row_units);
+  p.by_row = make_fastdiv(row_units * (Hq + Hkv));
+  p.by_vunit = make_fastdiv(d / 8);
+  const dim3 grid(static_cast<unsigned>((T + p.tokens - 1) / p.tokens));
+  const size_t smem = static_cast<size_t>(p.tokens) * axes * pairs * sizeof(float2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == RNN_BF16) kv_append_launch<true>(p, vec, grid, smem, s);
+  else kv_append_launch<false>(p, vec, grid, smem, s);
+  return launched();
+}
+
+}  // extern "C"
