@@ -3,10 +3,12 @@
 // for each query head, over the lens[b] cached rows of its sequence.
 //
 // Bound by memory: each cached row is read once for all the query heads that
-// share it (up to 16, the rows of one warp-level matrix instruction; more
-// heads read the rows again), and 2 x 16 x d multiply-adds a row are far
-// below what the legacy matrix path delivers, so tcgen05 would gain nothing
-// at 16 rows and cost a tensor-memory round trip per tile.
+// share it (up to 16; more heads read the rows again), and 2 x 16 x d
+// multiply-adds a row are far below what the warp-level matrix path delivers,
+// so tcgen05 would gain nothing at 8 or 16 rows and cost a tensor-memory round
+// trip per tile.  Keys are the 16 rows of the matrix instruction and the query
+// heads its 8 columns (S^T = K Q^T, then O^T += V^T P^T): with the heads as
+// rows, half of each instruction would be padding for up to 8 heads.
 //
 // Split.  The cache is cut into tiles of 4 x kKeys keys; the tiles of all
 // (sequence, key head) pairs form one list, which the CTAs (two per SM) cut
@@ -15,8 +17,12 @@
 // their running maximum and total in the workspace, and a second kernel joins
 // them in a fixed order.  Each of the four warps loads and reduces its own
 // kKeys keys of a tile with its own softmax state, so the loop has no block
-// barrier; the warps meet once per pair.  The loads run kStages tiles ahead,
-// over the ends of pairs.
+// barrier; the warps meet once per pair.  The loads run kStages - 1 tiles
+// ahead, over the ends of pairs.
+//
+// The reference maximum of a head moves only when a score exceeds it by more
+// than 2^8 (its weights then reach 2^8, far inside fp32 and the 16-bit
+// types): one vote per tile instead of a reduction across the warp.
 #pragma once
 #include <cstdint>
 #include "ptx.cuh"
@@ -27,19 +33,21 @@ namespace rnn {
 constexpr int kDecWarps = 4;
 constexpr int kDecRows = 16;    // query heads per unit
 
-// kDP: channels padded to 64 or 128.  kKeys: keys per warp and tile.
+// kDP: channels padded to 64 or 128.  kKeys: keys per warp and tile, 8 KB of
+// keys and values in either case.
 template <int kDP>
 struct DecShape {
-  static constexpr int kKeys = 16;
+  static constexpr int kKeys = 2048 / kDP;
   static constexpr int kTile = kDecWarps * kKeys;
   static constexpr int kRowBytes = kDP * 2;
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // per warp, K then V
-  static constexpr int kStages = 384 / kDP;
-  static constexpr int kMergeBytes = 2 * kDecRows * kDP * 4;
+  static constexpr int kStages = 3;
+  static constexpr int kMergeRow = kDP + 4;                  // floats; 4 against bank conflicts
+  static constexpr int kMergeBytes = 2 * 8 * kMergeRow * 4;  // of two warps, 8 heads
   static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes + kMergeBytes +
                                   kDecWarps * kDecRows * 8 + kDecWarps * kStages * 4;
 };
-constexpr int kDecTile = DecShape<128>::kTile;
+constexpr float kDecSlack = 8.f;  // log2 growth of the maximum before a rescale
 
 struct DecodeParams {
   const uint16_t *q, *kc, *vc;
@@ -51,6 +59,7 @@ struct DecodeParams {
   int64_t table_bs, num_pages;
   int B, Hq, Hkv, group, hblocks;  // group: query heads per key head; hblocks = ceil(group/16)
   int d, max_pages;
+  int page16;                      // page_size is a multiple of 16
   FastDiv page;
   float scale, c;                  // c = scale * log2(e)
   float* part;                     // [grid][2][16][kDP] unnormalised parts
@@ -75,20 +84,23 @@ __device__ __forceinline__ int dec_owner(int64_t w, int64_t total, int64_t grid)
   return static_cast<int>(c);
 }
 
-template <bool kBf16, int kDP>
+template <bool kBf16, int kDP, int kNT>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const DecodeParams p) {
   using S = DecShape<kDP>;
   constexpr int kKeys = S::kKeys, kStages = S::kStages;
-  constexpr int kSteps = kDP / 16;       // depth steps of Q K^T
-  constexpr int kTilesN = kDP / 8;       // 8-channel columns of the output
+  constexpr int kMT = kKeys / 16;        // 16-key groups
+  constexpr int kSteps = kDP / 16;       // depth steps of K Q^T, channel groups of V^T P^T
   constexpr int kChunks = kDP / 8;       // 16-byte chunks of a row
   constexpr int kRowsPer = 32 / kChunks; // rows moved by one warp-wide copy
-  constexpr float kBias = kBf16 ? 0.f : 15.f;
+  // fp16 keeps a probability down to 2^-24 only: scaled by 2^7 at the reference
+  // (2^15 with the slack), many small ones do not vanish from the weighted sum
+  // while the fp32 total keeps them
+  constexpr float kBias = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(dec_smem) + warp * kStages * S::kStageBytes;
   float* merge = reinterpret_cast<float*>(dec_smem + kDecWarps * kStages * S::kStageBytes);
-  float2* ml = reinterpret_cast<float2*>(merge + 2 * kDecRows * kDP);     // [warp][16]
+  float2* ml = reinterpret_cast<float2*>(merge + 2 * 8 * S::kMergeRow);  // [warp][16]
   uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
 
   const int Hv = p.Hkv * p.hblocks;
@@ -157,7 +169,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
       k.n = (k.len + S::kTile - 1) / S::kTile;
     } while (k.n == 0);
   };
-  // page of this lane's key (lane % kKeys) of a tile, -1 where there is none
+  // Page of key (lane % kKeys) of a tile, -1 where there is none.
   const int my_row = lane & (kKeys - 1);
   auto page_of = [&](const Cursor& k) -> int {
     const int t = k.j * S::kTile + warp * kKeys + my_row;
@@ -169,14 +181,38 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   const int ch = lane % kChunks, sub = lane / kChunks;
   const bool ch_live = ch * 8 < p.d;
   auto issue = [&](int stage, const Cursor& k, int id) {
-    const int t = k.j * S::kTile + warp * kKeys + my_row;
-    const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
-    const int hk = k.h / p.hblocks;
-    const int64_t ko = id * p.k_ps + row * p.k_ts + hk * p.k_hs;
-    const int64_t vo = id * p.v_ps + row * p.v_ts + hk * p.v_hs;
-    const unsigned valid = __ballot_sync(0xffffffffu, id >= 0) & ((1u << kKeys) - 1u);
+    const int t0 = k.j * S::kTile + warp * kKeys;
+    const int hk = p.hblocks == 1 ? k.h : k.h / p.hblocks;
+    const unsigned valid = __ballot_sync(0xffffffffu, id >= 0) &
+                           static_cast<unsigned>((1ull << kKeys) - 1u);
     if (lane == 0) masks[stage] = valid;
     const uint32_t dst = ring + stage * S::kStageBytes;
+    if (p.page16) {
+      // pages are whole 16-key groups: one base per group, no shuffles per row
+#pragma unroll
+      for (int g = 0; g < kMT; ++g) {
+        const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
+        const int t = t0 + g * 16;
+        const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div) + sub;
+        const uint16_t* ks = p.kc + (page * p.k_ps + hk * p.k_hs + row * p.k_ts + ch * 8);
+        const uint16_t* vs = p.vc + (page * p.v_ps + hk * p.v_hs + row * p.v_ts + ch * 8);
+#pragma unroll
+        for (int i = 0; i < 16 / kRowsPer; ++i) {
+          const int r = g * 16 + i * kRowsPer + sub;
+          const bool live = ((valid >> r) & 1u) && ch_live;
+          const uint32_t at = dst + r * S::kRowBytes + ((ch ^ (r & 7)) << 4);
+          cp_async16(at, live ? ks : p.kc, live);
+          cp_async16(at + kKeys * S::kRowBytes, live ? vs : p.vc, live);
+          ks += kRowsPer * p.k_ts;
+          vs += kRowsPer * p.v_ts;
+        }
+      }
+      return;
+    }
+    const int t = t0 + my_row;
+    const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
+    const int64_t ko = id * p.k_ps + row * p.k_ts + hk * p.k_hs;
+    const int64_t vo = id * p.v_ps + row * p.v_ts + hk * p.v_hs;
 #pragma unroll
     for (int i = 0; i < kKeys / kRowsPer; ++i) {
       const int r = i * kRowsPer + sub;
@@ -209,109 +245,137 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 #pragma unroll 1
   for (int s = 0; s < kStages - 1; ++s) issue_next();
 
-  uint32_t qf[kSteps][4];
-  float o[kTilesN][4];
-  float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
-  const int g = lane >> 2, q2 = (lane & 3) * 2;  // fragment row and column
+  uint32_t qf[kNT][kSteps][2];
+  float o[kNT][kSteps][4];   // channel 16 c + lane/4 (+ 8), head 8 n + 2 (lane%4) (+ 1)
+  float m[kNT][2], l[kNT][2];
+  const int g = lane >> 2, q2 = (lane & 3) * 2;
   bool fresh = true;
-  bool whole = cur.j == 0;  // the pair started in this share
+  bool whole = cur.j == 0;   // the pair started in this share
 #pragma unroll 1
   for (int64_t i = 0; i < work; ++i) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
     issue_next();
-    const int hk = cur.h / p.hblocks, hb = cur.h - hk * p.hblocks;
+    const int hk = p.hblocks == 1 ? cur.h : cur.h / p.hblocks, hb = cur.h - hk * p.hblocks;
     const int rows = min(kDecRows, p.group - hb * kDecRows);
     const int head0 = hk * p.group + hb * kDecRows;
     if (fresh) {
       const uint16_t* qb = p.q + cur.b * p.q_bs;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
+      for (int n = 0; n < kNT; ++n) {
+        const bool row_live = n * 8 + g < rows;
+        const uint16_t* qr = qb + (head0 + (row_live ? n * 8 + g : 0)) * p.q_hs;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = g + (e & 1) * 8, c = s * 16 + q2 + (e >> 1) * 8;
-          qf[s][e] = (r < rows && c < p.d)
-                         ? *reinterpret_cast<const uint32_t*>(qb + (head0 + r) * p.q_hs + c)
-                         : 0u;
+        for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = s * 16 + q2 + e * 8;
+            qf[n][s][e] = row_live && c < p.d ? *reinterpret_cast<const uint32_t*>(qr + c) : 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][s][e] = 0.f;
         }
-#pragma unroll
-      for (int n = 0; n < kTilesN; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-      m0 = m1 = kNegInf;
-      l0 = l1 = 0.f;
+        m[n][0] = m[n][1] = kNegInf;
+        l[n][0] = l[n][1] = 0.f;
+      }
       fresh = false;
     }
     const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + kKeys * S::kRowBytes;
     const uint32_t valid = masks[stage];
     if (valid) {
-      float s[2][4] = {};
-      {
-        // ldmatrix rows: keys (lane % 8) and 8 + (lane % 8), depth halves
-        const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+      float s[kMT][kNT][4];
+#pragma unroll
+      for (int t = 0; t < kMT; ++t) {
+        // two chains of products per score tile, added at the end
+        float s1[kNT][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][n][e] = s1[n][e] = 0.f;
+        const int r = t * 16 + (lane & 15), half = lane >> 4;
         const uint32_t rb = kb + r * S::kRowBytes;
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
           uint32_t f[4];
           ldsm_x4(rb + (((2 * st + half) ^ (r & 7)) << 4), f);
-          mma_16816<kBf16>(s[0], qf[st], f[0], f[1]);
-          mma_16816<kBf16>(s[1], qf[st], f[2], f[3]);
-        }
-      }
-      if (valid != (1u << kKeys) - 1u) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < kNT; ++n)
+            mma_16816<kBf16>(st & 1 ? s1[n] : s[t][n], f, qf[n][st][0], qf[n][st][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][n][e] += s1[n][e];
+      }
+      if (valid != static_cast<unsigned>((1ull << kKeys) - 1u)) {
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!((valid >> (n * 8 + q2 + (e & 1))) & 1u)) s[n][e] = kNegInf;
-      }
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      const bool up = x0 > m0 || x1 > m1;
-      if (__any_sync(0xffffffffu, up)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float a0 = m0 == kNegInf ? 0.f : exp2_approx((m0 - n0) * p.c);
-        const float a1 = m1 == kNegInf ? 0.f : exp2_approx((m1 - n1) * p.c);
-        m0 = n0;
-        m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
+            if (!((valid >> (t * 16 + g + (e >> 1) * 8)) & 1u))
 #pragma unroll
-        for (int n = 0; n < kTilesN; ++n) {
-          o[n][0] *= a0;
-          o[n][1] *= a0;
-          o[n][2] *= a1;
-          o[n][3] *= a1;
+              for (int n = 0; n < kNT; ++n) s[t][n][e] = kNegInf;
+      }
+      float x[kNT][2];
+      bool up = false;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+          for (int t = 1; t < kMT; ++t) x[n][e] = fmax3(x[n][e], s[t][n][e], s[t][n][e + 2]);
+          up = up || (x[n][e] - m[n][e]) * p.c > kDecSlack;  // also from -inf to a number
+        }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = x[n][e];
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            y = fmaxf(y, m[n][e]);
+            const float a = m[n][e] == kNegInf ? 0.f : exp2_approx((m[n][e] - y) * p.c);
+            m[n][e] = y;
+            l[n][e] *= a;
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c) {
+              o[n][c][e] *= a;
+              o[n][c][e + 2] *= a;
+            }
+          }
+      }
+      uint32_t pf[kMT][kNT][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const float z0 = (m[n][0] == kNegInf ? 0.f : m[n][0] * p.c) - kBias;
+        const float z1 = (m[n][1] == kNegInf ? 0.f : m[n][1] * p.c) - kBias;
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) {
+          const float e0 = exp2_approx(fmaf(s[t][n][0], p.c, -z0));
+          const float e1 = exp2_approx(fmaf(s[t][n][1], p.c, -z1));
+          const float e2 = exp2_approx(fmaf(s[t][n][2], p.c, -z0));
+          const float e3 = exp2_approx(fmaf(s[t][n][3], p.c, -z1));
+          l[n][0] += e0 + e2;
+          l[n][1] += e1 + e3;
+          // probabilities round to the value type for the second product; the
+          // totals above keep them in fp32
+          pf[t][n][0] = movmatrix_t(pack2<kBf16>(e0, e1));
+          pf[t][n][1] = movmatrix_t(pack2<kBf16>(e2, e3));
         }
       }
-      const float z0 = (m0 == kNegInf ? 0.f : m0 * p.c) - kBias;
-      const float z1 = (m1 == kNegInf ? 0.f : m1 * p.c) - kBias;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = exp2_approx(fmaf(s[n][0], p.c, -z0));
-        s[n][1] = exp2_approx(fmaf(s[n][1], p.c, -z0));
-        s[n][2] = exp2_approx(fmaf(s[n][2], p.c, -z1));
-        s[n][3] = exp2_approx(fmaf(s[n][3], p.c, -z1));
-        l0 += s[n][0] + s[n][1];
-        l1 += s[n][2] + s[n][3];
-      }
-      // probabilities round to the value type for the second product; the
-      // totals above keep them in fp32
-      const uint32_t a[4] = {pack2<kBf16>(s[0][0], s[0][1]), pack2<kBf16>(s[0][2], s[0][3]),
-                             pack2<kBf16>(s[1][0], s[1][1]), pack2<kBf16>(s[1][2], s[1][3])};
-      {
-        const int r = lane & 15, hi8 = lane >> 4;
+      for (int t = 0; t < kMT; ++t) {
+        const int r = t * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
         const uint32_t rb = vb + r * S::kRowBytes;
 #pragma unroll
-        for (int n = 0; n < kTilesN; n += 2) {
+        for (int c = 0; c < kSteps; ++c) {
           uint32_t f[4];
-          ldsm_x4_t(rb + (((n + hi8) ^ (r & 7)) << 4), f);
-          mma_16816<kBf16>(o[n], a, f[0], f[1]);
-          mma_16816<kBf16>(o[n + 1], a, f[2], f[3]);
+          ldsm_x4_t(rb + (((2 * c + half) ^ (r & 7)) << 4), f);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) mma_16816<kBf16>(o[n][c], f, pf[t][n][0], pf[t][n][1]);
         }
       }
     }
@@ -319,99 +383,89 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
     const bool last = cur.j == cur.n - 1;
     if (last || i == work - 1) {
       // ---- the pair ends here, or goes on in the next share
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-      if ((lane & 3) == 0) {
-        ml[warp * kDecRows + g] = make_float2(m0, l0);
-        ml[warp * kDecRows + g + 8] = make_float2(m1, l1);
-      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = l[n][e];
+          y += __shfl_xor_sync(0xffffffffu, y, 4);
+          y += __shfl_xor_sync(0xffffffffu, y, 8);
+          y += __shfl_xor_sync(0xffffffffu, y, 16);
+          if (g == 0) ml[warp * kDecRows + n * 8 + q2 + e] = make_float2(m[n][e], y);
+        }
       __syncthreads();
-      float M0 = kNegInf, M1 = kNegInf, L0 = 0.f, L1 = 0.f;
+      const bool done = whole && last;
+      // a pair that began in an earlier share fills slot 0, one that goes on slot 1
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (whole ? 1 : 0);
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        M0 = fmaxf(M0, ml[w * kDecRows + g].x);
-        M1 = fmaxf(M1, ml[w * kDecRows + g + 8].x);
-      }
+      for (int n = 0; n < kNT; ++n) {
+        if (n * 8 >= rows) break;
+        float f[2];
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float2 a = ml[w * kDecRows + g], b = ml[w * kDecRows + g + 8];
-        if (a.x != kNegInf) L0 += a.y * exp2_approx((a.x - M0) * p.c);
-        if (b.x != kNegInf) L1 += b.y * exp2_approx((b.x - M1) * p.c);
-      }
-      const float f0 = m0 == kNegInf ? 0.f : exp2_approx((m0 - M0) * p.c);
-      const float f1 = m1 == kNegInf ? 0.f : exp2_approx((m1 - M1) * p.c);
+        for (int e = 0; e < 2; ++e) {
+          float M = kNegInf;
 #pragma unroll
-      for (int n = 0; n < kTilesN; ++n) {
-        o[n][0] *= f0;
-        o[n][1] *= f0;
-        o[n][2] *= f1;
-        o[n][3] *= f1;
-      }
-      // warps 2 and 3 hand theirs to 0 and 1, then warp 1 to warp 0
-      auto put = [&](float* at) {
+          for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + n * 8 + q2 + e].x);
+          f[e] = m[n][e] == kNegInf ? 0.f : exp2_approx((m[n][e] - M) * p.c);
+        }
+        float* buf = merge + (warp & 1) * 8 * S::kMergeRow;
+        auto put = [&]() {
 #pragma unroll
-        for (int n = 0; n < kTilesN; ++n)
+          for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) at[(n * 4 + e) * 32 + lane] = o[n][e];
-      };
-      auto add = [&](const float* at) {
+            for (int e = 0; e < 4; ++e)
+              buf[(q2 + (e & 1)) * S::kMergeRow + c * 16 + g + (e >> 1) * 8] =
+                  o[n][c][e] * f[e & 1];
+        };
+        auto add = [&]() {
 #pragma unroll
-        for (int n = 0; n < kTilesN; ++n)
+          for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] += at[(n * 4 + e) * 32 + lane];
-      };
-      if (warp >= 2) put(merge + (warp - 2) * kDecRows * kDP);
-      __syncthreads();
-      if (warp < 2) add(merge + warp * kDecRows * kDP);
-      if (warp == 1) put(merge + kDecRows * kDP);
-      __syncthreads();
-      if (warp == 0) {
-        add(merge + kDecRows * kDP);
-        if (whole && last) {
-          const float i0 = L0 > 0.f ? 1.f / L0 : 0.f, i1 = L1 > 0.f ? 1.f / L1 : 0.f;
-          uint16_t* ob = p.out + cur.b * p.o_bs;
+            for (int e = 0; e < 4; ++e) {
+              float& at = buf[(q2 + (e & 1)) * S::kMergeRow + c * 16 + g + (e >> 1) * 8];
+              at = fmaf(o[n][c][e], f[e & 1], at);
+            }
+        };
+        if (warp >= 2) put();      // warps 2 and 3, then 0 and 1 on top
+        __syncthreads();
+        if (warp < 2) add();
+        __syncthreads();
+        for (int r = warp; r < 8 && n * 8 + r < rows; r += kDecWarps) {
+          const int row = n * 8 + r;
+          float M = kNegInf, L = 0.f;
 #pragma unroll
-          for (int n = 0; n < kTilesN; ++n) {
-            const int c = n * 8 + q2;
-            if (c < p.d && g < rows)
-              *reinterpret_cast<uint32_t*>(ob + (head0 + g) * p.o_hs + c) =
-                  pack2<kBf16>(o[n][0] * i0, o[n][1] * i0);
-            if (c < p.d && g + 8 < rows)
-              *reinterpret_cast<uint32_t*>(ob + (head0 + g + 8) * p.o_hs + c) =
-                  pack2<kBf16>(o[n][2] * i1, o[n][3] * i1);
+          for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + row].x);
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float2 a = ml[w * kDecRows + row];
+            if (a.x != kNegInf) L += a.y * exp2_approx((a.x - M) * p.c);
           }
-          if (p.lse && (lane & 3) == 0) {
-            float* lb = p.lse + static_cast<int64_t>(cur.b) * p.Hq + head0;
-            if (g < rows)
-              lb[g] = L0 > 0.f ? M0 * p.scale + (log2f(L0) - kBias) * 0.69314718f : kNegInf;
-            if (g + 8 < rows)
-              lb[g + 8] = L1 > 0.f ? M1 * p.scale + (log2f(L1) - kBias) * 0.69314718f : kNegInf;
-          }
-        } else {
-          // a pair that began in an earlier share fills slot 0, one that goes on slot 1
-          const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (whole ? 1 : 0);
-          float* pb = p.part + slot * kDecRows * kDP;
-#pragma unroll
-          for (int n = 0; n < kTilesN; ++n) {
-            const int c = n * 8 + q2;
-            if (g < rows)
-              *reinterpret_cast<float2*>(pb + g * kDP + c) = make_float2(o[n][0], o[n][1]);
-            if (g + 8 < rows)
-              *reinterpret_cast<float2*>(pb + (g + 8) * kDP + c) = make_float2(o[n][2], o[n][3]);
-          }
-          if ((lane & 3) == 0) {
-            p.part_ml[slot * kDecRows + g] = make_float2(M0, L0);
-            p.part_ml[slot * kDecRows + g + 8] = make_float2(M1, L1);
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const float* b0 = merge + r * S::kMergeRow;
+          const float* b1 = b0 + 8 * S::kMergeRow;
+          if (done) {
+            uint16_t* ob = p.out + cur.b * p.o_bs + (head0 + row) * p.o_hs;
+            for (int c = lane * 2; c < p.d; c += 64)
+              *reinterpret_cast<uint32_t*>(ob + c) =
+                  pack2<kBf16>((b0[c] + b1[c]) * inv, (b0[c + 1] + b1[c + 1]) * inv);
+            if (p.lse && lane == 0)
+              p.lse[static_cast<int64_t>(cur.b) * p.Hq + head0 + row] =
+                  L > 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
+          } else {
+            float* pb = p.part + (slot * kDecRows + row) * kDP;
+            for (int c = lane * 2; c < kDP; c += 64)
+              *reinterpret_cast<float2*>(pb + c) = make_float2(b0[c] + b1[c], b0[c + 1] + b1[c + 1]);
+            if (lane == 0) p.part_ml[slot * kDecRows + row] = make_float2(M, L);
           }
         }
-        if (whole && lane == 0) {
-          int c1 = blockIdx.x;
-          if (!last) c1 = dec_owner(lo + i + (cur.n - 1 - cur.j), total, grid);
-          p.span[static_cast<int64_t>(cur.b) * Hv + cur.h] = make_int2(blockIdx.x, c1);
-        }
+        if (n + 1 < kNT) __syncthreads();  // the next heads reuse the buffer
       }
+      if (whole && threadIdx.x == 0) {
+        int c1 = blockIdx.x;
+        if (!last) c1 = dec_owner(lo + i + (cur.n - 1 - cur.j), total, grid);
+        p.span[static_cast<int64_t>(cur.b) * Hv + cur.h] = make_int2(blockIdx.x, c1);
+      }
+      __syncthreads();  // the next pair's totals and sums come behind these reads
       fresh = true;
       whole = true;
     }
@@ -426,7 +480,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 template <bool kBf16, int kDP>
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParams p) {
   constexpr int kVals = kDP / 32;  // channels per lane
-  constexpr float kBias = kBf16 ? 0.f : 15.f;
+  constexpr float kBias = kBf16 ? 0.f : 7.f;
   __shared__ float acc[4][kDP];
   __shared__ float tot[4];
   pdl_wait();

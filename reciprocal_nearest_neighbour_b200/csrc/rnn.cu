@@ -3002,10 +3002,14 @@ static rnn_status attn_setup(DeviceInfo* di) {
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   const int d64 = static_cast<int>(DecShape<64>::kSmem), d128 = static_cast<int>(DecShape<128>::kSmem);
   const int p64 = static_cast<int>(AttnShape<64>::kSmem), p128 = static_cast<int>(AttnShape<128>::kSmem);
-  if (cudaFuncSetAttribute(attn_decode_kernel<true, 64>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 64>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<true, 128>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 128>, attr, d128) != cudaSuccess ||
+  if (cudaFuncSetAttribute(attn_decode_kernel<true, 64, 1>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 64, 1>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<true, 128, 1>, attr, d128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 128, 1>, attr, d128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<true, 64, 2>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 64, 2>, attr, d64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<true, 128, 2>, attr, d128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_decode_kernel<false, 128, 2>, attr, d128) != cudaSuccess ||
       cudaFuncSetAttribute(attn_prompt_kernel<true, 64>, attr, p64) != cudaSuccess ||
       cudaFuncSetAttribute(attn_prompt_kernel<false, 64>, attr, p64) != cudaSuccess ||
       cudaFuncSetAttribute(attn_prompt_kernel<true, 128>, attr, p128) != cudaSuccess ||
@@ -3109,6 +3113,25 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   return launched();
 }
 
+}  // extern "C"
+
+template <bool kBf16, int kDP>
+static rnn_status decode_launch(const DecodeParams& p, dim3 grid, cudaStream_t s) {
+  const dim3 block(kDecWarps * 32);
+  const size_t sm = DecShape<kDP>::kSmem;
+  if (p.group <= 8)
+    attn_decode_kernel<kBf16, kDP, 1><<<grid, block, sm, s>>>(p);
+  else
+    attn_decode_kernel<kBf16, kDP, 2><<<grid, block, sm, s>>>(p);
+  const rnn_status r = launched();
+  if (r != RNN_OK) return r;
+  launch_k(attn_decode_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
+           0, s, true, p);
+  return launched();
+}
+
+extern "C" {
+
 // Grid of the decode kernel: two CTAs per SM, or one per tile when there are fewer.
 constexpr int kDecMaxGrid = 2 * 160;
 struct DecWs {
@@ -3190,6 +3213,7 @@ rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int
   p.d = d;
   p.max_pages = max_pages;
   p.page = make_fastdiv(page_size);
+  p.page16 = page_size % 16 == 0;
   p.scale = scale;
   p.c = scale * 1.44269504f;
   p.part = w.part;
@@ -3198,29 +3222,14 @@ rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int
   p.err = w.err;
   const int64_t room = static_cast<int64_t>(max_pages) * page_size;
   const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
-  const int64_t tiles = (keys + kDecTile - 1) / kDecTile * B * Hkv * p.hblocks;
+  const int per_tile = d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile;
+  const int64_t tiles = (keys + per_tile - 1) / per_tile * B * Hkv * p.hblocks;
   const int most = std::min(2 * di->sms, kDecMaxGrid);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(kDecWarps * 32);
-  const dim3 jgrid(static_cast<unsigned>(B) * Hq);
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
   const bool bf = dtype == RNN_BF16;
-  if (d <= 64) {
-    const size_t sm = DecShape<64>::kSmem;
-    if (bf) attn_decode_kernel<true, 64><<<grid, block, sm, s>>>(p);
-    else attn_decode_kernel<false, 64><<<grid, block, sm, s>>>(p);
-  } else {
-    const size_t sm = DecShape<128>::kSmem;
-    if (bf) attn_decode_kernel<true, 128><<<grid, block, sm, s>>>(p);
-    else attn_decode_kernel<false, 128><<<grid, block, sm, s>>>(p);
-  }
-  if ((r = launched()) != RNN_OK) return r;
-  if (d <= 64) {
-    if (bf) launch_k(attn_decode_join_kernel<true, 64>, jgrid, dim3(128), 0, s, true, p);
-    else launch_k(attn_decode_join_kernel<false, 64>, jgrid, dim3(128), 0, s, true, p);
-  } else {
-    if (bf) launch_k(attn_decode_join_kernel<true, 128>, jgrid, dim3(128), 0, s, true, p);
-    else launch_k(attn_decode_join_kernel<false, 128>, jgrid, dim3(128), 0, s, true, p);
-  }
-  return launched();
+  if (d <= 64)
+    return bf ? decode_launch<true, 64>(p, grid, s) : decode_launch<false, 64>(p, grid, s);
+  return bf ? decode_launch<true, 128>(p, grid, s) : decode_launch<false, 128>(p, grid, s);
 }
 
 }  // extern "C"

@@ -55,6 +55,13 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// An 8x8 matrix of 16-bit values transposed across the warp.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 // c (16x8, fp32) += a (16x16) * b (16x8)
 template <bool kBf16>
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -97,10 +104,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// fp16 keeps probabilities down to 2^-24 only, so that many small ones would
-// vanish from the weighted sum while the fp32 total keeps them.  The fp16
-// forms scale them by 2^15 at the running maximum, the largest power of two
-// that fp16 holds, which cancels when the sum is divided by the total.
 constexpr float kNegInf = -__builtin_huge_valf();
 
 }  // namespace rnn
