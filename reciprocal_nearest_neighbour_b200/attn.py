@@ -56,50 +56,68 @@ def _strides(t: torch.Tensor, name: str):
     return out
 
 
-def _rows(t: Optional[torch.Tensor], name: str) -> _lib.Rows:
+_NO_ROWS = _lib.Rows(None, 0, 0)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, d: int) -> _lib.Rows:
     if t is None:
-        return _lib.Rows(None, 0, 0)
-    token, head = _strides(t, name)
-    return _lib.Rows(t.data_ptr(), token, head)
+        return _NO_ROWS
+    token, head, one = t.stride()
+    at = t.data_ptr()
+    if one != 1 or token < d or head < d or (token | head) & 7 or at & 15:
+        token, head = _strides(t, name)     # a dimension of size 1, or an error
+    return _lib.Rows(at, token, head)
 
 
-def _pages(t: torch.Tensor, name: str) -> _lib.Pages:
-    return _lib.Pages(t.data_ptr(), *_strides(t, name))
+def _pages(t: torch.Tensor, name: str, d: int) -> _lib.Pages:
+    page, token, head, one = t.stride()
+    at = t.data_ptr()
+    if one != 1 or page < d or token < d or head < d or (page | token | head) & 7 or at & 15:
+        page, token, head = _strides(t, name)
+    return _lib.Pages(at, page, token, head)
 
 
 def _ints(t, name: str, device, size: int) -> None:
     _check(t, name, 1, torch.int32, device)
-    if t.shape[0] != size:
-        raise ValueError(f"{name} must have {size} values, got {t.shape[0]}")
-    if size > 1 and t.stride(0) != 1:
+    if len(t) != size:
+        raise ValueError(f"{name} must have {size} values, got {len(t)}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _cu(t, name: str, device) -> int:
     _check(t, name, 1, torch.int32, device)
-    if t.shape[0] < 1:
+    n = len(t)
+    if n < 1:
         raise ValueError(f"{name} must have one value more than there are sequences")
-    _ints(t, name, device, t.shape[0])
-    return t.shape[0] - 1
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return n - 1
 
 
 def _table(t, device, B: int):
+    """Row stride and row length of the page table."""
     _check(t, "page_table", 2, torch.int32, device)
-    if t.shape[0] != B or t.shape[1] < 1:
+    rows, n = t.shape
+    if rows != B or n < 1:
         raise ValueError(f"page_table must have shape [{B}, pages >= 1], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    stride, one = t.stride()
+    if n > 1 and one != 1:
         raise ValueError("rows of page_table must be contiguous")
-    return t.stride(0) if B > 1 else t.shape[1]
+    return (stride if B > 1 else n), n
 
 
-def _cache(k_cache, v_cache, kind, device, heads: int, d: int) -> None:
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, name, 4, kind, device)
-        if t.shape[2:] != (heads, d) or t.shape[0] < 1 or t.shape[1] < 1:
-            raise ValueError(f"{name} must have shape [pages, page_size, {heads}, {d}], got "
-                             f"{tuple(t.shape)}")
-    if k_cache.shape != v_cache.shape:
+def _cache(k_cache, v_cache, kind, device, heads: int, d: int):
+    """Number of pages and page size."""
+    _check(k_cache, "k_cache", 4, kind, device)
+    _check(v_cache, "v_cache", 4, kind, device)
+    pages, size, h, dim = shape = k_cache.shape
+    if h != heads or dim != d or pages < 1 or size < 1:
+        raise ValueError(f"k_cache must have shape [pages, page_size, {heads}, {d}], got "
+                         f"{tuple(shape)}")
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
+    return pages, size
 
 
 def _heads(hq: int, hkv: int, d: int, d_max: int) -> None:
@@ -118,9 +136,11 @@ def _scale(scale: Optional[float], d: int) -> float:
     return scale
 
 
-def _like(out, want: torch.Size, kind, device, name: str) -> torch.Tensor:
-    if out is None:
-        return torch.empty(want, dtype=kind, device=device)
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _given(out, want: torch.Size, kind, device, name: str) -> torch.Tensor:
     _check(out, name, len(want), kind, device)
     if out.shape != want:
         raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(out.shape)}")
@@ -136,8 +156,16 @@ def _scratch(workspace, need: int, device) -> torch.Tensor:
     return workspace
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(fn, name: str, t: torch.Tensor, *args) -> None:
+    """``fn(*args, stream)`` with the device of `t` current, on its current stream."""
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _lib.check(code, name)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -184,10 +212,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         raise ValueError(f"channels per head must be a multiple of 8 up to 256, got {d}")
     if max(hq, hkv) > _lib.RNN_ATTN_MAX_HEADS:
         raise ValueError(f"at most {_lib.RNN_ATTN_MAX_HEADS} heads")
-    _cache(k_cache, v_cache, kind, dev, hkv, d)
+    num_pages, size = _cache(k_cache, v_cache, kind, dev, hkv, d)
     B = _cu(cu, "cu", dev)
     _ints(start, "start", dev, B)
-    table_stride = _table(page_table, dev, B)
+    table_stride, max_pages = _table(page_table, dev, B)
     pairs = axes = pos_stride = 0
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", 1, torch.float64, dev)
@@ -212,19 +240,18 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if 2 * pairs * axes > d:
         raise ValueError(f"{2 * pairs * axes} rotated channels do not fit into {d}")
     if q is not None:
-        q_out = _like(q_out, q.shape, kind, dev, "q_out")
-    if with_k or k_out is not None:
-        k_out = _like(k_out, k.shape, kind, dev, "k_out")
-    lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.rnn_kv_append(
-            _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), T, hq, hkv, d, _DT[kind],
-            _pages(k_cache, "k_cache"), _pages(v_cache, "v_cache"), k_cache.shape[0],
-            k_cache.shape[1], page_table.data_ptr(), table_stride, page_table.shape[1],
-            start.data_ptr(), cu.data_ptr(), B,
-            None if positions is None else positions.data_ptr(), pos_stride,
-            None if inv_freq is None else inv_freq.data_ptr(), pairs, axes, int(paired),
-            _rows(q_out, "q_out"), _rows(k_out, "k_out"), _stream(dev)), "rnn_kv_append")
+        q_out = _packed(q) if q_out is None else _given(q_out, q.shape, kind, dev, "q_out")
+    if k_out is not None:
+        _given(k_out, k.shape, kind, dev, "k_out")
+    elif with_k:
+        k_out = _packed(k)
+    _call(_lib.load().rnn_kv_append, "rnn_kv_append", k, _rows(q, "q", d), _rows(k, "k", d),
+          _rows(v, "v", d), T, hq, hkv, d, _DT[kind], _pages(k_cache, "k_cache", d),
+          _pages(v_cache, "v_cache", d), num_pages, size, page_table.data_ptr(), table_stride,
+          max_pages, start.data_ptr(), cu.data_ptr(), B,
+          None if positions is None else positions.data_ptr(), pos_stride,
+          None if inv_freq is None else inv_freq.data_ptr(), pairs, axes, paired,
+          _rows(q_out, "q_out", d), _rows(k_out, "k_out", d))
     return q_out, k_out
 
 
@@ -250,26 +277,26 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     _check(k, "k", 3, kind, dev)
     _check(v, "v", 3, kind, dev)
     Tq, hq, d = q.shape
-    Tk, hkv = k.shape[:2]
-    if k.shape != v.shape or k.shape[2] != d:
+    Tk, hkv, dk = k.shape
+    if dk != d or k.shape != v.shape:
         raise ValueError(f"k and v must have shape [tokens, heads, {d}], got {tuple(k.shape)} "
                          f"and {tuple(v.shape)}")
     _heads(hq, hkv, d, _lib.RNN_ATTN_MAX_DIM)
     B = _cu(cu_q, "cu_q", dev)
     if cu_k is None:
         cu_k = cu_q
-    _ints(cu_k, "cu_k", dev, B + 1)
+    else:
+        _ints(cu_k, "cu_k", dev, B + 1)
     scale = _scale(scale, d)
-    out = _like(out, q.shape, kind, dev, "out")
-    lse = torch.empty((Tq, hq), dtype=torch.float32, device=dev) if with_lse else None
     lib = _lib.load()
-    ws = _scratch(workspace, lib.rnn_attn_prompt_workspace_size(), dev)
-    with torch.cuda.device(dev):
-        _lib.check(lib.rnn_attn_prompt(
-            _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), Tq, Tk, hq, hkv, d, _DT[kind],
-            cu_q.data_ptr(), cu_k.data_ptr(), B, int(causal), scale, _rows(out, "out"),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
-            "rnn_attn_prompt")
+    out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
+    lse = torch.empty((Tq, hq), dtype=torch.float32, device=dev) if with_lse else None
+    need = lib.rnn_attn_prompt_workspace_size()
+    ws = _scratch(workspace, need, dev)
+    _call(lib.rnn_attn_prompt, "rnn_attn_prompt", q, _rows(q, "q", d), _rows(k, "k", d),
+          _rows(v, "v", d), Tq, Tk, hq, hkv, d, _DT[kind], cu_q.data_ptr(), cu_k.data_ptr(), B,
+          causal, scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(),
+          ws.data_ptr(), ws.numel())
     return (out, lse) if with_lse else out
 
 
@@ -292,19 +319,17 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
     hkv = k_cache.shape[2]
     _heads(hq, hkv, d, _lib.RNN_ATTN_MAX_DIM)
-    _cache(k_cache, v_cache, kind, dev, hkv, d)
+    num_pages, size = _cache(k_cache, v_cache, kind, dev, hkv, d)
     _ints(lens, "lens", dev, B)
-    table_stride = _table(page_table, dev, B)
+    table_stride, max_pages = _table(page_table, dev, B)
     scale = _scale(scale, d)
-    out = _like(out, q.shape, kind, dev, "out")
-    lse = torch.empty((B, hq), dtype=torch.float32, device=dev) if with_lse else None
     lib = _lib.load()
+    out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
+    lse = torch.empty((B, hq), dtype=torch.float32, device=dev) if with_lse else None
     ws = _scratch(workspace, lib.rnn_attn_decode_workspace_size(B, hq, hkv, d), dev)
-    with torch.cuda.device(dev):
-        _lib.check(lib.rnn_attn_decode(
-            _rows(q, "q"), _pages(k_cache, "k_cache"), _pages(v_cache, "v_cache"),
-            k_cache.shape[0], k_cache.shape[1], page_table.data_ptr(), table_stride,
-            page_table.shape[1], lens.data_ptr(), B, hq, hkv, d, _DT[kind], scale,
-            _rows(out, "out"), None if lse is None else lse.data_ptr(), ws.data_ptr(),
-            ws.numel(), _stream(dev)), "rnn_attn_decode")
+    _call(lib.rnn_attn_decode, "rnn_attn_decode", q, _rows(q, "q", d),
+          _pages(k_cache, "k_cache", d), _pages(v_cache, "v_cache", d), num_pages, size,
+          page_table.data_ptr(), table_stride, max_pages, lens.data_ptr(), B, hq, hkv, d,
+          _DT[kind], scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(),
+          ws.data_ptr(), ws.numel())
     return (out, lse) if with_lse else out
