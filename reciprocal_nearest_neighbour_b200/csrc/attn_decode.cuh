@@ -25,6 +25,7 @@
 // types): one vote per tile instead of a reduction across the warp.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include "ptx.cuh"
 #include "warp_mma.cuh"
 
@@ -47,6 +48,11 @@ struct DecShape {
   static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes + kMergeBytes +
                                   kDecWarps * kDecRows * 8 + kDecWarps * kStages * 4;
 };
+// What a pair costs beside its tiles (its queries' latency, the warps' merge),
+// in tiles, counted when the list is cut into shares.  96 streams of 50 to 8000
+// keys, 8 key heads of 128: 145 us without it, 108 at 2, 109 at 4, 114 at 8;
+// even lengths change by 1 %.
+constexpr int kDecPairCost = 2;
 constexpr float kDecSlack = 8.f;  // log2 growth of the maximum before a rescale
 
 struct DecodeParams {
@@ -73,10 +79,16 @@ __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
   const int64_t n = __ldg(p.lens + b);
   return static_cast<int>(n < 0 ? 0 : (n < room ? n : room));
 }
+// places of a sequence's pairs in the list: per pair its cost, then its tiles
+template <int kTile>
+__device__ __forceinline__ int64_t dec_places(const DecodeParams& p, int b) {
+  const int n = dec_len(p, b);
+  return n > 0 ? (n + kTile - 1) / kTile + kDecPairCost : 0;
+}
 __device__ __forceinline__ int64_t dec_share(int64_t c, int64_t total, int64_t grid) {
   return c * total / grid;
 }
-// the CTA whose share holds tile w
+// the CTA whose share holds place w
 __device__ __forceinline__ int dec_owner(int64_t w, int64_t total, int64_t grid) {
   int64_t c = w * grid / total;
   while (c + 1 < grid && dec_share(c + 1, total, grid) <= w) ++c;
@@ -111,7 +123,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   const int per = (p.B + kDecWarps * 32 - 1) / (kDecWarps * 32);
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += (dec_len(p, b) + S::kTile - 1) / S::kTile;
+  for (int b = b_lo; b < b_hi; ++b) mine += dec_places<S::kTile>(p, b);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -121,13 +133,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   if (lane == 31) scan[warp] = incl;
   if (threadIdx.x == 0) sh_b = p.B;
   __syncthreads();
-  int64_t before = incl - mine, tiles = 0;
+  int64_t before = incl - mine, places = 0;
   for (int w = 0; w < kDecWarps; ++w) {
     if (w < warp) before += scan[w];
-    tiles += scan[w];
+    places += scan[w];
   }
-  const int64_t total = tiles * Hv;
-  // CTAs with a share: no more than tiles, so that none inside a pair's span is empty
+  const int64_t total = places * Hv;
+  // CTAs with a share: no more than places, so that none inside a pair's span is empty
   const int64_t grid = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= grid) return;
   const int64_t lo = dec_share(blockIdx.x, total, grid);
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   if (lo >= before * Hv && lo < (before + mine) * Hv) {
     int64_t at = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t n = (dec_len(p, b) + S::kTile - 1) / S::kTile;
+      const int64_t n = dec_places<S::kTile>(p, b);
       if (lo < (at + n) * Hv) {
         sh_b = b;
         sh_before = at;
@@ -148,19 +160,24 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 
   struct Cursor {
     int b, h, j, n, len;  // sequence, head unit, tile, tiles, keys
+    int64_t at;           // place of the tile in the list
   } ld, cur;
   ld.b = sh_b;
   ld.len = dec_len(p, ld.b);
   ld.n = (ld.len + S::kTile - 1) / S::kTile;
   {
-    const int64_t r = lo - sh_before * Hv;
-    ld.h = static_cast<int>(r / ld.n);
-    ld.j = static_cast<int>(r - static_cast<int64_t>(ld.h) * ld.n);
+    // the share's first place is a tile, or stands for its pair's cost
+    const int64_t r = lo - sh_before * Hv, per_pair = ld.n + kDecPairCost;
+    ld.h = static_cast<int>(r / per_pair);
+    ld.j = max(0, static_cast<int>(r - ld.h * per_pair) - kDecPairCost);
+    ld.at = sh_before * Hv + ld.h * per_pair + kDecPairCost + ld.j;
   }
   cur = ld;
   auto advance = [&](Cursor& k) {
+    ++k.at;
     if (++k.j < k.n) return;
     k.j = 0;
+    k.at += kDecPairCost;
     if (++k.h < Hv) return;
     k.h = 0;
     do {
@@ -177,7 +194,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
     const int id = __ldg(p.table + k.b * p.table_bs + fdiv(t, p.page));
     return (id >= 0 && id < p.num_pages) ? id : -1;
   };
-  const int64_t work = hi - lo;
   const int ch = lane % kChunks, sub = lane / kChunks;
   const bool ch_live = ch * 8 < p.d;
   auto issue = [&](int stage, const Cursor& k, int id) {
@@ -225,20 +241,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
     }
   };
 
-  int64_t issued = 0;
   int fill = 0, stage = 0;  // ring places of the next load and of the current tile
   int next_id = page_of(ld);
   auto issue_next = [&]() {
-    if (issued < work) {
+    if (ld.at < hi) {
       const Cursor now = ld;
       const int id = next_id;
-      if (issued + 1 < work) {  // the next tile's pages are looked up a tile ahead
-        advance(ld);
-        next_id = page_of(ld);
-      }
+      advance(ld);
+      if (ld.at < hi) next_id = page_of(ld);  // the next tile's pages are looked up a tile ahead
       issue(fill, now, id);
     }
-    ++issued;
     fill = fill + 1 == kStages ? 0 : fill + 1;
     cp_async_commit();
   };
@@ -252,14 +264,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   bool fresh = true;
   bool whole = cur.j == 0;   // the pair started in this share
 #pragma unroll 1
-  for (int64_t i = 0; i < work; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    issue_next();
+  while (cur.at < hi) {
     const int hk = p.hblocks == 1 ? cur.h : cur.h / p.hblocks, hb = cur.h - hk * p.hblocks;
     const int rows = min(kDecRows, p.group - hb * kDecRows);
     const int head0 = hk * p.group + hb * kDecRows;
-    if (fresh) {
+    if (fresh) {  // under the wait for the first tile
       const uint16_t* qb = p.q + cur.b * p.q_bs;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
@@ -280,6 +289,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
       }
       fresh = false;
     }
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    issue_next();
     const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + kKeys * S::kRowBytes;
     const uint32_t valid = masks[stage];
     if (valid) {
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
     const bool last = cur.j == cur.n - 1;
-    if (last || i == work - 1) {
+    if (last || cur.at + 1 >= hi) {
       // ---- the pair ends here, or goes on in the next share
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
       }
       if (whole && threadIdx.x == 0) {
         int c1 = blockIdx.x;
-        if (!last) c1 = dec_owner(lo + i + (cur.n - 1 - cur.j), total, grid);
+        if (!last) c1 = dec_owner(cur.at + (cur.n - 1 - cur.j), total, grid);
         p.span[static_cast<int64_t>(cur.b) * Hv + cur.h] = make_int2(blockIdx.x, c1);
       }
       __syncthreads();  // the next pair's totals and sums come behind these reads
@@ -481,8 +493,9 @@ template <bool kBf16, int kDP>
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParams p) {
   constexpr int kVals = kDP / 32;  // channels per lane
   constexpr float kBias = kBf16 ? 0.f : 7.f;
+  using VecT = std::conditional_t<kVals == 4, float4, float2>;
   __shared__ float acc[4][kDP];
-  __shared__ float tot[4];
+  __shared__ float2 tot[4];
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
   const int b = blockIdx.x / p.Hq, head = blockIdx.x - b * p.Hq;
@@ -497,28 +510,38 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParam
   const int hb = in / kDecRows, row = in - hb * kDecRows;
   const int2 sp = p.span[static_cast<int64_t>(b) * (p.Hkv * p.hblocks) + hk * p.hblocks + hb];
   if (sp.x == sp.y) return;
-  auto slot_of = [&](int c) { return static_cast<int64_t>(c) * 2 + (c == sp.x ? 1 : 0); };
-  float M = kNegInf;
-  for (int c = sp.x + lane; c <= sp.y; c += 32) M = fmaxf(M, p.part_ml[slot_of(c) * kDecRows + row].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float v[kVals] = {}, L = 0.f;
+  // each warp reduces its parts with a running maximum (no pass for the maximum
+  // first: a part's totals and sums are fetched together), then the four meet
+  float v[kVals] = {}, M = kNegInf, L = 0.f;
+#pragma unroll 4
   for (int c = sp.x + warp; c <= sp.y; c += 4) {
-    const float2 a = p.part_ml[slot_of(c) * kDecRows + row];
-    const float f = a.x == kNegInf ? 0.f : exp2_approx((a.x - M) * p.c);
-    L += a.y * f;
-    const float* pb = p.part + (slot_of(c) * kDecRows + row) * kDP + lane * kVals;
+    const int64_t at = (static_cast<int64_t>(c) * 2 + (c == sp.x ? 1 : 0)) * kDecRows + row;
+    const float2 a = p.part_ml[at];
+    const VecT x = *reinterpret_cast<const VecT*>(p.part + at * kDP + lane * kVals);
+    const float* xs = reinterpret_cast<const float*>(&x);
+    const float top = fmaxf(M, a.x);
+    const float f = a.x == kNegInf ? 0.f : exp2_approx((a.x - top) * p.c);
+    const float h = M == kNegInf ? 0.f : exp2_approx((M - top) * p.c);
+    M = top;
+    L = L * h + a.y * f;
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) v[e] += pb[e] * f;
+    for (int e = 0; e < kVals; ++e) v[e] = v[e] * h + xs[e] * f;
   }
 #pragma unroll
   for (int e = 0; e < kVals; ++e) acc[warp][lane * kVals + e] = v[e];
-  if (lane == 0) tot[warp] = L;
+  if (lane == 0) tot[warp] = make_float2(M, L);
   __syncthreads();
-  L = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+  M = fmaxf(fmaxf(tot[0].x, tot[1].x), fmaxf(tot[2].x, tot[3].x));
+  float f[4];
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = tot[w].x == kNegInf ? 0.f : exp2_approx((tot[w].x - M) * p.c);
+    L += tot[w].y * f[w];
+  }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-    const float x = ((acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c])) * inv;
+    const float x = ((acc[0][c] * f[0] + acc[1][c] * f[1]) + (acc[2][c] * f[2] + acc[3][c] * f[3])) * inv;
     ob[c] = kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
                   : __half_as_ushort(__float2half_rn(x));
   }
