@@ -6,12 +6,13 @@
 // table[b][number / page_size].  A rotated pair of channels (x1, x2) becomes
 // (x1 cos a - x2 sin a, x2 cos a + x1 sin a) with a = position * inv_freq[i].
 //
-// Bound by memory: every channel is read once and written once or twice.  A
-// block takes a few tokens: first a warp per token looks its sequence and its
-// cache row up and makes the token's cosines and sines once (in 64 bits up to
-// the fraction of a turn: at position 10^6 a 32-bit angle is off by 0.06),
-// then all threads move the heads' channels in units of up to 2 x 16 bytes
-// (both halves of kVec pairs), which read the angles from shared memory.
+// Bound by memory: every channel is read once and written once or twice.  One
+// warp takes a token (for few tokens up to 8 warps share one), so nothing
+// waits at block level: it fetches its first units, looks the token's sequence
+// and cache row up under that latency, makes the token's cosines and sines once
+// (in 64 bits up to the fraction of a turn: at position 10^6 a 32-bit angle is
+// off by 0.06), and then moves the heads' channels in batches of kAppBatch units
+// of up to 2 x 16 bytes a lane, which keeps 4 KB a warp in flight.
 #pragma once
 #include <cstdint>
 #include "ptx.cuh"
@@ -19,8 +20,8 @@
 
 namespace rnn {
 
-constexpr int kAppThreads = 256;
-constexpr int kAppMaxTokens = 8;
+constexpr int kAppWarps = 8;
+constexpr int kAppBatch = 4;
 
 struct AppendParams {
   const uint16_t *q, *k, *v;        // q may be null
@@ -35,9 +36,8 @@ struct AppendParams {
   int max_pages, page_size;
   int pairs, axes;                  // channel pairs per axis, axes (0: no rotation)
   int paired;                       // pairs side by side instead of half a block apart
-  int tokens;                       // tokens per block
-  FastDiv by_row, by_unit, by_vunit;  // units of a token's rotated rows, of one such row, of a
-                                      // value row
+  int share;                        // log2 of the warps that share a token
+  FastDiv by_unit, by_vunit;        // units of a query or key row, of a value row
 };
 
 // Sequence of token t: the last b with cu[b] <= t, -1 before the first and B
@@ -73,129 +73,158 @@ __device__ __forceinline__ uint16_t app_bits(float x) {
                : __half_as_ushort(__float2half_rn(x));
 }
 
-// One unit of a rotated row: kVec pairs, or kVec channels behind the rotated
-// ones.  Outputs are rounded once from fp32.
-template <bool kBf16, int kVec>
-__device__ __forceinline__ void app_unit(const uint16_t* src, uint16_t* dst0, uint16_t* dst1,
-                                         int unit, const AppendParams& p, const float2* turn) {
+// A unit of a query or key row: kVec pairs (two vectors), or kVec channels
+// behind the rotated ones (one vector).
+template <int kVec>
+struct AppUnit {
   using V = typename VecOf<kVec>::T;
+  V a, b;
+};
+struct AppPlace {
+  int ca, cb, turn;  // channels of the two vectors (cb < 0: one), first pair's angle
+};
+template <int kVec>
+__device__ __forceinline__ AppPlace app_place(int unit, const AppendParams& p) {
   const int per_axis = p.pairs / kVec, rot = p.axes * per_axis;
+  AppPlace at;
   if (unit >= rot) {
-    const int c = 2 * p.axes * p.pairs + (unit - rot) * kVec;
-    const V x = *reinterpret_cast<const V*>(src + c);
-    if (dst0) *reinterpret_cast<V*>(dst0 + c) = x;
-    if (dst1) *reinterpret_cast<V*>(dst1 + c) = x;
-    return;
+    at.ca = 2 * p.axes * p.pairs + (unit - rot) * kVec;
+    at.cb = -1;
+    at.turn = 0;
+    return at;
   }
-  const int axis = (p.axes > 1 && unit >= per_axis) ? 1 : 0;
-  const int i0 = (unit - axis * per_axis) * kVec;          // first pair
+  const int axis = unit >= per_axis ? 1 : 0;
+  const int i0 = (unit - axis * per_axis) * kVec;  // first pair
   const int base = 2 * axis * p.pairs;
-  const int ca = base + (p.paired ? 2 * i0 : i0);
-  const int cb = p.paired ? ca + kVec : ca + p.pairs;
+  at.ca = base + (p.paired ? 2 * i0 : i0);
+  at.cb = p.paired ? at.ca + kVec : at.ca + p.pairs;
+  at.turn = axis * p.pairs + i0;
+  return at;
+}
+
+// Rotated in fp32, rounded once.
+template <bool kBf16, int kVec>
+__device__ __forceinline__ void app_rotate(AppUnit<kVec>& u, const float2* cs, bool paired) {
+  using V = typename VecOf<kVec>::T;
   union { V v[2]; uint16_t h[2 * kVec]; } x, y;
-  x.v[0] = *reinterpret_cast<const V*>(src + ca);
-  x.v[1] = *reinterpret_cast<const V*>(src + cb);
-  const float2* cs = turn + axis * p.pairs + i0;
+  x.v[0] = u.a;
+  x.v[1] = u.b;
+  if (paired) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) {
-    const float2 t = cs[e];
-    // pair e: elements (e, kVec + e) of halves, (2e, 2e + 1) side by side
-    const float a0 = app_float<kBf16>(x.h[e]), a1 = app_float<kBf16>(x.h[kVec + e]);
-    const float b0 = app_float<kBf16>(x.h[2 * e]), b1 = app_float<kBf16>(x.h[2 * e + 1]);
-    const float x1 = p.paired ? b0 : a0, x2 = p.paired ? b1 : a1;
-    const uint16_t r1 = app_bits<kBf16>(x1 * t.x - x2 * t.y);
-    const uint16_t r2 = app_bits<kBf16>(x2 * t.x + x1 * t.y);
-    if (p.paired) {
-      y.h[2 * e] = r1;
-      y.h[2 * e + 1] = r2;
-    } else {
-      y.h[e] = r1;
-      y.h[kVec + e] = r2;
+    for (int e = 0; e < kVec; ++e) {
+      const float2 t = cs[e];
+      const float x1 = app_float<kBf16>(x.h[2 * e]), x2 = app_float<kBf16>(x.h[2 * e + 1]);
+      y.h[2 * e] = app_bits<kBf16>(x1 * t.x - x2 * t.y);
+      y.h[2 * e + 1] = app_bits<kBf16>(x2 * t.x + x1 * t.y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const float2 t = cs[e];
+      const float x1 = app_float<kBf16>(x.h[e]), x2 = app_float<kBf16>(x.h[kVec + e]);
+      y.h[e] = app_bits<kBf16>(x1 * t.x - x2 * t.y);
+      y.h[kVec + e] = app_bits<kBf16>(x2 * t.x + x1 * t.y);
     }
   }
-  if (dst0) {
-    *reinterpret_cast<V*>(dst0 + ca) = y.v[0];
-    *reinterpret_cast<V*>(dst0 + cb) = y.v[1];
-  }
-  if (dst1) {
-    *reinterpret_cast<V*>(dst1 + ca) = y.v[0];
-    *reinterpret_cast<V*>(dst1 + cb) = y.v[1];
-  }
+  u.a = y.v[0];
+  u.b = y.v[1];
 }
 
 template <bool kBf16, int kVec>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendParams p) {
-  extern __shared__ float2 app_turn[];  // [tokens][axes * pairs] cos, sin
-  __shared__ int64_t k_at[kAppMaxTokens], v_at[kAppMaxTokens];  // cache rows, -1: nowhere
-  __shared__ int alive[kAppMaxTokens];
+__global__ void __launch_bounds__(kAppWarps * 32) kv_append_kernel(const AppendParams p) {
+  using V = typename VecOf<kVec>::T;
+  extern __shared__ __align__(16) float2 app_turns[];  // [warp][axes * pairs] cos, sin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * p.tokens;
-  const int nt = min(p.tokens, p.T - t0);
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kAppWarps + warp;
+  if ((gw >> p.share) >= p.T) return;
+  const int t = static_cast<int>(gw >> p.share);
+  const int part = static_cast<int>(gw) & ((1 << p.share) - 1);
+  const int first = part * 32 + lane, step = 32 << p.share;
   const int angles = p.axes * p.pairs;
-  for (int i = warp; i < nt; i += kAppThreads / 32) {
-    const int t = t0 + i;
-    const int b = find_sequence(p.cu, p.B, t, lane);
-    const bool live = b >= 0 && b < p.B;
-    int64_t place = 0, ka = -1, va = -1;
-    if (live) {
-      place = static_cast<int64_t>(__ldg(p.start + b)) + t - __ldg(p.cu + b);
-      if (place >= 0 && place < static_cast<int64_t>(p.max_pages) * p.page_size) {
-        const int pg = static_cast<int>(place / p.page_size);
-        const int row = static_cast<int>(place - static_cast<int64_t>(pg) * p.page_size);
-        const int64_t id = __ldg(p.table + b * p.table_bs + pg);
-        if (id >= 0 && id < p.num_pages) {
-          ka = id * p.kc_ps + row * p.kc_ts;
-          va = id * p.vc_ps + row * p.vc_ts;
-        }
-      }
-      for (int a = lane; a < angles; a += 32) {
-        const int axis = a >= p.pairs ? 1 : 0;
-        const double pos = p.positions
-                               ? static_cast<double>(p.positions[t * p.pos_ts + axis])
-                               : static_cast<double>(place);
-        double turns = pos * __ldg(p.inv_freq + (a - axis * p.pairs)) * 0.15915494309189533577;
-        turns -= rint(turns);
-        float s, c;
-        sincospif(2.0f * static_cast<float>(turns), &s, &c);
-        app_turn[i * angles + a] = make_float2(c, s);
-      }
+  float2* turn = app_turns + warp * angles;
+  const int row_units = p.by_unit.div;
+  const int n_units = (p.Hq + p.Hkv) * row_units;
+  const uint16_t* q_row = p.q + t * p.q_ts;  // never read without queries
+  const uint16_t* k_row = p.k + t * p.k_ts;
+  AppUnit<kVec> u[kAppBatch];
+  auto fetch = [&](int u0) {
+#pragma unroll
+    for (int i = 0; i < kAppBatch; ++i) {
+      const int r = u0 + i * step;
+      if (r >= n_units) break;
+      const int h = fdiv(r, p.by_unit);
+      const AppPlace at = app_place<kVec>(r - h * row_units, p);
+      const uint16_t* src = h < p.Hq ? q_row + h * p.q_hs : k_row + (h - p.Hq) * p.k_hs;
+      u[i].a = *reinterpret_cast<const V*>(src + at.ca);
+      if (at.cb >= 0) u[i].b = *reinterpret_cast<const V*>(src + at.cb);
     }
-    if (lane == 0) {
-      alive[i] = live;
-      k_at[i] = ka;
-      v_at[i] = va;
+  };
+  fetch(first);
+  // ---- the token's sequence, cache row and angles
+  const int b = find_sequence(p.cu, p.B, t, lane);
+  if (b < 0 || b >= p.B) return;
+  const int64_t place = static_cast<int64_t>(__ldg(p.start + b)) + t - __ldg(p.cu + b);
+  int64_t ka = -1, va = -1;  // its row in the caches, -1: nowhere
+  if (place >= 0 && place < static_cast<int64_t>(p.max_pages) * p.page_size) {
+    const int pg = static_cast<int>(place / p.page_size);
+    const int row = static_cast<int>(place - static_cast<int64_t>(pg) * p.page_size);
+    const int64_t id = __ldg(p.table + b * p.table_bs + pg);
+    if (id >= 0 && id < p.num_pages) {
+      ka = id * p.kc_ps + row * p.kc_ts;
+      va = id * p.vc_ps + row * p.vc_ts;
     }
   }
-  __syncthreads();
-  const int row_units = p.by_unit.div, tok_units = p.by_row.div;  // rotated rows
-  const int n_rot = nt * tok_units;
-  for (int u = threadIdx.x; u < n_rot; u += kAppThreads) {
-    const int i = fdiv(u, p.by_row);
-    if (!alive[i]) continue;
-    const int r = u - i * tok_units;
-    const int h = fdiv(r, p.by_unit), unit = r - h * row_units;
-    const int64_t t = t0 + i;
-    const uint16_t* src;
-    uint16_t *dst0, *dst1 = nullptr;
-    if (h < p.Hq) {
-      src = p.q + t * p.q_ts + h * p.q_hs;
-      dst0 = p.q_out + t * p.qo_ts + h * p.qo_hs;
-    } else {
-      const int hk = h - p.Hq;
-      src = p.k + t * p.k_ts + hk * p.k_hs;
-      dst0 = p.k_out ? p.k_out + t * p.ko_ts + hk * p.ko_hs : nullptr;
-      dst1 = k_at[i] >= 0 ? p.kc + k_at[i] + hk * p.kc_hs : nullptr;
-    }
-    app_unit<kBf16, kVec>(src, dst0, dst1, unit, p, app_turn + i * angles);
+  for (int a = lane; a < angles; a += 32) {
+    const int axis = a >= p.pairs ? 1 : 0;
+    const double pos = p.positions ? static_cast<double>(__ldg(p.positions + t * p.pos_ts + axis))
+                                   : static_cast<double>(place);
+    double turns = pos * __ldg(p.inv_freq + (a - axis * p.pairs)) * 0.15915494309189533577;
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.0f * static_cast<float>(turns), &s, &c);
+    turn[a] = make_float2(c, s);
   }
-  const int vrow = p.by_vunit.div, tok_v = p.Hkv * vrow;
-  for (int i = 0; i < nt; ++i) {
-    if (v_at[i] < 0) continue;
-    const int64_t t = t0 + i;
-    for (int r = threadIdx.x; r < tok_v; r += kAppThreads) {
-      const int h = fdiv(r, p.by_vunit), c = (r - h * vrow) * 8;
-      *reinterpret_cast<uint4*>(p.vc + v_at[i] + h * p.vc_hs + c) =
-          *reinterpret_cast<const uint4*>(p.v + t * p.v_ts + h * p.v_hs + c);
+  __syncwarp();
+  // ---- queries and keys
+  for (int u0 = first; u0 < n_units; u0 += kAppBatch * step) {
+    if (u0 != first) fetch(u0);
+#pragma unroll
+    for (int i = 0; i < kAppBatch; ++i) {
+      const int r = u0 + i * step;
+      if (r >= n_units) break;
+      const int h = fdiv(r, p.by_unit);
+      const AppPlace at = app_place<kVec>(r - h * row_units, p);
+      const bool two = at.cb >= 0;
+      if (two) app_rotate<kBf16, kVec>(u[i], turn + at.turn, p.paired != 0);
+      auto store = [&](uint16_t* dst) {
+        *reinterpret_cast<V*>(dst + at.ca) = u[i].a;
+        if (two) *reinterpret_cast<V*>(dst + at.cb) = u[i].b;
+      };
+      if (h < p.Hq) {
+        store(p.q_out + t * p.qo_ts + h * p.qo_hs);
+      } else {
+        if (p.k_out) store(p.k_out + t * p.ko_ts + (h - p.Hq) * p.ko_hs);
+        if (ka >= 0) store(p.kc + ka + (h - p.Hq) * p.kc_hs);
+      }
+    }
+  }
+  // ---- values
+  if (va < 0) return;
+  const int vrow = p.by_vunit.div, n_v = p.Hkv * vrow;
+  const uint16_t* v_row = p.v + t * p.v_ts;
+  uint16_t* v_dst = p.vc + va;
+  for (int r0 = first; r0 < n_v; r0 += kAppBatch * step) {
+    uint4 x[kAppBatch];
+#pragma unroll
+    for (int i = 0; i < kAppBatch; ++i) {
+      const int r = r0 + i * step, h = fdiv(r, p.by_vunit);
+      if (r < n_v)
+        x[i] = *reinterpret_cast<const uint4*>(v_row + h * p.v_hs + (r - h * vrow) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kAppBatch; ++i) {
+      const int r = r0 + i * step, h = fdiv(r, p.by_vunit);
+      if (r < n_v) *reinterpret_cast<uint4*>(v_dst + h * p.vc_hs + (r - h * vrow) * 8) = x[i];
     }
   }
 }

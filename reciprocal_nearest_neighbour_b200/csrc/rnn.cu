@@ -3236,10 +3236,10 @@ rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int
 
 template <bool kBf16>
 static void kv_append_launch(const AppendParams& p, int vec, dim3 grid, size_t smem, cudaStream_t s) {
-  if (vec == 8) kv_append_kernel<kBf16, 8><<<grid, kAppThreads, smem, s>>>(p);
-  else if (vec == 4) kv_append_kernel<kBf16, 4><<<grid, kAppThreads, smem, s>>>(p);
-  else if (vec == 2) kv_append_kernel<kBf16, 2><<<grid, kAppThreads, smem, s>>>(p);
-  else kv_append_kernel<kBf16, 1><<<grid, kAppThreads, smem, s>>>(p);
+  if (vec == 8) kv_append_kernel<kBf16, 8><<<grid, kAppWarps * 32, smem, s>>>(p);
+  else if (vec == 4) kv_append_kernel<kBf16, 4><<<grid, kAppWarps * 32, smem, s>>>(p);
+  else if (vec == 2) kv_append_kernel<kBf16, 2><<<grid, kAppWarps * 32, smem, s>>>(p);
+  else kv_append_kernel<kBf16, 1><<<grid, kAppWarps * 32, smem, s>>>(p);
 }
 
 extern "C" {
@@ -3313,13 +3313,12 @@ rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, 
   p.paired = paired != 0;
   const int vec = pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
   const int row_units = (axes * pairs + d - 2 * axes * pairs) / vec;
-  // one token a block until the blocks fill the GPU several times over
-  p.tokens = static_cast<int>(std::min<int64_t>(kAppMaxTokens, std::max<int64_t>(1, T / (16 * di->sms))));
+  // few tokens: up to 8 warps each, while all of them fit on the GPU at once
+  while (p.share < 3 && (T << (p.share + 1)) <= 16 * di->sms) ++p.share;
   p.by_unit = make_fastdiv(row_units);
-  p.by_row = make_fastdiv(row_units * (Hq + Hkv));
   p.by_vunit = make_fastdiv(d / 8);
-  const dim3 grid(static_cast<unsigned>((T + p.tokens - 1) / p.tokens));
-  const size_t smem = static_cast<size_t>(p.tokens) * axes * pairs * sizeof(float2);
+  const dim3 grid(static_cast<unsigned>(((T << p.share) + kAppWarps - 1) / kAppWarps));
+  const size_t smem = static_cast<size_t>(kAppWarps) * axes * pairs * sizeof(float2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == RNN_BF16) kv_append_launch<true>(p, vec, grid, smem, s);
   else kv_append_launch<false>(p, vec, grid, smem, s);
