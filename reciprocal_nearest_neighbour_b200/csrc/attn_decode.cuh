@@ -33,6 +33,7 @@ namespace rnn {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecRows = 16;    // query heads per unit
+constexpr int kDecMaxKeys = 0x7fffffff - 1023;  // whole tiles stay below 2^31
 
 // kDP: channels padded to 64 or 128.  kKeys: keys per warp and tile, 8 KB of
 // keys and values in either case.
@@ -75,7 +76,8 @@ struct DecodeParams {
 };
 
 __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
-  const int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
+  int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
+  if (room > kDecMaxKeys) room = kDecMaxKeys;
   const int64_t n = __ldg(p.lens + b);
   return static_cast<int>(n < 0 ? 0 : (n < room ? n : room));
 }

@@ -3047,6 +3047,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   if (Tq < 0 || Tk < 0 || Tq > INT32_MAX || Tk > INT32_MAX || B < 0) return RNN_EINVAL;
   rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
   if (r != RNN_OK) return r;
+  if (Tq > INT32_MAX - 1024 || Tk > INT32_MAX - 1024) return RNN_EUNSUPPORTED;
   if (!(scale > 0.f) || !(scale < 3e38f)) return RNN_EINVAL;
   if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return RNN_EINVAL;
   if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
