@@ -12,8 +12,11 @@
 //                   its 128 scores (tcgen05.ld), exponentiates them and writes
 //                   the probabilities back (tcgen05.st) over the scores as the
 //                   16-bit A operand of the second product
-//   warp 8          issues S = Q K^T and O += P V (tcgen05.mma), owns tensor memory
+//   warps 8, 10     issue S = Q K^T and O += P V (tcgen05.mma) of query tile 0 and
+//                   1; each wait and commit costs the issuing warp over a hundred
+//                   cycles, and one warp for both tiles bounds the kernel
 //   warp 9          TMA: query tiles, then a ring of alternating K and V tiles
+//   warps 12-15     outputs: normalise and store a finished unit's rows
 // Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
 //
 // A CTA is persistent.  The grid has one block per unit (a pair of query
@@ -45,12 +48,12 @@ namespace rnn {
 
 constexpr int kAttnM = 128;            // query rows per tile
 constexpr int kAttnN = 128;            // keys per tile
-constexpr int kAttnThreads = 384;      // three warpgroups; warps 10 and 11 only complete the third
-// Registers: launched with 168 a thread (65536 / 384 rounded down to 8), the
-// softmax warps hold 128 scores each and take what the third group gives up:
-// 256 * 208 + 128 * 88 = 384 * 168.
-constexpr int kAttnRegsSoftmax = 208, kAttnRegsOther = 88;
-constexpr int kAttnMmaWarp = 8, kAttnTmaWarp = 9;
+constexpr int kAttnThreads = 512;      // four warpgroups; warp 11 only completes the third
+// Registers: launched with 128 a thread, the softmax warps hold 128 scores each
+// and take what the other groups give up: 256 * 176 + 256 * 80 = 512 * 128.
+constexpr int kAttnRegsSoftmax = 176, kAttnRegsOther = 80;
+constexpr int kAttnMmaWarp = 8, kAttnTmaWarp = 9, kAttnMmaWarp2 = 10,
+              kAttnOutWarp = 12;
 constexpr float kAttnSlack = 8.f;      // log2 growth of the maximum before a rescale
 
 template <int kDP>
@@ -58,9 +61,21 @@ struct AttnShape {
   static constexpr int kBlocks = kDP / 64;               // 64-channel column blocks
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
-  static constexpr int kStages = kDP == 128 ? 5 : 8;
-  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 512;
+  static constexpr int kStages = kDP == 128 ? 4 : 8;
+  static constexpr int kStoreBytes = 32 * 128;           // a warp's rows, 64 channels at a time
+  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 4 * kStoreBytes + 2048 + 512;
+  // Tensor-memory columns: scores at 0 and 128, outputs at 256.  With 64
+  // channels the probabilities have columns of their own behind the outputs, so
+  // the next scores are made while these are exponentiated; with 128 they lie
+  // over the scores, and go to the second product in two halves, so that it
+  // starts while the second half is exponentiated.
+  static constexpr bool kOwnP = kDP == 64;
+  static constexpr int kOutCol = 2 * kAttnN;
+  static constexpr int kProbCol = kOwnP ? kOutCol + 2 * kDP : 0;
+  static constexpr int kProbStep = kOwnP ? kAttnN / 2 : kAttnN;  // between the two tiles
+  static constexpr int kParts = kOwnP ? 1 : 2;
 };
+constexpr int kTurnPolls = 100, kTurnChunk = 3;
 
 struct PromptParams {
   const int32_t *cu_q, *cu_k;
@@ -78,14 +93,41 @@ struct PromptParams {
   int stall_loads;
 };
 
-__device__ __forceinline__ void umma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
+// Four depth steps of D (+)= A B^T with one election: 64 channels of S = Q K^T
+// (both operands in shared memory, 32 bytes apart), or 64 keys of O += P V (A in
+// tensor memory, 8 columns apart; B 2048 bytes apart).  Issued one by one, each
+// with its own election, a product instruction costs its warp over a hundred
+// cycles, and the issuing warp bounds the kernel.
+__device__ __forceinline__ void umma_ss_x4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_x4(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -96,6 +138,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
       "r"(taddr)
+      : "memory");
+}
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -168,6 +223,36 @@ struct PromptTiles {
   }
 };
 
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t f2_make(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_get(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A count in shared memory, with the writes before it.
+__device__ __forceinline__ void st_release(int* at, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(at)), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int* at) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(at)) : "memory");
+  return v;
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -184,27 +269,36 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                    const __grid_constant__ CUtensorMap vmap) {
   using S = AttnShape<kDP>;
   constexpr float kBias = kBf16 ? 0.f : 7.f;
-  constexpr int kUnitReaders = 9;  // softmax warps and the MMA warp
+  constexpr int kUnitReaders = 14;  // softmax, MMA and output warps
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* q_tiles = smem;
   uint8_t* ring = smem + 2 * S::kTileBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S::kStages * S::kTileBytes);
+  uint8_t* staging = ring + S::kStages * S::kTileBytes;
+  float2* row_ml = reinterpret_cast<float2*>(staging + 4 * S::kStoreBytes);  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(row_ml + 2 * kAttnM);
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = full_bar + S::kStages;
   uint64_t* qfull_bar = empty_bar + S::kStages;
   uint64_t* qempty_bar = qfull_bar + 1;
   uint64_t* s_bar = qempty_bar + 1;  // scores of tile i are in tensor memory
-  uint64_t* p_bar = s_bar + 2;       // its probabilities are
-  uint64_t* o_bar = p_bar + 2;       // its output is complete
+  uint64_t* sfree_bar = s_bar + 2;   // its scores are in registers (kOwnP)
+  uint64_t* p_bar = sfree_bar + 2;   // its probabilities are there, by parts
+  uint64_t* o_bar = p_bar + 4;       // its output is complete; with kOwnP, so far
   uint64_t* ofree_bar = o_bar + 2;   // its output has been read
   uint64_t* ufull_bar = ofree_bar + 2;
   uint64_t* uempty_bar = ufull_bar + 2;
-  uint64_t* ask_bar = uempty_bar + 2;
+  uint64_t* ml_bar = uempty_bar + 2;  // its rows' maxima and totals are there
+  uint64_t* mlfree_bar = ml_bar + 2;  // and have been read
+  uint64_t* ask_bar = mlfree_bar + 2;
   uint64_t* drain_bar = ask_bar + 1;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  // counts that only grow, where a reader may be any number of steps behind
+  int* zero_at = reinterpret_cast<int*>(misc + 2);  // ragged V tiles whose end is zeroed
+  volatile int* turn_at = reinterpret_cast<volatile int*>(misc + 4);  // per softmax warp: steps
+                                                                      // whose exponentials are out
   __shared__ __align__(16) uint8_t answer[16];
   __shared__ PromptUnit units[2];
 
@@ -213,20 +307,26 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(smem_u32(&full_bar[s]), 1);
-      mbar_init(smem_u32(&empty_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 2);
     }
     mbar_init(smem_u32(qfull_bar), 1);
-    mbar_init(smem_u32(qempty_bar), 1);
+    mbar_init(smem_u32(qempty_bar), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_bar[i]), 1);
+      mbar_init(smem_u32(&sfree_bar[i]), 4);
       mbar_init(smem_u32(&p_bar[i]), 4);
+      mbar_init(smem_u32(&p_bar[2 + i]), 4);
       mbar_init(smem_u32(&o_bar[i]), 1);
       mbar_init(smem_u32(&ofree_bar[i]), 4);
+      mbar_init(smem_u32(&ml_bar[i]), 4);
+      mbar_init(smem_u32(&mlfree_bar[i]), 4);
       mbar_init(smem_u32(&ufull_bar[i]), 1);
       mbar_init(smem_u32(&uempty_bar[i]), kUnitReaders);
     }
+    for (int w = 0; w < 8; ++w) turn_at[w] = 0;
+    *zero_at = 0;
     mbar_init(smem_u32(ask_bar), 1);
-    mbar_init(smem_u32(drain_bar), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -263,7 +363,40 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   if (warp == kAttnTmaWarp) {
     // ------------------------------------------------- units and loads
     const int span = p.pair_heads ? kAttnM : 2 * kAttnM;  // tokens per unit
-    int base_b = 0, base_tile = 0;  // a group of 32 sequences and the tiles before it
+    // The sequences in groups of 32, the lanes of this warp: a group's are dealt
+    // longest keys first, so that the last units are short ones.
+    int base_b = 0, base_tile = 0, loaded = -1;
+    int g_q0 = 0, g_nq = 0, g_k0 = 0, g_nk = 0, g_tiles = 0, g_incl = 0;
+    auto load_group = [&]() {
+      const int b = base_b + lane;
+      int q0 = 0, nq = 0, k0 = 0, nk = -1;
+      if (b < p.B) {
+        q0 = clamp_at(p.cu_q, b, p.Tq);
+        nq = max(0, clamp_at(p.cu_q, b + 1, p.Tq) - q0);
+        k0 = clamp_at(p.cu_k, b, p.Tk);
+        nk = max(0, clamp_at(p.cu_k, b + 1, p.Tk) - k0);
+      }
+      const int members = min(32, p.B - base_b);
+      int rank = 0, src = 0;
+      for (int o = 0; o < members; ++o) {
+        const int x = __shfl_sync(0xffffffffu, nk, o);
+        rank += x > nk || (x == nk && o < lane);
+      }
+      for (int o = 0; o < members; ++o)
+        if (__shfl_sync(0xffffffffu, rank, o) == lane) src = o;
+      g_q0 = __shfl_sync(0xffffffffu, q0, src);
+      g_nq = __shfl_sync(0xffffffffu, nq, src);
+      g_k0 = __shfl_sync(0xffffffffu, k0, src);
+      g_nk = __shfl_sync(0xffffffffu, nk, src);
+      g_tiles = lane < members ? (g_nq + span - 1) / span : 0;
+      g_incl = g_tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, g_incl, o);
+        if (lane >= o) g_incl += y;
+      }
+      loaded = base_b;
+    };
     int block = blockIdx.x, issued = 0, q_loads = 0;
     int asked = 0;
     bool ok = true;
@@ -293,32 +426,20 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         u.hu = block - tile * p.head_units;
         if (tile < base_tile) base_b = base_tile = 0;  // blocks come in order, as a rule
         while (base_b < p.B) {
-          const int b = base_b + lane;
-          int q0 = 0, nq = 0;
-          if (b < p.B) {
-            q0 = clamp_at(p.cu_q, b, p.Tq);
-            nq = max(0, clamp_at(p.cu_q, b + 1, p.Tq) - q0);
-          }
-          const int tiles = (nq + span - 1) / span;
-          int incl = tiles;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          const unsigned behind = __ballot_sync(0xffffffffu, tile < base_tile + incl);
+          if (loaded != base_b) load_group();
+          const unsigned behind = __ballot_sync(0xffffffffu, tile < base_tile + g_incl);
           if (behind) {
             const int src = __ffs(behind) - 1;
-            const int before = __shfl_sync(0xffffffffu, incl - tiles, src) + base_tile;
-            const int n = __shfl_sync(0xffffffffu, tiles, src);
-            u.q0 = __shfl_sync(0xffffffffu, q0, src);
-            u.nq = __shfl_sync(0xffffffffu, nq, src);
+            const int before = __shfl_sync(0xffffffffu, g_incl - g_tiles, src) + base_tile;
+            const int n = __shfl_sync(0xffffffffu, g_tiles, src);
+            u.q0 = __shfl_sync(0xffffffffu, g_q0, src);
+            u.nq = __shfl_sync(0xffffffffu, g_nq, src);
+            u.k0 = __shfl_sync(0xffffffffu, g_k0, src);
+            u.nk = __shfl_sync(0xffffffffu, g_nk, src);
             u.m = (n - 1 - (tile - before)) * span;  // the rows with the most keys first
-            u.k0 = clamp_at(p.cu_k, base_b + src, p.Tk);
-            u.nk = max(0, clamp_at(p.cu_k, base_b + src + 1, p.Tk) - u.k0);
             break;
           }
-          base_tile += __shfl_sync(0xffffffffu, incl, 31);
+          base_tile += __shfl_sync(0xffffffffu, g_incl, 31);
           base_b += 32;
         }
         if (u.nq >= 0) break;
@@ -339,7 +460,6 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       }
       __syncwarp();
       if (u.nq < 0 || p.stall_loads) break;
-      ask();
       const PromptTiles t(p, u);
       if (t.n_max > 0 && lane == 0) {
         ok = mbar_wait_sleep(smem_u32(qempty_bar), (q_loads & 1) ^ 1u, abort_flag, p.err,
@@ -369,7 +489,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok || !answered()) break;
+      if (!ok) break;
+      // only now, a ring's length before the unit ends: a unit asked for early
+      // would wait here while other CTAs run out of work
+      ask();
+      if (!answered()) break;
     }
     if (lane == 0) {
       // no copy, and no arrival of a product's completion, is under way when the
@@ -393,109 +517,224 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           settle(&empty_bar[q % S::kStages], (q / S::kStages) & 1);
       }
     }
-  } else if (warp == kAttnMmaWarp) {
+  } else if (warp == kAttnMmaWarp || warp == kAttnMmaWarp2) {
     // ---------------------------------------------------------- products
+    const int i = warp == kAttnMmaWarp ? 0 : 1;  // this warp's query tile
     const int dsteps = (p.d + 15) / 16;
-    const uint64_t q_desc = make_sdesc(smem_u32(q_tiles), 64);
+    const uint64_t q_desc = make_sdesc(smem_u32(q_tiles) + i * S::kTileBytes, 64);
     const uint64_t k_desc = make_sdesc(smem_u32(ring), 64);
     const uint64_t v_desc = make_vdesc(smem_u32(ring));
     bool ok = true, any = false;
     int used = 0, q_used = 0;       // loads taken so far
-    int turns[2] = {0, 0};          // score tiles made so far per query tile
+    int turns = 0;                  // score tiles made so far
+    int zeroed = 0;                 // ragged V tiles so far
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, p.err,
-                                                   kErrWaitMma, lim));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(smem_u32(bar), parity, abort_flag, p.err,
+                                                        kErrWaitMma, lim));
       return ok;
     };
     auto slot_of = [&](int x) { return x % S::kStages; };
-    auto phase_of = [&](int x) { return static_cast<uint32_t>((x / S::kStages) & 1); };
+    auto wait_load = [&](int x) { return wait(&full_bar[slot_of(x)], (x / S::kStages) & 1); };
+    // this warp is done with a buffer: when its products so far are, or at once
+    auto release = [&](uint64_t* bar, bool behind_products) {
+      if (behind_products)
+        umma_commit_warp(smem_u32(bar));
+      else if (lane == 0)
+        mbar_arrive(smem_u32(bar));
+    };
+    auto scores = [&](int slot) {  // S_i = Q_i K^T
+      const uint64_t k_at = k_desc + static_cast<uint64_t>(slot * (S::kTileBytes >> 4));
+      // a last block with 16, 32 or 48 channels takes single steps
+      const int whole = dsteps >> 2;
+#pragma unroll
+      for (int c = 0; c < S::kBlocks; ++c) {
+        const uint32_t at = c * (S::kBlockBytes >> 4);
+        if (c < whole) {
+          umma_ss_x4(tmem + i * kAttnN, q_desc + at, k_at + at, p.idesc_s, c > 0);
+        } else {
+          for (int k = 0; k < dsteps - 4 * c; ++k)
+            umma_f16_warp(tmem + i * kAttnN, q_desc + at + 2 * k, k_at + at + 2 * k, p.idesc_s,
+                          c > 0 || k > 0);
+        }
+      }
+      umma_commit_warp(smem_u32(&s_bar[i]));
+      any = true;
+    };
     PromptUnit u;
     for (int it = 0; ok && take_unit(it, kErrWaitMma, u); ++it) {
       const PromptTiles t(p, u);
+      const int n = i ? t.n[1] : t.n[0];
+      // the last unit's output must have been read before this one's begins (its
+      // scores may go first); waited for at every unit, so that the parity is
+      // that of the last one
+      auto outputs_free = [&]() { return it == 0 || wait(&ofree_bar[i], (it - 1) & 1); };
+      if (n == 0 && !outputs_free()) break;
       if (t.n_max == 0) continue;
-      auto scores = [&](int i, int slot) {  // S_i = Q_i K^T
-        const uint64_t a = q_desc + static_cast<uint64_t>(i * (S::kTileBytes >> 4));
-        const uint64_t b = k_desc + static_cast<uint64_t>(slot * (S::kTileBytes >> 4));
-        for (int k = 0; k < dsteps; ++k) {
-          const uint32_t at = (k >> 2) * (S::kBlockBytes >> 4) + (k & 3) * 2;
-          umma_f16_warp(tmem + i * kAttnN, a + at, b + at, p.idesc_s, k > 0);
-        }
-        umma_commit_warp(smem_u32(&s_bar[i]));
-        any = true;
-      };
-      if (!wait(qfull_bar, q_used & 1) || !wait(&full_bar[slot_of(used)], phase_of(used))) break;
+      if (!wait(qfull_bar, q_used & 1) || !wait_load(used)) break;
       ++q_used;
       tc_fence_after();
       // the scores may overwrite the last unit's probabilities: the tensor pipe
       // works in order
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (t.n[i] > 0) scores(i, slot_of(used));
-      umma_commit_warp(smem_u32(&empty_bar[slot_of(used)]));
-      if (t.n_max == 1) umma_commit_warp(smem_u32(qempty_bar));
+      if (n > 0) scores(slot_of(used));
+      release(&empty_bar[slot_of(used)], n > 0);
+      if (n <= 1) release(qempty_bar, n == 1);
       __syncwarp();
-      for (int j = 0; j < t.n_max && ok; ++j) {
+      for (int j = 0; j < t.n_max; ++j) {
         const int kx = used + 2 * j + 2, vx = used + 2 * j + 1, vs = slot_of(vx);
-        if (!wait(&full_bar[vs], phase_of(vx))) break;
+        if (!wait_load(vx)) break;
         const int left = u.nk - j * kAttnN;
         if (left < kAttnN) {
           // rows behind the last key belong to other sequences: whatever they
           // hold, their probabilities are 0 and 0 * NaN must not reach the sum
-          uint8_t* vt = ring + vs * S::kTileBytes;
-          const int chunks = (kAttnN - left) * 8;
-          for (int c = 0; c < S::kBlocks; ++c)
-            for (int e = lane; e < chunks; e += 32)
-              *reinterpret_cast<uint4*>(vt + c * S::kBlockBytes + left * 128 + e * 16) =
-                  make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        bool k_ready = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (j >= t.n[i]) continue;
-          if (!wait(&p_bar[i], (turns[i] + j) & 1)) break;
-          // the last unit's output must have been read before this one's begins
-          if (j == 0 && it > 0 && !wait(&ofree_bar[i], (it - 1) & 1)) break;
-          tc_fence_after();
-          const uint64_t b = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
-#pragma unroll
-          for (int k = 0; k < kAttnN / 16; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
-            umma_f16_ts_warp(tmem + 2 * kAttnN + i * kDP, tmem + i * kAttnN + k * 8,
-                             b + static_cast<uint64_t>(k * (2048 >> 4)), p.idesc_o,
-                             (j > 0 || k > 0) ? 1u : 0u);
-          if (j + 1 < t.n[i]) {
-            if (!k_ready) {
-              if (!wait(&full_bar[slot_of(kx)], phase_of(kx))) break;
-              k_ready = true;
-              tc_fence_after();
-            }
-            scores(i, slot_of(kx));
+          if (i == 0) {
+            uint8_t* vt = ring + vs * S::kTileBytes;
+            const int chunks = (kAttnN - left) * 8;
+            for (int c = 0; c < S::kBlocks; ++c)
+              for (int e = lane; e < chunks; e += 32)
+                *reinterpret_cast<uint4*>(vt + c * S::kBlockBytes + left * 128 + e * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) st_release(zero_at, zeroed + 1);
           } else {
-            umma_commit_warp(smem_u32(&o_bar[i]));
+            const uint64_t t0 = globaltimer_ns();
+            while (ld_acquire(zero_at) <= zeroed) {
+              if (*abort_flag || globaltimer_ns() - t0 > lim) {
+                *abort_flag = 1;
+                atomicOr(p.err, kErrWaitMma);
+                ok = false;
+                break;
+              }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          ++zeroed;
+        }
+        if (j >= n) {
+          release(&empty_bar[vs], false);
+          if (j + 1 < t.n_max) {
+            if (!wait_load(kx)) break;
+            release(&empty_bar[slot_of(kx)], false);
           }
           __syncwarp();
+          continue;
+        }
+        auto next_scores = [&]() {
+          if constexpr (S::kOwnP)
+            if (!wait(&sfree_bar[i], (turns + j) & 1)) return;
+          tc_fence_after();
+          scores(slot_of(kx));
+        };
+        // (before the wait for the probabilities: a look at a barrier takes a couple
+        // of hundred cycles even when it is complete)
+        if (j + 1 < t.n_max && !wait_load(kx)) break;
+        if constexpr (S::kOwnP)
+          if (j + 1 < n) next_scores();
+        if (j == 0) outputs_free();
+        if (!ok) break;
+        const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h) {
+          constexpr int kGroups = kAttnN / 64 / S::kParts;  // of 64 keys
+          if (!wait(&p_bar[2 * h + i], (turns + j) & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = h * kGroups; k < (h + 1) * kGroups; ++k)
+            umma_ts_x4(tmem + S::kOutCol + i * kDP, tmem + S::kProbCol + i * S::kProbStep + k * 32,
+                       v_at + static_cast<uint64_t>(k * (8192 >> 4)), p.idesc_o,
+                       (j > 0 || k > 0) ? 1u : 0u);
         }
         if (!ok) break;
-        umma_commit_warp(smem_u32(&empty_bar[vs]));
-        if (j + 1 < t.n_max) umma_commit_warp(smem_u32(&empty_bar[slot_of(kx)]));
-        if (j + 2 == t.n_max) umma_commit_warp(smem_u32(qempty_bar));
+        if (S::kOwnP || j + 1 == n) umma_commit_warp(smem_u32(&o_bar[i]));
+        if constexpr (!S::kOwnP)
+          if (j + 1 < n) next_scores();
+        if (!ok) break;
+        release(&empty_bar[vs], true);
+        if (j + 1 < t.n_max) release(&empty_bar[slot_of(kx)], j + 1 < n);
+        if (j + 2 == n) release(qempty_bar, true);
         __syncwarp();
       }
       used += 2 * t.n_max;
-      turns[0] += t.n[0];
-      turns[1] += t.n[1];
+      turns += n;
     }
     if (*abort_flag && any) {
       // let every product issued finish before tensor memory is released
-      umma_commit_warp(smem_u32(drain_bar));
+      umma_commit_warp(smem_u32(&drain_bar[i]));
       __syncwarp();
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(drain_bar), 0)) {
+      while (!mbar_try_wait(smem_u32(&drain_bar[i]), 0)) {
         if (globaltimer_ns() - t0 > lim) {
           if (lane == 0) atomicOr(p.err, kErrDrain);
           break;
         }
+      }
+    }
+  } else if (warp >= kAttnOutWarp) {
+    // ----------------------------------------------------------- outputs
+    const int quad = warp & 3;
+    const uint32_t lane_at = static_cast<uint32_t>(quad * 32) << 16;
+    uint8_t* mine = staging + quad * S::kStoreBytes;
+    int outs[2] = {0, 0};
+    bool ok = true;
+    PromptUnit u;
+    for (int it = 0; ok && take_unit(it, kErrWaitEpilogue, u); ++it) {
+      const PromptTiles t(p, u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (the last totals being there, the output's phase before the last is over)
+        if (t.n[i] > 0) outs[i] += S::kOwnP ? t.n[i] : 1;
+        ok = ok && mbar_wait_sleep(smem_u32(&ml_bar[i]), it & 1, abort_flag, p.err,
+                                   kErrWaitEpilogue, lim);
+        const float2 ml = row_ml[i * kAttnM + quad * 32 + lane];
+        ok = ok && (t.n[i] == 0 ||
+                    mbar_wait_sleep(smem_u32(&o_bar[i]), (outs[i] - 1) & 1, abort_flag, p.err,
+                                    kErrWaitEpilogue, lim));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(smem_u32(&mlfree_bar[i]));
+        tc_fence_after();
+        const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
+        const int row = t.row0[i] + quad * 32;  // the warp's first row in the sequence
+        const int rows = min(32, u.nq - row);
+        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+        uint16_t* ob = p.out + static_cast<int64_t>(u.q0 + row) * p.o_ts + t.head[i] * p.o_hs;
+        // 64 channels at a time through shared memory (16-byte chunks, swizzled), so
+        // that a store covers 4 whole 128-byte rows; straight from its row, each
+        // thread would write 16 bytes of 32 different lines
+#pragma unroll 1
+        for (int c = 0; c < S::kBlocks; ++c) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float o[16];
+            if (t.n[i] > 0) tmem_ld16(o_at + c * 64 + g * 16, o);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = ml.y > 0.f ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
+                                  : 0u;
+              *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (c == S::kBlocks - 1) tc_fence_before();
+          __syncwarp();
+          if (c == S::kBlocks - 1 && lane == 0) mbar_arrive(smem_u32(&ofree_bar[i]));
+          const int ch = lane & 7, col = c * 64 + ch * 8;
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const int x = h * 4 + (lane >> 3);
+            if (x < rows && col < p.d)
+              *reinterpret_cast<uint4*>(ob + x * p.o_ts + col) =
+                  *reinterpret_cast<const uint4*>(mine + x * 128 + ((ch ^ (x & 7)) << 4));
+          }
+          __syncwarp();
+        }
+        if (p.lse && lane < rows)
+          p.lse[static_cast<int64_t>(u.q0 + row + lane) * p.Hq + t.head[i]] =
+              ml.y > 0.f ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
       }
     }
   }
@@ -506,13 +745,15 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     const int r = (warp & 3) * 32 + lane;     // row of the tile
     const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lane_at + i * kAttnN;
-    const uint32_t o_at = tmem + lane_at + 2 * kAttnN + i * kDP;
-    int turns = 0, outs = 0;                  // score tiles and outputs taken so far
+    const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
+    const uint32_t p_at = tmem + lane_at + S::kProbCol + i * S::kProbStep;
+    int turns = 0;                            // score tiles taken so far
+    int turns_o = 0;                          // the other tile's score tiles
     bool ok = true;
     PromptUnit u;
     for (int it = 0; take_unit(it, kErrWaitEpilogue, u); ++it) {
       const PromptTiles t(p, u);
-      const int n = i ? t.n[1] : t.n[0], head = i ? t.head[1] : t.head[0];
+      const int n = i ? t.n[1] : t.n[0], n_o = i ? t.n[0] : t.n[1];
       const int row0 = i ? t.row0[1] : t.row0[0];
       const int row = row0 + r;               // row of the sequence
       const int seen = p.causal ? min(u.nk, row + t.shift + 1) : u.nk;  // keys of this row
@@ -520,7 +761,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       float m = kNegInf, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        if (!mbar_wait(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, p.err, kErrWaitEpilogue,
+        if (!mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, p.err, kErrWaitEpilogue,
                        lim)) {
           ok = false;
           break;
@@ -532,6 +773,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         tmem_wait_ld_regs(s[0]);
 #pragma unroll
         for (int c = 1; c < 4; ++c) reg_fence(s[c]);
+        if constexpr (S::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sfree_bar[i]));
+        }
         if ((j + 1) * kAttnN > seen_all) {
           const int lim_col = seen - j * kAttnN;
 #pragma unroll
@@ -541,6 +787,15 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
               if (c * 32 + e >= lim_col) s[c][e] = kNegInf;
         }
         const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+        if constexpr (S::kOwnP) {
+          // the product before has read these columns, and its sum is complete
+          if (turns + j > 0 && !mbar_wait_spin(smem_u32(&o_bar[i]), (turns + j - 1) & 1, abort_flag,
+                                               p.err, kErrWaitEpilogue, lim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
         if (j == 0) {
           m = x;
         } else {
@@ -565,64 +820,55 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           }
         }
         const float z = (m == kNegInf ? 0.f : m * p.c) - kBias;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
+        // The two warps of a scheduler take turns at the exponential unit, tile 0's
+        // step j, tile 1's step j, tile 0's step j + 1: left alone they fall into
+        // step, and both leave it idle while both load and compare.  Order only: no
+        // result depends on it, and after kTurnPolls looks a warp goes on anyway.
+        const int j_o = i ? j : j - 1;  // the other's step to wait for
+        if (j_o >= 0 && j_o < n_o) {
+#pragma unroll 1
+          for (int k = 0; k < kTurnPolls && turn_at[warp ^ 4] <= turns_o + j_o; ++k) {
+          }
+        }
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a = exp2_approx(fmaf(s[c][2 * e], p.c, -z));
-            const float b = exp2_approx(fmaf(s[c][2 * e + 1], p.c, -z));
-            sum[e & 3] += a + b;
+            float a, b;
+            f2_get(f2_fma(f2_make(s[c][2 * e], s[c][2 * e + 1]), c2, z2), a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            sum[e & 1] = f2_add(sum[e & 1], f2_make(a, b));
             // the second product takes the probabilities in the value type
             // (half a step: 2^-9 of bf16, 2^-12 of fp16, of each weight); the
             // total keeps them in fp32
             w[e] = pack2<kBf16>(a, b);
           }
-          tmem_st16(s_at + c * 16, w);
+          if (c == kTurnChunk && lane == 0) turn_at[warp] = turns + j + 1;
+          tmem_st16(p_at + c * 16, w);
+          if ((c + 1) % (4 / S::kParts) == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_bar[2 * (c / (4 / S::kParts)) + i]));
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_bar[i]));
+        float a, b;
+        f2_get(f2_add(sum[0], sum[1]), a, b);
+        l += a + b;
       }
-      if (n > 0 && ok) {
-        ok = mbar_wait(smem_u32(&o_bar[i]), outs & 1, abort_flag, p.err, kErrWaitEpilogue, lim);
-        ++outs;
-        turns += n;
-      }
+      turns += n;
+      turns_o += n_o;
+      if (it > 0)
+        ok = ok && mbar_wait(smem_u32(&mlfree_bar[i]), (it - 1) & 1, abort_flag, p.err,
+                             kErrWaitEpilogue, lim);
       if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const bool live = row < u.nq;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      uint16_t* ob = p.out + static_cast<int64_t>(u.q0 + row) * p.o_ts + head * p.o_hs;
-#pragma unroll
-      for (int c = 0; c < kDP / 32; ++c) {
-        float o[32];
-        if (n > 0) {
-          tmem_ld32(o_at + c * 32, o);
-          tmem_wait_ld_regs(o);
-        }
-        if (c == kDP / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ofree_bar[i]));
-        }
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int col = c * 32 + h * 8;
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = l > 0.f ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv) : 0u;
-          if (live && col < p.d)
-            *reinterpret_cast<uint4*>(ob + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if (live && p.lse)
-        p.lse[static_cast<int64_t>(u.q0 + row) * p.Hq + head] =
-            l > 0.f ? m * p.scale + (log2f(l) - kBias) * 0.69314718f : kNegInf;
+      row_ml[i * kAttnM + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ml_bar[i]));
     }
   }
 
