@@ -538,8 +538,8 @@ rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, 
  *   scale    > 0, multiplies the scores.
  *   out      [Tq][Hq][d].
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
- * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded: see
- * rnn_workspace_status.
+ * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded; with a workspace (it
+ * may be NULL) rnn_workspace_status tells whether one ran out.
  */
 size_t rnn_attn_prompt_workspace_size(void);
 rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64_t Tk, int Hq,

@@ -10,6 +10,7 @@ pass as they are.  Calls run on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
@@ -29,6 +30,15 @@ def _check(t, name: str, ndim: int, dtype, device=None) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _all(kind, device, ndim: int, **tensors) -> None:
+    """Each of the tensors has this type, device and number of dimensions (else the error)."""
+    for t in tensors.values():
+        if not (isinstance(t, torch.Tensor) and t.dtype is kind and t.device == device
+                and t.dim() == ndim and t.is_cuda):
+            for name, u in tensors.items():
+                _check(u, name, ndim, kind, device)
 
 
 def _value_dtype(t, name: str):
@@ -78,17 +88,16 @@ def _pages(t: torch.Tensor, name: str, d: int) -> _lib.Pages:
 
 
 def _ints(t, name: str, device, size: int) -> None:
-    _check(t, name, 1, torch.int32, device)
-    if len(t) != size:
-        raise ValueError(f"{name} must have {size} values, got {len(t)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if _cu(t, name, device, 0) != size - 1:
+        raise ValueError(f"{name} must have {size} values, got {t.shape[0]}")
 
 
-def _cu(t, name: str, device) -> int:
-    _check(t, name, 1, torch.int32, device)
-    n = len(t)
-    if n < 1:
+def _cu(t, name: str, device, least: int = 1) -> int:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device
+            and t.dim() == 1 and t.is_cuda):
+        _check(t, name, 1, torch.int32, device)
+    n, = t.shape
+    if n < least:
         raise ValueError(f"{name} must have one value more than there are sequences")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -109,8 +118,7 @@ def _table(t, device, B: int):
 
 def _cache(k_cache, v_cache, kind, device, heads: int, d: int):
     """Number of pages and page size."""
-    _check(k_cache, "k_cache", 4, kind, device)
-    _check(v_cache, "v_cache", 4, kind, device)
+    _all(kind, device, 4, k_cache=k_cache, v_cache=v_cache)
     pages, size, h, dim = shape = k_cache.shape
     if h != heads or dim != d or pages < 1 or size < 1:
         raise ValueError(f"k_cache must have shape [pages, page_size, {heads}, {d}], got "
@@ -147,19 +155,25 @@ def _given(out, want: torch.Size, kind, device, name: str) -> torch.Tensor:
     return out
 
 
-def _scratch(workspace, need: int, device) -> torch.Tensor:
+def _given_scratch(workspace, device):
+    """Address and size of the caller's workspace, or none."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return None, 0
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
             workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel()
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_need(B: int, hq: int, hkv: int, d: int) -> int:
+    return _lib.load().rnn_attn_decode_workspace_size(B, hq, hkv, d)
 
 
 def _call(fn, name: str, t: torch.Tensor, *args) -> None:
     """``fn(*args, stream)`` with the device of `t` current, on its current stream."""
     index = t.get_device()
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -192,17 +206,16 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     exist is not stored.
     """
     kind = _value_dtype(k, "k")
-    _check(k, "k", 3, kind)
     dev = k.device
-    T, hkv, d = k.shape
-    _check(v, "v", 3, kind, dev)
-    if v.shape != k.shape:
+    _all(kind, dev, 3, k=k, v=v)
+    T, hkv, d = shape = k.shape
+    if v.shape != shape:
         raise ValueError(f"v must have the shape of k, got {tuple(v.shape)}")
     hq = 0
     if q is not None:
-        _check(q, "q", 3, kind, dev)
-        hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != d or hq < 1:
+        _all(kind, dev, 3, q=q)
+        tq, hq, dq = q.shape
+        if tq != T or dq != d or hq < 1:
             raise ValueError(f"q must have shape [{T}, heads, {d}], got {tuple(q.shape)}")
         if inv_freq is None:
             raise ValueError("q is only rotated: it needs inv_freq")
@@ -218,9 +231,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     table_stride, max_pages = _table(page_table, dev, B)
     pairs = axes = pos_stride = 0
     if inv_freq is not None:
-        _check(inv_freq, "inv_freq", 1, torch.float64, dev)
+        _all(torch.float64, dev, 1, inv_freq=inv_freq)
         pairs, axes = inv_freq.shape[0], 1
-        if pairs < 1 or (pairs > 1 and inv_freq.stride(0) != 1):
+        if pairs < 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous and not empty")
     if positions is not None:
         if inv_freq is None:
@@ -269,13 +282,13 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
 
     Returns ``out [Tq, Hq, d]``, or ``(out, lse)`` with ``lse [Tq, Hq]`` float32
     the log-sum-exp of the scaled scores.  A row that sees no key is 0 with
-    ``lse`` -inf; rows outside the sequences are not written.
+    ``lse`` -inf; rows outside the sequences are not written.  With a
+    ``workspace`` (uint8, 256 bytes) ``workspace_status`` tells whether a wait
+    of the kernel ran out.
     """
     kind = _value_dtype(q, "q")
-    _check(q, "q", 3, kind)
     dev = q.device
-    _check(k, "k", 3, kind, dev)
-    _check(v, "v", 3, kind, dev)
+    _all(kind, dev, 3, q=q, k=k, v=v)
     Tq, hq, d = q.shape
     Tk, hkv, dk = k.shape
     if dk != d or k.shape != v.shape:
@@ -291,12 +304,11 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     lib = _lib.load()
     out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
     lse = torch.empty((Tq, hq), dtype=torch.float32, device=dev) if with_lse else None
-    need = lib.rnn_attn_prompt_workspace_size()
-    ws = _scratch(workspace, need, dev)
+    ws, ws_bytes = _given_scratch(workspace, dev)
     _call(lib.rnn_attn_prompt, "rnn_attn_prompt", q, _rows(q, "q", d), _rows(k, "k", d),
           _rows(v, "v", d), Tq, Tk, hq, hkv, d, _DT[kind], cu_q.data_ptr(), cu_k.data_ptr(), B,
-          causal, scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          causal, scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(), ws,
+          ws_bytes)
     return (out, lse) if with_lse else out
 
 
@@ -312,8 +324,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``(out, lse [B, Hq])``.
     """
     kind = _value_dtype(q, "q")
-    _check(q, "q", 3, kind)
     dev = q.device
+    _all(kind, dev, 3, q=q)
     B, hq, d = q.shape
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
@@ -326,10 +338,12 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     lib = _lib.load()
     out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
     lse = torch.empty((B, hq), dtype=torch.float32, device=dev) if with_lse else None
-    ws = _scratch(workspace, lib.rnn_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    if workspace is None:
+        workspace = torch.empty(_decode_need(B, hq, hkv, d), dtype=torch.uint8, device=dev)
+    ws, ws_bytes = _given_scratch(workspace, dev)
     _call(lib.rnn_attn_decode, "rnn_attn_decode", q, _rows(q, "q", d),
           _pages(k_cache, "k_cache", d), _pages(v_cache, "v_cache", d), num_pages, size,
           page_table.data_ptr(), table_stride, max_pages, lens.data_ptr(), B, hq, hkv, d,
-          _DT[kind], scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          _DT[kind], scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(), ws,
+          ws_bytes)
     return (out, lse) if with_lse else out

@@ -88,7 +88,7 @@ struct PromptParams {
   int causal;
   float scale, c;              // c = scale * log2(e)
   uint32_t idesc_s, idesc_o;   // instruction descriptors of the two products
-  int* err;
+  int* err;                    // status word or null
   unsigned long long wait_limit_ns;
   int stall_loads;
 };
@@ -243,6 +243,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return r;
 }
 
+// A load that nothing waits for.
+__device__ __forceinline__ void touch(const int32_t* at) {
+  asm volatile("{\n\t.reg .s32 v;\n\tld.global.nc.s32 v, [%0];\n\t}" ::"l"(at));
+}
+
 // A count in shared memory, with the writes before it.
 __device__ __forceinline__ void st_release(int* at, int v) {
   asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(at)), "r"(v) : "memory");
@@ -303,42 +308,57 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   __shared__ PromptUnit units[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
-      mbar_init(smem_u32(&empty_bar[s]), 2);
-    }
+  // without a caller's word, a wait that runs out is noted here and only ends the kernel
+  int* const err = p.err ? p.err : reinterpret_cast<int*>(misc + 3);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
+  if (threadIdx.x < S::kStages) {
+    mbar_init(smem_u32(&full_bar[threadIdx.x]), 1);
+    mbar_init(smem_u32(&empty_bar[threadIdx.x]), 2);
+    fence_barrier_init();
+  } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
+    const int i = threadIdx.x - 32;
+    mbar_init(smem_u32(&s_bar[i]), 1);
+    mbar_init(smem_u32(&sfree_bar[i]), 4);
+    mbar_init(smem_u32(&p_bar[i]), 4);
+    mbar_init(smem_u32(&p_bar[2 + i]), 4);
+    mbar_init(smem_u32(&o_bar[i]), 1);
+    fence_barrier_init();
+  } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
+    const int i = threadIdx.x - 64;
+    mbar_init(smem_u32(&ofree_bar[i]), 4);
+    mbar_init(smem_u32(&ml_bar[i]), 4);
+    mbar_init(smem_u32(&mlfree_bar[i]), 4);
+    mbar_init(smem_u32(&ufull_bar[i]), 1);
+    mbar_init(smem_u32(&uempty_bar[i]), kUnitReaders);
+    mbar_init(smem_u32(&drain_bar[i]), 1);
+    fence_barrier_init();
+  } else if (threadIdx.x == 96) {
     mbar_init(smem_u32(qfull_bar), 1);
     mbar_init(smem_u32(qempty_bar), 2);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s_bar[i]), 1);
-      mbar_init(smem_u32(&sfree_bar[i]), 4);
-      mbar_init(smem_u32(&p_bar[i]), 4);
-      mbar_init(smem_u32(&p_bar[2 + i]), 4);
-      mbar_init(smem_u32(&o_bar[i]), 1);
-      mbar_init(smem_u32(&ofree_bar[i]), 4);
-      mbar_init(smem_u32(&ml_bar[i]), 4);
-      mbar_init(smem_u32(&mlfree_bar[i]), 4);
-      mbar_init(smem_u32(&ufull_bar[i]), 1);
-      mbar_init(smem_u32(&uempty_bar[i]), kUnitReaders);
-    }
-    for (int w = 0; w < 8; ++w) turn_at[w] = 0;
-    *zero_at = 0;
     mbar_init(smem_u32(ask_bar), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
-    *abort_flag = 0;
     fence_barrier_init();
+  } else if (threadIdx.x >= 128 && threadIdx.x < 136) {
+    turn_at[threadIdx.x - 128] = 0;
+    if (threadIdx.x == 128) {
+      *zero_at = 0;
+      *abort_flag = 0;
+    }
   }
   constexpr uint32_t kCols = 512;
   if (warp == kAttnMmaWarp) {
     tmem_alloc(smem_u32(misc), kCols);
     tmem_relinquish();
   }
-  if (warp == kAttnTmaWarp && lane == 0) {
-    tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
+  if (warp == kAttnTmaWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&qmap);
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+    if (lane <= p.B) {  // the first offsets, into the cache under the set-up
+      touch(p.cu_q + lane);
+      touch(p.cu_k + lane);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -350,7 +370,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   auto take_unit = [&](int it, int code, PromptUnit& u) {
     const int slot = it & 1;
     if (!__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ufull_bar[slot]), (it >> 1) & 1,
-                                                 abort_flag, p.err, code, lim)))
+                                                 abort_flag, err, code, lim)))
       return false;
     u = units[slot];
     __syncwarp();
@@ -359,385 +379,385 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   };
 
   if (warp >= kAttnMmaWarp) {
-  regs_give<kAttnRegsOther>();
-  if (warp == kAttnTmaWarp) {
-    // ------------------------------------------------- units and loads
-    const int span = p.pair_heads ? kAttnM : 2 * kAttnM;  // tokens per unit
-    // The sequences in groups of 32, the lanes of this warp: a group's are dealt
-    // longest keys first, so that the last units are short ones.
-    int base_b = 0, base_tile = 0, loaded = -1;
-    int g_q0 = 0, g_nq = 0, g_k0 = 0, g_nk = 0, g_tiles = 0, g_incl = 0;
-    auto load_group = [&]() {
-      const int b = base_b + lane;
-      int q0 = 0, nq = 0, k0 = 0, nk = -1;
-      if (b < p.B) {
-        q0 = clamp_at(p.cu_q, b, p.Tq);
-        nq = max(0, clamp_at(p.cu_q, b + 1, p.Tq) - q0);
-        k0 = clamp_at(p.cu_k, b, p.Tk);
-        nk = max(0, clamp_at(p.cu_k, b + 1, p.Tk) - k0);
-      }
-      const int members = min(32, p.B - base_b);
-      int rank = 0, src = 0;
-      for (int o = 0; o < members; ++o) {
-        const int x = __shfl_sync(0xffffffffu, nk, o);
-        rank += x > nk || (x == nk && o < lane);
-      }
-      for (int o = 0; o < members; ++o)
-        if (__shfl_sync(0xffffffffu, rank, o) == lane) src = o;
-      g_q0 = __shfl_sync(0xffffffffu, q0, src);
-      g_nq = __shfl_sync(0xffffffffu, nq, src);
-      g_k0 = __shfl_sync(0xffffffffu, k0, src);
-      g_nk = __shfl_sync(0xffffffffu, nk, src);
-      g_tiles = lane < members ? (g_nq + span - 1) / span : 0;
-      g_incl = g_tiles;
+    regs_give<kAttnRegsOther>();
+    if (warp == kAttnTmaWarp) {
+      // ------------------------------------------------- units and loads
+      const int span = p.pair_heads ? kAttnM : 2 * kAttnM;  // tokens per unit
+      // The sequences in groups of 32, the lanes of this warp: a group's are dealt
+      // longest keys first, so that the last units are short ones.
+      int base_b = 0, base_tile = 0, loaded = -1;
+      int g_q0 = 0, g_nq = 0, g_k0 = 0, g_nk = 0, g_tiles = 0, g_incl = 0;
+      auto load_group = [&]() {
+        const int b = base_b + lane;
+        int q0 = 0, nq = 0, k0 = 0, nk = -1;
+        if (b < p.B) {
+          q0 = clamp_at(p.cu_q, b, p.Tq);
+          nq = max(0, clamp_at(p.cu_q, b + 1, p.Tq) - q0);
+          k0 = clamp_at(p.cu_k, b, p.Tk);
+          nk = max(0, clamp_at(p.cu_k, b + 1, p.Tk) - k0);
+        }
+        const int members = min(32, p.B - base_b);
+        int rank = 0, src = 0;
+        for (int o = 0; o < members; ++o) {
+          const int x = __shfl_sync(0xffffffffu, nk, o);
+          rank += x > nk || (x == nk && o < lane);
+        }
+        for (int o = 0; o < members; ++o)
+          if (__shfl_sync(0xffffffffu, rank, o) == lane) src = o;
+        g_q0 = __shfl_sync(0xffffffffu, q0, src);
+        g_nq = __shfl_sync(0xffffffffu, nq, src);
+        g_k0 = __shfl_sync(0xffffffffu, k0, src);
+        g_nk = __shfl_sync(0xffffffffu, nk, src);
+        g_tiles = lane < members ? (g_nq + span - 1) / span : 0;
+        g_incl = g_tiles;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, g_incl, o);
-        if (lane >= o) g_incl += y;
-      }
-      loaded = base_b;
-    };
-    int block = blockIdx.x, issued = 0, q_loads = 0;
-    int asked = 0;
-    bool ok = true;
-    auto answered = [&]() {
-      if (!__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(ask_bar), (asked - 1) & 1, abort_flag,
-                                                   p.err, kErrWaitProducer, lim)))
-        return false;
-      block = next_block_read(smem_u32(answer));
-      fence_proxy_async_smem();  // read before the next answer is written
-      __syncwarp();
-      return true;
-    };
-    auto ask = [&]() {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(smem_u32(ask_bar), 16);
-        next_block_request(smem_u32(answer), smem_u32(ask_bar));
-      }
-      ++asked;
-      __syncwarp();
-    };
-    for (int it = 0;; ++it) {
-      PromptUnit u;
-      u.nq = -1;
-      while (block >= 0 && ok) {
-        // the sequences' query tiles make one list, head units inside
-        const int tile = block / p.head_units;
-        u.hu = block - tile * p.head_units;
-        if (tile < base_tile) base_b = base_tile = 0;  // blocks come in order, as a rule
-        while (base_b < p.B) {
-          if (loaded != base_b) load_group();
-          const unsigned behind = __ballot_sync(0xffffffffu, tile < base_tile + g_incl);
-          if (behind) {
-            const int src = __ffs(behind) - 1;
-            const int before = __shfl_sync(0xffffffffu, g_incl - g_tiles, src) + base_tile;
-            const int n = __shfl_sync(0xffffffffu, g_tiles, src);
-            u.q0 = __shfl_sync(0xffffffffu, g_q0, src);
-            u.nq = __shfl_sync(0xffffffffu, g_nq, src);
-            u.k0 = __shfl_sync(0xffffffffu, g_k0, src);
-            u.nk = __shfl_sync(0xffffffffu, g_nk, src);
-            u.m = (n - 1 - (tile - before)) * span;  // the rows with the most keys first
-            break;
-          }
-          base_tile += __shfl_sync(0xffffffffu, g_incl, 31);
-          base_b += 32;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, g_incl, o);
+          if (lane >= o) g_incl += y;
         }
-        if (u.nq >= 0) break;
-        // behind the last tile (the grid is an upper bound): take the rest of the
-        // blocks off the queue, so that none starts only to find nothing
-        ask();
-        ok = answered();
-      }
-      if (!ok) break;
-      const int slot = it & 1;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait_sleep(smem_u32(&uempty_bar[slot]), ((it >> 1) & 1) ^ 1u, abort_flag,
-                                      p.err, kErrWaitProducer, lim));
-      if (!ok) break;
-      if (lane == 0) {
-        units[slot] = u;
-        mbar_arrive(smem_u32(&ufull_bar[slot]));
-      }
-      __syncwarp();
-      if (u.nq < 0 || p.stall_loads) break;
-      const PromptTiles t(p, u);
-      if (t.n_max > 0 && lane == 0) {
-        ok = mbar_wait_sleep(smem_u32(qempty_bar), (q_loads & 1) ^ 1u, abort_flag, p.err,
-                             kErrWaitProducer, lim);
-        if (ok) {
-          const uint32_t qb = smem_u32(qfull_bar);
-          mbar_arrive_expect_tx(qb, 2 * S::kTileBytes);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            for (int c = 0; c < S::kBlocks; ++c)
-              tma_load_3d(smem_u32(q_tiles) + i * S::kTileBytes + c * S::kBlockBytes, &qmap, qb,
-                          c * 64, t.head[i], u.q0 + t.row0[i]);
-          ++q_loads;
-        }
-        const int kv_head = t.head[0] / p.group;
-        for (int j = 0; j < 2 * t.n_max && ok; ++j) {
-          const int s = issued % S::kStages;
-          ok = mbar_wait_sleep(smem_u32(&empty_bar[s]), ((issued / S::kStages) & 1) ^ 1u,
-                               abort_flag, p.err, kErrWaitProducer, lim);
-          if (!ok) break;
-          const uint32_t fb = smem_u32(&full_bar[s]);
-          mbar_arrive_expect_tx(fb, S::kTileBytes);
-          for (int c = 0; c < S::kBlocks; ++c)
-            tma_load_3d(smem_u32(ring) + s * S::kTileBytes + c * S::kBlockBytes,
-                        j & 1 ? &vmap : &kmap, fb, c * 64, kv_head, u.k0 + (j >> 1) * kAttnN);
-          ++issued;
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      // only now, a ring's length before the unit ends: a unit asked for early
-      // would wait here while other CTAs run out of work
-      ask();
-      if (!answered()) break;
-    }
-    if (lane == 0) {
-      // no copy, and no arrival of a product's completion, is under way when the
-      // CTA exits, whatever the other roles did
-      auto settle = [&](uint64_t* bar, uint32_t parity) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(smem_u32(bar), parity)) {
-          if (globaltimer_ns() - t0 > lim) {
-            atomicOr(p.err, kErrDrain);
-            return;
-          }
-        }
+        loaded = base_b;
       };
-      if (asked > 0) settle(ask_bar, (asked - 1) & 1);
-      if (q_loads > 0) settle(qfull_bar, (q_loads - 1) & 1);
-      for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-        settle(&full_bar[q % S::kStages], (q / S::kStages) & 1);
-      if (!*abort_flag) {
-        if (q_loads > 0) settle(qempty_bar, (q_loads - 1) & 1);
-        for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-          settle(&empty_bar[q % S::kStages], (q / S::kStages) & 1);
-      }
-    }
-  } else if (warp == kAttnMmaWarp || warp == kAttnMmaWarp2) {
-    // ---------------------------------------------------------- products
-    const int i = warp == kAttnMmaWarp ? 0 : 1;  // this warp's query tile
-    const int dsteps = (p.d + 15) / 16;
-    const uint64_t q_desc = make_sdesc(smem_u32(q_tiles) + i * S::kTileBytes, 64);
-    const uint64_t k_desc = make_sdesc(smem_u32(ring), 64);
-    const uint64_t v_desc = make_vdesc(smem_u32(ring));
-    bool ok = true, any = false;
-    int used = 0, q_used = 0;       // loads taken so far
-    int turns = 0;                  // score tiles made so far
-    int zeroed = 0;                 // ragged V tiles so far
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(smem_u32(bar), parity, abort_flag, p.err,
-                                                        kErrWaitMma, lim));
-      return ok;
-    };
-    auto slot_of = [&](int x) { return x % S::kStages; };
-    auto wait_load = [&](int x) { return wait(&full_bar[slot_of(x)], (x / S::kStages) & 1); };
-    // this warp is done with a buffer: when its products so far are, or at once
-    auto release = [&](uint64_t* bar, bool behind_products) {
-      if (behind_products)
-        umma_commit_warp(smem_u32(bar));
-      else if (lane == 0)
-        mbar_arrive(smem_u32(bar));
-    };
-    auto scores = [&](int slot) {  // S_i = Q_i K^T
-      const uint64_t k_at = k_desc + static_cast<uint64_t>(slot * (S::kTileBytes >> 4));
-      // a last block with 16, 32 or 48 channels takes single steps
-      const int whole = dsteps >> 2;
-#pragma unroll
-      for (int c = 0; c < S::kBlocks; ++c) {
-        const uint32_t at = c * (S::kBlockBytes >> 4);
-        if (c < whole) {
-          umma_ss_x4(tmem + i * kAttnN, q_desc + at, k_at + at, p.idesc_s, c > 0);
-        } else {
-          for (int k = 0; k < dsteps - 4 * c; ++k)
-            umma_f16_warp(tmem + i * kAttnN, q_desc + at + 2 * k, k_at + at + 2 * k, p.idesc_s,
-                          c > 0 || k > 0);
-        }
-      }
-      umma_commit_warp(smem_u32(&s_bar[i]));
-      any = true;
-    };
-    PromptUnit u;
-    for (int it = 0; ok && take_unit(it, kErrWaitMma, u); ++it) {
-      const PromptTiles t(p, u);
-      const int n = i ? t.n[1] : t.n[0];
-      // the last unit's output must have been read before this one's begins (its
-      // scores may go first); waited for at every unit, so that the parity is
-      // that of the last one
-      auto outputs_free = [&]() { return it == 0 || wait(&ofree_bar[i], (it - 1) & 1); };
-      if (n == 0 && !outputs_free()) break;
-      if (t.n_max == 0) continue;
-      if (!wait(qfull_bar, q_used & 1) || !wait_load(used)) break;
-      ++q_used;
-      tc_fence_after();
-      // the scores may overwrite the last unit's probabilities: the tensor pipe
-      // works in order
-      if (n > 0) scores(slot_of(used));
-      release(&empty_bar[slot_of(used)], n > 0);
-      if (n <= 1) release(qempty_bar, n == 1);
-      __syncwarp();
-      for (int j = 0; j < t.n_max; ++j) {
-        const int kx = used + 2 * j + 2, vx = used + 2 * j + 1, vs = slot_of(vx);
-        if (!wait_load(vx)) break;
-        const int left = u.nk - j * kAttnN;
-        if (left < kAttnN) {
-          // rows behind the last key belong to other sequences: whatever they
-          // hold, their probabilities are 0 and 0 * NaN must not reach the sum
-          if (i == 0) {
-            uint8_t* vt = ring + vs * S::kTileBytes;
-            const int chunks = (kAttnN - left) * 8;
-            for (int c = 0; c < S::kBlocks; ++c)
-              for (int e = lane; e < chunks; e += 32)
-                *reinterpret_cast<uint4*>(vt + c * S::kBlockBytes + left * 128 + e * 16) =
-                    make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) st_release(zero_at, zeroed + 1);
-          } else {
-            const uint64_t t0 = globaltimer_ns();
-            while (ld_acquire(zero_at) <= zeroed) {
-              if (*abort_flag || globaltimer_ns() - t0 > lim) {
-                *abort_flag = 1;
-                atomicOr(p.err, kErrWaitMma);
-                ok = false;
-                break;
-              }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
-          ++zeroed;
-        }
-        if (j >= n) {
-          release(&empty_bar[vs], false);
-          if (j + 1 < t.n_max) {
-            if (!wait_load(kx)) break;
-            release(&empty_bar[slot_of(kx)], false);
-          }
-          __syncwarp();
-          continue;
-        }
-        auto next_scores = [&]() {
-          if constexpr (S::kOwnP)
-            if (!wait(&sfree_bar[i], (turns + j) & 1)) return;
-          tc_fence_after();
-          scores(slot_of(kx));
-        };
-        // (before the wait for the probabilities: a look at a barrier takes a couple
-        // of hundred cycles even when it is complete)
-        if (j + 1 < t.n_max && !wait_load(kx)) break;
-        if constexpr (S::kOwnP)
-          if (j + 1 < n) next_scores();
-        if (j == 0) outputs_free();
-        if (!ok) break;
-        const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
-#pragma unroll
-        for (int h = 0; h < S::kParts; ++h) {
-          constexpr int kGroups = kAttnN / 64 / S::kParts;  // of 64 keys
-          if (!wait(&p_bar[2 * h + i], (turns + j) & 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int k = h * kGroups; k < (h + 1) * kGroups; ++k)
-            umma_ts_x4(tmem + S::kOutCol + i * kDP, tmem + S::kProbCol + i * S::kProbStep + k * 32,
-                       v_at + static_cast<uint64_t>(k * (8192 >> 4)), p.idesc_o,
-                       (j > 0 || k > 0) ? 1u : 0u);
-        }
-        if (!ok) break;
-        if (S::kOwnP || j + 1 == n) umma_commit_warp(smem_u32(&o_bar[i]));
-        if constexpr (!S::kOwnP)
-          if (j + 1 < n) next_scores();
-        if (!ok) break;
-        release(&empty_bar[vs], true);
-        if (j + 1 < t.n_max) release(&empty_bar[slot_of(kx)], j + 1 < n);
-        if (j + 2 == n) release(qempty_bar, true);
+      int block = blockIdx.x, issued = 0, q_loads = 0;
+      int asked = 0;
+      bool ok = true;
+      auto answered = [&]() {
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(ask_bar), (asked - 1) & 1, abort_flag,
+                                                     err, kErrWaitProducer, lim)))
+          return false;
+        block = next_block_read(smem_u32(answer));
+        fence_proxy_async_smem();  // read before the next answer is written
         __syncwarp();
-      }
-      used += 2 * t.n_max;
-      turns += n;
-    }
-    if (*abort_flag && any) {
-      // let every product issued finish before tensor memory is released
-      umma_commit_warp(smem_u32(&drain_bar[i]));
-      __syncwarp();
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&drain_bar[i]), 0)) {
-        if (globaltimer_ns() - t0 > lim) {
-          if (lane == 0) atomicOr(p.err, kErrDrain);
-          break;
+        return true;
+      };
+      auto ask = [&]() {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_u32(ask_bar), 16);
+          next_block_request(smem_u32(answer), smem_u32(ask_bar));
         }
-      }
-    }
-  } else if (warp >= kAttnOutWarp) {
-    // ----------------------------------------------------------- outputs
-    const int quad = warp & 3;
-    const uint32_t lane_at = static_cast<uint32_t>(quad * 32) << 16;
-    uint8_t* mine = staging + quad * S::kStoreBytes;
-    int outs[2] = {0, 0};
-    bool ok = true;
-    PromptUnit u;
-    for (int it = 0; ok && take_unit(it, kErrWaitEpilogue, u); ++it) {
-      const PromptTiles t(p, u);
+        ++asked;
+        __syncwarp();
+      };
+      for (int it = 0;; ++it) {
+        PromptUnit u;
+        u.nq = -1;
+        while (block >= 0 && ok) {
+          // the sequences' query tiles make one list, head units inside
+          const int tile = block / p.head_units;
+          u.hu = block - tile * p.head_units;
+          if (tile < base_tile) base_b = base_tile = 0;  // blocks come in order, as a rule
+          while (base_b < p.B) {
+            if (loaded != base_b) load_group();
+            const unsigned behind = __ballot_sync(0xffffffffu, tile < base_tile + g_incl);
+            if (behind) {
+              const int src = __ffs(behind) - 1;
+              const int before = __shfl_sync(0xffffffffu, g_incl - g_tiles, src) + base_tile;
+              const int n = __shfl_sync(0xffffffffu, g_tiles, src);
+              u.q0 = __shfl_sync(0xffffffffu, g_q0, src);
+              u.nq = __shfl_sync(0xffffffffu, g_nq, src);
+              u.k0 = __shfl_sync(0xffffffffu, g_k0, src);
+              u.nk = __shfl_sync(0xffffffffu, g_nk, src);
+              u.m = (n - 1 - (tile - before)) * span;  // the rows with the most keys first
+              break;
+            }
+            base_tile += __shfl_sync(0xffffffffu, g_incl, 31);
+            base_b += 32;
+          }
+          if (u.nq >= 0) break;
+          // behind the last tile (the grid is an upper bound): take the rest of the
+          // blocks off the queue, so that none starts only to find nothing
+          ask();
+          ok = answered();
+        }
+        if (!ok) break;
+        const int slot = it & 1;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_sleep(smem_u32(&uempty_bar[slot]), ((it >> 1) & 1) ^ 1u, abort_flag,
+                                        err, kErrWaitProducer, lim));
+        if (!ok) break;
+        if (lane == 0) {
+          units[slot] = u;
+          mbar_arrive(smem_u32(&ufull_bar[slot]));
+        }
+        __syncwarp();
+        if (u.nq < 0 || p.stall_loads) break;
+        const PromptTiles t(p, u);
+        if (t.n_max > 0 && lane == 0) {
+          ok = mbar_wait_sleep(smem_u32(qempty_bar), (q_loads & 1) ^ 1u, abort_flag, err,
+                               kErrWaitProducer, lim);
+          if (ok) {
+            const uint32_t qb = smem_u32(qfull_bar);
+            mbar_arrive_expect_tx(qb, 2 * S::kTileBytes);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // (the last totals being there, the output's phase before the last is over)
-        if (t.n[i] > 0) outs[i] += S::kOwnP ? t.n[i] : 1;
-        ok = ok && mbar_wait_sleep(smem_u32(&ml_bar[i]), it & 1, abort_flag, p.err,
-                                   kErrWaitEpilogue, lim);
-        const float2 ml = row_ml[i * kAttnM + quad * 32 + lane];
-        ok = ok && (t.n[i] == 0 ||
-                    mbar_wait_sleep(smem_u32(&o_bar[i]), (outs[i] - 1) & 1, abort_flag, p.err,
-                                    kErrWaitEpilogue, lim));
+            for (int i = 0; i < 2; ++i)
+              for (int c = 0; c < S::kBlocks; ++c)
+                tma_load_3d(smem_u32(q_tiles) + i * S::kTileBytes + c * S::kBlockBytes, &qmap, qb,
+                            c * 64, t.head[i], u.q0 + t.row0[i]);
+            ++q_loads;
+          }
+          const int kv_head = t.head[0] / p.group;
+          for (int j = 0; j < 2 * t.n_max && ok; ++j) {
+            const int s = issued % S::kStages;
+            ok = mbar_wait_sleep(smem_u32(&empty_bar[s]), ((issued / S::kStages) & 1) ^ 1u,
+                                 abort_flag, err, kErrWaitProducer, lim);
+            if (!ok) break;
+            const uint32_t fb = smem_u32(&full_bar[s]);
+            mbar_arrive_expect_tx(fb, S::kTileBytes);
+            for (int c = 0; c < S::kBlocks; ++c)
+              tma_load_3d(smem_u32(ring) + s * S::kTileBytes + c * S::kBlockBytes,
+                          j & 1 ? &vmap : &kmap, fb, c * 64, kv_head, u.k0 + (j >> 1) * kAttnN);
+            ++issued;
+          }
+        }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(smem_u32(&mlfree_bar[i]));
-        tc_fence_after();
-        const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
-        const int row = t.row0[i] + quad * 32;  // the warp's first row in the sequence
-        const int rows = min(32, u.nq - row);
-        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
-        uint16_t* ob = p.out + static_cast<int64_t>(u.q0 + row) * p.o_ts + t.head[i] * p.o_hs;
-        // 64 channels at a time through shared memory (16-byte chunks, swizzled), so
-        // that a store covers 4 whole 128-byte rows; straight from its row, each
-        // thread would write 16 bytes of 32 different lines
-#pragma unroll 1
-        for (int c = 0; c < S::kBlocks; ++c) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float o[16];
-            if (t.n[i] > 0) tmem_ld16(o_at + c * 64 + g * 16, o);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = ml.y > 0.f ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
-                                  : 0u;
-              *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+        // only now, a ring's length before the unit ends: a unit asked for early
+        // would wait here while other CTAs run out of work
+        ask();
+        if (!answered()) break;
+      }
+      if (lane == 0) {
+        // no copy, and no arrival of a product's completion, is under way when the
+        // CTA exits, whatever the other roles did
+        auto settle = [&](uint64_t* bar, uint32_t parity) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(smem_u32(bar), parity)) {
+            if (globaltimer_ns() - t0 > lim) {
+              atomicOr(err, kErrDrain);
+              return;
             }
           }
-          if (c == S::kBlocks - 1) tc_fence_before();
-          __syncwarp();
-          if (c == S::kBlocks - 1 && lane == 0) mbar_arrive(smem_u32(&ofree_bar[i]));
-          const int ch = lane & 7, col = c * 64 + ch * 8;
+        };
+        if (asked > 0) settle(ask_bar, (asked - 1) & 1);
+        if (q_loads > 0) settle(qfull_bar, (q_loads - 1) & 1);
+        for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
+          settle(&full_bar[q % S::kStages], (q / S::kStages) & 1);
+        if (!*abort_flag) {
+          if (q_loads > 0) settle(qempty_bar, (q_loads - 1) & 1);
+          for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
+            settle(&empty_bar[q % S::kStages], (q / S::kStages) & 1);
+        }
+      }
+    } else if (warp == kAttnMmaWarp || warp == kAttnMmaWarp2) {
+      // ---------------------------------------------------------- products
+      const int i = warp == kAttnMmaWarp ? 0 : 1;  // this warp's query tile
+      const int dsteps = (p.d + 15) / 16;
+      const uint64_t q_desc = make_sdesc(smem_u32(q_tiles) + i * S::kTileBytes, 64);
+      const uint64_t k_desc = make_sdesc(smem_u32(ring), 64);
+      const uint64_t v_desc = make_vdesc(smem_u32(ring));
+      bool ok = true, any = false;
+      int used = 0, q_used = 0;       // loads taken so far
+      int turns = 0;                  // score tiles made so far
+      int zeroed = 0;                 // ragged V tiles so far
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(smem_u32(bar), parity, abort_flag, err,
+                                                          kErrWaitMma, lim));
+        return ok;
+      };
+      auto slot_of = [&](int x) { return x % S::kStages; };
+      auto wait_load = [&](int x) { return wait(&full_bar[slot_of(x)], (x / S::kStages) & 1); };
+      // this warp is done with a buffer: when its products so far are, or at once
+      auto release = [&](uint64_t* bar, bool behind_products) {
+        if (behind_products)
+          umma_commit_warp(smem_u32(bar));
+        else if (lane == 0)
+          mbar_arrive(smem_u32(bar));
+      };
+      auto scores = [&](int slot) {  // S_i = Q_i K^T
+        const uint64_t k_at = k_desc + static_cast<uint64_t>(slot * (S::kTileBytes >> 4));
+        // a last block with 16, 32 or 48 channels takes single steps
+        const int whole = dsteps >> 2;
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const int x = h * 4 + (lane >> 3);
-            if (x < rows && col < p.d)
-              *reinterpret_cast<uint4*>(ob + x * p.o_ts + col) =
-                  *reinterpret_cast<const uint4*>(mine + x * 128 + ((ch ^ (x & 7)) << 4));
+        for (int c = 0; c < S::kBlocks; ++c) {
+          const uint32_t at = c * (S::kBlockBytes >> 4);
+          if (c < whole) {
+            umma_ss_x4(tmem + i * kAttnN, q_desc + at, k_at + at, p.idesc_s, c > 0);
+          } else {
+            for (int k = 0; k < dsteps - 4 * c; ++k)
+              umma_f16_warp(tmem + i * kAttnN, q_desc + at + 2 * k, k_at + at + 2 * k, p.idesc_s,
+                            c > 0 || k > 0);
           }
+        }
+        umma_commit_warp(smem_u32(&s_bar[i]));
+        any = true;
+      };
+      PromptUnit u;
+      for (int it = 0; ok && take_unit(it, kErrWaitMma, u); ++it) {
+        const PromptTiles t(p, u);
+        const int n = i ? t.n[1] : t.n[0];
+        // the last unit's output must have been read before this one's begins (its
+        // scores may go first); waited for at every unit, so that the parity is
+        // that of the last one
+        auto outputs_free = [&]() { return it == 0 || wait(&ofree_bar[i], (it - 1) & 1); };
+        if (n == 0 && !outputs_free()) break;
+        if (t.n_max == 0) continue;
+        if (!wait(qfull_bar, q_used & 1) || !wait_load(used)) break;
+        ++q_used;
+        tc_fence_after();
+        // the scores may overwrite the last unit's probabilities: the tensor pipe
+        // works in order
+        if (n > 0) scores(slot_of(used));
+        release(&empty_bar[slot_of(used)], n > 0);
+        if (n <= 1) release(qempty_bar, n == 1);
+        __syncwarp();
+        for (int j = 0; j < t.n_max; ++j) {
+          const int kx = used + 2 * j + 2, vx = used + 2 * j + 1, vs = slot_of(vx);
+          if (!wait_load(vx)) break;
+          const int left = u.nk - j * kAttnN;
+          if (left < kAttnN) {
+            // rows behind the last key belong to other sequences: whatever they
+            // hold, their probabilities are 0 and 0 * NaN must not reach the sum
+            if (i == 0) {
+              uint8_t* vt = ring + vs * S::kTileBytes;
+              const int chunks = (kAttnN - left) * 8;
+              for (int c = 0; c < S::kBlocks; ++c)
+                for (int e = lane; e < chunks; e += 32)
+                  *reinterpret_cast<uint4*>(vt + c * S::kBlockBytes + left * 128 + e * 16) =
+                      make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) st_release(zero_at, zeroed + 1);
+            } else {
+              const uint64_t t0 = globaltimer_ns();
+              while (ld_acquire(zero_at) <= zeroed) {
+                if (*abort_flag || globaltimer_ns() - t0 > lim) {
+                  *abort_flag = 1;
+                  atomicOr(err, kErrWaitMma);
+                  ok = false;
+                  break;
+                }
+              }
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            ++zeroed;
+          }
+          if (j >= n) {
+            release(&empty_bar[vs], false);
+            if (j + 1 < t.n_max) {
+              if (!wait_load(kx)) break;
+              release(&empty_bar[slot_of(kx)], false);
+            }
+            __syncwarp();
+            continue;
+          }
+          auto next_scores = [&]() {
+            if constexpr (S::kOwnP)
+              if (!wait(&sfree_bar[i], (turns + j) & 1)) return;
+            tc_fence_after();
+            scores(slot_of(kx));
+          };
+          // (before the wait for the probabilities: a look at a barrier takes a couple
+          // of hundred cycles even when it is complete)
+          if (j + 1 < t.n_max && !wait_load(kx)) break;
+          if constexpr (S::kOwnP)
+            if (j + 1 < n) next_scores();
+          if (j == 0) outputs_free();
+          if (!ok) break;
+          const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
+#pragma unroll
+          for (int h = 0; h < S::kParts; ++h) {
+            constexpr int kGroups = kAttnN / 64 / S::kParts;  // of 64 keys
+            if (!wait(&p_bar[2 * h + i], (turns + j) & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = h * kGroups; k < (h + 1) * kGroups; ++k)
+              umma_ts_x4(tmem + S::kOutCol + i * kDP, tmem + S::kProbCol + i * S::kProbStep + k * 32,
+                         v_at + static_cast<uint64_t>(k * (8192 >> 4)), p.idesc_o,
+                         (j > 0 || k > 0) ? 1u : 0u);
+          }
+          if (!ok) break;
+          if (S::kOwnP || j + 1 == n) umma_commit_warp(smem_u32(&o_bar[i]));
+          if constexpr (!S::kOwnP)
+            if (j + 1 < n) next_scores();
+          if (!ok) break;
+          release(&empty_bar[vs], true);
+          if (j + 1 < t.n_max) release(&empty_bar[slot_of(kx)], j + 1 < n);
+          if (j + 2 == n) release(qempty_bar, true);
           __syncwarp();
         }
-        if (p.lse && lane < rows)
-          p.lse[static_cast<int64_t>(u.q0 + row + lane) * p.Hq + t.head[i]] =
-              ml.y > 0.f ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
+        used += 2 * t.n_max;
+        turns += n;
+      }
+      if (*abort_flag && any) {
+        // let every product issued finish before tensor memory is released
+        umma_commit_warp(smem_u32(&drain_bar[i]));
+        __syncwarp();
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&drain_bar[i]), 0)) {
+          if (globaltimer_ns() - t0 > lim) {
+            if (lane == 0) atomicOr(err, kErrDrain);
+            break;
+          }
+        }
+      }
+    } else if (warp >= kAttnOutWarp) {
+      // ----------------------------------------------------------- outputs
+      const int quad = warp & 3;
+      const uint32_t lane_at = static_cast<uint32_t>(quad * 32) << 16;
+      uint8_t* mine = staging + quad * S::kStoreBytes;
+      int outs[2] = {0, 0};
+      bool ok = true;
+      PromptUnit u;
+      for (int it = 0; ok && take_unit(it, kErrWaitEpilogue, u); ++it) {
+        const PromptTiles t(p, u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // (the last totals being there, the output's phase before the last is over)
+          if (t.n[i] > 0) outs[i] += S::kOwnP ? t.n[i] : 1;
+          ok = ok && mbar_wait_sleep(smem_u32(&ml_bar[i]), it & 1, abort_flag, err,
+                                     kErrWaitEpilogue, lim);
+          const float2 ml = row_ml[i * kAttnM + quad * 32 + lane];
+          ok = ok && (t.n[i] == 0 ||
+                      mbar_wait_sleep(smem_u32(&o_bar[i]), (outs[i] - 1) & 1, abort_flag, err,
+                                      kErrWaitEpilogue, lim));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(smem_u32(&mlfree_bar[i]));
+          tc_fence_after();
+          const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
+          const int row = t.row0[i] + quad * 32;  // the warp's first row in the sequence
+          const int rows = min(32, u.nq - row);
+          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+          uint16_t* ob = p.out + static_cast<int64_t>(u.q0 + row) * p.o_ts + t.head[i] * p.o_hs;
+          // 64 channels at a time through shared memory (16-byte chunks, swizzled), so
+          // that a store covers 4 whole 128-byte rows; straight from its row, each
+          // thread would write 16 bytes of 32 different lines
+#pragma unroll 1
+          for (int c = 0; c < S::kBlocks; ++c) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float o[16];
+              if (t.n[i] > 0) tmem_ld16(o_at + c * 64 + g * 16, o);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = ml.y > 0.f ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
+                                    : 0u;
+                *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            if (c == S::kBlocks - 1) tc_fence_before();
+            __syncwarp();
+            if (c == S::kBlocks - 1 && lane == 0) mbar_arrive(smem_u32(&ofree_bar[i]));
+            const int ch = lane & 7, col = c * 64 + ch * 8;
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+              const int x = h * 4 + (lane >> 3);
+              if (x < rows && col < p.d)
+                *reinterpret_cast<uint4*>(ob + x * p.o_ts + col) =
+                    *reinterpret_cast<const uint4*>(mine + x * 128 + ((ch ^ (x & 7)) << 4));
+            }
+            __syncwarp();
+          }
+          if (p.lse && lane < rows)
+            p.lse[static_cast<int64_t>(u.q0 + row + lane) * p.Hq + t.head[i]] =
+                ml.y > 0.f ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
+        }
       }
     }
-  }
   } else {
     // ----------------------------------------------------------- softmax
     regs_take<kAttnRegsSoftmax>();
@@ -761,7 +781,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       float m = kNegInf, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        if (!mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, p.err, kErrWaitEpilogue,
+        if (!mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, err, kErrWaitEpilogue,
                        lim)) {
           ok = false;
           break;
@@ -790,7 +810,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         if constexpr (S::kOwnP) {
           // the product before has read these columns, and its sum is complete
           if (turns + j > 0 && !mbar_wait_spin(smem_u32(&o_bar[i]), (turns + j - 1) & 1, abort_flag,
-                                               p.err, kErrWaitEpilogue, lim)) {
+                                               err, kErrWaitEpilogue, lim)) {
             ok = false;
             break;
           }
@@ -863,7 +883,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       turns += n;
       turns_o += n_o;
       if (it > 0)
-        ok = ok && mbar_wait(smem_u32(&mlfree_bar[i]), (it - 1) & 1, abort_flag, p.err,
+        ok = ok && mbar_wait(smem_u32(&mlfree_bar[i]), (it - 1) & 1, abort_flag, err,
                              kErrWaitEpilogue, lim);
       if (!__all_sync(0xffffffffu, ok)) break;
       row_ml[i * kAttnM + r] = make_float2(m, l);

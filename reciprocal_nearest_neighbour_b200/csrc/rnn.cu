@@ -3053,7 +3053,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
       (r = check_rows(&v, Tk, Hkv, d)) != RNN_OK || (r = check_rows(&out, Tq, Hq, d)) != RNN_OK)
     return r;
-  if (!workspace || !aligned256(workspace) || ws_bytes < rnn_attn_prompt_workspace_size())
+  if (workspace && (!aligned256(workspace) || ws_bytes < rnn_attn_prompt_workspace_size()))
     return RNN_EWORKSPACE;
   PromptParams p;
   std::memset(&p, 0, sizeof(p));
@@ -3068,6 +3068,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* err = static_cast<int*>(workspace);
   if (Tq == 0 || B == 0) {
+    if (!err) return RNN_OK;
     zero_words_kernel<<<1, 32, 0, s>>>(err, 1);
     return launched();
   }

@@ -49,7 +49,7 @@ def test_prompt_errors(lib):
         assert call(**{name: rows(h, token=260)}) == EALIGN
         assert call(**{name: rows(h, head=68)}) == EALIGN
         assert call(**{name: rows(h, head=0)}) == EINVAL
-    assert call(ws=None) == EWS and call(ws=FAKE + 16) == EWS and call(n=need - 1) == EWS
+    assert call(ws=FAKE + 16) == EWS and call(n=need - 1) == EWS
 
 
 def test_decode_errors(lib):
