@@ -12,7 +12,7 @@
 // and cache row up under that latency, makes the token's cosines and sines once
 // (in 64 bits up to the fraction of a turn: at position 10^6 a 32-bit angle is
 // off by 0.06), and then moves the heads' channels in batches of kAppBatch units
-// of up to 2 x 16 bytes a lane, which keeps 4 KB a warp in flight.
+// of up to 2 x 16 bytes a lane.
 #pragma once
 #include <cstdint>
 #include "ptx.cuh"
@@ -20,8 +20,12 @@
 
 namespace rnn {
 
-constexpr int kAppWarps = 8;
-constexpr int kAppBatch = 4;
+// Blocks of 4 warps of at most 64 registers, 3 units in flight a lane.  14 prompt
+// chunks (21326 tokens, 32/8 heads of 128, 568 MB) and 24 frames (18432 tokens, 12
+// heads of 64, 198 MB): 107 and 35 us; blocks of 8 warps with 4 units 110 and 39,
+// of 2 warps with 3 units 110 and 35.
+constexpr int kAppWarps = 4;
+constexpr int kAppBatch = 3;
 
 struct AppendParams {
   const uint16_t *q, *k, *v;        // q may be null
@@ -131,7 +135,7 @@ __device__ __forceinline__ void app_rotate(AppUnit<kVec>& u, const float2* cs, b
 }
 
 template <bool kBf16, int kVec>
-__global__ void __launch_bounds__(kAppWarps * 32) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppWarps * 32, 8) kv_append_kernel(const AppendParams p) {
   using V = typename VecOf<kVec>::T;
   extern __shared__ __align__(16) float2 app_turns[];  // [warp][axes * pairs] cos, sin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
