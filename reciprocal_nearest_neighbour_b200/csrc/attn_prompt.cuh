@@ -779,10 +779,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       const int seen = p.causal ? min(u.nk, row + t.shift + 1) : u.nk;  // keys of this row
       const int seen_all = p.causal ? min(u.nk, row0 + t.shift + 1) : u.nk;  // of every row
       float m = kNegInf, l = 0.f;
+      bool s_there = false;  // the step's scores have been seen to be there
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        if (!mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, err, kErrWaitEpilogue,
-                       lim)) {
+        if (!s_there && !mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, err,
+                                        kErrWaitEpilogue, lim)) {
           ok = false;
           break;
         }
@@ -793,6 +794,10 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         tmem_wait_ld_regs(s[0]);
 #pragma unroll
         for (int c = 1; c < 4; ++c) reg_fence(s[c]);
+        // a look at a barrier takes a couple of hundred cycles: this one's answer is
+        // used behind the comparisons, the one for the next scores in the next step
+        bool o_there = !S::kOwnP || turns + j == 0;
+        if (!o_there) o_there = mbar_test_wait(smem_u32(&o_bar[i]), (turns + j - 1) & 1);
         if constexpr (S::kOwnP) {
           tc_fence_before();
           __syncwarp();
@@ -809,8 +814,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
         if constexpr (S::kOwnP) {
           // the product before has read these columns, and its sum is complete
-          if (turns + j > 0 && !mbar_wait_spin(smem_u32(&o_bar[i]), (turns + j - 1) & 1, abort_flag,
-                                               err, kErrWaitEpilogue, lim)) {
+          if (!o_there && !mbar_wait_spin(smem_u32(&o_bar[i]), (turns + j - 1) & 1, abort_flag, err,
+                                          kErrWaitEpilogue, lim)) {
             ok = false;
             break;
           }
@@ -868,6 +873,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             w[e] = pack2<kBf16>(a, b);
           }
           if (c == kTurnChunk && lane == 0) turn_at[warp] = turns + j + 1;
+          if (c == 3) s_there = S::kOwnP && mbar_test_wait(smem_u32(&s_bar[i]), (turns + j + 1) & 1);
           tmem_st16(p_at + c * 16, w);
           if ((c + 1) % (4 / S::kParts) == 0) {
             tmem_wait_st();
