@@ -535,8 +535,8 @@ rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, 
  *   causal   nonzero: row i of nq sees the keys t <= i + nk - nq, so the last
  *            query sees the last key (nk > nq: the keys in front are earlier
  *            tokens; nk < nq: the first rows see nothing).  0: all nk keys.
- *   scale    > 0, multiplies the scores.
- *   out      [Tq][Hq][d].
+ *   scale    > 0 and < 2e38, multiplies the scores.
+ *   out      [Tq][Hq][d], apart from the inputs.
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded; with a workspace (it
  * may be NULL) rnn_workspace_status tells whether one ran out.
@@ -552,7 +552,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
  * q, out [B][Hq][d] (the sequence in the place of the token), lse [B][Hq] or
  * NULL.  lens [B] int32: tokens of each sequence in the cache, the new one's
  * included (values below 0 count as 0, values beyond max_pages * page_size as
- * that).  Keys whose page is outside [0, num_pages) count as absent; rows of
+ * that).  scale as above.  Keys whose page is outside [0, num_pages) count as absent; rows of
  * a page behind the last key may hold anything.
  * d <= RNN_ATTN_MAX_DIM.
  */

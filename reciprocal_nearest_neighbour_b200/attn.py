@@ -6,7 +6,8 @@ sequences, ``attn_decode`` attends from one new token per sequence over the
 cache.  Tensors are fp16 or bf16 CUDA tensors whose last dimension (the
 channels of a head) is contiguous; the other dimensions may have any strides
 that are multiples of 8 elements, so slices of a fused projection's output
-pass as they are.  Calls run on the current stream of the tensors' device.
+pass as they are.  Calls run on the current stream of the tensors' device, and
+their results carry no gradient.
 """
 from __future__ import annotations
 
@@ -139,8 +140,8 @@ def _heads(hq: int, hkv: int, d: int, d_max: int) -> None:
 
 def _scale(scale: Optional[float], d: int) -> float:
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    if not (scale > 0.0 and scale < 3e38):
-        raise ValueError(f"scale must be positive and finite, got {scale}")
+    if not 0.0 < scale < 2e38:
+        raise ValueError(f"scale must be positive and below 2e38, got {scale}")
     return scale
 
 
@@ -272,7 +273,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
                 cu_k: Optional[torch.Tensor] = None, *, causal: bool = True,
                 scale: Optional[float] = None, with_lse: bool = False,
                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
-    """Attention of packed sequences: ``q [Tq, Hq, d]`` over ``k, v [Tk, Hkv, d]``.
+    """Attention of packed sequences: ``q [Tq, Hq, d]`` over ``k, v [Tk, Hkv, d]``, ``d <= 128``.
 
     Sequence ``b`` has the queries ``cu_q[b]:cu_q[b+1]`` and the keys
     ``cu_k[b]:cu_k[b+1]`` (int32 on the device; ``cu_k`` defaults to

@@ -86,6 +86,7 @@ struct PromptParams {
   int pair_heads;              // the two tiles are heads 2u, 2u + 1 of the same tokens
   int head_units;              // Hq / 2 or Hq
   int causal;
+  int sort;                    // more units than SMs: the order of the units matters
   float scale, c;              // c = scale * log2(e)
   uint32_t idesc_s, idesc_o;   // instruction descriptors of the two products
   int* err;                    // status word or null
@@ -397,13 +398,16 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           nk = max(0, clamp_at(p.cu_k, b + 1, p.Tk) - k0);
         }
         const int members = min(32, p.B - base_b);
-        int rank = 0, src = 0;
-        for (int o = 0; o < members; ++o) {
-          const int x = __shfl_sync(0xffffffffu, nk, o);
-          rank += x > nk || (x == nk && o < lane);
+        int src = lane;
+        if (p.sort) {
+          int rank = 0;
+          for (int o = 0; o < members; ++o) {
+            const int x = __shfl_sync(0xffffffffu, nk, o);
+            rank += x > nk || (x == nk && o < lane);
+          }
+          for (int o = 0; o < members; ++o)
+            if (__shfl_sync(0xffffffffu, rank, o) == lane) src = o;
         }
-        for (int o = 0; o < members; ++o)
-          if (__shfl_sync(0xffffffffu, rank, o) == lane) src = o;
         g_q0 = __shfl_sync(0xffffffffu, q0, src);
         g_nq = __shfl_sync(0xffffffffu, nq, src);
         g_k0 = __shfl_sync(0xffffffffu, k0, src);

@@ -3048,7 +3048,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
   if (r != RNN_OK) return r;
   if (Tq > INT32_MAX - 1024 || Tk > INT32_MAX - 1024) return RNN_EUNSUPPORTED;
-  if (!(scale > 0.f) || !(scale < 3e38f)) return RNN_EINVAL;
+  if (!(scale > 0.f) || !(scale < 2e38f)) return RNN_EINVAL;
   if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return RNN_EINVAL;
   if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
       (r = check_rows(&v, Tk, Hkv, d)) != RNN_OK || (r = check_rows(&out, Tq, Hq, d)) != RNN_OK)
@@ -3093,6 +3093,7 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
   p.Hq = Hq;
   p.d = d;
   p.causal = causal != 0;
+  p.sort = units > di->sms && B > 1;
   p.scale = scale;
   p.c = scale * 1.44269504f;
   p.idesc_s = make_idesc(dtype, kAttnN);
@@ -3169,7 +3170,7 @@ rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int
     return RNN_EINVAL;
   rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
   if (r != RNN_OK) return r;
-  if (!(scale > 0.f) || !(scale < 3e38f)) return RNN_EINVAL;
+  if (!(scale > 0.f) || !(scale < 2e38f)) return RNN_EINVAL;
   if ((B > 0 && (!page_table || !lens)) || !aligned4(page_table) || !aligned4(lens) || !aligned4(lse))
     return RNN_EINVAL;
   if ((r = check_rows(&q, B, Hq, d)) != RNN_OK || (r = check_rows(&out, B, Hq, d)) != RNN_OK ||

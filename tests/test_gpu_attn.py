@@ -1,5 +1,8 @@
 """Attention operators against the double-precision oracle (needs a B200)."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -513,3 +516,45 @@ def test_decode_row_offsets_beyond_32_bits():
     out = rnn.attn_decode(q, kc, vc, table, ints([70]))
     ref = oa.prompt(f64(q), f64(k), f64(v), [0, 1], [0, 70], False, 1 / math.sqrt(d))
     check_attention(out, None, ref, BF, d, 6.0)
+
+
+def test_calls_at_once_on_two_streams():
+    g = gen_of(15)
+    lens = [1500, 33]
+    dq, kc, vc, table, want, want_lse = run_decode(BF, lens, 16, 8, 2, 64, 15)
+    tab, lt = torch.from_numpy(table).cuda(), ints(lens)
+    q, k, v, cu_q, cu_k, pout, plse = run_prompt(BF, [200, 900], [200, 900], 2, 1, 64, True, 16)
+    cq, ck = ints(cu_q), ints(cu_k)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(rnn.attn_decode(dq, kc, vc, tab, lt, with_lse=True) +
+                       rnn.attn_prompt(q, k, v, cq, ck, with_lse=True))
+    torch.cuda.synchronize()
+    for a, al, b, bl in got:
+        assert torch.equal(a, want) and torch.equal(al, want_lse)
+        assert torch.equal(b, pout) and torch.equal(bl, plse)
+
+
+FIRST_IN_CAPTURE = """
+import torch, reciprocal_nearest_neighbour_b200 as rnn
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+q = torch.randn(20, 2, 64, device="cuda").bfloat16()
+kc = torch.zeros(3, 16, 2, 64, device="cuda").bfloat16()
+vc, table, zero, cu, n = kc.clone(), i(2, 0).view(1, 2), i(0), i(0, 20), i(20)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    rnn.kv_append(q, q, kc, vc, table, zero, cu)
+    a = rnn.attn_prompt(q, q, q, cu, causal=False)
+    b = rnn.attn_decode(q[19:], kc, vc, table, n)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(kc[2], q[:16]) and (a[19].float() - b[0].float()).abs().max() < 0.05
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], check=True, timeout=300, cwd=root)
