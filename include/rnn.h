@@ -476,6 +476,8 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  *   - A row that sees no key gets zeros, and -infinity as its log-sum.
  *   - Queries, and the keys and values of a sequence, must be finite.  What
  *     lies outside the sequences may hold anything.
+ *   - Arguments come in a structure, which is only read during the call;
+ *     dtype is an rnn_dtype.
  *   - Softmax statistics and sums are fp32; each product's probabilities are
  *     rounded to the 16-bit type once, outputs once.
  */
@@ -521,13 +523,15 @@ typedef struct rnn_pages {
  *                channels 2i and 2i + 1.
  * d <= 256.  No workspace: nothing waits on the device.
  */
-rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, int Hkv, int d,
-                         rnn_dtype dtype, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
-                         int page_size, const int32_t *page_table, int64_t table_stride,
-                         int max_pages, const int32_t *start, const int32_t *cu, int B,
-                         const int32_t *positions, int64_t position_stride,
-                         const double *inv_freq, int pairs, int axes, int paired, rnn_rows q_out,
-                         rnn_rows k_out, rnn_stream_t stream);
+typedef struct rnn_kv_append_args {
+  rnn_rows q, k, v, q_out, k_out;
+  rnn_pages k_cache, v_cache;
+  const int32_t *page_table, *start, *cu, *positions;
+  const double *inv_freq;
+  int64_t T, num_pages, table_stride, position_stride;
+  int32_t Hq, Hkv, d, dtype, page_size, max_pages, B, pairs, axes, paired;
+} rnn_kv_append_args;
+rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
 
 /*
  * Attention of packed sequences: q [Tq][Hq][d] of sequences cu_q over k, v
@@ -541,11 +545,18 @@ rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, 
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded; with a workspace (it
  * may be NULL) rnn_workspace_status tells whether one ran out.
  */
+typedef struct rnn_attn_prompt_args {
+  rnn_rows q, k, v, out;
+  const int32_t *cu_q, *cu_k;
+  float *lse;
+  void *workspace;
+  uint64_t ws_bytes;
+  int64_t Tq, Tk;
+  int32_t Hq, Hkv, d, dtype, B, causal;
+  float scale;
+} rnn_attn_prompt_args;
 size_t rnn_attn_prompt_workspace_size(void);
-rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64_t Tk, int Hq,
-                           int Hkv, int d, rnn_dtype dtype, const int32_t *cu_q,
-                           const int32_t *cu_k, int B, int causal, float scale, rnn_rows out,
-                           float *lse, void *workspace, size_t ws_bytes, rnn_stream_t stream);
+rnn_status rnn_attn_prompt(const rnn_attn_prompt_args *args, rnn_stream_t stream);
 
 /*
  * Attention of one new token of each of B sequences over a paged cache:
@@ -556,12 +567,19 @@ rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64
  * a page behind the last key may hold anything.
  * d <= RNN_ATTN_MAX_DIM.
  */
+typedef struct rnn_attn_decode_args {
+  rnn_rows q, out;
+  rnn_pages k_cache, v_cache;
+  const int32_t *page_table, *lens;
+  float *lse;
+  void *workspace;
+  uint64_t ws_bytes;
+  int64_t num_pages, table_stride;
+  int32_t page_size, max_pages, B, Hq, Hkv, d, dtype;
+  float scale;
+} rnn_attn_decode_args;
 size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
-rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
-                           int page_size, const int32_t *page_table, int64_t table_stride,
-                           int max_pages, const int32_t *lens, int B, int Hq, int Hkv, int d,
-                           rnn_dtype dtype, float scale, rnn_rows out, float *lse,
-                           void *workspace, size_t ws_bytes, rnn_stream_t stream);
+rnn_status rnn_attn_decode(const rnn_attn_decode_args *args, rnn_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics for benchmarking (no effect on results).

@@ -83,6 +83,34 @@ class Pages(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+def _fields(**groups):
+    """Structure fields from ``type="names"`` groups in order."""
+    types = {"rows": Rows, "pages": Pages, "ptr": ctypes.c_void_p, "u64": ctypes.c_uint64,
+             "i64": ctypes.c_int64, "i32": ctypes.c_int32, "f32": ctypes.c_float}
+    return [(n, types[t.rstrip("_")]) for t, names in groups.items() for n in names.split()]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """``rnn_kv_append_args``"""
+    _fields_ = _fields(rows="q k v q_out k_out", pages="k_cache v_cache",
+                       ptr="page_table start cu positions inv_freq",
+                       i64="T num_pages table_stride position_stride",
+                       i32="Hq Hkv d dtype page_size max_pages B pairs axes paired")
+
+
+class AttnPromptArgs(ctypes.Structure):
+    """``rnn_attn_prompt_args``"""
+    _fields_ = _fields(rows="q k v out", ptr="cu_q cu_k lse workspace", u64="ws_bytes",
+                       i64="Tq Tk", i32="Hq Hkv d dtype B causal", f32="scale")
+
+
+class AttnDecodeArgs(ctypes.Structure):
+    """``rnn_attn_decode_args``"""
+    _fields_ = _fields(rows="q out", pages="k_cache v_cache", ptr="page_table lens lse workspace",
+                       u64="ws_bytes", i64="num_pages table_stride",
+                       i32="page_size max_pages B Hq Hkv d dtype", f32="scale")
+
+
 class RNNLibraryError(RuntimeError):
     pass
 
@@ -156,14 +184,11 @@ def load():
                                      ctypes.c_float, P, I64, P, P, P, P, SZ, P]),
         "rnn_frm_graph_launch": (I, [P, P]),
         "rnn_frm_graph_destroy": (None, [P]),
-        "rnn_kv_append": (I, [Rows, Rows, Rows, I64, I, I, I, I, Pages, Pages, I64, I, P, I64, I,
-                              P, P, I, P, I64, P, I, I, I, Rows, Rows, P]),
+        "rnn_kv_append": (I, [P, P]),
         "rnn_attn_prompt_workspace_size": (SZ, []),
-        "rnn_attn_prompt": (I, [Rows, Rows, Rows, I64, I64, I, I, I, I, P, P, I, I,
-                                ctypes.c_float, Rows, P, P, SZ, P]),
+        "rnn_attn_prompt": (I, [P, P]),
         "rnn_attn_decode_workspace_size": (SZ, [I, I, I, I]),
-        "rnn_attn_decode": (I, [Rows, Pages, Pages, I64, I, P, I64, I, P, I, I, I, I, I,
-                                ctypes.c_float, Rows, P, P, SZ, P]),
+        "rnn_attn_decode": (I, [P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import functools
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -20,6 +21,13 @@ import torch
 from . import _lib
 
 _DT = {torch.float16: _lib.RNN_F16, torch.bfloat16: _lib.RNN_BF16}
+
+# The argument structures of the C entry points (KvAppendArgs, AttnPromptArgs and AttnDecodeArgs of
+# _lib), packed in one step: a ctypes structure filled field by field takes microseconds.
+_ROWS, _PAGES = "Qqq", "Qqqq"
+_APPEND = struct.Struct("=" + 5 * _ROWS + 2 * _PAGES + "5Q4q10i")
+_PROMPT = struct.Struct("=" + 4 * _ROWS + "4QQ2q6if4x")
+_DECODE = struct.Struct("=" + 2 * _ROWS + 2 * _PAGES + "4QQ2q7if")
 
 
 def _check(t, name: str, ndim: int, dtype, device=None) -> None:
@@ -33,12 +41,12 @@ def _check(t, name: str, ndim: int, dtype, device=None) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _all(kind, device, ndim: int, **tensors) -> None:
-    """Each of the tensors has this type, device and number of dimensions (else the error)."""
-    for t in tensors.values():
+def _all(kind, device, ndim: int, *named) -> None:
+    """Each ``tensor, name`` has this type, device and number of dimensions (else the error)."""
+    for t in named[::2]:
         if not (isinstance(t, torch.Tensor) and t.dtype is kind and t.device == device
                 and t.dim() == ndim and t.is_cuda):
-            for name, u in tensors.items():
+            for u, name in zip(named[::2], named[1::2]):
                 _check(u, name, ndim, kind, device)
 
 
@@ -67,25 +75,23 @@ def _strides(t: torch.Tensor, name: str):
     return out
 
 
-_NO_ROWS = _lib.Rows(None, 0, 0)
+_NO_ROWS = (0, 0, 0)
 
 
-def _rows(t: Optional[torch.Tensor], name: str, d: int) -> _lib.Rows:
-    if t is None:
-        return _NO_ROWS
+def _rows(t: torch.Tensor, name: str, d: int):
     token, head, one = t.stride()
     at = t.data_ptr()
     if one != 1 or token < d or head < d or (token | head) & 7 or at & 15:
         token, head = _strides(t, name)     # a dimension of size 1, or an error
-    return _lib.Rows(at, token, head)
+    return at, token, head
 
 
-def _pages(t: torch.Tensor, name: str, d: int) -> _lib.Pages:
+def _pages(t: torch.Tensor, name: str, d: int):
     page, token, head, one = t.stride()
     at = t.data_ptr()
     if one != 1 or page < d or token < d or head < d or (page | token | head) & 7 or at & 15:
         page, token, head = _strides(t, name)
-    return _lib.Pages(at, page, token, head)
+    return at, page, token, head
 
 
 def _ints(t, name: str, device, size: int) -> None:
@@ -119,7 +125,7 @@ def _table(t, device, B: int):
 
 def _cache(k_cache, v_cache, kind, device, heads: int, d: int):
     """Number of pages and page size."""
-    _all(kind, device, 4, k_cache=k_cache, v_cache=v_cache)
+    _all(kind, device, 4, k_cache, "k_cache", v_cache, "v_cache")
     pages, size, h, dim = shape = k_cache.shape
     if h != heads or dim != d or pages < 1 or size < 1:
         raise ValueError(f"k_cache must have shape [pages, page_size, {heads}, {d}], got "
@@ -159,7 +165,7 @@ def _given(out, want: torch.Size, kind, device, name: str) -> torch.Tensor:
 def _given_scratch(workspace, device):
     """Address and size of the caller's workspace, or none."""
     if workspace is None:
-        return None, 0
+        return 0, 0
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
             workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
@@ -171,14 +177,14 @@ def _decode_need(B: int, hq: int, hkv: int, d: int) -> int:
     return _lib.load().rnn_attn_decode_workspace_size(B, hq, hkv, d)
 
 
-def _call(fn, name: str, t: torch.Tensor, *args) -> None:
-    """``fn(*args, stream)`` with the device of `t` current, on its current stream."""
+def _call(fn, name: str, t: torch.Tensor, args: bytes) -> None:
+    """``fn(args, stream)`` with the device of `t` current, on its current stream."""
     index = t.get_device()
     if index == torch._C._cuda_getDevice():
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        code = fn(args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            code = fn(args, torch._C._cuda_getCurrentRawStream(index))
     if code:
         _lib.check(code, name)
 
@@ -208,13 +214,13 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     """
     kind = _value_dtype(k, "k")
     dev = k.device
-    _all(kind, dev, 3, k=k, v=v)
+    _all(kind, dev, 3, k, "k", v, "v")
     T, hkv, d = shape = k.shape
     if v.shape != shape:
         raise ValueError(f"v must have the shape of k, got {tuple(v.shape)}")
     hq = 0
     if q is not None:
-        _all(kind, dev, 3, q=q)
+        _all(kind, dev, 3, q, "q")
         tq, hq, dq = q.shape
         if tq != T or dq != d or hq < 1:
             raise ValueError(f"q must have shape [{T}, heads, {d}], got {tuple(q.shape)}")
@@ -232,7 +238,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     table_stride, max_pages = _table(page_table, dev, B)
     pairs = axes = pos_stride = 0
     if inv_freq is not None:
-        _all(torch.float64, dev, 1, inv_freq=inv_freq)
+        _all(torch.float64, dev, 1, inv_freq, "inv_freq")
         pairs, axes = inv_freq.shape[0], 1
         if pairs < 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be contiguous and not empty")
@@ -259,13 +265,14 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         _given(k_out, k.shape, kind, dev, "k_out")
     elif with_k:
         k_out = _packed(k)
-    _call(_lib.load().rnn_kv_append, "rnn_kv_append", k, _rows(q, "q", d), _rows(k, "k", d),
-          _rows(v, "v", d), T, hq, hkv, d, _DT[kind], _pages(k_cache, "k_cache", d),
-          _pages(v_cache, "v_cache", d), num_pages, size, page_table.data_ptr(), table_stride,
-          max_pages, start.data_ptr(), cu.data_ptr(), B,
-          None if positions is None else positions.data_ptr(), pos_stride,
-          None if inv_freq is None else inv_freq.data_ptr(), pairs, axes, paired,
-          _rows(q_out, "q_out", d), _rows(k_out, "k_out", d))
+    _call(_lib.load().rnn_kv_append, "rnn_kv_append", k, _APPEND.pack(
+        *(_NO_ROWS if q is None else _rows(q, "q", d)), *_rows(k, "k", d), *_rows(v, "v", d),
+        *(_NO_ROWS if q is None else _rows(q_out, "q_out", d)),
+        *(_NO_ROWS if k_out is None else _rows(k_out, "k_out", d)),
+        *_pages(k_cache, "k_cache", d), *_pages(v_cache, "v_cache", d), page_table.data_ptr(),
+        start.data_ptr(), cu.data_ptr(), 0 if positions is None else positions.data_ptr(),
+        0 if inv_freq is None else inv_freq.data_ptr(), T, num_pages, table_stride, pos_stride,
+        hq, hkv, d, _DT[kind], size, max_pages, B, pairs, axes, bool(paired)))
     return q_out, k_out
 
 
@@ -289,7 +296,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     """
     kind = _value_dtype(q, "q")
     dev = q.device
-    _all(kind, dev, 3, q=q, k=k, v=v)
+    _all(kind, dev, 3, q, "q", k, "k", v, "v")
     Tq, hq, d = q.shape
     Tk, hkv, dk = k.shape
     if dk != d or k.shape != v.shape:
@@ -302,14 +309,13 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     else:
         _ints(cu_k, "cu_k", dev, B + 1)
     scale = _scale(scale, d)
-    lib = _lib.load()
     out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
     lse = torch.empty((Tq, hq), dtype=torch.float32, device=dev) if with_lse else None
     ws, ws_bytes = _given_scratch(workspace, dev)
-    _call(lib.rnn_attn_prompt, "rnn_attn_prompt", q, _rows(q, "q", d), _rows(k, "k", d),
-          _rows(v, "v", d), Tq, Tk, hq, hkv, d, _DT[kind], cu_q.data_ptr(), cu_k.data_ptr(), B,
-          causal, scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(), ws,
-          ws_bytes)
+    _call(_lib.load().rnn_attn_prompt, "rnn_attn_prompt", q, _PROMPT.pack(
+        *_rows(q, "q", d), *_rows(k, "k", d), *_rows(v, "v", d), *_rows(out, "out", d),
+        cu_q.data_ptr(), cu_k.data_ptr(), 0 if lse is None else lse.data_ptr(), ws, ws_bytes, Tq,
+        Tk, hq, hkv, d, _DT[kind], B, bool(causal), scale))
     return (out, lse) if with_lse else out
 
 
@@ -326,7 +332,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     """
     kind = _value_dtype(q, "q")
     dev = q.device
-    _all(kind, dev, 3, q=q)
+    _all(kind, dev, 3, q, "q")
     B, hq, d = q.shape
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
@@ -336,15 +342,14 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _ints(lens, "lens", dev, B)
     table_stride, max_pages = _table(page_table, dev, B)
     scale = _scale(scale, d)
-    lib = _lib.load()
     out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
     lse = torch.empty((B, hq), dtype=torch.float32, device=dev) if with_lse else None
     if workspace is None:
         workspace = torch.empty(_decode_need(B, hq, hkv, d), dtype=torch.uint8, device=dev)
     ws, ws_bytes = _given_scratch(workspace, dev)
-    _call(lib.rnn_attn_decode, "rnn_attn_decode", q, _rows(q, "q", d),
-          _pages(k_cache, "k_cache", d), _pages(v_cache, "v_cache", d), num_pages, size,
-          page_table.data_ptr(), table_stride, max_pages, lens.data_ptr(), B, hq, hkv, d,
-          _DT[kind], scale, _rows(out, "out", d), None if lse is None else lse.data_ptr(), ws,
-          ws_bytes)
+    _call(_lib.load().rnn_attn_decode, "rnn_attn_decode", q, _DECODE.pack(
+        *_rows(q, "q", d), *_rows(out, "out", d), *_pages(k_cache, "k_cache", d),
+        *_pages(v_cache, "v_cache", d), page_table.data_ptr(), lens.data_ptr(),
+        0 if lse is None else lse.data_ptr(), ws, ws_bytes, num_pages, table_stride, size,
+        max_pages, B, hq, hkv, d, _DT[kind], scale))
     return (out, lse) if with_lse else out

@@ -3039,11 +3039,18 @@ extern "C" {
 
 size_t rnn_attn_prompt_workspace_size(void) { return kAlign; }
 
-rnn_status rnn_attn_prompt(rnn_rows q, rnn_rows k, rnn_rows v, int64_t Tq, int64_t Tk, int Hq,
-                           int Hkv, int d, rnn_dtype dtype, const int32_t* cu_q,
-                           const int32_t* cu_k, int B, int causal, float scale, rnn_rows out,
-                           float* lse, void* workspace, size_t ws_bytes, rnn_stream_t stream) {
+rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream) {
   NvtxRange nvtx_range("rnn_attn_prompt");
+  if (!args) return RNN_EINVAL;
+  rnn_rows q = args->q, k = args->k, v = args->v, out = args->out;
+  const int64_t Tq = args->Tq, Tk = args->Tk;
+  const int Hq = args->Hq, Hkv = args->Hkv, d = args->d, B = args->B, causal = args->causal;
+  const rnn_dtype dtype = static_cast<rnn_dtype>(args->dtype);
+  const int32_t *cu_q = args->cu_q, *cu_k = args->cu_k;
+  float* lse = args->lse;
+  void* workspace = args->workspace;
+  const size_t ws_bytes = args->ws_bytes;
+  const float scale = args->scale;
   if (Tq < 0 || Tk < 0 || Tq > INT32_MAX || Tk > INT32_MAX || B < 0) return RNN_EINVAL;
   rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
   if (r != RNN_OK) return r;
@@ -3159,12 +3166,20 @@ size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
   return dec_layout(nullptr, B, Hkv, Hq / Hkv, d, &w);
 }
 
-rnn_status rnn_attn_decode(rnn_rows q, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
-                           int page_size, const int32_t* page_table, int64_t table_stride,
-                           int max_pages, const int32_t* lens, int B, int Hq, int Hkv, int d,
-                           rnn_dtype dtype, float scale, rnn_rows out, float* lse,
-                           void* workspace, size_t ws_bytes, rnn_stream_t stream) {
+rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream) {
   NvtxRange nvtx_range("rnn_attn_decode");
+  if (!args) return RNN_EINVAL;
+  rnn_rows q = args->q, out = args->out;
+  rnn_pages k_cache = args->k_cache, v_cache = args->v_cache;
+  const int32_t *page_table = args->page_table, *lens = args->lens;
+  const int64_t num_pages = args->num_pages, table_stride = args->table_stride;
+  const int page_size = args->page_size, max_pages = args->max_pages, B = args->B;
+  const int Hq = args->Hq, Hkv = args->Hkv, d = args->d;
+  const rnn_dtype dtype = static_cast<rnn_dtype>(args->dtype);
+  float* lse = args->lse;
+  void* workspace = args->workspace;
+  const size_t ws_bytes = args->ws_bytes;
+  const float scale = args->scale;
   if (B < 0 || num_pages < 1 || num_pages > INT32_MAX || page_size < 1 || max_pages < 1 ||
       table_stride < 0)
     return RNN_EINVAL;
@@ -3247,14 +3262,20 @@ static void kv_append_launch(const AppendParams& p, int vec, dim3 grid, size_t s
 
 extern "C" {
 
-rnn_status rnn_kv_append(rnn_rows q, rnn_rows k, rnn_rows v, int64_t T, int Hq, int Hkv, int d,
-                         rnn_dtype dtype, rnn_pages k_cache, rnn_pages v_cache, int64_t num_pages,
-                         int page_size, const int32_t* page_table, int64_t table_stride,
-                         int max_pages, const int32_t* start, const int32_t* cu, int B,
-                         const int32_t* positions, int64_t position_stride,
-                         const double* inv_freq, int pairs, int axes, int paired, rnn_rows q_out,
-                         rnn_rows k_out, rnn_stream_t stream) {
+rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
   NvtxRange nvtx_range("rnn_kv_append");
+  if (!args) return RNN_EINVAL;
+  rnn_rows q = args->q, k = args->k, v = args->v, q_out = args->q_out, k_out = args->k_out;
+  rnn_pages k_cache = args->k_cache, v_cache = args->v_cache;
+  const int32_t *page_table = args->page_table, *start = args->start, *cu = args->cu;
+  const int32_t* positions = args->positions;
+  const double* inv_freq = args->inv_freq;
+  const int64_t T = args->T, num_pages = args->num_pages, table_stride = args->table_stride;
+  const int64_t position_stride = args->position_stride;
+  const int Hq = args->Hq, Hkv = args->Hkv, d = args->d, page_size = args->page_size;
+  const int max_pages = args->max_pages, B = args->B, pairs = args->pairs, axes = args->axes;
+  const int paired = args->paired;
+  const rnn_dtype dtype = static_cast<rnn_dtype>(args->dtype);
   if (T < 0 || T > INT32_MAX || B < 0 || B == INT32_MAX || Hq < 0 || Hkv < 1 || num_pages < 1 ||
       num_pages > INT32_MAX || page_size < 1 || max_pages < 1 || table_stride < 0 || d < 1 ||
       !valid_dtype(dtype))

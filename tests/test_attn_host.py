@@ -1,4 +1,6 @@
 """Refusals of the attention entry points (no GPU: nothing is launched)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -24,6 +26,22 @@ def pages(heads=2, d=64, size=16, p=FAKE, page=None, token=None, head=None):
                       heads * d if token is None else token, d if head is None else head)
 
 
+def test_packed_structures_match(lib):
+    from reciprocal_nearest_neighbour_b200 import attn
+
+    for kind, packed in ((_lib.KvAppendArgs, attn._APPEND), (_lib.AttnPromptArgs, attn._PROMPT),
+                         (_lib.AttnDecodeArgs, attn._DECODE)):
+        assert ctypes.sizeof(kind) == packed.size
+        raw = (bytes(range(256)) * 2)[:packed.size]
+        flat = packed.unpack(raw)
+        s = kind.from_buffer_copy(raw)
+        mine = []
+        for name, _ in kind._fields_:
+            v = getattr(s, name)
+            mine += [getattr(v, f) for f, _ in v._fields_] if hasattr(v, "_fields_") else [v]
+        assert mine == list(flat)
+
+
 def test_prompt_errors(lib):
     need = lib.rnn_attn_prompt_workspace_size()
 
@@ -31,7 +49,12 @@ def test_prompt_errors(lib):
         a = dict(q=rows(4), k=rows(), v=rows(), tq=10, tk=10, hq=4, hkv=2, d=64, dt=0, cq=FAKE,
                  ck=FAKE, B=1, causal=1, scale=0.1, out=rows(4), lse=None, ws=FAKE, n=need)
         a.update(kw)
-        return lib.rnn_attn_prompt(*a.values(), None)
+        return lib.rnn_attn_prompt(ctypes.byref(_lib.AttnPromptArgs(
+            q=a["q"], k=a["k"], v=a["v"], out=a["out"], cu_q=a["cq"], cu_k=a["ck"], lse=a["lse"],
+            workspace=a["ws"], ws_bytes=a["n"], Tq=a["tq"], Tk=a["tk"], Hq=a["hq"], Hkv=a["hkv"],
+            d=a["d"], dtype=a["dt"], B=a["B"], causal=a["causal"], scale=a["scale"])), None)
+
+    assert lib.rnn_attn_prompt(None, None) == EINVAL
 
     assert call(tq=-1) == EINVAL and call(B=-1) == EINVAL and call(tk=1 << 31) == EINVAL
     assert call(hq=0) == EINVAL and call(hq=3) == EINVAL and call(hkv=0) == EINVAL
@@ -63,7 +86,13 @@ def test_decode_errors(lib):
                  B=3, hq=4, hkv=2, d=64, dt=1, scale=0.1, out=rows(4), lse=None, ws=FAKE,
                  wsn=need)
         a.update(kw)
-        return lib.rnn_attn_decode(*a.values(), None)
+        return lib.rnn_attn_decode(ctypes.byref(_lib.AttnDecodeArgs(
+            q=a["q"], out=a["out"], k_cache=a["k"], v_cache=a["v"], page_table=a["table"],
+            lens=a["lens"], lse=a["lse"], workspace=a["ws"], ws_bytes=a["wsn"], num_pages=a["n"],
+            table_stride=a["ts"], page_size=a["size"], max_pages=a["mp"], B=a["B"], Hq=a["hq"],
+            Hkv=a["hkv"], d=a["d"], dtype=a["dt"], scale=a["scale"])), None)
+
+    assert lib.rnn_attn_decode(None, None) == EINVAL
 
     assert call(B=-1) == EINVAL and call(n=0) == EINVAL and call(size=0) == EINVAL
     assert call(mp=0) == EINVAL and call(ts=-1) == EINVAL and call(hq=5) == EINVAL
@@ -88,7 +117,15 @@ def test_append_errors(lib):
                  pos=None, ps=0, inv=FAKE, pairs=32, axes=1, paired=0, qo=rows(4),
                  ko=_lib.Rows(None, 0, 0))
         a.update(kw)
-        return lib.rnn_kv_append(*a.values(), None)
+        return lib.rnn_kv_append(ctypes.byref(_lib.KvAppendArgs(
+            q=a["q"], k=a["k"], v=a["v"], q_out=a["qo"], k_out=a["ko"], k_cache=a["kc"],
+            v_cache=a["vc"], page_table=a["table"], start=a["start"], cu=a["cu"],
+            positions=a["pos"], inv_freq=a["inv"], T=a["T"], num_pages=a["n"],
+            table_stride=a["ts"], position_stride=a["ps"], Hq=a["hq"], Hkv=a["hkv"], d=a["d"],
+            dtype=a["dt"], page_size=a["size"], max_pages=a["mp"], B=a["B"], pairs=a["pairs"],
+            axes=a["axes"], paired=a["paired"])), None)
+
+    assert lib.rnn_kv_append(None, None) == EINVAL
 
     assert call(T=-1) == EINVAL and call(B=-1) == EINVAL and call(hkv=0) == EINVAL
     assert call(d=20) == EALIGN and call(dt=2) == EINVAL and call(mp=0) == EINVAL
