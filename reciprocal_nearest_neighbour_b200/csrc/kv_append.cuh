@@ -22,8 +22,9 @@ namespace rnn {
 
 // Blocks of 4 warps of at most 64 registers, 3 units in flight a lane.  14 prompt
 // chunks (21326 tokens, 32/8 heads of 128, 568 MB) and 24 frames (18432 tokens, 12
-// heads of 64, 198 MB): 107 and 35 us; blocks of 8 warps with 4 units 110 and 39,
-// of 2 warps with 3 units 110 and 35.
+// heads of 64, 198 MB): 99 and 35 us; with 4 units 97 and 36.  (Before the words were
+// converted in pairs: 107 and 35, blocks of 8 warps with 4 units 110 and 39, blocks
+// of 2 warps 110 and 35.)
 constexpr int kAppWarps = 4;
 constexpr int kAppBatch = 3;
 
@@ -106,32 +107,45 @@ __device__ __forceinline__ AppPlace app_place(int unit, const AppendParams& p) {
   return at;
 }
 
-// Rotated in fp32, rounded once.
+// Rotated in fp32, rounded once.  Two channels a word: (x1, x2) of one pair when
+// they lie side by side, else two pairs' x1 in `a` and their x2 in `b`.
 template <bool kBf16, int kVec>
 __device__ __forceinline__ void app_rotate(AppUnit<kVec>& u, const float2* cs, bool paired) {
-  using V = typename VecOf<kVec>::T;
-  union { V v[2]; uint16_t h[2 * kVec]; } x, y;
-  x.v[0] = u.a;
-  x.v[1] = u.b;
-  if (paired) {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float2 t = cs[e];
-      const float x1 = app_float<kBf16>(x.h[2 * e]), x2 = app_float<kBf16>(x.h[2 * e + 1]);
-      y.h[2 * e] = app_bits<kBf16>(x1 * t.x - x2 * t.y);
-      y.h[2 * e + 1] = app_bits<kBf16>(x2 * t.x + x1 * t.y);
-    }
+  if constexpr (kVec == 1) {
+    const float x1 = app_float<kBf16>(u.a), x2 = app_float<kBf16>(u.b);
+    u.a = app_bits<kBf16>(x1 * cs->x - x2 * cs->y);
+    u.b = app_bits<kBf16>(x2 * cs->x + x1 * cs->y);
   } else {
+    constexpr int kWords = kVec / 2;
+    union Words { typename VecOf<kVec>::T v; uint32_t w[kWords]; } a, b;
+    a.v = u.a;
+    b.v = u.b;
+    const float4* turns = reinterpret_cast<const float4*>(cs);  // cos, sin of two pairs
+    if (paired) {
+      uint32_t x[2 * kWords];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float2 t = cs[e];
-      const float x1 = app_float<kBf16>(x.h[e]), x2 = app_float<kBf16>(x.h[kVec + e]);
-      y.h[e] = app_bits<kBf16>(x1 * t.x - x2 * t.y);
-      y.h[kVec + e] = app_bits<kBf16>(x2 * t.x + x1 * t.y);
+      for (int e = 0; e < kWords; ++e) x[e] = a.w[e], x[kWords + e] = b.w[e];
+#pragma unroll
+      for (int e = 0; e < kWords; ++e) {
+        const float4 t = turns[e];
+        const float2 p = unpack2<kBf16>(x[2 * e]), q = unpack2<kBf16>(x[2 * e + 1]);
+        x[2 * e] = pack2<kBf16>(p.x * t.x - p.y * t.y, p.y * t.x + p.x * t.y);
+        x[2 * e + 1] = pack2<kBf16>(q.x * t.z - q.y * t.w, q.y * t.z + q.x * t.w);
+      }
+#pragma unroll
+      for (int e = 0; e < kWords; ++e) a.w[e] = x[e], b.w[e] = x[kWords + e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWords; ++e) {
+        const float4 t = turns[e];
+        const float2 x1 = unpack2<kBf16>(a.w[e]), x2 = unpack2<kBf16>(b.w[e]);
+        a.w[e] = pack2<kBf16>(x1.x * t.x - x2.x * t.y, x1.y * t.z - x2.y * t.w);
+        b.w[e] = pack2<kBf16>(x2.x * t.x + x1.x * t.y, x2.y * t.z + x1.y * t.w);
+      }
     }
+    u.a = a.v;
+    u.b = b.v;
   }
-  u.a = y.v[0];
-  u.b = y.v[1];
 }
 
 template <bool kBf16, int kVec>
