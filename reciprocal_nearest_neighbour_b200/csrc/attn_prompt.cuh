@@ -10,33 +10,39 @@
 // that one tile's softmax runs under the other's matrix products:
 //   warps 0-3, 4-7  softmax of query tile 0 and 1: one thread per row reads
 //                   its 128 scores (tcgen05.ld), exponentiates them and writes
-//                   the probabilities back (tcgen05.st) over the scores as the
-//                   16-bit A operand of the second product
+//                   the probabilities (tcgen05.st) as the 16-bit A operand of
+//                   the second product
 //   warps 8, 10     issue S = Q K^T and O += P V (tcgen05.mma) of query tile 0 and
 //                   1; each wait and commit costs the issuing warp over a hundred
 //                   cycles, and one warp for both tiles bounds the kernel
 //   warp 9          TMA: query tiles, then a ring of alternating K and V tiles
 //   warps 12-15     outputs: normalise and store a finished unit's rows
-// Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
+// Tensor memory: two score tiles of 128 columns, two output tiles of kDP, and with
+// 64 channels two probability tiles (AttnShape).
 //
 // A CTA is persistent.  The grid has one block per unit (a pair of query
 // tiles); a running CTA asks for the next unit by cancelling a block that has
 // not started (clusterlaunchcontrol), so units of any length are dealt as CTAs
-// come free, without a counter to clear.  The TMA warp fetches units a step
-// ahead and loads the next unit's tiles while the last products and the
-// epilogue of this one run: the output is read, normalised and stored by the
-// softmax warps while the tensor cores start on the next unit's scores.
+// come free, without a counter to clear.  The TMA warp fetches the next unit and
+// its tiles, and the output warps read, normalise and store a finished unit's
+// rows, while the products and the softmax of the one in between run.
 //
 // Rescaling.  A row's reference maximum only moves when its true maximum has
-// grown by more than 2^8 over it (the weights then exceed 1 by at most that,
-// far inside fp32 and the 16-bit types), so the output accumulator is read
-// back and rescaled rarely; the softmax warps do it themselves: the barrier
-// that hands them the next scores also tells that the product before it is
-// complete, since the tensor pipe works in order.
+// grown by more than 2^8 over it (a weight is then at most 2^8, far inside fp32
+// and the 16-bit types), so the output accumulator is read back and rescaled
+// rarely; the softmax warps do it themselves.  At 128 channels the barrier that
+// hands them the next scores also tells that the product before it is complete,
+// since the tensor pipe works in order; at 64 the next scores come earlier, and
+// they look at the output's barrier.
 //
-// Bound: 4*128*128*d flops and 128*128 exponentials per tile pair; at d = 128
-// the two take the same time on an SM (16 exponentials, 8192 flops a cycle),
-// at d = 64 the exponentials take twice as long as the products.
+// Bound: 4*128*128*d flops and 128*128 exponentials per query tile and key tile;
+// at d = 128 the two take the same time on an SM (16 exponentials, 8192 flops a
+// cycle), at d = 64 the exponentials take twice as long as the products.
+// Measured (32/8 heads, bf16): 2 x 8192 tokens, full, 128 channels 1.80 ms, 1.22
+// PFLOP/s, 0.75 of the library product's burst rate; 64 channels 1.40 ms, 0.78
+// PFLOP/s, 0.70 of the exponentials' rate; one causal prompt of 16384 tokens of 128
+// channels 1.82 ms.  The same loop without its arithmetic between tcgen05.ld and
+// tcgen05.st runs at 1.62 and 1.22 PFLOP/s.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -63,7 +69,8 @@ struct AttnShape {
   static constexpr int kBlockBytes = kAttnM * 128;
   static constexpr int kStages = kDP == 128 ? 4 : 8;
   static constexpr int kStoreBytes = 32 * 128;           // a warp's rows, 64 channels at a time
-  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 4 * kStoreBytes + 2048 + 512;
+  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 4 * kStoreBytes +
+                                  2048 + 512;
   // Tensor-memory columns: scores at 0 and 128, outputs at 256.  With 64
   // channels the probabilities have columns of their own behind the outputs, so
   // the next scores are made while these are exponentiated; with 128 they lie
@@ -75,6 +82,9 @@ struct AttnShape {
   static constexpr int kProbStep = kOwnP ? kAttnN / 2 : kAttnN;  // between the two tiles
   static constexpr int kParts = kOwnP ? 1 : 2;
 };
+// Looks at the other warp's count before going on anyway, and the 32-column chunk
+// behind which a warp hands over: 64 channels 1475 us in turns, 1616 without; 128
+// channels 1.80 and 2.22 ms (2 x 8192 tokens, full).
 constexpr int kTurnPolls = 100, kTurnChunk = 3;
 
 struct PromptParams {
@@ -475,8 +485,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         if (!ok) break;
         const int slot = it & 1;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_sleep(smem_u32(&uempty_bar[slot]), ((it >> 1) & 1) ^ 1u, abort_flag,
-                                        err, kErrWaitProducer, lim));
+                        mbar_wait_sleep(smem_u32(&uempty_bar[slot]), ((it >> 1) & 1) ^ 1u,
+                                        abort_flag, err, kErrWaitProducer, lim));
         if (!ok) break;
         if (lane == 0) {
           units[slot] = u;
@@ -665,7 +675,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             tc_fence_after();
 #pragma unroll
             for (int k = h * kGroups; k < (h + 1) * kGroups; ++k)
-              umma_ts_x4(tmem + S::kOutCol + i * kDP, tmem + S::kProbCol + i * S::kProbStep + k * 32,
+              umma_ts_x4(tmem + S::kOutCol + i * kDP,
+                         tmem + S::kProbCol + i * S::kProbStep + k * 32,
                          v_at + static_cast<uint64_t>(k * (8192 >> 4)), p.idesc_o,
                          (j > 0 || k > 0) ? 1u : 0u);
           }
@@ -737,8 +748,9 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  w[e] = ml.y > 0.f ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
-                                    : 0u;
+                  w[e] = ml.y > 0.f
+                             ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
+                             : 0u;
                 *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
               }
@@ -877,7 +889,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             w[e] = pack2<kBf16>(a, b);
           }
           if (c == kTurnChunk && lane == 0) turn_at[warp] = turns + j + 1;
-          if (c == 3) s_there = S::kOwnP && mbar_test_wait(smem_u32(&s_bar[i]), (turns + j + 1) & 1);
+          if (S::kOwnP && c == 3)
+            s_there = mbar_test_wait(smem_u32(&s_bar[i]), (turns + j + 1) & 1);
           tmem_st16(p_at + c * 16, w);
           if ((c + 1) % (4 / S::kParts) == 0) {
             tmem_wait_st();

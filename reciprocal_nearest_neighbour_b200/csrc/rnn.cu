@@ -3065,6 +3065,9 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   PromptParams p;
   std::memset(&p, 0, sizeof(p));
   p.group = Hq / Hkv;
+  // two heads that share their keys, or two neighbouring token tiles of one head (which
+  // see different numbers of keys): 20 causal prompts of 17 to 4001 tokens, 32/8 heads
+  // of 128, 277 us with pairs of heads, 290 with pairs of token tiles
   p.pair_heads = p.group % 2 == 0;
   p.head_units = p.pair_heads ? Hq / 2 : Hq;
   // every sequence may end in a partial tile
@@ -3100,6 +3103,8 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   p.Hq = Hq;
   p.d = d;
   p.causal = causal != 0;
+  // longest sequences first once units queue: 9 sequences of 700 to 10 207 keys 321 us,
+  // 358 in the given order (24 equal ones 107 and 104; 3 short ones 8.6 and 8.2)
   p.sort = units > di->sms && B > 1;
   p.scale = scale;
   p.c = scale * 1.44269504f;
@@ -3129,6 +3134,8 @@ template <bool kBf16, int kDP>
 static rnn_status decode_launch(const DecodeParams& p, dim3 grid, cudaStream_t s) {
   const dim3 block(kDecWarps * 32);
   const size_t sm = DecShape<kDP>::kSmem;
+  // up to 8 heads one column block: 96 streams of 4 heads a key head 108 us, 109 with
+  // two, one stream 7.7 and 8.2
   if (p.group <= 8)
     attn_decode_kernel<kBf16, kDP, 1><<<grid, block, sm, s>>>(p);
   else
@@ -3231,6 +3238,7 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
   p.d = d;
   p.max_pages = max_pages;
   p.page = make_fastdiv(page_size);
+  // one page look-up and no shuffles per 16 keys: 96 streams 108 us, 110 row by row
   p.page16 = page_size % 16 == 0;
   p.scale = scale;
   p.c = scale * 1.44269504f;
@@ -3335,9 +3343,12 @@ rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
   p.pairs = pairs;
   p.axes = axes;
   p.paired = paired != 0;
+  // the widest unit that divides the pairs: 16 and 8 bytes a vector take 99 and 133 us
+  // for 21 326 prompt tokens of 32/8 heads of 128
   const int vec = pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
   const int row_units = (axes * pairs + d - 2 * axes * pairs) / vec;
-  // few tokens: up to 8 warps each, while all of them fit on the GPU at once
+  // few tokens: up to 8 warps each, while all of them fit on the GPU at once (one token
+  // 3.2 us, 4.2 with one warp; 200 tokens of 32/8 heads of 128 4.6 and 8.4)
   while (p.share < 3 && (T << (p.share + 1)) <= 16 * di->sms) ++p.share;
   p.by_unit = make_fastdiv(row_units);
   p.by_vunit = make_fastdiv(d / 8);
