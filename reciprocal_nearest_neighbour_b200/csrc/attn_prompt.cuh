@@ -38,11 +38,10 @@
 // Bound: 4*128*128*d flops and 128*128 exponentials per query tile and key tile;
 // at d = 128 the two take the same time on an SM (16 exponentials, 8192 flops a
 // cycle), at d = 64 the exponentials take twice as long as the products.
-// Measured (32/8 heads, bf16): 2 x 8192 tokens, full, 128 channels 1.80 ms, 1.22
-// PFLOP/s, 0.75 of the library product's burst rate; 64 channels 1.40 ms, 0.78
-// PFLOP/s, 0.70 of the exponentials' rate; one causal prompt of 16384 tokens of 128
-// channels 1.82 ms.  The same loop without its arithmetic between tcgen05.ld and
-// tcgen05.st runs at 1.62 and 1.22 PFLOP/s.
+// Measured (32/8 heads, bf16): 2 x 8192 tokens, full, 128 channels 1.70 ms, 1.29
+// PFLOP/s, 0.80 of the library product's burst rate (the power limit moves it up to
+// 5 % from run to run); 64 channels 1.43 ms, 0.77 PFLOP/s, 0.65 of the exponentials'
+// rate at 1965 MHz; one causal prompt of 16384 tokens of 128 channels 1.73 ms.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -82,10 +81,11 @@ struct AttnShape {
   static constexpr int kProbStep = kOwnP ? kAttnN / 2 : kAttnN;  // between the two tiles
   static constexpr int kParts = kOwnP ? 1 : 2;
 };
-// Looks at the other warp's count before going on anyway, and the 32-column chunk
-// behind which a warp hands over: 64 channels 1475 us in turns, 1616 without; 128
-// channels 1.80 and 2.22 ms (2 x 8192 tokens, full).
-constexpr int kTurnPolls = 100, kTurnChunk = 3;
+// Looks at the other warp's count, 40 ns apart, before going on anyway, and the
+// 32-column chunk behind which a warp hands over.  2 x 8192 tokens, full: 64 channels
+// 1.43 ms behind the third chunk, 1.47 behind the second, 1.59 behind the last and
+// 1.65 without turns; 128 channels 1.70, 1.92, 1.70 and 2.25 ms.
+constexpr int kTurnPolls = 100, kTurnChunk = 2;
 
 struct PromptParams {
   const int32_t *cu_q, *cu_k;
@@ -259,13 +259,43 @@ __device__ __forceinline__ void touch(const int32_t* at) {
   asm volatile("{\n\t.reg .s32 v;\n\tld.global.nc.s32 v, [%0];\n\t}" ::"l"(at));
 }
 
-// A count in shared memory, with the writes before it.
-__device__ __forceinline__ void st_release(int* at, int v) {
-  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(at)), "r"(v) : "memory");
-}
-__device__ __forceinline__ int ld_acquire(const int* at) {
+// Shared memory by 32-bit address.
+__device__ __forceinline__ int lds_volatile(uint32_t at) {
   int v;
-  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(at)) : "memory");
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_volatile(uint32_t at, int v) {
+  asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f2(uint32_t at, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+// A count, with the writes before it.
+__device__ __forceinline__ void st_release(uint32_t at, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire(uint32_t at) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
 
@@ -287,77 +317,96 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   constexpr int kUnitReaders = 14;  // softmax, MMA and output warps
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* q_tiles = smem;
-  uint8_t* ring = smem + 2 * S::kTileBytes;
-  uint8_t* staging = ring + S::kStages * S::kTileBytes;
-  float2* row_ml = reinterpret_cast<float2*>(staging + 4 * S::kStoreBytes);  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(row_ml + 2 * kAttnM);
-  uint64_t* full_bar = bars;
-  uint64_t* empty_bar = full_bar + S::kStages;
-  uint64_t* qfull_bar = empty_bar + S::kStages;
-  uint64_t* qempty_bar = qfull_bar + 1;
-  uint64_t* s_bar = qempty_bar + 1;  // scores of tile i are in tensor memory
-  uint64_t* sfree_bar = s_bar + 2;   // its scores are in registers (kOwnP)
-  uint64_t* p_bar = sfree_bar + 2;   // its probabilities are there, by parts
-  uint64_t* o_bar = p_bar + 4;       // its output is complete; with kOwnP, so far
-  uint64_t* ofree_bar = o_bar + 2;   // its output has been read
-  uint64_t* ufull_bar = ofree_bar + 2;
-  uint64_t* uempty_bar = ufull_bar + 2;
-  uint64_t* ml_bar = uempty_bar + 2;  // its rows' maxima and totals are there
-  uint64_t* mlfree_bar = ml_bar + 2;  // and have been read
-  uint64_t* ask_bar = mlfree_bar + 2;
-  uint64_t* drain_bar = ask_bar + 1;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(drain_bar + 2);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  // Shared memory by 32-bit addresses: one base, everything else a constant away.
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_tiles = smem;
+  const uint32_t ring = smem + 2 * S::kTileBytes;
+  const uint32_t staging = ring + S::kStages * S::kTileBytes;
+  const uint32_t row_ml = staging + 4 * S::kStoreBytes;  // float2 [2][128]
+  const uint32_t bars = row_ml + 2 * kAttnM * 8;
+  const uint32_t full_bar = bars;
+  const uint32_t empty_bar = full_bar + 8 * S::kStages;
+  const uint32_t qfull_bar = empty_bar + 8 * S::kStages;
+  const uint32_t qempty_bar = qfull_bar + 8;
+  const uint32_t s_bar = qempty_bar + 8;    // scores of tile i are in tensor memory
+  const uint32_t sfree_bar = s_bar + 16;    // its scores are in registers (kOwnP)
+  const uint32_t p_bar = sfree_bar + 16;    // its probabilities are there, by parts
+  const uint32_t o_bar = p_bar + 32;        // its output is complete; with kOwnP, so far
+  const uint32_t ofree_bar = o_bar + 16;    // its output has been read
+  const uint32_t ufull_bar = ofree_bar + 16;
+  const uint32_t uempty_bar = ufull_bar + 16;
+  const uint32_t ml_bar = uempty_bar + 16;  // its rows' maxima and totals are there
+  const uint32_t mlfree_bar = ml_bar + 16;  // and have been read
+  const uint32_t ask_bar = mlfree_bar + 16;
+  const uint32_t drain_bar = ask_bar + 8;
+  const uint32_t tmem_slot = drain_bar + 16;
+  const uint32_t abort_at = tmem_slot + 4;
   // counts that only grow, where a reader may be any number of steps behind
-  int* zero_at = reinterpret_cast<int*>(misc + 2);  // ragged V tiles whose end is zeroed
-  volatile int* turn_at = reinterpret_cast<volatile int*>(misc + 4);  // per softmax warp: steps
-                                                                      // whose exponentials are out
+  const uint32_t zero_at = tmem_slot + 8;   // ragged V tiles whose end is zeroed
+  const uint32_t turn_at = tmem_slot + 16;  // per softmax warp: steps whose exponentials are out
   __shared__ __align__(16) uint8_t answer[16];
   __shared__ PromptUnit units[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // without a caller's word, a wait that runs out is noted here and only ends the kernel
-  int* const err = p.err ? p.err : reinterpret_cast<int*>(misc + 3);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
+  // Waits: the outcome is the same in all lanes of a warp (they look at the same
+  // words).  They suspend the warp: spinning ones take issue slots from the softmax
+  // warps of the same scheduler (128 channels: a tenth slower).  The limits are read from the parameters where they are needed, so that
+  // no register holds them, nor an address of a barrier, through the loops.
+  auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
+  auto give_up = [&](int code) {
+    sts_volatile(abort_at, 1);
+    if (p.err) atomicOr(p.err, code);  // without a caller's word it only ends the kernel
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (true) {
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+      if (aborted()) return false;
+      if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+        give_up(code);
+        return false;
+      }
+    }
+  };
   if (threadIdx.x < S::kStages) {
-    mbar_init(smem_u32(&full_bar[threadIdx.x]), 1);
-    mbar_init(smem_u32(&empty_bar[threadIdx.x]), 2);
+    mbar_init(full_bar + 8 * threadIdx.x, 1);
+    mbar_init(empty_bar + 8 * threadIdx.x, 2);
     fence_barrier_init();
   } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
     const int i = threadIdx.x - 32;
-    mbar_init(smem_u32(&s_bar[i]), 1);
-    mbar_init(smem_u32(&sfree_bar[i]), 4);
-    mbar_init(smem_u32(&p_bar[i]), 4);
-    mbar_init(smem_u32(&p_bar[2 + i]), 4);
-    mbar_init(smem_u32(&o_bar[i]), 1);
+    mbar_init(s_bar + 8 * i, 1);
+    mbar_init(sfree_bar + 8 * i, 4);
+    mbar_init(p_bar + 8 * i, 4);
+    mbar_init(p_bar + 8 * (2 + i), 4);
+    mbar_init(o_bar + 8 * i, 1);
     fence_barrier_init();
   } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
     const int i = threadIdx.x - 64;
-    mbar_init(smem_u32(&ofree_bar[i]), 4);
-    mbar_init(smem_u32(&ml_bar[i]), 4);
-    mbar_init(smem_u32(&mlfree_bar[i]), 4);
-    mbar_init(smem_u32(&ufull_bar[i]), 1);
-    mbar_init(smem_u32(&uempty_bar[i]), kUnitReaders);
-    mbar_init(smem_u32(&drain_bar[i]), 1);
+    mbar_init(ofree_bar + 8 * i, 4);
+    mbar_init(ml_bar + 8 * i, 4);
+    mbar_init(mlfree_bar + 8 * i, 4);
+    mbar_init(ufull_bar + 8 * i, 1);
+    mbar_init(uempty_bar + 8 * i, kUnitReaders);
+    mbar_init(drain_bar + 8 * i, 1);
     fence_barrier_init();
   } else if (threadIdx.x == 96) {
-    mbar_init(smem_u32(qfull_bar), 1);
-    mbar_init(smem_u32(qempty_bar), 2);
-    mbar_init(smem_u32(ask_bar), 1);
+    mbar_init(qfull_bar, 1);
+    mbar_init(qempty_bar, 2);
+    mbar_init(ask_bar, 1);
     fence_barrier_init();
   } else if (threadIdx.x >= 128 && threadIdx.x < 136) {
-    turn_at[threadIdx.x - 128] = 0;
+    sts_volatile(turn_at + 4 * (threadIdx.x - 128), 0);
     if (threadIdx.x == 128) {
-      *zero_at = 0;
-      *abort_flag = 0;
+      sts_volatile(zero_at, 0);
+      sts_volatile(abort_at, 0);
     }
   }
   constexpr uint32_t kCols = 512;
   if (warp == kAttnMmaWarp) {
-    tmem_alloc(smem_u32(misc), kCols);
+    tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
   if (warp == kAttnTmaWarp) {
@@ -374,18 +423,16 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[0];
-  const uint64_t lim = p.wait_limit_ns;
+  const uint32_t tmem = lds_volatile(tmem_slot);
 
   // Unit number `it` of this CTA, as the TMA warp published it.
   auto take_unit = [&](int it, int code, PromptUnit& u) {
     const int slot = it & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ufull_bar[slot]), (it >> 1) & 1,
-                                                 abort_flag, err, code, lim)))
+    if (!__all_sync(0xffffffffu, wait(ufull_bar + 8 * slot, (it >> 1) & 1, code)))
       return false;
     u = units[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&uempty_bar[slot]));
+    if (lane == 0) mbar_arrive(uempty_bar + 8 * slot);
     return u.nq >= 0;
   };
 
@@ -435,8 +482,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       int asked = 0;
       bool ok = true;
       auto answered = [&]() {
-        if (!__all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(ask_bar), (asked - 1) & 1, abort_flag,
-                                                     err, kErrWaitProducer, lim)))
+        if (!__all_sync(0xffffffffu, wait(ask_bar, (asked - 1) & 1, kErrWaitProducer)))
           return false;
         block = next_block_read(smem_u32(answer));
         fence_proxy_async_smem();  // read before the next answer is written
@@ -445,8 +491,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       };
       auto ask = [&]() {
         if (lane == 0) {
-          mbar_arrive_expect_tx(smem_u32(ask_bar), 16);
-          next_block_request(smem_u32(answer), smem_u32(ask_bar));
+          mbar_arrive_expect_tx(ask_bar, 16);
+          next_block_request(smem_u32(answer), ask_bar);
         }
         ++asked;
         __syncwarp();
@@ -485,39 +531,36 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         if (!ok) break;
         const int slot = it & 1;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_sleep(smem_u32(&uempty_bar[slot]), ((it >> 1) & 1) ^ 1u,
-                                        abort_flag, err, kErrWaitProducer, lim));
+                        wait(uempty_bar + 8 * slot, ((it >> 1) & 1) ^ 1u, kErrWaitProducer));
         if (!ok) break;
         if (lane == 0) {
           units[slot] = u;
-          mbar_arrive(smem_u32(&ufull_bar[slot]));
+          mbar_arrive(ufull_bar + 8 * slot);
         }
         __syncwarp();
         if (u.nq < 0 || p.stall_loads) break;
         const PromptTiles t(p, u);
         if (t.n_max > 0 && lane == 0) {
-          ok = mbar_wait_sleep(smem_u32(qempty_bar), (q_loads & 1) ^ 1u, abort_flag, err,
-                               kErrWaitProducer, lim);
+          ok = wait(qempty_bar, (q_loads & 1) ^ 1u, kErrWaitProducer);
           if (ok) {
-            const uint32_t qb = smem_u32(qfull_bar);
+            const uint32_t qb = qfull_bar;
             mbar_arrive_expect_tx(qb, 2 * S::kTileBytes);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               for (int c = 0; c < S::kBlocks; ++c)
-                tma_load_3d(smem_u32(q_tiles) + i * S::kTileBytes + c * S::kBlockBytes, &qmap, qb,
+                tma_load_3d(q_tiles + i * S::kTileBytes + c * S::kBlockBytes, &qmap, qb,
                             c * 64, t.head[i], u.q0 + t.row0[i]);
             ++q_loads;
           }
           const int kv_head = t.head[0] / p.group;
           for (int j = 0; j < 2 * t.n_max && ok; ++j) {
             const int s = issued % S::kStages;
-            ok = mbar_wait_sleep(smem_u32(&empty_bar[s]), ((issued / S::kStages) & 1) ^ 1u,
-                                 abort_flag, err, kErrWaitProducer, lim);
+            ok = wait(empty_bar + 8 * s, ((issued / S::kStages) & 1) ^ 1u, kErrWaitProducer);
             if (!ok) break;
-            const uint32_t fb = smem_u32(&full_bar[s]);
+            const uint32_t fb = full_bar + 8 * s;
             mbar_arrive_expect_tx(fb, S::kTileBytes);
             for (int c = 0; c < S::kBlocks; ++c)
-              tma_load_3d(smem_u32(ring) + s * S::kTileBytes + c * S::kBlockBytes,
+              tma_load_3d(ring + s * S::kTileBytes + c * S::kBlockBytes,
                           j & 1 ? &vmap : &kmap, fb, c * 64, kv_head, u.k0 + (j >> 1) * kAttnN);
             ++issued;
           }
@@ -532,11 +575,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       if (lane == 0) {
         // no copy, and no arrival of a product's completion, is under way when the
         // CTA exits, whatever the other roles did
-        auto settle = [&](uint64_t* bar, uint32_t parity) {
+        auto settle = [&](uint32_t bar, uint32_t parity) {
           const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(smem_u32(bar), parity)) {
-            if (globaltimer_ns() - t0 > lim) {
-              atomicOr(err, kErrDrain);
+          while (!mbar_try_wait(bar, parity)) {
+            if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+              if (p.err) atomicOr(p.err, kErrDrain);
               return;
             }
           }
@@ -544,37 +587,38 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         if (asked > 0) settle(ask_bar, (asked - 1) & 1);
         if (q_loads > 0) settle(qfull_bar, (q_loads - 1) & 1);
         for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-          settle(&full_bar[q % S::kStages], (q / S::kStages) & 1);
-        if (!*abort_flag) {
+          settle(full_bar + 8 * (q % S::kStages), (q / S::kStages) & 1);
+        if (!aborted()) {
           if (q_loads > 0) settle(qempty_bar, (q_loads - 1) & 1);
           for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-            settle(&empty_bar[q % S::kStages], (q / S::kStages) & 1);
+            settle(empty_bar + 8 * (q % S::kStages), (q / S::kStages) & 1);
         }
       }
     } else if (warp == kAttnMmaWarp || warp == kAttnMmaWarp2) {
       // ---------------------------------------------------------- products
       const int i = warp == kAttnMmaWarp ? 0 : 1;  // this warp's query tile
       const int dsteps = (p.d + 15) / 16;
-      const uint64_t q_desc = make_sdesc(smem_u32(q_tiles) + i * S::kTileBytes, 64);
-      const uint64_t k_desc = make_sdesc(smem_u32(ring), 64);
-      const uint64_t v_desc = make_vdesc(smem_u32(ring));
+      const uint64_t q_desc = make_sdesc(q_tiles + i * S::kTileBytes, 64);
+      const uint64_t k_desc = make_sdesc(ring, 64);
+      const uint64_t v_desc = make_vdesc(ring);
       bool ok = true, any = false;
       int used = 0, q_used = 0;       // loads taken so far
       int turns = 0;                  // score tiles made so far
       int zeroed = 0;                 // ragged V tiles so far
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(smem_u32(bar), parity, abort_flag, err,
-                                                          kErrWaitMma, lim));
+      auto wait_mma = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, wait(bar, parity, kErrWaitMma));
         return ok;
       };
       auto slot_of = [&](int x) { return x % S::kStages; };
-      auto wait_load = [&](int x) { return wait(&full_bar[slot_of(x)], (x / S::kStages) & 1); };
+      auto wait_load = [&](int x) {
+        return wait_mma(full_bar + 8 * slot_of(x), (x / S::kStages) & 1);
+      };
       // this warp is done with a buffer: when its products so far are, or at once
-      auto release = [&](uint64_t* bar, bool behind_products) {
+      auto release = [&](uint32_t bar, bool behind_products) {
         if (behind_products)
-          umma_commit_warp(smem_u32(bar));
+          umma_commit_warp(bar);
         else if (lane == 0)
-          mbar_arrive(smem_u32(bar));
+          mbar_arrive(bar);
       };
       auto scores = [&](int slot) {  // S_i = Q_i K^T
         const uint64_t k_at = k_desc + static_cast<uint64_t>(slot * (S::kTileBytes >> 4));
@@ -591,7 +635,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                             c > 0 || k > 0);
           }
         }
-        umma_commit_warp(smem_u32(&s_bar[i]));
+        umma_commit_warp(s_bar + 8 * i);
         any = true;
       };
       PromptUnit u;
@@ -601,16 +645,16 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         // the last unit's output must have been read before this one's begins (its
         // scores may go first); waited for at every unit, so that the parity is
         // that of the last one
-        auto outputs_free = [&]() { return it == 0 || wait(&ofree_bar[i], (it - 1) & 1); };
+        auto outputs_free = [&]() { return it == 0 || wait_mma(ofree_bar + 8 * i, (it - 1) & 1); };
         if (n == 0 && !outputs_free()) break;
         if (t.n_max == 0) continue;
-        if (!wait(qfull_bar, q_used & 1) || !wait_load(used)) break;
+        if (!wait_mma(qfull_bar, q_used & 1) || !wait_load(used)) break;
         ++q_used;
         tc_fence_after();
         // the scores may overwrite the last unit's probabilities: the tensor pipe
         // works in order
         if (n > 0) scores(slot_of(used));
-        release(&empty_bar[slot_of(used)], n > 0);
+        release(empty_bar + 8 * slot_of(used), n > 0);
         if (n <= 1) release(qempty_bar, n == 1);
         __syncwarp();
         for (int j = 0; j < t.n_max; ++j) {
@@ -621,21 +665,19 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             // rows behind the last key belong to other sequences: whatever they
             // hold, their probabilities are 0 and 0 * NaN must not reach the sum
             if (i == 0) {
-              uint8_t* vt = ring + vs * S::kTileBytes;
+              const uint32_t vt = ring + vs * S::kTileBytes + left * 128;
               const int chunks = (kAttnN - left) * 8;
               for (int c = 0; c < S::kBlocks; ++c)
                 for (int e = lane; e < chunks; e += 32)
-                  *reinterpret_cast<uint4*>(vt + c * S::kBlockBytes + left * 128 + e * 16) =
-                      make_uint4(0, 0, 0, 0);
+                  sts_v4(vt + c * S::kBlockBytes + e * 16, make_uint4(0, 0, 0, 0));
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) st_release(zero_at, zeroed + 1);
             } else {
               const uint64_t t0 = globaltimer_ns();
               while (ld_acquire(zero_at) <= zeroed) {
-                if (*abort_flag || globaltimer_ns() - t0 > lim) {
-                  *abort_flag = 1;
-                  atomicOr(err, kErrWaitMma);
+                if (!aborted() && globaltimer_ns() - t0 > p.wait_limit_ns) give_up(kErrWaitMma);
+                if (aborted()) {
                   ok = false;
                   break;
                 }
@@ -646,17 +688,17 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             ++zeroed;
           }
           if (j >= n) {
-            release(&empty_bar[vs], false);
+            release(empty_bar + 8 * vs, false);
             if (j + 1 < t.n_max) {
               if (!wait_load(kx)) break;
-              release(&empty_bar[slot_of(kx)], false);
+              release(empty_bar + 8 * slot_of(kx), false);
             }
             __syncwarp();
             continue;
           }
           auto next_scores = [&]() {
             if constexpr (S::kOwnP)
-              if (!wait(&sfree_bar[i], (turns + j) & 1)) return;
+              if (!wait_mma(sfree_bar + 8 * i, (turns + j) & 1)) return;
             tc_fence_after();
             scores(slot_of(kx));
           };
@@ -671,7 +713,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
 #pragma unroll
           for (int h = 0; h < S::kParts; ++h) {
             constexpr int kGroups = kAttnN / 64 / S::kParts;  // of 64 keys
-            if (!wait(&p_bar[2 * h + i], (turns + j) & 1)) break;
+            if (!wait_mma(p_bar + 8 * (2 * h + i), (turns + j) & 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int k = h * kGroups; k < (h + 1) * kGroups; ++k)
@@ -681,26 +723,26 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                          (j > 0 || k > 0) ? 1u : 0u);
           }
           if (!ok) break;
-          if (S::kOwnP || j + 1 == n) umma_commit_warp(smem_u32(&o_bar[i]));
+          if (S::kOwnP || j + 1 == n) umma_commit_warp(o_bar + 8 * i);
           if constexpr (!S::kOwnP)
             if (j + 1 < n) next_scores();
           if (!ok) break;
-          release(&empty_bar[vs], true);
-          if (j + 1 < t.n_max) release(&empty_bar[slot_of(kx)], j + 1 < n);
+          release(empty_bar + 8 * vs, true);
+          if (j + 1 < t.n_max) release(empty_bar + 8 * slot_of(kx), j + 1 < n);
           if (j + 2 == n) release(qempty_bar, true);
           __syncwarp();
         }
         used += 2 * t.n_max;
         turns += n;
       }
-      if (*abort_flag && any) {
+      if (aborted() && any) {
         // let every product issued finish before tensor memory is released
-        umma_commit_warp(smem_u32(&drain_bar[i]));
+        umma_commit_warp(drain_bar + 8 * i);
         __syncwarp();
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(smem_u32(&drain_bar[i]), 0)) {
-          if (globaltimer_ns() - t0 > lim) {
-            if (lane == 0) atomicOr(err, kErrDrain);
+        while (!mbar_try_wait(drain_bar + 8 * i, 0)) {
+          if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+            if (lane == 0 && p.err) atomicOr(p.err, kErrDrain);
             break;
           }
         }
@@ -709,7 +751,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       // ----------------------------------------------------------- outputs
       const int quad = warp & 3;
       const uint32_t lane_at = static_cast<uint32_t>(quad * 32) << 16;
-      uint8_t* mine = staging + quad * S::kStoreBytes;
+      const uint32_t mine = staging + quad * S::kStoreBytes;
       int outs[2] = {0, 0};
       bool ok = true;
       PromptUnit u;
@@ -719,15 +761,13 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         for (int i = 0; i < 2; ++i) {
           // (the last totals being there, the output's phase before the last is over)
           if (t.n[i] > 0) outs[i] += S::kOwnP ? t.n[i] : 1;
-          ok = ok && mbar_wait_sleep(smem_u32(&ml_bar[i]), it & 1, abort_flag, err,
-                                     kErrWaitEpilogue, lim);
-          const float2 ml = row_ml[i * kAttnM + quad * 32 + lane];
+          ok = ok && wait(ml_bar + 8 * i, it & 1, kErrWaitEpilogue);
+          const float2 ml = lds_f2(row_ml + 8 * (i * kAttnM + quad * 32 + lane));
           ok = ok && (t.n[i] == 0 ||
-                      mbar_wait_sleep(smem_u32(&o_bar[i]), (outs[i] - 1) & 1, abort_flag, err,
-                                      kErrWaitEpilogue, lim));
+                      wait(o_bar + 8 * i, (outs[i] - 1) & 1, kErrWaitEpilogue));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) mbar_arrive(smem_u32(&mlfree_bar[i]));
+          if (lane == 0) mbar_arrive(mlfree_bar + 8 * i);
           tc_fence_after();
           const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
           const int row = t.row0[i] + quad * 32;  // the warp's first row in the sequence
@@ -751,20 +791,20 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                   w[e] = ml.y > 0.f
                              ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
                              : 0u;
-                *reinterpret_cast<uint4*>(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                sts_v4(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4),
+                       make_uint4(w[0], w[1], w[2], w[3]));
               }
             }
             if (c == S::kBlocks - 1) tc_fence_before();
             __syncwarp();
-            if (c == S::kBlocks - 1 && lane == 0) mbar_arrive(smem_u32(&ofree_bar[i]));
+            if (c == S::kBlocks - 1 && lane == 0) mbar_arrive(ofree_bar + 8 * i);
             const int ch = lane & 7, col = c * 64 + ch * 8;
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
               const int x = h * 4 + (lane >> 3);
               if (x < rows && col < p.d)
                 *reinterpret_cast<uint4*>(ob + x * p.o_ts + col) =
-                    *reinterpret_cast<const uint4*>(mine + x * 128 + ((ch ^ (x & 7)) << 4));
+                    lds_v4(mine + x * 128 + ((ch ^ (x & 7)) << 4));
             }
             __syncwarp();
           }
@@ -798,8 +838,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       bool s_there = false;  // the step's scores have been seen to be there
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        if (!s_there && !mbar_wait_spin(smem_u32(&s_bar[i]), (turns + j) & 1, abort_flag, err,
-                                        kErrWaitEpilogue, lim)) {
+        if (!s_there && !wait(s_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue)) {
           ok = false;
           break;
         }
@@ -813,11 +852,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         // a look at a barrier takes a couple of hundred cycles: this one's answer is
         // used behind the comparisons, the one for the next scores in the next step
         bool o_there = !S::kOwnP || turns + j == 0;
-        if (!o_there) o_there = mbar_test_wait(smem_u32(&o_bar[i]), (turns + j - 1) & 1);
+        if (!o_there) o_there = mbar_test_wait(o_bar + 8 * i, (turns + j - 1) & 1);
         if constexpr (S::kOwnP) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sfree_bar[i]));
+          if (lane == 0) mbar_arrive(sfree_bar + 8 * i);
         }
         if ((j + 1) * kAttnN > seen_all) {
           const int lim_col = seen - j * kAttnN;
@@ -830,8 +869,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
         if constexpr (S::kOwnP) {
           // the product before has read these columns, and its sum is complete
-          if (!o_there && !mbar_wait_spin(smem_u32(&o_bar[i]), (turns + j - 1) & 1, abort_flag, err,
-                                          kErrWaitEpilogue, lim)) {
+          if (!o_there && !wait(o_bar + 8 * i, (turns + j - 1) & 1, kErrWaitEpilogue)) {
             ok = false;
             break;
           }
@@ -869,7 +907,9 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         const int j_o = i ? j : j - 1;  // the other's step to wait for
         if (j_o >= 0 && j_o < n_o) {
 #pragma unroll 1
-          for (int k = 0; k < kTurnPolls && turn_at[warp ^ 4] <= turns_o + j_o; ++k) {
+          for (int k = 0; k < kTurnPolls; ++k) {
+            if (lds_volatile(turn_at + 4 * (warp ^ 4)) > turns_o + j_o) break;
+            __nanosleep(40);
           }
         }
         uint64_t sum[2] = {0, 0};
@@ -888,15 +928,15 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
             // total keeps them in fp32
             w[e] = pack2<kBf16>(a, b);
           }
-          if (c == kTurnChunk && lane == 0) turn_at[warp] = turns + j + 1;
+          if (c == kTurnChunk && lane == 0) sts_volatile(turn_at + 4 * warp, turns + j + 1);
           if (S::kOwnP && c == 3)
-            s_there = mbar_test_wait(smem_u32(&s_bar[i]), (turns + j + 1) & 1);
+            s_there = mbar_test_wait(s_bar + 8 * i, (turns + j + 1) & 1);
           tmem_st16(p_at + c * 16, w);
           if ((c + 1) % (4 / S::kParts) == 0) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_bar[2 * (c / (4 / S::kParts)) + i]));
+            if (lane == 0) mbar_arrive(p_bar + 8 * (2 * (c / (4 / S::kParts)) + i));
           }
         }
         float a, b;
@@ -906,12 +946,11 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       turns += n;
       turns_o += n_o;
       if (it > 0)
-        ok = ok && mbar_wait(smem_u32(&mlfree_bar[i]), (it - 1) & 1, abort_flag, err,
-                             kErrWaitEpilogue, lim);
+        ok = ok && wait(mlfree_bar + 8 * i, (it - 1) & 1, kErrWaitEpilogue);
       if (!__all_sync(0xffffffffu, ok)) break;
-      row_ml[i * kAttnM + r] = make_float2(m, l);
+      sts_f2(row_ml + 8 * (i * kAttnM + r), m, l);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ml_bar[i]));
+      if (lane == 0) mbar_arrive(ml_bar + 8 * i);
     }
   }
 
