@@ -474,7 +474,9 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  *     fall, in device memory.  Lengths may be 0.  Rows before cu[0] and
  *     from cu[B] on are not touched.
  *   - A row that sees no key gets zeros, and -infinity as its log-sum.
- *   - Queries, and the keys and values of a sequence, must be finite.  What
+ *   - Queries, and the keys and values of a sequence, must be finite.  A row
+ *     that sees a NaN or +infinite score becomes NaN, its log-sum too; a value
+ *     that is not finite may reach earlier rows of its sequence as well.  What
  *     lies outside the sequences may hold anything.
  *   - Arguments come in a structure, which is only read during the call;
  *     dtype is an rnn_dtype.
@@ -563,8 +565,8 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args *args, rnn_stream_t stream
  * q, out [B][Hq][d] (the sequence in the place of the token), lse [B][Hq] or
  * NULL.  lens [B] int32: tokens of each sequence in the cache, the new one's
  * included (values below 0 count as 0, values beyond max_pages * page_size as
- * that).  scale as above.  Keys whose page is outside [0, num_pages) count as absent; rows of
- * a page behind the last key may hold anything.
+ * that).  scale as above.  Keys whose page is outside [0, num_pages) count as
+ * absent; rows of a page behind the last key may hold anything.
  * d <= RNN_ATTN_MAX_DIM.
  */
 typedef struct rnn_attn_decode_args {

@@ -457,9 +457,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) {
             const float2 a = ml[w * kDecRows + row];
-            if (a.x != kNegInf) L += a.y * exp2_approx((a.x - M) * p.c);
+            // without a reference the total is 0, or NaN if its scores were
+            L += a.x == kNegInf ? a.y : a.y * exp2_approx((a.x - M) * p.c);
           }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const float inv = L != 0.f ? 1.f / L : 0.f;
           const float* b0 = merge + r * S::kMergeRow;
           const float* b1 = b0 + 8 * S::kMergeRow;
           if (done) {
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
                   pack2<kBf16>((b0[c] + b1[c]) * inv, (b0[c + 1] + b1[c + 1]) * inv);
             if (p.lse && lane == 0)
               p.lse[static_cast<int64_t>(cur.b) * p.Hq + head0 + row] =
-                  L > 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
+                  L != 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
           } else {
             float* pb = p.part + (slot * kDecRows + row) * kDP;
             for (int c = lane * 2; c < kDP; c += 64)
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParam
     f[w] = tot[w].x == kNegInf ? 0.f : exp2_approx((tot[w].x - M) * p.c);
     L += tot[w].y * f[w];
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
     const float x =
         ((acc[0][c] * f[0] + acc[1][c] * f[1]) + (acc[2][c] * f[2] + acc[3][c] * f[3])) * inv;
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParam
   }
   if (p.lse && threadIdx.x == 0)
     p.lse[static_cast<int64_t>(b) * p.Hq + head] =
-        L > 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
+        L != 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
 }
 
 }  // namespace rnn

@@ -772,7 +772,9 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
           const int row = t.row0[i] + quad * 32;  // the warp's first row in the sequence
           const int rows = min(32, u.nq - row);
-          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+          // no key seen: the total is 0; NaN scores make it NaN, and the row with it
+          const bool seen = ml.y != 0.f;
+          const float inv = seen ? 1.f / ml.y : 0.f;
           uint16_t* ob = p.out + static_cast<int64_t>(u.q0 + row) * p.o_ts + t.head[i] * p.o_hs;
           // 64 channels at a time through shared memory (16-byte chunks, swizzled), so
           // that a store covers 4 whole 128-byte rows; straight from its row, each
@@ -788,7 +790,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  w[e] = ml.y > 0.f
+                  w[e] = seen
                              ? pack2<kBf16>(o[h * 8 + 2 * e] * inv, o[h * 8 + 2 * e + 1] * inv)
                              : 0u;
                 sts_v4(mine + lane * 128 + (((2 * g + h) ^ (lane & 7)) << 4),
@@ -810,7 +812,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           }
           if (p.lse && lane < rows)
             p.lse[static_cast<int64_t>(u.q0 + row + lane) * p.Hq + t.head[i]] =
-                ml.y > 0.f ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
+                seen ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
         }
       }
     }

@@ -3054,7 +3054,8 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   if (Tq < 0 || Tk < 0 || Tq > INT32_MAX || Tk > INT32_MAX || B < 0) return RNN_EINVAL;
   rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
   if (r != RNN_OK) return r;
-  if (Tq > INT32_MAX - 1024 || Tk > INT32_MAX - 1024) return RNN_EUNSUPPORTED;
+  if (Tq > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1024)
+    return RNN_EUNSUPPORTED;
   if (!(scale > 0.f) || !(scale < 2e38f)) return RNN_EINVAL;
   if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return RNN_EINVAL;
   if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
@@ -3199,7 +3200,7 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
       (r = check_pages(&k_cache, num_pages, page_size, Hkv, d)) != RNN_OK ||
       (r = check_pages(&v_cache, num_pages, page_size, Hkv, d)) != RNN_OK)
     return r;
-  if (static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
+  if (B > INT32_MAX - 1024 || static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
   if (!workspace || !aligned256(workspace) ||
       ws_bytes < rnn_attn_decode_workspace_size(B, Hq, Hkv, d))
     return RNN_EWORKSPACE;
@@ -3289,7 +3290,9 @@ rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
       !valid_dtype(dtype))
     return RNN_EINVAL;
   if (d % 8) return RNN_EALIGN;
-  if (d > 256 || Hq > RNN_ATTN_MAX_HEADS || Hkv > RNN_ATTN_MAX_HEADS) return RNN_EUNSUPPORTED;
+  if (d > 256 || Hq > RNN_ATTN_MAX_HEADS || Hkv > RNN_ATTN_MAX_HEADS || B > INT32_MAX - 1024 ||
+      T > INT32_MAX - 1024)
+    return RNN_EUNSUPPORTED;
   if (pairs < 0 || axes < 0 || axes > 2 || (pairs == 0) != (axes == 0) || 2 * pairs * axes > d ||
       (pairs > 0 && !inv_freq) || (axes == 2 && !positions) ||
       (positions && T > 1 && position_stride < axes))

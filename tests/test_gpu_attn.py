@@ -158,6 +158,28 @@ def test_prompt_neighbours_do_not_leak():
             t[n:] = 0
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prompt_bad_scores_show(dtype, d, bad):
+    """A score that is not a number makes the rows that see it NaN, and no others."""
+    g = gen_of(12)
+    n, at = 300, 140
+    q = normal(g, (n, 4, d), dtype)
+    q[:, :, 0] = 1.0                  # so that the score of an infinite key is infinite
+    k, v = (normal(g, (n, 2, d), dtype) for _ in range(2))
+    good, good_lse = rnn.attn_prompt(q, k, v, ints([0, n]), with_lse=True)
+    k[at, 1, 0] = bad
+    out, lse = rnn.attn_prompt(q, k, v, ints([0, n]), with_lse=True)
+    assert torch.equal(out[:, :2], good[:, :2]) and torch.equal(lse[:, :2], good_lse[:, :2])
+    assert torch.equal(out[:at], good[:at]) and torch.equal(lse[:at], good_lse[:at])
+    assert out[at:, 2:].isnan().all() and lse[at:, 2:].isnan().all()
+    k[:, 1, 0] = float("nan")         # rows without a single number
+    out, lse = rnn.attn_prompt(q, k, v, ints([0, n]), causal=False, with_lse=True)
+    assert out[:, 2:].isnan().all() and lse[:, 2:].isnan().all()
+    assert out[:, :2].isfinite().all() and lse[:, :2].isfinite().all()
+
+
 def test_prompt_nothing_to_do():
     z = torch.zeros((0, 2, 64), dtype=BF, device="cuda")
     kv = torch.zeros((5, 2, 64), dtype=BF, device="cuda")
@@ -271,6 +293,27 @@ def test_decode_lengths_beyond_the_table():
     out = rnn.attn_decode(q, kc, vc, torch.from_numpy(table).cuda(), ints([2000000000, 20]))
     ref = oa.decode(f64(q), f64(kc), f64(vc), table, [32, 20], 1 / 8)
     check_attention(out, None, ref, BF, 64, 6.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens", [[70, 33], [4000, 90]])   # pairs in one share, and joined
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decode_bad_scores_show(dtype, lens, bad):
+    g = gen_of(13)
+    kc, vc, table = paged(g, lens, 16, 2, 64, dtype)
+    q = normal(g, (2, 4, 64), dtype)
+    q[:, :, 0] = 1.0
+    t = torch.from_numpy(table).cuda()
+    good, good_lse = rnn.attn_decode(q, kc, vc, t, ints(lens), with_lse=True)
+    kc[int(table[0, 3]), 5, 1, 0] = bad           # token 53 of the first sequence
+    out, lse = rnn.attn_decode(q, kc, vc, t, ints(lens), with_lse=True)
+    for b, h in ((0, 0), (0, 1), (1, 0), (1, 1), (1, 2), (1, 3)):
+        assert torch.equal(out[b, h], good[b, h]) and torch.equal(lse[b, h], good_lse[b, h])
+    assert out[0, 2:].isnan().all() and lse[0, 2:].isnan().all()
+    kc[:, :, 1, 0] = float("nan")
+    out, lse = rnn.attn_decode(q, kc, vc, t, ints(lens), with_lse=True)
+    assert out[:, 2:].isnan().all() and lse[:, 2:].isnan().all()
+    assert torch.equal(out[:, :2], good[:, :2]) and torch.equal(lse[:, :2], good_lse[:, :2])
 
 
 def test_decode_missing_pages():
