@@ -1,0 +1,150 @@
+"""attn_prompt beyond one unit a CTA (more units than SMs, units of very different
+length), and attn_decode with large groups of heads."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import reciprocal_nearest_neighbour_b200 as rnn
+from attn_bounds import check_attention
+from oracle.attention import Attn
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cum(lens):
+    return [0] + np.cumsum(lens).tolist()
+
+
+def normal(gen, shape, dtype):
+    return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+
+def reference(q, k, v, cu_q, cu_k, causal, scale) -> Attn:
+    """Attention in 64 bits, a sequence at a time, with what the error bounds need."""
+    tq, hq, d = q.shape
+    group = hq // k.shape[1]
+    opt = dict(dtype=torch.float64, device="cuda")
+    out, spread = torch.zeros(q.shape, **opt), torch.zeros(q.shape, **opt)
+    lse, reach = torch.full((tq, hq), -math.inf, **opt), torch.zeros((tq, hq), **opt)
+    keys = torch.zeros((tq, hq), dtype=torch.int64, device="cuda")
+    for b in range(len(cu_q) - 1):
+        nq, nk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        if nq == 0 or nk == 0:
+            continue
+        seen = torch.arange(nq, device="cuda") + (nk - nq + 1) if causal else \
+            torch.full((nq,), nk, device="cuda")
+        seen = seen.clamp(0, nk)
+        hidden = torch.arange(nk, device="cuda")[None] >= seen[:, None]
+        some = seen > 0
+        for h in range(hq):
+            K = k[cu_k[b]:cu_k[b + 1], h // group].double()
+            V = v[cu_k[b]:cu_k[b + 1], h // group].double()
+            Q = q[cu_q[b]:cu_q[b + 1], h].double()
+            s = ((Q @ K.T) * scale).masked_fill(hidden, -math.inf)
+            top = s.amax(1, keepdim=True).masked_fill(~some[:, None], 0.0)
+            w = (s - top).exp()
+            total = w.sum(1, keepdim=True)
+            one = torch.where(some[:, None], total, 1.0)
+            at = slice(cu_q[b], cu_q[b + 1])
+            out[at, h], spread[at, h] = (w @ V) / one, (w @ V.abs()) / one
+            lse[at, h] = torch.where(some, (top + one.log())[:, 0], -math.inf)
+            reach[at, h] = ((Q.abs() @ K.abs().T) * scale).masked_fill(hidden, 0.0).amax(1)
+            keys[at, h] = seen
+    return Attn(*(x.cpu().numpy() for x in (out, lse, spread, reach, keys)))
+
+
+def ragged(seed):
+    """72 sequences (three groups of 32 as the kernel deals them): long ones between ones
+    without keys, without queries, and with rows or whole tiles that see nothing."""
+    rng = np.random.default_rng(seed)
+    nq, nk = [], []
+    for b in range(72):
+        kind = b % 9
+        n = int(rng.integers(1, 420))
+        if kind < 4:                       # as many keys as queries, or more
+            nq.append(n)
+            nk.append(n + int(rng.integers(0, 500)) * (kind & 1))
+        elif kind == 4:                    # the first 128 rows see nothing, the next do
+            nq.append(200 + n % 50)
+            nk.append(60 + n % 30)
+        elif kind == 5:                    # only the last rows of several tiles see a key
+            nq.append(n + 300)
+            nk.append(1 + n % 20)
+        elif kind == 6:                    # many key tiles for a few queries
+            nq.append(1 + n % 9)
+            nk.append(900 + 2 * n)
+        elif kind == 7:
+            nq.append(n)
+            nk.append(0)
+        else:
+            nq.append(0)
+            nk.append(n)
+    return nq, nk
+
+
+def inputs(dtype, nq, nk, hq, hkv, d, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    q, k, v = (normal(g, (sum(n), h, d), dtype) for n, h in ((nq, hq), (nk, hkv), (nk, hkv)))
+    return q, k, v, cum(nq), cum(nk)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2)])     # pairs of heads, pairs of token tiles
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_ragged_units(dtype, d, hq, hkv, causal):
+    q, k, v, cu_q, cu_k = inputs(dtype, *ragged(d + hq), hq, hkv, d, 21)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    args = (q, k, v, ints(cu_q), ints(cu_k))
+    out, lse = rnn.attn_prompt(*args, causal=causal, with_lse=True, workspace=ws)
+    rnn.workspace_status(ws)
+    ref = reference(q, k, v, cu_q, cu_k, causal, 1 / math.sqrt(d))
+    check_attention(out, lse, ref, dtype, d, float(v.abs().max()))
+    for _ in range(3):                    # units are dealt as CTAs come free, results are not
+        again, lse2 = rnn.attn_prompt(*args, causal=causal, with_lse=True)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("d", [40, 64, 96, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (9, 3)])
+def test_many_units_of_one_sequence(d, hq, hkv):
+    """More units than SMs, up to 41 key tiles each, and more keys than queries."""
+    nq, nk = [5003], [5201]
+    q, k, v, cu_q, cu_k = inputs(BF, nq, nk, hq, hkv, d, 22)
+    for causal in (True, False):
+        out, lse = rnn.attn_prompt(q, k, v, ints(cu_q), ints(cu_k), causal=causal, with_lse=True)
+        ref = reference(q, k, v, cu_q, cu_k, causal, 1 / math.sqrt(d))
+        check_attention(out, lse, ref, BF, d, float(v.abs().max()))
+
+
+# ---------------------------------------------------- decode forms of large groups
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(9, 1), (16, 1), (34, 2), (40, 1)])
+@pytest.mark.parametrize("lens", [[130, 0, 5, 64], [3777, 20]])  # in one share, and joined
+def test_decode_groups(dtype, d, hq, hkv, lens):
+    """More than 8 query heads a key head, and more than the 16 of one unit."""
+    g = torch.Generator("cuda").manual_seed(hq + d)
+    size = 48
+    need = [-(-n // size) for n in lens]
+    deal = torch.randperm(sum(need) + 1, generator=g, device="cuda").int()
+    table = torch.zeros((len(lens), max(need)), dtype=torch.int32, device="cuda")
+    kc, vc = (normal(g, (sum(need) + 1, size, hkv, d), dtype) for _ in range(2))
+    at, rows = 0, []
+    for b, n in enumerate(need):
+        table[b, :n] = deal[at:at + n]
+        rows.append(deal[at:at + n].long())
+        at += n
+    q = normal(g, (len(lens), hq, d), dtype)
+    out, lse = rnn.attn_decode(q, kc, vc, table, ints(lens), with_lse=True)
+    k, v = (torch.cat([c[r].flatten(0, 1)[:n] for r, n in zip(rows, lens)]) for c in (kc, vc))
+    ref = reference(q, k, v, list(range(len(lens) + 1)), cum(lens), False, 1 / math.sqrt(d))
+    check_attention(out, lse, ref, dtype, d, float(v.abs().max()))
