@@ -544,7 +544,8 @@ rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
  *   scale    > 0 and < 2e38, multiplies the scores.
  *   out      [Tq][Hq][d], apart from the inputs.
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
- * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded; with a workspace (it
+ * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded (those that last as
+ * long as a sequence has keys count from its last step); with a workspace (it
  * may be NULL) rnn_workspace_status tells whether one ran out.
  */
 typedef struct rnn_attn_prompt_args {

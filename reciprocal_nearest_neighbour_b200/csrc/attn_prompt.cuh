@@ -60,6 +60,8 @@ constexpr int kAttnRegsSoftmax = 176, kAttnRegsOther = 80;
 constexpr int kAttnMmaWarp = 8, kAttnTmaWarp = 9, kAttnMmaWarp2 = 10,
               kAttnOutWarp = 12;
 constexpr float kAttnSlack = 8.f;      // log2 growth of the maximum before a rescale
+// Up to this many keys in a call no unit has more than 512 steps, about a millisecond.
+constexpr int64_t kAttnShortKeys = 65536;
 
 template <int kDP>
 struct AttnShape {
@@ -308,7 +310,24 @@ __device__ __forceinline__ void regs_give() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <bool kBf16, int kDP>
+// Wait for what must not be under way when the CTA exits.  It gives up when the limit
+// has passed and 64 more looks, 20 us each, were in vain: a CTA that was itself stopped
+// for that long (its GPU taken by another process) has time of its own first.
+__device__ __noinline__ void settle_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  int late = 0;
+#pragma unroll 1
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (globaltimer_ns() - t0 > limit_ns && ++late > 64) {
+      if (err) atomicOr(err, kErrDrain);
+      return;
+    }
+  }
+}
+
+// kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time.
+template <bool kBf16, int kDP, bool kLong>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -358,13 +377,22 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     sts_volatile(abort_at, 1);
     if (p.err) atomicOr(p.err, code);  // without a caller's word it only ends the kernel
   };
-  auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+  // Most last a step or two.  `whole_unit` marks those that last as long as a unit has
+  // keys: where that may be long, their limit counts from the last step that a tile's
+  // first softmax warp has done.
+  auto wait = [&](uint32_t bar, uint32_t parity, int code, bool whole_unit = false) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    int steps = 0;
 #pragma unroll 1
     while (true) {
       if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
       if (aborted()) return false;
+      if (kLong && whole_unit) {
+        const int now = lds_volatile(turn_at) + lds_volatile(turn_at + 16);
+        if (now != steps) t0 = globaltimer_ns();
+        steps = now;
+      }
       if (globaltimer_ns() - t0 > p.wait_limit_ns) {
         give_up(code);
         return false;
@@ -428,7 +456,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   // Unit number `it` of this CTA, as the TMA warp published it.
   auto take_unit = [&](int it, int code, PromptUnit& u) {
     const int slot = it & 1;
-    if (!__all_sync(0xffffffffu, wait(ufull_bar + 8 * slot, (it >> 1) & 1, code)))
+    if (!__all_sync(0xffffffffu, wait(ufull_bar + 8 * slot, (it >> 1) & 1, code, true)))
       return false;
     u = units[slot];
     __syncwarp();
@@ -576,13 +604,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         // no copy, and no arrival of a product's completion, is under way when the
         // CTA exits, whatever the other roles did
         auto settle = [&](uint32_t bar, uint32_t parity) {
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(bar, parity)) {
-            if (globaltimer_ns() - t0 > p.wait_limit_ns) {
-              if (p.err) atomicOr(p.err, kErrDrain);
-              return;
-            }
-          }
+          settle_phase(bar, parity, p.wait_limit_ns, p.err);
         };
         if (asked > 0) settle(ask_bar, (asked - 1) & 1);
         if (q_loads > 0) settle(qfull_bar, (q_loads - 1) & 1);
@@ -739,13 +761,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         // let every product issued finish before tensor memory is released
         umma_commit_warp(drain_bar + 8 * i);
         __syncwarp();
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain_bar + 8 * i, 0)) {
-          if (globaltimer_ns() - t0 > p.wait_limit_ns) {
-            if (lane == 0 && p.err) atomicOr(p.err, kErrDrain);
-            break;
-          }
-        }
+        settle_phase(drain_bar + 8 * i, 0, p.wait_limit_ns, p.err);
       }
     } else if (warp >= kAttnOutWarp) {
       // ----------------------------------------------------------- outputs
@@ -761,7 +777,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         for (int i = 0; i < 2; ++i) {
           // (the last totals being there, the output's phase before the last is over)
           if (t.n[i] > 0) outs[i] += S::kOwnP ? t.n[i] : 1;
-          ok = ok && wait(ml_bar + 8 * i, it & 1, kErrWaitEpilogue);
+          ok = ok && wait(ml_bar + 8 * i, it & 1, kErrWaitEpilogue, true);
           const float2 ml = lds_f2(row_ml + 8 * (i * kAttnM + quad * 32 + lane));
           ok = ok && (t.n[i] == 0 ||
                       wait(o_bar + 8 * i, (outs[i] - 1) & 1, kErrWaitEpilogue));

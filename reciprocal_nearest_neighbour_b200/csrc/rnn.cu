@@ -3010,10 +3010,14 @@ static rnn_status attn_setup(DeviceInfo* di) {
       cudaFuncSetAttribute(attn_decode_kernel<false, 64, 2>, attr, d64) != cudaSuccess ||
       cudaFuncSetAttribute(attn_decode_kernel<true, 128, 2>, attr, d128) != cudaSuccess ||
       cudaFuncSetAttribute(attn_decode_kernel<false, 128, 2>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 64>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 64>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 128>, attr, p128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 128>, attr, p128) != cudaSuccess)
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 64, false>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 64, false>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 128, false>, attr, p128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 128, false>, attr, p128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 64, true>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 64, true>, attr, p64) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<true, 128, true>, attr, p128) != cudaSuccess ||
+      cudaFuncSetAttribute(attn_prompt_kernel<false, 128, true>, attr, p128) != cudaSuccess)
     return RNN_ECUDA;
   di->attn_smem_set = true;
   return RNN_OK;
@@ -3033,6 +3037,16 @@ static rnn_status make_rows_map(CUtensorMap* m, const rnn_rows& r, int64_t token
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return c == CUDA_SUCCESS ? RNN_OK : RNN_ECUDA;
+}
+
+template <bool kBf16, int kDP>
+static void prompt_launch(const PromptParams& p, unsigned grid, const CUtensorMap& q,
+                          const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  const size_t sm = AttnShape<kDP>::kSmem;
+  if (p.Tk > kAttnShortKeys)
+    attn_prompt_kernel<kBf16, kDP, true><<<grid, kAttnThreads, sm, s>>>(p, q, k, v);
+  else
+    attn_prompt_kernel<kBf16, kDP, false><<<grid, kAttnThreads, sm, s>>>(p, q, k, v);
 }
 
 extern "C" {
@@ -3115,17 +3129,12 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   p.stall_loads = g_stall_loads.load(std::memory_order_relaxed);
   p.wait_limit_ns = p.stall_loads ? g_stall_limit_ns.load(std::memory_order_relaxed)
                                   : kWaitLimitNs;
-  const dim3 grid(static_cast<unsigned>(units)), block(kAttnThreads);
+  const unsigned grid = static_cast<unsigned>(units);
   const bool bf = dtype == RNN_BF16;
-  if (d <= 64) {
-    const size_t sm = AttnShape<64>::kSmem;
-    if (bf) attn_prompt_kernel<true, 64><<<grid, block, sm, s>>>(p, mq, mk, mv);
-    else attn_prompt_kernel<false, 64><<<grid, block, sm, s>>>(p, mq, mk, mv);
-  } else {
-    const size_t sm = AttnShape<128>::kSmem;
-    if (bf) attn_prompt_kernel<true, 128><<<grid, block, sm, s>>>(p, mq, mk, mv);
-    else attn_prompt_kernel<false, 128><<<grid, block, sm, s>>>(p, mq, mk, mv);
-  }
+  if (d <= 64)
+    bf ? prompt_launch<true, 64>(p, grid, mq, mk, mv, s) : prompt_launch<false, 64>(p, grid, mq, mk, mv, s);
+  else
+    bf ? prompt_launch<true, 128>(p, grid, mq, mk, mv, s) : prompt_launch<false, 128>(p, grid, mq, mk, mv, s);
   return launched();
 }
 

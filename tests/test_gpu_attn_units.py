@@ -1,5 +1,5 @@
 """attn_prompt beyond one unit a CTA (more units than SMs, units of very different
-length), and attn_decode with large groups of heads."""
+length, waits that last a whole unit), and attn_decode with large groups of heads."""
 import math
 
 import numpy as np
@@ -148,3 +148,19 @@ def test_decode_groups(dtype, d, hq, hkv, lens):
     k, v = (torch.cat([c[r].flatten(0, 1)[:n] for r, n in zip(rows, lens)]) for c in (kc, vc))
     ref = reference(q, k, v, list(range(len(lens) + 1)), cum(lens), False, 1 / math.sqrt(d))
     check_attention(out, lse, ref, dtype, d, float(v.abs().max()))
+
+
+# ------------------------------------------------------------------ long waits
+def test_unit_longer_than_the_wait_limit():
+    """One query over 250 million keys: a single unit of two million steps, well over the
+    second after which a wait gives up."""
+    n = 250_000_037
+    kv = torch.ones((n, 1, 8), dtype=BF, device="cuda")
+    q = torch.zeros((1, 1, 8), dtype=BF, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    out, lse = rnn.attn_prompt(q, kv, kv, ints([0, 1]), ints([0, n]), causal=False, with_lse=True,
+                               workspace=ws)
+    rnn.workspace_status(ws)
+    assert out.isfinite().all()
+    # equal scores: the total, n below 2^28 in steps of 128, rounds in its last addition only
+    assert abs(float(lse) - math.log(n)) <= math.log(n) * 2.0 ** -22 + 2.0 ** -20
