@@ -313,8 +313,9 @@ __device__ __forceinline__ void regs_give() {
 // Wait for what must not be under way when the CTA exits.  It gives up when the limit
 // has passed and 64 more looks, 20 us each, were in vain: a CTA that was itself stopped
 // for that long (its GPU taken by another process) has time of its own first.
-__device__ __noinline__ void settle_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                          int* err) {
+__device__ __forceinline__ void settle_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                             int* err) {
+  if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
   int late = 0;
 #pragma unroll 1
@@ -600,21 +601,25 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         ask();
         if (!answered()) break;
       }
-      if (lane == 0) {
-        // no copy, and no arrival of a product's completion, is under way when the
-        // CTA exits, whatever the other roles did
-        auto settle = [&](uint32_t bar, uint32_t parity) {
-          settle_phase(bar, parity, p.wait_limit_ns, p.err);
-        };
-        if (asked > 0) settle(ask_bar, (asked - 1) & 1);
-        if (q_loads > 0) settle(qfull_bar, (q_loads - 1) & 1);
-        for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-          settle(full_bar + 8 * (q % S::kStages), (q / S::kStages) & 1);
-        if (!aborted()) {
-          if (q_loads > 0) settle(qempty_bar, (q_loads - 1) & 1);
-          for (int q = max(0, issued - static_cast<int>(S::kStages)); q < issued; ++q)
-            settle(empty_bar + 8 * (q % S::kStages), (q / S::kStages) & 1);
+      // no copy, and no arrival of a product's completion, is under way when the CTA
+      // exits, whatever the other roles did; a lane for each barrier
+      {
+        issued = __shfl_sync(0xffffffffu, issued, 0);
+        q_loads = __shfl_sync(0xffffffffu, q_loads, 0);
+        constexpr int kEmpty = 3 + S::kStages;  // the first lane of the freed places
+        static_assert(kEmpty + S::kStages <= 32, "");
+        uint32_t bar = lane == 0 ? ask_bar : lane == 1 ? qfull_bar : qempty_bar;
+        int phase = (lane == 0 ? asked : q_loads) - 1;
+        if (lane >= 3) {
+          const bool empty = lane >= kEmpty;
+          const int x = max(0, issued - static_cast<int>(S::kStages)) + lane - (empty ? kEmpty : 3);
+          bar = (empty ? empty_bar : full_bar) + 8 * (x % S::kStages);
+          phase = x < issued ? x / S::kStages : -1;
         }
+        // after an abort nobody may free the rest
+        if (phase >= 0 && !((lane == 2 || lane >= kEmpty) && aborted()))
+          settle_phase(bar, phase & 1, p.wait_limit_ns, p.err);
+        __syncwarp();
       }
     } else if (warp == kAttnMmaWarp || warp == kAttnMmaWarp2) {
       // ---------------------------------------------------------- products
