@@ -59,8 +59,12 @@ constexpr int kAttnRegsSoftmax = 176, kAttnRegsOther = 80;
 constexpr int kAttnMmaWarp = 8, kAttnTmaWarp = 9, kAttnMmaWarp2 = 10,
               kAttnOutWarp = 12;
 constexpr float kAttnSlack = 8.f;      // log2 growth of the maximum before a rescale
-// Up to this many keys in a call no unit has more than 512 steps, about a millisecond.
+// Calls with more keys take the kernel's kLong form.  Up to this many, a unit has 512
+// steps at most, about a millisecond, and what the accumulator cuts off (n 2^-27 of a
+// sum of n weights of one size) stays below 2^-11, half a step of fp16.
 constexpr int64_t kAttnShortKeys = 65536;
+// In the kLong form a row's sums leave the accumulator this often, every 65536 keys.
+constexpr int kAttnHoldSteps = 512;
 
 template <int kDP>
 struct AttnShape {
@@ -326,7 +330,12 @@ __device__ __forceinline__ void settle_phase(uint32_t bar, uint32_t parity, uint
   }
 }
 
-// kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time.
+// kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time,
+// and its sums may lose their small terms: the tensor pipe cuts what it adds off at the
+// accumulator's last bits instead of rounding it (2^20 equal weights lost 0.7 % of a sum
+// of values of one sign, 2.5 10^8 of them three quarters).  There a softmax warp takes
+// its rows out of the accumulator every kAttnHoldSteps steps and adds them up itself,
+// rounded to nearest, in local memory.
 template <bool kBf16, int kDP, bool kLong>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
@@ -370,8 +379,9 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
   // Waits: the outcome is the same in all lanes of a warp (they look at the same
   // words).  They suspend the warp: spinning ones take issue slots from the softmax
-  // warps of the same scheduler (128 channels: a tenth slower).  The limits are read from the parameters where they are needed, so that
-  // no register holds them, nor an address of a barrier, through the loops.
+  // warps of the same scheduler (128 channels: a tenth slower).  The limits are read
+  // from the parameters where they are needed, so that no register holds them, nor an
+  // address of a barrier, through the loops.
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto give_up = [&](int code) {
     sts_volatile(abort_at, 1);
@@ -866,114 +876,158 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       const int seen = p.causal ? min(u.nk, row + t.shift + 1) : u.nk;  // keys of this row
       const int seen_all = p.causal ? min(u.nk, row0 + t.shift + 1) : u.nk;  // of every row
       float m = kNegInf, l = 0.f;
-      bool s_there = false;  // the step's scores have been seen to be there
-#pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        if (!s_there && !wait(s_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue)) {
-          ok = false;
-          break;
-        }
+      // the sums taken out so far, then their total and their reference maximum
+      float held[kDP + 2];
+      held[kDP + 1] = kNegInf;
+      // out of the accumulator, once the product of step j is complete; after the last
+      // step back into it
+      auto take_out = [&](int j) {
+        ok = ok && wait(o_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
         tc_fence_after();
-        float s[4][32];
+        const bool last = j + 1 == n, first = j + 1 == kAttnHoldSteps;
+        const float f =
+            held[kDP + 1] == kNegInf ? 0.f : exp2_approx((held[kDP + 1] - m) * p.c);
+#pragma unroll 1
+        for (int c = 0; c < kDP; c += 16) {
+          float o[16];
+          tmem_ld16(o_at + c, o);
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s[c]);
-        tmem_wait_ld_regs(s[0]);
-#pragma unroll
-        for (int c = 1; c < 4; ++c) reg_fence(s[c]);
-        // a look at a barrier takes a couple of hundred cycles: this one's answer is
-        // used behind the comparisons, the one for the next scores in the next step
-        bool o_there = !S::kOwnP || turns + j == 0;
-        if (!o_there) o_there = mbar_test_wait(o_bar + 8 * i, (turns + j - 1) & 1);
-        if constexpr (S::kOwnP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sfree_bar + 8 * i);
+          for (int e = 0; e < 16; ++e) {
+            if (!first) o[e] = fmaf(held[c + e], f, o[e]);
+            held[c + e] = o[e];
+            w[e] = last ? __float_as_uint(o[e]) : 0u;
+          }
+          tmem_st16(o_at + c, w);
         }
-        if ((j + 1) * kAttnN > seen_all) {
-          const int lim_col = seen - j * kAttnN;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= lim_col) s[c][e] = kNegInf;
-        }
-        const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
-        if constexpr (S::kOwnP) {
-          // the product before has read these columns, and its sum is complete
-          if (!o_there && !wait(o_bar + 8 * i, (turns + j - 1) & 1, kErrWaitEpilogue)) {
+        tmem_wait_st();
+        tc_fence_before();
+        if (!first) l = fmaf(held[kDP], f, l);
+        held[kDP] = l;
+        held[kDP + 1] = m;
+        if (!last) l = 0.f;
+        return true;
+      };
+      bool s_there = false;  // the step's scores have been seen to be there
+      int j = 0;
+      // (a look after every step costs the 64-channel form 8 %, the loop of segments the
+      // 128-channel form 4 %, where no row has that many keys)
+      do {
+        const int j_end = kLong && S::kOwnP ? min(n, j + kAttnHoldSteps) : n;
+#pragma unroll 1
+        for (; j < j_end; ++j) {
+          if (!s_there && !wait(s_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue)) {
             ok = false;
             break;
           }
           tc_fence_after();
-        }
-        if (j == 0) {
-          m = x;
-        } else {
-          const bool grow = (x - m) * p.c > kAttnSlack;  // also from -inf to a number
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? exp2_approx((m - x) * p.c) : 1.f;
-            if (grow) m = x;
-            l *= f;
+          float s[4][32];
 #pragma unroll
-            for (int c = 0; c < kDP / 32; ++c) {
-              float o[32];
-              tmem_ld32(o_at + c * 32, o);
-              tmem_wait_ld_regs(o);
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s[c]);
+          tmem_wait_ld_regs(s[0]);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[16];
+          for (int c = 1; c < 4; ++c) reg_fence(s[c]);
+          // a look at a barrier takes a couple of hundred cycles: this one's answer is
+          // used behind the comparisons, the one for the next scores in the next step
+          bool o_there = !S::kOwnP || turns + j == 0;
+          if (!o_there) o_there = mbar_test_wait(o_bar + 8 * i, (turns + j - 1) & 1);
+          if constexpr (S::kOwnP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfree_bar + 8 * i);
+          }
+          if ((j + 1) * kAttnN > seen_all) {
+            const int lim_col = seen - j * kAttnN;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
-                tmem_st16(o_at + c * 32 + h * 16, w);
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= lim_col) s[c][e] = kNegInf;
+          }
+          const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+          if constexpr (S::kOwnP) {
+            // the product before has read these columns, and its sum is complete
+            if (!o_there && !wait(o_bar + 8 * i, (turns + j - 1) & 1, kErrWaitEpilogue)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (j == 0) {
+            m = x;
+          } else {
+            const bool grow = (x - m) * p.c > kAttnSlack;  // also from -inf to a number
+            if (__any_sync(0xffffffffu, grow)) {
+              const float f = grow ? exp2_approx((m - x) * p.c) : 1.f;
+              if (grow) m = x;
+              l *= f;
+#pragma unroll
+              for (int c = 0; c < kDP / 32; ++c) {
+                float o[32];
+                tmem_ld32(o_at + c * 32, o);
+                tmem_wait_ld_regs(o);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t w[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
+                  tmem_st16(o_at + c * 32 + h * 16, w);
+                }
               }
             }
           }
-        }
-        const float z = (m == kNegInf ? 0.f : m * p.c) - kBias;
-        const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
-        // The two warps of a scheduler take turns at the exponential unit, tile 0's
-        // step j, tile 1's step j, tile 0's step j + 1: left alone they fall into
-        // step, and both leave it idle while both load and compare.  Order only: no
-        // result depends on it, and after kTurnPolls looks a warp goes on anyway.
-        const int j_o = i ? j : j - 1;  // the other's step to wait for
-        if (j_o >= 0 && j_o < n_o) {
+          const float z = (m == kNegInf ? 0.f : m * p.c) - kBias;
+          const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
+          // The two warps of a scheduler take turns at the exponential unit, tile 0's
+          // step j, tile 1's step j, tile 0's step j + 1: left alone they fall into
+          // step, and both leave it idle while both load and compare.  Order only: no
+          // result depends on it, and after kTurnPolls looks a warp goes on anyway.
+          const int j_o = i ? j : j - 1;  // the other's step to wait for
+          if (j_o >= 0 && j_o < n_o) {
 #pragma unroll 1
-          for (int k = 0; k < kTurnPolls; ++k) {
-            if (lds_volatile(turn_at + 4 * (warp ^ 4)) > turns_o + j_o) break;
-            __nanosleep(40);
+            for (int k = 0; k < kTurnPolls; ++k) {
+              if (lds_volatile(turn_at + 4 * (warp ^ 4)) > turns_o + j_o) break;
+              __nanosleep(40);
+            }
           }
-        }
-        uint64_t sum[2] = {0, 0};
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a, b;
-            f2_get(f2_fma(f2_make(s[c][2 * e], s[c][2 * e + 1]), c2, z2), a, b);
-            a = exp2_approx(a);
-            b = exp2_approx(b);
-            sum[e & 1] = f2_add(sum[e & 1], f2_make(a, b));
-            // the second product takes the probabilities in the value type
-            // (half a step: 2^-9 of bf16, 2^-12 of fp16, of each weight); the
-            // total keeps them in fp32
-            w[e] = pack2<kBf16>(a, b);
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              f2_get(f2_fma(f2_make(s[c][2 * e], s[c][2 * e + 1]), c2, z2), a, b);
+              a = exp2_approx(a);
+              b = exp2_approx(b);
+              sum[e & 1] = f2_add(sum[e & 1], f2_make(a, b));
+              // the second product takes the probabilities in the value type
+              // (half a step: 2^-9 of bf16, 2^-12 of fp16, of each weight); the
+              // total keeps them in fp32
+              w[e] = pack2<kBf16>(a, b);
+            }
+            if (c == kTurnChunk && lane == 0) sts_volatile(turn_at + 4 * warp, turns + j + 1);
+            if (S::kOwnP && c == 3)
+              s_there = mbar_test_wait(s_bar + 8 * i, (turns + j + 1) & 1);
+            tmem_st16(p_at + c * 16, w);
+            if ((c + 1) % (4 / S::kParts) == 0) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_bar + 8 * (2 * (c / (4 / S::kParts)) + i));
+            }
           }
-          if (c == kTurnChunk && lane == 0) sts_volatile(turn_at + 4 * warp, turns + j + 1);
-          if (S::kOwnP && c == 3)
-            s_there = mbar_test_wait(s_bar + 8 * i, (turns + j + 1) & 1);
-          tmem_st16(p_at + c * 16, w);
-          if ((c + 1) % (4 / S::kParts) == 0) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_bar + 8 * (2 * (c / (4 / S::kParts)) + i));
-          }
+          float a, b;
+          f2_get(f2_add(sum[0], sum[1]), a, b);
+          l += a + b;
+          if (kLong && !S::kOwnP && n > kAttnHoldSteps &&
+              ((j + 1) % kAttnHoldSteps == 0 || j + 1 == n))
+            if (!take_out(j)) break;
         }
-        float a, b;
-        f2_get(f2_add(sum[0], sum[1]), a, b);
-        l += a + b;
-      }
+        if (kLong && S::kOwnP && n > kAttnHoldSteps && !take_out(j - 1)) break;
+      } while (kLong && S::kOwnP && j < n);
       turns += n;
       turns_o += n_o;
       if (it > 0)

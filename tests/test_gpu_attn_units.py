@@ -164,3 +164,49 @@ def test_unit_longer_than_the_wait_limit():
     assert out.isfinite().all()
     # equal scores: the total, n below 2^28 in steps of 128, rounds in its last addition only
     assert abs(float(lse) - math.log(n)) <= math.log(n) * 2.0 ** -22 + 2.0 ** -20
+
+
+# ------------------------------------------------------------------- long sums
+def held(ref, segment):
+    """The oracle's results with the number of keys that meet in one accumulator: `segment`
+    of them, then one addition for each of the segments."""
+    ref.keys = np.minimum(ref.keys, segment) + ref.keys // segment
+    return ref
+
+
+def test_sum_of_many_equal_weights():
+    """250 million equal scores.  Values that are powers of two make every partial sum of up
+    to 65536 of them exact; the other additions are rounded to nearest."""
+    n = 250_000_037
+    values = torch.tensor([2.0 ** (c - 4) for c in range(8)], device="cuda").to(BF)
+    kv = torch.empty((n, 1, 8), dtype=BF, device="cuda")
+    kv[:] = values
+    q = torch.zeros((1, 1, 8), dtype=BF, device="cuda")
+    out = rnn.attn_prompt(q, kv, kv, ints([0, 1]), ints([0, n]), causal=False)
+    # 3815 additions of a power of two (exact below 2^24 of them) and the ragged end
+    assert torch.equal(out[0, 0], values)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [40, 64, 96, 128])
+@pytest.mark.parametrize("hq", [2, 3])
+def test_prompt_long_sums(dtype, d, hq):
+    """Values of one sign: what an accumulator loses shows in every channel.  Beside the
+    long sequence short ones, and one whose scores grow and fall over its length, so that
+    parts taken out early and late count."""
+    g = torch.Generator("cuda").manual_seed(d)
+    nq, nk = [3, 40, 150, 2], [1 << 22, 40, 70_001, 65_537]
+    cu_q, cu_k = cum(nq), cum(nk)
+    q = normal(g, (sum(nq), hq, d), dtype) * 0.5
+    k = normal(g, (sum(nk), 1, d), dtype)
+    v = torch.rand((sum(nk), 1, d), generator=g, device="cuda").add(0.5).to(dtype)
+    q[cu_q[2]:cu_q[3], :, 0] = math.sqrt(d)         # scaled scores from -8 to 8
+    k[cu_k[2]:cu_k[3], 0, 0] = (torch.linspace(0, 2 * math.pi, nk[2], device="cuda").sin()
+                                * 8).to(dtype)
+    for causal in (False, True):
+        ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+        out, lse = rnn.attn_prompt(q, k, v, ints(cu_q), ints(cu_k), causal=causal, with_lse=True,
+                                   workspace=ws)
+        rnn.workspace_status(ws)
+        ref = held(reference(q, k, v, cu_q, cu_k, causal, 1 / math.sqrt(d)), 65536)
+        check_attention(out, lse, ref, dtype, d, 1.5)
