@@ -481,7 +481,10 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  *   - Arguments come in a structure, which is only read during the call;
  *     dtype is an rnn_dtype.
  *   - Softmax statistics and sums are fp32; each product's probabilities are
- *     rounded to the 16-bit type once, outputs once.
+ *     rounded to the 16-bit type once, outputs once.  The tensor cores cut sums
+ *     off at fp32's last bits instead of rounding them; no more than 65536 keys
+ *     of a row meet in one of their accumulators, which is a relative 2^-11 at
+ *     most.
  */
 #define RNN_ATTN_MAX_DIM 128
 #define RNN_ATTN_MAX_HEADS 1024

@@ -39,6 +39,8 @@ namespace rnn {
 constexpr int kDecWarps = 4;
 constexpr int kDecRows = 16;    // query heads per unit
 constexpr int kDecMaxKeys = 0x7fffffff - 1023;  // whole tiles stay below 2^31
+// Keys that meet in one accumulator.  A warp takes a quarter of a pair's keys at most.
+constexpr int kDecHoldKeys = 65536, kDecShortKeys = 4 * kDecHoldKeys;
 
 // kDP: channels padded to 64 or 128.  kKeys: keys per warp and tile, 8 KB of
 // keys and values in either case.
@@ -103,7 +105,12 @@ __device__ __forceinline__ int dec_owner(int64_t w, int64_t total, int64_t grid)
   return static_cast<int>(c);
 }
 
-template <bool kBf16, int kDP, int kNT>
+// kLong: page tables with room for more than kDecShortKeys keys.  The matrix instruction
+// cuts what it adds off at the accumulator's last bits instead of rounding it, so a sum
+// of n weights of one size loses about n 2^-27 (65536 keys: less than 2^-11, half a step
+// of fp16; 2^22 in one warp: 2.7 %).  There a warp takes its sums out of the accumulator
+// every kDecHoldKeys keys and adds them up itself, rounded to nearest, in local memory.
+template <bool kBf16, int kDP, int kNT, bool kLong>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const DecodeParams p) {
   using S = DecShape<kDP>;
   constexpr int kKeys = S::kKeys, kStages = S::kStages;
@@ -268,6 +275,27 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   float o[kNT][kSteps][4];   // channel 16 c + lane/4 (+ 8), head 8 n + 2 (lane%4) (+ 1)
   float m[kNT][2], l[kNT][2];
   const int g = lane >> 2, q2 = (lane & 3) * 2;
+  // sums taken out so far, then their totals and reference maxima; tiles until the next
+  constexpr int kSums = kNT * kSteps * 4, kHoldTiles = kDecHoldKeys / kKeys;
+  volatile float held[kSums + 4 * kNT];
+  bool any_held = false;
+  int until = kHoldTiles;
+  // m, l and o with what is held added to them
+  auto add_held = [&]() {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = held[kSums + 2 * kNT + 2 * n + e];
+        const float f = ref == kNegInf ? 0.f : exp2_approx((ref - m[n][e]) * p.c);
+        l[n][e] = fmaf(held[kSums + 2 * n + e], f, l[n][e]);
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+          for (int h = e; h < 4; h += 2)
+            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], f, o[n][c][h]);
+      }
+  };
   bool fresh = true;
   bool whole = cur.j == 0;   // the pair started in this share
 #pragma unroll 1
@@ -400,7 +428,32 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
     const bool last = cur.j == cur.n - 1;
+    if (kLong && --until == 0) {
+      if (any_held) add_held();
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          held[kSums + 2 * n + e] = l[n][e];
+          held[kSums + 2 * kNT + 2 * n + e] = m[n][e];
+          l[n][e] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+            for (int h = e; h < 4; h += 2) {
+              held[(n * kSteps + c) * 4 + h] = o[n][c][h];
+              o[n][c][h] = 0.f;
+            }
+        }
+      any_held = true;
+      until = kHoldTiles;
+    }
     if (last || cur.at + 1 >= hi) {
+      if (kLong) {
+        if (any_held) add_held();
+        any_held = false;
+        until = kHoldTiles;
+      }
       // ---- the pair ends here, or goes on in the next share
 #pragma unroll
       for (int n = 0; n < kNT; ++n)

@@ -2999,25 +2999,26 @@ static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 static rnn_status attn_setup(DeviceInfo* di) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (di->attn_smem_set) return RNN_OK;
-  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const int d64 = static_cast<int>(DecShape<64>::kSmem), d128 = static_cast<int>(DecShape<128>::kSmem);
-  const int p64 = static_cast<int>(AttnShape<64>::kSmem), p128 = static_cast<int>(AttnShape<128>::kSmem);
-  if (cudaFuncSetAttribute(attn_decode_kernel<true, 64, 1>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 64, 1>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<true, 128, 1>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 128, 1>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<true, 64, 2>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 64, 2>, attr, d64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<true, 128, 2>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_decode_kernel<false, 128, 2>, attr, d128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 64, false>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 64, false>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 128, false>, attr, p128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 128, false>, attr, p128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 64, true>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 64, true>, attr, p64) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<true, 128, true>, attr, p128) != cudaSuccess ||
-      cudaFuncSetAttribute(attn_prompt_kernel<false, 128, true>, attr, p128) != cudaSuccess)
+  const auto set = [](size_t bytes, auto... kernels) {
+    return ((cudaFuncSetAttribute(kernels, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(bytes)) == cudaSuccess) && ...);
+  };
+  if (!set(DecShape<64>::kSmem, attn_decode_kernel<true, 64, 1, false>,
+           attn_decode_kernel<false, 64, 1, false>, attn_decode_kernel<true, 64, 2, false>,
+           attn_decode_kernel<false, 64, 2, false>, attn_decode_kernel<true, 64, 1, true>,
+           attn_decode_kernel<false, 64, 1, true>, attn_decode_kernel<true, 64, 2, true>,
+           attn_decode_kernel<false, 64, 2, true>) ||
+      !set(DecShape<128>::kSmem, attn_decode_kernel<true, 128, 1, false>,
+           attn_decode_kernel<false, 128, 1, false>, attn_decode_kernel<true, 128, 2, false>,
+           attn_decode_kernel<false, 128, 2, false>, attn_decode_kernel<true, 128, 1, true>,
+           attn_decode_kernel<false, 128, 1, true>, attn_decode_kernel<true, 128, 2, true>,
+           attn_decode_kernel<false, 128, 2, true>) ||
+      !set(AttnShape<64>::kSmem, attn_prompt_kernel<true, 64, false>,
+           attn_prompt_kernel<false, 64, false>, attn_prompt_kernel<true, 64, true>,
+           attn_prompt_kernel<false, 64, true>) ||
+      !set(AttnShape<128>::kSmem, attn_prompt_kernel<true, 128, false>,
+           attn_prompt_kernel<false, 128, false>, attn_prompt_kernel<true, 128, true>,
+           attn_prompt_kernel<false, 128, true>))
     return RNN_ECUDA;
   di->attn_smem_set = true;
   return RNN_OK;
@@ -3146,10 +3147,13 @@ static rnn_status decode_launch(const DecodeParams& p, dim3 grid, cudaStream_t s
   const size_t sm = DecShape<kDP>::kSmem;
   // up to 8 heads one column block: 96 streams of 4 heads a key head 108 us, 109 with
   // two, one stream 7.7 and 8.2
+  const bool many = static_cast<int64_t>(p.max_pages) * p.page.div > kDecShortKeys;
   if (p.group <= 8)
-    attn_decode_kernel<kBf16, kDP, 1><<<grid, block, sm, s>>>(p);
+    many ? attn_decode_kernel<kBf16, kDP, 1, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_kernel<kBf16, kDP, 1, false><<<grid, block, sm, s>>>(p);
   else
-    attn_decode_kernel<kBf16, kDP, 2><<<grid, block, sm, s>>>(p);
+    many ? attn_decode_kernel<kBf16, kDP, 2, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_kernel<kBf16, kDP, 2, false><<<grid, block, sm, s>>>(p);
   const rnn_status r = launched();
   if (r != RNN_OK) return r;
   launch_k(attn_decode_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),

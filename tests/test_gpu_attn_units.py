@@ -1,6 +1,9 @@
 """attn_prompt beyond one unit a CTA (more units than SMs, units of very different
 length, waits that last a whole unit), and attn_decode with large groups of heads."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -210,3 +213,59 @@ def test_prompt_long_sums(dtype, d, hq):
         rnn.workspace_status(ws)
         ref = held(reference(q, k, v, cu_q, cu_k, causal, 1 / math.sqrt(d)), 65536)
         check_attention(out, lse, ref, dtype, d, 1.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d,hq", [(8, 3), (72, 3), (8, 10), (72, 10)])
+def test_decode_long_sums(dtype, d, hq):
+    """300 sequences on the same pages, so that a warp takes four million keys of one of
+    them; values of one sign, equal scores, and scores that grow and fall."""
+    g = torch.Generator("cuda").manual_seed(d)
+    n, size, B = (1 << 24) + 70_001, 64, 300
+    pages = -(-n // size)
+    k, v = (torch.zeros((pages, size, 1, d), dtype=dtype, device="cuda") for _ in range(2))
+    k.normal_(generator=g)
+    v.uniform_(0.5, 1.5, generator=g)
+    q = normal(g, (3, hq, d), dtype) * 0.5
+    q[1:, :, 0] = math.sqrt(d)                          # scaled scores of -8 to 8
+    q[0] = 0
+    k.view(-1, d)[:, 0] = (torch.linspace(0, 6 * math.pi, pages * size, device="cuda").sin()
+                           * 8).to(dtype)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, -1)
+    kind = [0, 1, 2] * (B // 3)
+    lens = [(n, n, 70_001)[x] for x in kind]
+    out, lse = rnn.attn_decode(q[kind], k, v, table, ints(lens), with_lse=True)
+    for r, many in enumerate((n, n, 70_001)):
+        ref = held(reference(q[r:r + 1], k.view(-1, 1, d), v.view(-1, 1, d), [0, 1], [0, many],
+                             False, 1 / math.sqrt(d)), 65536)
+        for b in (r, 150 + r, B - 3 + r):
+            check_attention(out[b:b + 1], lse[b:b + 1], ref, dtype, d, 1.5)
+
+
+LONG_FIRST_IN_CAPTURE = """
+import torch, reciprocal_nearest_neighbour_b200 as rnn
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+n = 300000
+q = torch.randn(4, 2, 64, device="cuda").bfloat16()
+kc = torch.randn(n // 64 + 1, 64, 2, 64, device="cuda").bfloat16()
+kv = kc.view(-1, 2, 64)[:n]
+table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda").view(1, -1)
+cu, ck, lens, one = i(0, 4), i(0, n), i(n), i(n)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = rnn.attn_prompt(q, kv, kv, cu, ck, causal=False)
+    b = rnn.attn_decode(q[3:], kc, kc, table, lens)
+for x in (a, b):
+    x.fill_(7)
+g.replay()
+torch.cuda.synchronize()
+s = torch.einsum("hc,khc->hk", q[3].double(), kv.double()) / 8
+want = torch.einsum("hk,khc->hc", s.softmax(1), kv.double())
+for x in (a[3], b[0]):
+    assert (x.double() - want).abs().max() < 2e-2
+"""
+
+
+def test_first_long_call_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", LONG_FIRST_IN_CAPTURE], check=True, timeout=300, cwd=root)
