@@ -549,7 +549,8 @@ rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded (those that last as
  * long as a sequence has keys count from its last step); with a workspace (it
- * may be NULL) rnn_workspace_status tells whether one ran out.
+ * may be NULL) rnn_workspace_status tells whether one ran out.  The rows that
+ * were then not computed are NaN, their log-sums too.
  */
 typedef struct rnn_attn_prompt_args {
   rnn_rows q, k, v, out;
@@ -611,10 +612,12 @@ void rnn_set_kernel_timer(void *const *start_events, void *const *stop_events, i
 /*
  * Failure-detection test hook (no use in production).  While `on` is
  * nonzero, every launch of the fused similarity+argmax kernel loads no
- * candidate tile (and one of rnn_attn_prompt no tile at all), so the bounded
- * wait of its MMA warps on the first tile runs out after `wait_limit_ns` (0: the default of 1 s); the kernel then stops
- * all its warps, frees tensor memory and returns, and the call's workspace
- * status reads RNN_ETIMEOUT (rnn_workspace_status).  Results of those calls
+ * candidate tile, so the bounded wait of its MMA warps on the first tile runs
+ * out after `wait_limit_ns` (0: the default of 1 s); the kernel then stops all
+ * its warps, frees tensor memory and returns, and the call's workspace status
+ * reads RNN_ETIMEOUT (rnn_workspace_status).  A launch of rnn_attn_prompt loads
+ * no tile at all, or with on = 2 none behind the first unit of work of each of
+ * its thread blocks; the rows concerned are NaN.  Results of the other calls
  * are undefined but every index written is in range.  Nothing faults, traps
  * or hangs; later calls with the hook off are unaffected.  Global to the
  * process, not thread-safe against concurrent calls.

@@ -291,8 +291,9 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     Returns ``out [Tq, Hq, d]``, or ``(out, lse)`` with ``lse [Tq, Hq]`` float32
     the log-sum-exp of the scaled scores.  A row that sees no key is 0 with
     ``lse`` -inf, one that sees a score that is not a number is NaN; rows
-    outside the sequences are not written.  With a ``workspace`` (uint8, 256
-    bytes) ``workspace_status`` tells whether a wait of the kernel ran out.
+    outside the sequences are not written.  Should a wait of the kernel run out,
+    the rows not computed are NaN; with a ``workspace`` (uint8, 256 bytes)
+    ``workspace_status`` tells.
     """
     kind = _value_dtype(q, "q")
     dev = q.device

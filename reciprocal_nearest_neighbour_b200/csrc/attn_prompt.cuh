@@ -316,18 +316,19 @@ __device__ __forceinline__ void regs_give() {
 // Wait for what must not be under way when the CTA exits.  It gives up when the limit
 // has passed and 64 more looks, 20 us each, were in vain: a CTA that was itself stopped
 // for that long (its GPU taken by another process) has time of its own first.
-__device__ __forceinline__ void settle_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+__device__ __forceinline__ bool settle_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                              int* err) {
-  if (mbar_try_wait(bar, parity)) return;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   int late = 0;
 #pragma unroll 1
   while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
     if (globaltimer_ns() - t0 > limit_ns && ++late > 64) {
       if (err) atomicOr(err, kErrDrain);
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 // kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time,
@@ -373,7 +374,13 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   const uint32_t zero_at = tmem_slot + 8;   // ragged V tiles whose end is zeroed
   const uint32_t turn_at = tmem_slot + 16;  // per softmax warp: steps whose exponentials are out
   __shared__ __align__(16) uint8_t answer[16];
-  __shared__ PromptUnit units[2];
+  // Units published in turn (two at a time, and those before them as long as an output
+  // warp may have them in hand), how many so far, and one that was taken and not published.
+  __shared__ PromptUnit units[4], unpublished;
+  __shared__ int dealt;
+  // What an output warp has not written when it stops: unit number x and, if y is below
+  // 2, the tiles of the unit before it from tile y on.
+  __shared__ int2 unwritten[4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
@@ -440,6 +447,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     if (threadIdx.x == 128) {
       sts_volatile(zero_at, 0);
       sts_volatile(abort_at, 0);
+      dealt = 0;
+      unpublished.nq = -1;
     }
   }
   constexpr uint32_t kCols = 512;
@@ -468,7 +477,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     const int slot = it & 1;
     if (!__all_sync(0xffffffffu, wait(ufull_bar + 8 * slot, (it >> 1) & 1, code, true)))
       return false;
-    u = units[slot];
+    u = units[it & 3];
     __syncwarp();
     if (lane == 0) mbar_arrive(uempty_bar + 8 * slot);
     return u.nq >= 0;
@@ -519,9 +528,13 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       int block = blockIdx.x, issued = 0, q_loads = 0;
       int asked = 0;
       bool ok = true;
+      // (not cut short by an abort: a block that was handed over will not start)
       auto answered = [&]() {
-        if (!__all_sync(0xffffffffu, wait(ask_bar, (asked - 1) & 1, kErrWaitProducer)))
+        if (!__all_sync(0xffffffffu,
+                        settle_phase(ask_bar, (asked - 1) & 1, p.wait_limit_ns, p.err))) {
+          give_up(kErrWaitProducer);
           return false;
+        }
         block = next_block_read(smem_u32(answer));
         fence_proxy_async_smem();  // read before the next answer is written
         __syncwarp();
@@ -570,13 +583,17 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         const int slot = it & 1;
         ok = __all_sync(0xffffffffu,
                         wait(uempty_bar + 8 * slot, ((it >> 1) & 1) ^ 1u, kErrWaitProducer));
-        if (!ok) break;
+        if (!ok) {
+          if (lane == 0) unpublished = u;
+          break;
+        }
         if (lane == 0) {
-          units[slot] = u;
+          units[it & 3] = u;
+          dealt = it + 1;
           mbar_arrive(ufull_bar + 8 * slot);
         }
         __syncwarp();
-        if (u.nq < 0 || p.stall_loads) break;
+        if (u.nq < 0 || (p.stall_loads && it + 1 >= p.stall_loads)) break;
         const PromptTiles t(p, u);
         if (t.n_max > 0 && lane == 0) {
           ok = wait(qempty_bar, (q_loads & 1) ^ 1u, kErrWaitProducer);
@@ -794,7 +811,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       int outs[2] = {0, 0};
       bool ok = true;
       PromptUnit u;
-      for (int it = 0; ok && take_unit(it, kErrWaitEpilogue, u); ++it) {
+      int it = 0, tile = 2;
+      for (; ok && take_unit(it, kErrWaitEpilogue, u); ++it) {
         const PromptTiles t(p, u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -805,7 +823,10 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           ok = ok && (t.n[i] == 0 ||
                       wait(o_bar + 8 * i, (outs[i] - 1) & 1, kErrWaitEpilogue));
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (!ok) {
+            tile = i;
+            break;
+          }
           if (lane == 0) mbar_arrive(mlfree_bar + 8 * i);
           tc_fence_after();
           const uint32_t o_at = tmem + lane_at + S::kOutCol + i * kDP;
@@ -854,6 +875,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                 seen ? ml.x * p.scale + (log2f(ml.y) - kBias) * 0.69314718f : kNegInf;
         }
       }
+      if (lane == 0) unwritten[quad] = make_int2(it, tile);
     }
   } else {
     // ----------------------------------------------------------- softmax
@@ -1044,6 +1066,32 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   if (warp == kAttnMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
+  }
+  if (warp >= kAttnOutWarp && aborted()) {
+    // what was given up becomes NaN, so that nobody takes the buffer's old bytes for rows
+    const uint32_t nan2 = kBf16 ? 0x7FC07FC0u : 0x7E007E00u;
+    const int2 from = unwritten[warp & 3];
+#pragma unroll 1
+    for (int k = from.x - 1; k <= dealt; ++k) {
+      if (k < from.x && from.y == 2) continue;
+      const PromptUnit u = k < dealt ? units[k & 3] : unpublished;
+      if (u.nq < 0) continue;
+      const int tile = k < from.x ? from.y : 0;
+      const PromptTiles t(p, u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i < tile) continue;
+        const int row = t.row0[i] + (warp & 3) * 32, rows = min(32, u.nq - row);
+        for (int x = 0; x < rows; ++x) {
+          const int64_t at = u.q0 + row + x;
+          if (lane * 8 < p.d)
+            *reinterpret_cast<uint4*>(p.out + at * p.o_ts + t.head[i] * p.o_hs + lane * 8) =
+                make_uint4(nan2, nan2, nan2, nan2);
+          if (p.lse && lane == 0)
+            p.lse[at * p.Hq + t.head[i]] = __uint_as_float(0x7FC00000u);
+        }
+      }
+    }
   }
 }
 

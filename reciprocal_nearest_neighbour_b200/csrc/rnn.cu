@@ -1971,7 +1971,7 @@ void rnn_set_kernel_timer(void* const* start_events, void* const* stop_events, i
 void rnn_test_stall_loads(int on, uint64_t wait_limit_ns) {
   g_stall_limit_ns.store(on && wait_limit_ns > 0 ? wait_limit_ns : kWaitLimitNs,
                          std::memory_order_relaxed);
-  g_stall_loads.store(on ? 1 : 0, std::memory_order_relaxed);
+  g_stall_loads.store(on, std::memory_order_relaxed);
 }
 
 rnn_status rnn_workspace_status(const void* workspace, rnn_stream_t stream) {

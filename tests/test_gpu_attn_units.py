@@ -1,5 +1,6 @@
 """attn_prompt beyond one unit a CTA (more units than SMs, units of very different
-length, waits that last a whole unit), and attn_decode with large groups of heads."""
+length, waits that last a whole unit, rows longer than one accumulator holds, units that
+are given up), and attn_decode with large groups of heads and long rows."""
 import math
 import os
 import subprocess
@@ -269,3 +270,42 @@ for x in (a[3], b[0]):
 def test_first_long_call_of_a_process_inside_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", LONG_FIRST_IN_CAPTURE], check=True, timeout=300, cwd=root)
+
+
+# --------------------------------------------------------------- units given up
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2)])
+@pytest.mark.parametrize("on", [1, 2])
+def test_rows_given_up_are_nan(d, hq, hkv, on):
+    """A wait that runs out leaves no old bytes in the rows, with or without a workspace; units
+    that a CTA had finished before keep their results."""
+    nq, nk = ragged(5)
+    nk = [max(1, n) for n in nk]
+    q, k, v, cu_q, cu_k = inputs(BF, nq, nk, hq, hkv, d, 23)
+    front = torch.full((3, hq, d), 7.0, dtype=BF, device="cuda")
+    args = (torch.cat([front, q]), k, v, ints([3 + x for x in cu_q]), ints(cu_k))
+    want, want_lse = rnn.attn_prompt(*args, causal=False, with_lse=True)
+    out = torch.full_like(want, 7.0)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    lib = rnn._lib.load()
+    lib.rnn_test_stall_loads(on, 20_000_000)
+    try:
+        _, lse = rnn.attn_prompt(*args, causal=False, with_lse=True, out=out, workspace=ws)
+        bare = rnn.attn_prompt(*args, causal=False)
+        torch.cuda.synchronize()
+    finally:
+        lib.rnn_test_stall_loads(0, 0)
+    with pytest.raises(rnn.RNNError):
+        rnn.workspace_status(ws)
+    assert (out[:3] == 7).all()
+    gone = out[3:].isnan()
+    assert torch.equal(gone.all(2), gone.any(2)) and torch.equal(gone.any(2), lse[3:].isnan())
+    assert gone.all() if on == 1 else 0.2 < gone.float().mean() < 0.8
+    assert torch.equal(out[3:][~gone], want[3:][~gone])
+    kept = ~gone.any(2)
+    assert torch.equal(lse[3:][kept], want_lse[3:][kept])
+    gone = bare[3:].isnan()
+    assert gone.any() and torch.equal(bare[3:][~gone], want[3:][~gone])
+    again = rnn.attn_prompt(*args, causal=False, workspace=ws)
+    rnn.workspace_status(ws)
+    assert torch.equal(again[3:], want[3:])
