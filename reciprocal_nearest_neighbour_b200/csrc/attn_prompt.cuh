@@ -384,8 +384,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
-  // Waits: the outcome is the same in all lanes of a warp (they look at the same
-  // words).  They suspend the warp: spinning ones take issue slots from the softmax
+  // Waits.  A lane's outcome is its own; the warp votes before it acts on one.  They
+  // suspend the warp: spinning ones take issue slots from the softmax
   // warps of the same scheduler (128 channels: a tenth slower).  The limits are read
   // from the parameters where they are needed, so that no register holds them, nor an
   // address of a barrier, through the loops.
@@ -940,10 +940,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         const int j_end = kLong && S::kOwnP ? min(n, j + kAttnHoldSteps) : n;
 #pragma unroll 1
         for (; j < j_end; ++j) {
-          if (!s_there && !wait(s_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue)) {
-            ok = false;
-            break;
-          }
+          ok = s_there || wait(s_bar + 8 * i, (turns + j) & 1, kErrWaitEpilogue);
+          __syncwarp();
           tc_fence_after();
           float s[4][32];
 #pragma unroll
@@ -971,32 +969,30 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           const float x = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
           if constexpr (S::kOwnP) {
             // the product before has read these columns, and its sum is complete
-            if (!o_there && !wait(o_bar + 8 * i, (turns + j - 1) & 1, kErrWaitEpilogue)) {
-              ok = false;
-              break;
-            }
+            ok = ok && (o_there || wait(o_bar + 8 * i, (turns + j - 1) & 1, kErrWaitEpilogue));
             tc_fence_after();
           }
-          if (j == 0) {
-            m = x;
-          } else {
-            const bool grow = (x - m) * p.c > kAttnSlack;  // also from -inf to a number
-            if (__any_sync(0xffffffffu, grow)) {
-              const float f = grow ? exp2_approx((m - x) * p.c) : 1.f;
-              if (grow) m = x;
-              l *= f;
+          if (j == 0) m = x;
+          const bool grow = (x - m) * p.c > kAttnSlack;  // also from -inf to a number
+          // one vote for both: a lane whose wait gave up takes the warp with it (votes at
+          // the waits themselves cost 2 %)
+          if (__any_sync(0xffffffffu, grow || !ok)) {
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const float f = grow ? exp2_approx((m - x) * p.c) : 1.f;
+            if (grow) m = x;
+            l *= f;
 #pragma unroll
-              for (int c = 0; c < kDP / 32; ++c) {
-                float o[32];
-                tmem_ld32(o_at + c * 32, o);
-                tmem_wait_ld_regs(o);
+            for (int c = 0; c < kDP / 32; ++c) {
+              float o[32];
+              tmem_ld32(o_at + c * 32, o);
+              tmem_wait_ld_regs(o);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint32_t w[16];
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[16];
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
-                  tmem_st16(o_at + c * 32 + h * 16, w);
-                }
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
+                tmem_st16(o_at + c * 32 + h * 16, w);
               }
             }
           }
