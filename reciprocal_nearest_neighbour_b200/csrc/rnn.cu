@@ -3220,7 +3220,10 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
   DeviceInfo* di = nullptr;
   if ((r = device_info(&di)) != RNN_OK || (r = attn_setup(di)) != RNN_OK) return r;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (B == 0) return RNN_OK;
+  if (B == 0) {
+    zero_words_kernel<<<1, 32, 0, s>>>(static_cast<int*>(workspace), 1);
+    return launched();
+  }
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   DecWs w;
