@@ -383,7 +383,6 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   __shared__ int2 unwritten[4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.err) *p.err = 0;
   // Waits.  A lane's outcome is its own; the warp votes before it acts on one.  They
   // suspend the warp: spinning ones take issue slots from the softmax
   // warps of the same scheduler (128 channels: a tenth slower).  The limits are read

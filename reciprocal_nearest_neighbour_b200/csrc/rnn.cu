@@ -3093,11 +3093,12 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   if ((r = device_info(&di)) != RNN_OK || (r = attn_setup(di)) != RNN_OK) return r;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* err = static_cast<int*>(workspace);
-  if (Tq == 0 || B == 0) {
-    if (!err) return RNN_OK;
+  if (err) {
+    // ahead of the kernel: none of its blocks is sure to start first, or at all
     zero_words_kernel<<<1, 32, 0, s>>>(err, 1);
-    return launched();
+    if ((r = launched()) != RNN_OK) return r;
   }
+  if (Tq == 0 || B == 0) return RNN_OK;
   CUtensorMap mq, mk, mv;
   if ((r = make_rows_map(&mq, q, Tq, Hq, d)) != RNN_OK) return r;
   if (Tk > 0) {

@@ -22,3 +22,12 @@ def test_decode_clears_the_word(streams):
                           ints([20] * streams), workspace=ws)
     rnn.workspace_status(ws)
     assert (out == 1).all()
+
+
+@pytest.mark.parametrize("tokens,cu", [(0, [0, 0]), (5, [0]), (5, [0, 5]), (5, [5, 5])])
+def test_prompt_clears_the_word(tokens, cu):
+    x = torch.ones((tokens, 2, 64), dtype=torch.float16, device="cuda")
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    out = rnn.attn_prompt(x, x, x, ints(cu), out=x.clone(), workspace=ws)
+    rnn.workspace_status(ws)
+    assert (out == 1).all()
