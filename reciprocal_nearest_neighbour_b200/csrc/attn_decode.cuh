@@ -397,8 +397,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
       uint32_t pf[kMT][kNT][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        const float z0 = (m[n][0] == kNegInf ? 0.f : m[n][0] * p.c) - kBias;
-        const float z1 = (m[n][1] == kNegInf ? 0.f : m[n][1] * p.c) - kBias;
+        // (the second terms make a reference beyond fp32 NaN: no key would have a weight)
+        const float m0 = m[n][0] == kNegInf ? 0.f : m[n][0] * p.c;
+        const float m1 = m[n][1] == kNegInf ? 0.f : m[n][1] * p.c;
+        const float z0 = fmaf(m0, 0.f, m0) - kBias, z1 = fmaf(m1, 0.f, m1) - kBias;
 #pragma unroll
         for (int t = 0; t < kMT; ++t) {
           const float e0 = exp2_approx(fmaf(s[t][n][0], p.c, -z0));

@@ -995,7 +995,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
               }
             }
           }
-          const float z = (m == kNegInf ? 0.f : m * p.c) - kBias;
+          // (the second term makes a reference beyond fp32 NaN: no key would have a weight)
+          const float mc = m == kNegInf ? 0.f : m * p.c, z = fmaf(mc, 0.f, mc) - kBias;
           const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
           // The two warps of a scheduler take turns at the exponential unit, tile 0's
           // step j, tile 1's step j, tile 0's step j + 1: left alone they fall into

@@ -309,3 +309,26 @@ def test_rows_given_up_are_nan(d, hq, hkv, on):
     again = rnn.attn_prompt(*args, causal=False, workspace=ws)
     rnn.workspace_status(ws)
     assert torch.equal(again[3:], want[3:])
+
+
+# ------------------------------------------------------------ scores beyond fp32
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scaled_scores_beyond_fp32_are_nan(dtype, d, sign):
+    """A scale that is allowed, and scores whose product with it is not a float: the row is NaN,
+    not the zeros of a row without a key.  Heads whose scores stay small keep their results."""
+    n = 300
+    q = torch.full((n, 2, d), 10.0 * sign, dtype=dtype, device="cuda")
+    q[:, 1] = 0
+    k = torch.full((n, 1, d), 10.0, dtype=dtype, device="cuda")
+    v = torch.ones((n, 1, d), dtype=dtype, device="cuda")
+    out, lse = rnn.attn_prompt(q, k, v, ints([0, n]), scale=1e38, with_lse=True)
+    assert out[:, 0].isnan().all() and lse[:, 0].isnan().all()
+    assert (out[:, 1] == 1).all()
+    assert (lse[:, 1] - torch.arange(1, n + 1, device="cuda").log()).abs().max() < 1e-5
+    cache = [torch.nn.functional.pad(x, (0, 0, 0, 0, 0, 20)).view(20, 16, 1, d) for x in (k, v)]
+    out, lse = rnn.attn_decode(q[:2], *cache, torch.arange(20, dtype=torch.int32, device="cuda")
+                               .expand(2, -1), ints([n, 3]), scale=1e38, with_lse=True)
+    assert out[:, 0].isnan().all() and lse[:, 0].isnan().all()
+    assert (out[:, 1] == 1).all() and abs(float(lse[0, 1]) - math.log(n)) < 1e-5
