@@ -466,7 +466,8 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  * Conventions beside those at the top of this file:
  *   - Rows of a head are d contiguous fp16 or bf16 channels; strides are in
  *     elements, at least d and multiples of 8 (a dimension of size 1 may have
- *     any stride).  d is a multiple of 8.
+ *     any stride), and such that no two rows of an output overlap.  d is a
+ *     multiple of 8.
  *   - Hq query heads share Hkv key heads in order: query head h reads key head
  *     h / (Hq / Hkv).  Hq is a multiple of Hkv.
  *   - Sequences are packed one behind the other: sequence b has the tokens

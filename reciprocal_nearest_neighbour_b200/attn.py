@@ -6,7 +6,7 @@ sequences, ``attn_decode`` attends from one new token per sequence over the
 cache.  Tensors are fp16 or bf16 CUDA tensors whose last dimension (the
 channels of a head) is contiguous; the other dimensions may have any strides
 that are multiples of 8 elements, so slices of a fused projection's output
-pass as they are.  Calls run on the current stream of the tensors' device, and
+pass as they are (no two rows of an output may overlap).  Calls run on the current stream of the tensors' device, and
 their results carry no gradient.
 """
 from __future__ import annotations

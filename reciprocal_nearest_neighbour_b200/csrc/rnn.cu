@@ -2970,13 +2970,32 @@ extern "C" rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream) {
 static int64_t stride_or(int64_t size, int64_t stride, int64_t other) {
   return size > 1 ? stride : other;
 }
-// rows of d contiguous 16-bit channels, every one 16-byte aligned, none overlapping
+// rows of d contiguous 16-bit channels, every one 16-byte aligned
 static rnn_status check_rows(rnn_rows* r, int64_t tokens, int heads, int d) {
   if (tokens > 0 && !r->data) return RNN_EINVAL;
   r->head_stride = stride_or(heads, r->head_stride, d);
   r->token_stride = stride_or(tokens, r->token_stride, static_cast<int64_t>(d) * heads);
   if (r->head_stride < d || r->token_stride < d) return RNN_EINVAL;
   if (!aligned16(r->data) || r->head_stride % 8 || r->token_stride % 8) return RNN_EALIGN;
+  return RNN_OK;
+}
+// Rows that are written have to be distinct.  Two of them overlap if a and b steps of the
+// two strides (not both 0) lie less than d apart: for each step of the larger stride only
+// the two nearest counts of the smaller one come into question.  (Nested strides, the
+// usual ones, are told at a glance.)
+static rnn_status check_written_rows(rnn_rows* r, int64_t tokens, int heads, int d) {
+  const rnn_status st = check_rows(r, tokens, heads, d);
+  if (st != RNN_OK || tokens < 2 || heads < 2) return st;
+  int64_t small = r->head_stride, large = r->token_stride, n_small = heads, n_large = tokens;
+  if (small > large) std::swap(small, large), std::swap(n_small, n_large);
+  // steps of the larger stride behind which the smaller one's rows reach no further
+  const int64_t reach = std::min(n_large - 1, ((n_small - 1) * small + d - 1) / large);
+  for (int64_t a = 1; a <= reach; ++a) {
+    const int64_t b = a * large / small;
+    if ((b < n_small && a * large - b * small < d) ||
+        (b + 1 < n_small && (b + 1) * small - a * large < d))
+      return RNN_EINVAL;
+  }
   return RNN_OK;
 }
 static rnn_status check_pages(rnn_pages* c, int64_t num_pages, int page_size, int heads, int d) {
@@ -3074,7 +3093,8 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   if (!(scale > 0.f) || !(scale < 2e38f)) return RNN_EINVAL;
   if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse)) return RNN_EINVAL;
   if ((r = check_rows(&q, Tq, Hq, d)) != RNN_OK || (r = check_rows(&k, Tk, Hkv, d)) != RNN_OK ||
-      (r = check_rows(&v, Tk, Hkv, d)) != RNN_OK || (r = check_rows(&out, Tq, Hq, d)) != RNN_OK)
+      (r = check_rows(&v, Tk, Hkv, d)) != RNN_OK ||
+      (r = check_written_rows(&out, Tq, Hq, d)) != RNN_OK)
     return r;
   if (workspace && (!aligned256(workspace) || ws_bytes < rnn_attn_prompt_workspace_size()))
     return RNN_EWORKSPACE;
@@ -3210,7 +3230,7 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
   if (!(scale > 0.f) || !(scale < 2e38f)) return RNN_EINVAL;
   if ((B > 0 && (!page_table || !lens)) || !aligned4(page_table) || !aligned4(lens) || !aligned4(lse))
     return RNN_EINVAL;
-  if ((r = check_rows(&q, B, Hq, d)) != RNN_OK || (r = check_rows(&out, B, Hq, d)) != RNN_OK ||
+  if ((r = check_rows(&q, B, Hq, d)) != RNN_OK || (r = check_written_rows(&out, B, Hq, d)) != RNN_OK ||
       (r = check_pages(&k_cache, num_pages, page_size, Hkv, d)) != RNN_OK ||
       (r = check_pages(&v_cache, num_pages, page_size, Hkv, d)) != RNN_OK)
     return r;
@@ -3323,9 +3343,9 @@ rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
       (r = check_pages(&v_cache, num_pages, page_size, Hkv, d)) != RNN_OK)
     return r;
   if (Hq > 0 && ((r = check_rows(&q, T, Hq, d)) != RNN_OK ||
-                 (r = check_rows(&q_out, T, Hq, d)) != RNN_OK))
+                 (r = check_written_rows(&q_out, T, Hq, d)) != RNN_OK))
     return r;
-  if (k_out.data && (r = check_rows(&k_out, T, Hkv, d)) != RNN_OK) return r;
+  if (k_out.data && (r = check_written_rows(&k_out, T, Hkv, d)) != RNN_OK) return r;
   DeviceInfo* di = nullptr;
   if ((r = device_info(&di)) != RNN_OK) return r;
   if (T == 0 || B == 0) return RNN_OK;
