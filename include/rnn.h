@@ -511,6 +511,8 @@ typedef struct rnn_pages {
  *                Hq = 0: no queries (q and q_out are ignored).
  *   k, v         [T][Hkv][d]; k_out.data may be NULL, else it gets the rotated
  *                keys packed as k is (for rnn_attn_prompt), and may be k.
+ *                Otherwise outputs lie apart from inputs and each other (those
+ *                that start at the same address are refused).
  *   page_table   [B][max_pages] int32, rows table_stride apart: the pages of
  *                each sequence.  Token t of sequence b is number
  *                start[b] + t - cu[b] of it and goes to row (number %
@@ -547,7 +549,7 @@ rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
  *            query sees the last key (nk > nq: the keys in front are earlier
  *            tokens; nk < nq: the first rows see nothing).  0: all nk keys.
  *   scale    > 0 and < 2e38, multiplies the scores.
- *   out      [Tq][Hq][d], apart from the inputs.
+ *   out      [Tq][Hq][d], apart from the inputs (k and v are refused).
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded (those that last as
  * long as a sequence has keys count from its last step); with a workspace (it

@@ -6,8 +6,8 @@ sequences, ``attn_decode`` attends from one new token per sequence over the
 cache.  Tensors are fp16 or bf16 CUDA tensors whose last dimension (the
 channels of a head) is contiguous; the other dimensions may have any strides
 that are multiples of 8 elements, so slices of a fused projection's output
-pass as they are (no two rows of an output may overlap).  Calls run on the current stream of the tensors' device, and
-their results carry no gradient.
+pass as they are (no two rows of an output may overlap).  Calls run on the
+current stream of the tensors' device, and their results carry no gradient.
 """
 from __future__ import annotations
 
@@ -208,7 +208,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 
     Returns ``(q_out, k_out)``: the rotated queries (``None`` without ``q``)
     and, ``with_k`` or into a given ``k_out``, the rotated keys packed like
-    ``k`` (``None`` otherwise).  ``q_out=q`` and ``k_out=k`` rotate in place.
+    ``k`` (``None`` otherwise).  ``q_out=q`` and ``k_out=k`` rotate in place;
+    otherwise outputs lie apart from the inputs.
     Rows outside the sequences are not written; a token whose page does not
     exist is not stored.
     """
@@ -288,10 +289,11 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     - nq``; else all keys of its sequence.  ``scale`` defaults to ``1/sqrt(d)``.
     Query head ``h`` reads key head ``h // (Hq // Hkv)``.
 
-    Returns ``out [Tq, Hq, d]``, or ``(out, lse)`` with ``lse [Tq, Hq]`` float32
-    the log-sum-exp of the scaled scores.  A row that sees no key is 0 with
-    ``lse`` -inf, one that sees a score that is not a number, or whose largest
-    scaled score leaves float32, is NaN (so values have to be finite); rows
+    Returns ``out [Tq, Hq, d]`` (a given one lies apart from the inputs), or
+    ``(out, lse)`` with ``lse [Tq, Hq]`` float32 the log-sum-exp of the scaled
+    scores.  A row that sees no key is 0 with ``lse`` -inf, one that sees a score
+    that is not a number, or whose largest scaled score leaves float32, is NaN;
+    a value that is not finite may reach earlier rows of its sequence too.  Rows
     outside the sequences are not written.  Should a wait of the kernel run out,
     the rows not computed are NaN; with a ``workspace`` (uint8, 256 bytes)
     ``workspace_status`` tells.

@@ -3098,6 +3098,7 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
     return r;
   if (workspace && (!aligned256(workspace) || ws_bytes < rnn_attn_prompt_workspace_size()))
     return RNN_EWORKSPACE;
+  if (Tq > 0 && Tk > 0 && (out.data == k.data || out.data == v.data)) return RNN_EINVAL;
   PromptParams p;
   std::memset(&p, 0, sizeof(p));
   p.group = Hq / Hkv;
@@ -3346,6 +3347,11 @@ rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
                  (r = check_written_rows(&q_out, T, Hq, d)) != RNN_OK))
     return r;
   if (k_out.data && (r = check_written_rows(&k_out, T, Hkv, d)) != RNN_OK) return r;
+  // in place only as q in q and k in k: other rows are read while these are written
+  if (T > 0 && ((Hq > 0 && (q_out.data == k.data || q_out.data == v.data)) ||
+                (k_out.data && (k_out.data == v.data || (Hq > 0 && (k_out.data == q.data ||
+                                                                    k_out.data == q_out.data))))))
+    return RNN_EINVAL;
   DeviceInfo* di = nullptr;
   if ((r = device_info(&di)) != RNN_OK) return r;
   if (T == 0 || B == 0) return RNN_OK;

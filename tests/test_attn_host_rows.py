@@ -80,3 +80,16 @@ def test_overlapping_packed_keys_are_refused(lib):
     assert append(lib, rows(4), k_out=rows(2, token=D, head=D)) == EINVAL
     # queries are read only, and theirs may overlap
     assert prompt(lib, rows(4), q=rows(4, token=D, head=D)) == EWS
+
+
+def test_outputs_in_place_of_other_inputs_are_refused(lib):
+    q, k, v, q_out, k_out = (FAKE << n for n in (4, 5, 6, 8, 9))
+    bad = [(k, k_out), (v, k_out), (q_out, v), (q_out, q), (q_out, q_out)]
+    for at, ko in bad:
+        assert append(lib, rows(4, at), k_out=rows(2, ko)) == EINVAL, (at, ko)
+    # the cached values would be read after the keys had been turned in their place
+    assert append(lib, rows(4, q_out), v=rows(2, k), k_out=rows(2, k)) == EINVAL
+    for at in (k, v):
+        assert lib.rnn_attn_prompt(ctypes.byref(_lib.AttnPromptArgs(
+            q=rows(4, q), k=rows(2, k), v=rows(2, v), out=rows(4, at), cu_q=FAKE, cu_k=FAKE,
+            Tq=10, Tk=10, Hq=4, Hkv=2, d=D, dtype=0, B=1, causal=1, scale=0.1)), None) == EINVAL
