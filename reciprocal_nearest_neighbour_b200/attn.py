@@ -229,7 +229,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
             raise ValueError("q is only rotated: it needs inv_freq")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if hkv < 1 or d < 8 or d % 8 or d > 256:
+    if hkv < 1:
+        raise ValueError("k and v have no heads")
+    if d < 8 or d % 8 or d > 256:
         raise ValueError(f"channels per head must be a multiple of 8 up to 256, got {d}")
     if max(hq, hkv) > _lib.RNN_ATTN_MAX_HEADS:
         raise ValueError(f"at most {_lib.RNN_ATTN_MAX_HEADS} heads")

@@ -1,10 +1,14 @@
-"""Outputs that the attention entry points refuse to write (no GPU: nothing is launched)."""
+"""Refusals of the attention entry points: outputs that cannot be written as they lie, and
+keys without heads (no GPU: nothing is launched)."""
 import ctypes
 import itertools
 
 import pytest
+import torch
 
+import reciprocal_nearest_neighbour_b200 as rnn
 from reciprocal_nearest_neighbour_b200 import _lib, build as rnn_build
+from test_attn_host import OnGpu
 
 FAKE = 0x10000  # never dereferenced: every call below fails validation
 EINVAL, EALIGN, EWS = 1, 2, 7
@@ -93,3 +97,10 @@ def test_outputs_in_place_of_other_inputs_are_refused(lib):
         assert lib.rnn_attn_prompt(ctypes.byref(_lib.AttnPromptArgs(
             q=rows(4, q), k=rows(2, k), v=rows(2, v), out=rows(4, at), cu_q=FAKE, cu_k=FAKE,
             Tq=10, Tk=10, Hq=4, Hkv=2, d=D, dtype=0, B=1, causal=1, scale=0.1)), None) == EINVAL
+
+
+def test_append_without_key_heads_says_so():
+    ints = dict(dtype=torch.int32)
+    k, cache = OnGpu(8, 0, 64), OnGpu(5, 16, 0, 64)
+    with pytest.raises(ValueError, match="no heads"):
+        rnn.kv_append(k, k, cache, cache, OnGpu(2, 3, **ints), OnGpu(2, **ints), OnGpu(3, **ints))
