@@ -476,8 +476,8 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  *     from cu[B] on are not touched.
  *   - A row that sees no key gets zeros, and -infinity as its log-sum.
  *   - Queries, and the keys and values of a sequence, must be finite.  A row
- *     that sees a NaN or +infinite score, or whose largest score leaves fp32
- *     when scaled, becomes NaN, its log-sum too; a value
+ *     that sees a NaN or +infinite score becomes NaN, its log-sum too (a log-sum
+ *     beyond fp32 is infinite); a value
  *     that is not finite may reach earlier rows of its sequence as well.  What
  *     lies outside the sequences may hold anything.
  *   - Arguments come in a structure, which is only read during the call;

@@ -294,11 +294,10 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
     Returns ``out [Tq, Hq, d]`` (a given one lies apart from the inputs), or
     ``(out, lse)`` with ``lse [Tq, Hq]`` float32 the log-sum-exp of the scaled
     scores.  A row that sees no key is 0 with ``lse`` -inf, one that sees a score
-    that is not a number, or whose largest scaled score leaves float32, is NaN;
-    a value that is not finite may reach earlier rows of its sequence too.  Rows
-    outside the sequences are not written.  Should a wait of the kernel run out,
-    the rows not computed are NaN; with a ``workspace`` (uint8, 256 bytes)
-    ``workspace_status`` tells.
+    that is not a number is NaN; a value that is not finite may reach earlier
+    rows of its sequence too.  Rows outside the sequences are not written.
+    Should a wait of the kernel run out, the rows not computed are NaN; with a
+    ``workspace`` (uint8, 256 bytes) ``workspace_status`` tells.
     """
     kind = _value_dtype(q, "q")
     dev = q.device

@@ -62,6 +62,10 @@ struct DecShape {
 // even lengths change by 1 %.
 constexpr int kDecPairCost = 2;
 constexpr float kDecSlack = 8.f;  // log2 growth of the maximum before a rescale
+// Scaled log2 scores beyond this lose their exponents' last bits (a sixteenth and more)
+// where the reference is taken off behind the scaling, and at 2^128 all of it; it is
+// taken off before for such heads.
+constexpr float kDecFar = 1048576.f;
 
 struct DecodeParams {
   const uint16_t *q, *kc, *vc;
@@ -296,6 +300,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
             o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], f, o[n][c][h]);
       }
   };
+  auto far = [&](float ref) { return fabsf(ref * p.c) > kDecFar && fabsf(ref) < -kNegInf; };
   bool fresh = true;
   bool whole = cur.j == 0;   // the pair started in this share
 #pragma unroll 1
@@ -372,7 +377,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
           x[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
 #pragma unroll
           for (int t = 1; t < kMT; ++t) x[n][e] = fmax3(x[n][e], s[t][n][e], s[t][n][e + 2]);
-          up = up || (x[n][e] - m[n][e]) * p.c > kDecSlack;  // also from -inf to a number
+          up = up || (x[n][e] - m[n][e]) * p.c > kDecSlack  // also from -inf to a number
+               || fabsf(m[n][e] * p.c) > kDecFar;
         }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -392,15 +398,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
               o[n][c][e] *= a;
               o[n][c][e + 2] *= a;
             }
+            const float ref = far(y) ? y : 0.f;
+#pragma unroll
+            for (int t = 0; t < kMT; ++t) {
+              s[t][n][e] -= ref;
+              s[t][n][e + 2] -= ref;
+            }
           }
       }
       uint32_t pf[kMT][kNT][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        // (the second terms make a reference beyond fp32 NaN: no key would have a weight)
-        const float m0 = m[n][0] == kNegInf ? 0.f : m[n][0] * p.c;
-        const float m1 = m[n][1] == kNegInf ? 0.f : m[n][1] * p.c;
-        const float z0 = fmaf(m0, 0.f, m0) - kBias, z1 = fmaf(m1, 0.f, m1) - kBias;
+        const float z0 = (m[n][0] == kNegInf || far(m[n][0]) ? 0.f : m[n][0] * p.c) - kBias;
+        const float z1 = (m[n][1] == kNegInf || far(m[n][1]) ? 0.f : m[n][1] * p.c) - kBias;
 #pragma unroll
         for (int t = 0; t < kMT; ++t) {
           const float e0 = exp2_approx(fmaf(s[t][n][0], p.c, -z0));

@@ -59,6 +59,10 @@ constexpr int kAttnRegsSoftmax = 176, kAttnRegsOther = 80;
 constexpr int kAttnMmaWarp = 8, kAttnTmaWarp = 9, kAttnMmaWarp2 = 10,
               kAttnOutWarp = 12;
 constexpr float kAttnSlack = 8.f;      // log2 growth of the maximum before a rescale
+// Scaled log2 scores beyond this lose their exponents' last bits (a sixteenth and more)
+// where the reference is taken off behind the scaling, and at 2^128 all of it; it is
+// taken off before for such rows.
+constexpr float kAttnFar = 1048576.f;
 // Calls with more keys take the kernel's kLong form.  Up to this many, a unit has 512
 // steps at most, about a millisecond, and what the accumulator cuts off (n 2^-27 of a
 // sum of n weights of one size) stays below 2^-11, half a step of fp16.
@@ -896,6 +900,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       const int row = row0 + r;               // row of the sequence
       const int seen = p.causal ? min(u.nk, row + t.shift + 1) : u.nk;  // keys of this row
       const int seen_all = p.causal ? min(u.nk, row0 + t.shift + 1) : u.nk;  // of every row
+      const float far = row < u.nq ? kAttnFar : -kNegInf;  // other rows do not matter
       float m = kNegInf, l = 0.f;
       // the sums taken out so far, then their total and their reference maximum
       float held[kDP + 2];
@@ -973,30 +978,42 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           }
           if (j == 0) m = x;
           const bool grow = (x - m) * p.c > kAttnSlack;  // also from -inf to a number
-          // one vote for both: a lane whose wait gave up takes the warp with it (votes at
+          float mc = m * p.c;
+          // one vote for all: a lane whose wait gave up takes the warp with it (votes at
           // the waits themselves cost 2 %)
-          if (__any_sync(0xffffffffu, grow || !ok)) {
+          if (__any_sync(0xffffffffu, grow || !ok || fabsf(mc) > far)) {
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const float f = grow ? exp2_approx((m - x) * p.c) : 1.f;
             if (grow) m = x;
+            mc = m == kNegInf ? 0.f : m * p.c;
+            const bool before = fabsf(mc) > far && fabsf(m) < -kNegInf;
+            if (__any_sync(0xffffffffu, before)) {
+              const float ref = before ? m : 0.f;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[c][e] -= ref;
+              if (before) mc = 0.f;
+            }
             l *= f;
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int c = 0; c < kDP / 32; ++c) {
-              float o[32];
-              tmem_ld32(o_at + c * 32, o);
-              tmem_wait_ld_regs(o);
+              for (int c = 0; c < kDP / 32; ++c) {
+                float o[32];
+                tmem_ld32(o_at + c * 32, o);
+                tmem_wait_ld_regs(o);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[16];
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
-                tmem_st16(o_at + c * 32 + h * 16, w);
+                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
+                  tmem_st16(o_at + c * 32 + h * 16, w);
+                }
               }
             }
           }
-          // (the second term makes a reference beyond fp32 NaN: no key would have a weight)
-          const float mc = m == kNegInf ? 0.f : m * p.c, z = fmaf(mc, 0.f, mc) - kBias;
+          const float z = mc - kBias;
           const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
           // The two warps of a scheduler take turns at the exponential unit, tile 0's
           // step j, tile 1's step j, tile 0's step j + 1: left alone they fall into

@@ -311,24 +311,60 @@ def test_rows_given_up_are_nan(d, hq, hkv, on):
     assert torch.equal(again[3:], want[3:])
 
 
-# ------------------------------------------------------------ scores beyond fp32
+# --------------------------------------------------------------- scores of any size
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("sign", [1.0, -1.0])
-def test_scaled_scores_beyond_fp32_are_nan(dtype, d, sign):
-    """A scale that is allowed, and scores whose product with it is not a float: the row is NaN,
-    not the zeros of a row without a key.  Heads whose scores stay small keep their results."""
+@pytest.mark.parametrize("size,scale", [(1.0, 1e38), (-1.0, 1e38), (1.0, 2.0 ** 30), (-1.0, 2e6)])
+def test_scores_of_any_size(dtype, d, size, scale):
+    """Scaled scores up to and beyond fp32's range, of either sign: equal ones weigh the same,
+    the others nothing.  All products are exact: keys of 8 and 16, and one of zeros."""
     n = 300
-    q = torch.full((n, 2, d), 10.0 * sign, dtype=dtype, device="cuda")
-    q[:, 1] = 0
-    k = torch.full((n, 1, d), 10.0, dtype=dtype, device="cuda")
+    q = torch.full((n, 2, d), size, dtype=dtype, device="cuda")
+    q[:, 1] = 0                                  # scores of 0 beside them
+    k = torch.full((n, 1, d), 8.0, dtype=dtype, device="cuda")
+    k[1::2] *= 2                                 # every second key
     v = torch.ones((n, 1, d), dtype=dtype, device="cuda")
-    out, lse = rnn.attn_prompt(q, k, v, ints([0, n]), scale=1e38, with_lse=True)
-    assert out[:, 0].isnan().all() and lse[:, 0].isnan().all()
-    assert (out[:, 1] == 1).all()
-    assert (lse[:, 1] - torch.arange(1, n + 1, device="cuda").log()).abs().max() < 1e-5
+    v[1::2] = 3
+    many = torch.arange(1, n + 1, device="cuda").float()
+    odd = (many / 2).floor()                     # keys of 16 among those seen
+    best = torch.where(odd > 0, 3.0, 1.0) if size > 0 else torch.ones_like(many)
+    want = best[:, None].expand(n, d)
+    out, lse = rnn.attn_prompt(q, k, v, ints([0, n]), scale=scale, with_lse=True)
+    assert torch.equal(out[:, 0].float(), want)
+    mean = (many + 2 * odd) / many
+    u = torch.finfo(dtype).eps / 2
+    assert ((out[:, 1, 0].float() - mean).abs() <= u * mean * (1 + 2.0 ** -8)).all()
+    top = (8.0 * d * size * torch.where(odd > 0, 2.0, 1.0) if size > 0 else
+           torch.full_like(many, 8.0 * d * size)).double() * float(torch.tensor(scale))
+    count = torch.where(odd > 0, odd, many) if size > 0 else many - odd
+    ref = top + count.double().log()
+    far = top.abs() > 3.4e38
+    assert torch.equal(lse[far, 0].double(), torch.sign(top[far]) * math.inf)
+    assert ((lse[:, 0] - ref).abs()[~far] <= ref.abs()[~far] * 2.0 ** -22 + 2.0 ** -20).all()
+    assert (lse[:, 1] - many.log()).abs().max() < 1e-5
     cache = [torch.nn.functional.pad(x, (0, 0, 0, 0, 0, 20)).view(20, 16, 1, d) for x in (k, v)]
-    out, lse = rnn.attn_decode(q[:2], *cache, torch.arange(20, dtype=torch.int32, device="cuda")
-                               .expand(2, -1), ints([n, 3]), scale=1e38, with_lse=True)
-    assert out[:, 0].isnan().all() and lse[:, 0].isnan().all()
-    assert (out[:, 1] == 1).all() and abs(float(lse[0, 1]) - math.log(n)) < 1e-5
+    table = torch.arange(20, dtype=torch.int32, device="cuda").expand(2, -1)
+    dec, dlse = rnn.attn_decode(q[:2], *cache, table, ints([n, 3]), scale=scale, with_lse=True)
+    for b, r in ((0, n - 1), (1, 2)):
+        assert torch.equal(dec[b, 0], out[r, 0])
+        assert abs(float(dec[b, 1, 0]) - float(mean[r])) <= u * float(mean[r]) * (1 + 2.0 ** -8)
+        assert torch.equal(dlse[b, 0], lse[r, 0]) or \
+            abs(float(dlse[b, 0] - lse[r, 0])) <= float(ref[r].abs()) * 2.0 ** -22 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_scores_growing(dtype, d):
+    """Scores of a hundred million that grow key by key: each row takes its last key."""
+    n = 500
+    q = torch.full((n, 1, d), 64.0, dtype=dtype, device="cuda")
+    k = (torch.arange(n, device="cuda").float() / 4).floor()[:, None, None].expand(n, 1, d)
+    k = (k * 2).to(dtype).contiguous()           # steps of 2 up to 248: exact in both types
+    v = torch.randn((n, 1, d), device="cuda").to(dtype)
+    out = rnn.attn_prompt(q, k, v, ints([0, n]), scale=64.0)
+    i = torch.arange(n, device="cuda")
+    first = i // 4 * 4
+    sums = torch.stack([v[first[r]:r + 1, 0].double().mean(0) for r in range(n)])
+    u = torch.finfo(dtype).eps / 2
+    # up to four equal weights, each exactly 1: the output's rounding and a few fp32 ones
+    assert ((out[:, 0].double() - sums).abs() <= sums.abs() * u * (1 + u) + 2.0 ** -20).all()
