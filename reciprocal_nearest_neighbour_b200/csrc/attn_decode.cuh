@@ -21,8 +21,8 @@
 // ahead, over the ends of pairs.
 //
 // The reference maximum of a head moves only when a score exceeds it by more
-// than 2^8 (its weights then reach 2^8, far inside fp32 and the 16-bit
-// types): one vote per tile instead of a reduction across the warp.
+// than 2^8 (its weights then reach 2^8, and 2^15 of fp16's 2^16 with that type's
+// factor of 2^7): one vote per tile instead of a reduction across the warp.
 //
 // Measured (bf16, 128 channels): 4 streams of 90 001 to 131 000 keys, 32/4 heads,
 // 0.96 GB, 148 us (6.5 TB/s, 0.99 of a copy's rate); 96 streams of 50 to 8000 keys,
@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   // (2^15 with the slack), many small ones do not vanish from the weighted sum
   // while the fp32 total keeps them
   constexpr float kBias = kBf16 ? 0.f : 7.f;
+  // with 0.6 for the exponent's rounding up to kDecFar
+  static_assert(kBias + kDecSlack + 0.6f < 15.99f, "weights have to stay inside fp16");
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(dec_smem) + warp * kStages * S::kStageBytes;

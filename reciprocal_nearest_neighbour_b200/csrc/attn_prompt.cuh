@@ -28,8 +28,9 @@
 // rows, while the products and the softmax of the one in between run.
 //
 // Rescaling.  A row's reference maximum only moves when its true maximum has
-// grown by more than 2^8 over it (a weight is then at most 2^8, far inside fp32
-// and the 16-bit types), so the output accumulator is read back and rescaled
+// grown by more than 2^8 over it (a weight is then at most 2^8; in fp16, where all
+// weights carry a factor of 2^7 against its short range below 1, 2^15 of the 2^16
+// that the type holds), so the output accumulator is read back and rescaled
 // rarely; the softmax warps do it themselves.  At 128 channels the next scores are
 // only made when the product before them is complete, so their barrier tells both;
 // at 64 they come earlier, and the softmax warps look at the output's barrier.
@@ -348,6 +349,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
                    const __grid_constant__ CUtensorMap vmap) {
   using S = AttnShape<kDP>;
   constexpr float kBias = kBf16 ? 0.f : 7.f;
+  // with 0.6 for the exponent's rounding up to kAttnFar
+  static_assert(kBias + kAttnSlack + 0.6f < 15.99f, "weights have to stay inside fp16");
   constexpr int kUnitReaders = 14;  // softmax, MMA and output warps
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // Shared memory by 32-bit addresses: one base, everything else a constant away.
