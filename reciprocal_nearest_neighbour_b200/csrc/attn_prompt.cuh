@@ -1064,8 +1064,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
               ((j + 1) % kAttnHoldSteps == 0 || j + 1 == n))
             if (!take_out(j)) break;
         }
-        if (kLong && S::kOwnP && n > kAttnHoldSteps && !take_out(j - 1)) break;
-      } while (kLong && S::kOwnP && j < n);
+        if (kLong && S::kOwnP && ok && n > kAttnHoldSteps) take_out(j - 1);
+      } while (kLong && S::kOwnP && ok && j < n);  // (ok is the same in all lanes here)
       turns += n;
       turns_o += n_o;
       if (it > 0)

@@ -276,11 +276,14 @@ def test_first_long_call_of_a_process_inside_a_capture():
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2)])
 @pytest.mark.parametrize("on", [1, 2])
-def test_rows_given_up_are_nan(d, hq, hkv, on):
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_given_up_are_nan(d, hq, hkv, on, many):
     """A wait that runs out leaves no old bytes in the rows, with or without a workspace; units
-    that a CTA had finished before keep their results."""
+    that a CTA had finished before keep their results.  With many keys in the call too."""
     nq, nk = ragged(5)
     nk = [max(1, n) for n in nk]
+    if many:
+        nq, nk = nq + [130], nk + [70_001]
     q, k, v, cu_q, cu_k = inputs(BF, nq, nk, hq, hkv, d, 23)
     front = torch.full((3, hq, d), 7.0, dtype=BF, device="cuda")
     args = (torch.cat([front, q]), k, v, ints([3 + x for x in cu_q]), ints(cu_k))
