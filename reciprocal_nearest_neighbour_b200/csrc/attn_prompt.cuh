@@ -38,10 +38,10 @@
 // Bound: 4*128*128*d flops and 128*128 exponentials per query tile and key tile;
 // at d = 128 the two take the same time on an SM (16 exponentials, 8192 flops a
 // cycle), at d = 64 the exponentials take twice as long as the products.
-// Measured (32/8 heads, bf16): 2 x 8192 tokens, full, 128 channels 1.70 ms, 1.29
-// PFLOP/s, 0.80 of the library product's burst rate (the power limit moves it up to
-// 5 % from run to run); 64 channels 1.43 ms, 0.77 PFLOP/s, 0.65 of the exponentials'
-// rate at 1965 MHz; one causal prompt of 16384 tokens of 128 channels 1.73 ms.
+// Measured (32/8 heads, bf16, in a CUDA graph): 2 x 8192 tokens, full, 128 channels
+// 1.85 ms, 1.19 PFLOP/s, 0.74 of the library product's burst rate; 64 channels 1.44 ms,
+// 0.76 PFLOP/s, 0.64 of the exponentials' rate at 1965 MHz; one causal prompt of 16384
+// tokens of 128 channels 1.85 to 1.95 ms with the power limit, 2.15 ms call after call.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -66,7 +66,9 @@ constexpr float kAttnSlack = 8.f;      // log2 growth of the maximum before a re
 constexpr float kAttnFar = 1048576.f;
 // Calls with more keys take the kernel's kLong form.  Up to this many, a unit has 512
 // steps at most, about a millisecond, and what the accumulator cuts off (n 2^-27 of a
-// sum of n weights of one size) stays below 2^-11, half a step of fp16.
+// sum of n weights of one size) stays below 2^-11, half a step of fp16.  Below the border
+// the kLong form takes 108 us for 24 frames of 768 tokens (16 heads of 64; 106), 280 for
+// 20 causal prompts of 17 to 4001 tokens (32/8 heads of 128; 265).
 constexpr int64_t kAttnShortKeys = 65536;
 // In the kLong form a row's sums leave the accumulator this often, every 65536 keys.
 constexpr int kAttnHoldSteps = 512;
@@ -93,8 +95,8 @@ struct AttnShape {
 };
 // Looks at the other warp's count, 40 ns apart, before going on anyway, and the
 // 32-column chunk behind which a warp hands over.  2 x 8192 tokens, full: 64 channels
-// 1.43 ms behind the third chunk, 1.47 behind the second, 1.59 behind the last and
-// 1.65 without turns; 128 channels 1.70, 1.92, 1.70 and 2.25 ms.
+// 1.44 ms behind the third chunk, 1.50 behind the second, 1.60 behind the last and
+// 1.53 without turns; 128 channels 1.84, 1.98, 1.85 and 2.00 ms.
 constexpr int kTurnPolls = 100, kTurnChunk = 2;
 
 struct PromptParams {
@@ -700,8 +702,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       // Where the probabilities lie over the scores, the product that reads them has to be
       // complete before other scores are made there: two products with different outputs
       // are not promised to run in the order of their issue.  Issued without this wait,
-      // the 20 causal prompts of 17 to 4001 tokens took 250 us instead of 266; scores in
-      // two products of 64 keys, of which only the second waits, 284 us.
+      // the 20 causal prompts of 17 to 4001 tokens took 250 us where this form took 266;
+      // scores in two products of 64 keys, of which only the second waits, 284 us.
       auto product_done = [&](int step) {
         ok = ok && __all_sync(0xffffffffu, mbar_try_wait(o_bar + 8 * i, step & 1) ||
                                                wait(o_bar + 8 * i, step & 1, kErrWaitMma));

@@ -3104,7 +3104,7 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   p.group = Hq / Hkv;
   // two heads that share their keys, or two neighbouring token tiles of one head (which
   // see different numbers of keys): 20 causal prompts of 17 to 4001 tokens, 32/8 heads
-  // of 128, 247 us with pairs of heads, 270 with pairs of token tiles
+  // of 128, 265 us with pairs of heads, 294 with pairs of token tiles
   p.pair_heads = p.group % 2 == 0;
   p.head_units = p.pair_heads ? Hq / 2 : Hq;
   // every sequence may end in a partial tile
@@ -3141,8 +3141,8 @@ rnn_status rnn_attn_prompt(const rnn_attn_prompt_args* args, rnn_stream_t stream
   p.Hq = Hq;
   p.d = d;
   p.causal = causal != 0;
-  // longest sequences first once units queue: 9 sequences of 700 to 10 207 keys 297 us,
-  // 333 in the given order (24 equal ones 103 and 102, 20 causal prompts 249 and 247)
+  // longest sequences first once units queue: 9 sequences of 700 to 10 207 keys 322 us,
+  // 361 in the given order (24 equal ones 105 and 103, 20 causal prompts 265 and 262)
   p.sort = units > di->sms && B > 1;
   p.scale = scale;
   p.c = scale * 1.44269504f;
