@@ -393,14 +393,14 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Waits.  A lane's outcome is its own; the warp votes before it acts on one.  They
-  // suspend the warp: spinning ones take issue slots from the softmax
-  // warps of the same scheduler (128 channels: a tenth slower).  The limits are read
-  // from the parameters where they are needed, so that no register holds them, nor an
-  // address of a barrier, through the loops.
+  // suspend the warp: spinning ones take issue slots from the softmax warps of the same
+  // scheduler (128 channels: a tenth slower).  The limits are read from the parameters
+  // where they are needed, so that no register holds them, nor an address of a barrier,
+  // through the loops.
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto give_up = [&](int code) {
     sts_volatile(abort_at, 1);
-    if (p.err) atomicOr(p.err, code);  // without a caller's word it only ends the kernel
+    if (p.err) atomicOr(p.err, code);
   };
   // Most last a step or two.  `whole_unit` marks those that last as long as a unit has
   // keys: where that may be long, their limit counts from the last step that a tile's
