@@ -552,7 +552,8 @@ rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
  *   out      [Tq][Hq][d], apart from the inputs (k and v are refused).
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded (those that last as
- * long as a sequence has keys count from its last step); with a workspace (it
+ * long as a sequence has keys, or as the search for one with rows, count from
+ * the last step done); with a workspace (it
  * may be NULL) rnn_workspace_status tells whether one ran out.  The rows that
  * were then not computed are NaN, their log-sums too.
  */

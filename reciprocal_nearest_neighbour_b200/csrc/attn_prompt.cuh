@@ -68,8 +68,10 @@ constexpr float kAttnFar = 1048576.f;
 // steps at most, about a millisecond, and what the accumulator cuts off (n 2^-27 of a
 // sum of n weights of one size) stays below 2^-11, half a step of fp16.  Below the border
 // the kLong form takes 108 us for 24 frames of 768 tokens (16 heads of 64; 106), 280 for
-// 20 causal prompts of 17 to 4001 tokens (32/8 heads of 128; 265).
-constexpr int64_t kAttnShortKeys = 65536;
+// 20 causal prompts of 17 to 4001 tokens (32/8 heads of 128; 265).  Calls with very many
+// sequences or blocks take it too: the search for the next unit goes past 10 sequences
+// without rows, or 3 blocks without a tile, in a microsecond.
+constexpr int64_t kAttnShortKeys = 65536, kAttnFewSeqs = 1 << 20, kAttnFewUnits = 1 << 24;
 // In the kLong form a row's sums leave the accumulator this often, every 65536 keys.
 constexpr int kAttnHoldSteps = 512;
 
@@ -338,12 +340,13 @@ __device__ __forceinline__ bool settle_phase(uint32_t bar, uint32_t parity, uint
   return true;
 }
 
-// kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time,
-// and its sums may lose their small terms: the tensor pipe cuts what it adds off at the
+// kLong: more than kAttnShortKeys keys in the call, so that a unit may last any time, and
+// its sums may lose their small terms: the tensor pipe cuts what it adds off at the
 // accumulator's last bits instead of rounding it (2^20 equal weights lost 0.7 % of a sum
 // of values of one sign, 2.5 10^8 of them three quarters).  There a softmax warp takes
 // its rows out of the accumulator every kAttnHoldSteps steps and adds them up itself,
-// rounded to nearest, in local memory.
+// rounded to nearest, in local memory.  Also with more than kAttnFewSeqs sequences or
+// kAttnFewUnits units, where the search for the next unit may last as long.
 template <bool kBf16, int kDP, bool kLong>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
@@ -382,6 +385,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
   // counts that only grow, where a reader may be any number of steps behind
   const uint32_t zero_at = tmem_slot + 8;   // ragged V tiles whose end is zeroed
   const uint32_t turn_at = tmem_slot + 16;  // per softmax warp: steps whose exponentials are out
+  const uint32_t search_at = turn_at + 32;  // groups and blocks looked at for units (kLong)
   __shared__ __align__(16) uint8_t answer[16];
   // Units published in turn (two at a time, and those before them as long as an output
   // warp may have them in hand), how many so far, and one that was taken and not published.
@@ -403,8 +407,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     if (p.err) atomicOr(p.err, code);
   };
   // Most last a step or two.  `whole_unit` marks those that last as long as a unit has
-  // keys: where that may be long, their limit counts from the last step that a tile's
-  // first softmax warp has done.
+  // keys, or as the search for the next one: where that may be long, their limit counts
+  // from the last step that a tile's first softmax warp, or the search, has done.
   auto wait = [&](uint32_t bar, uint32_t parity, int code, bool whole_unit = false) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
     uint64_t t0 = globaltimer_ns();
@@ -414,7 +418,8 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
       if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
       if (aborted()) return false;
       if (kLong && whole_unit) {
-        const int now = lds_volatile(turn_at) + lds_volatile(turn_at + 16);
+        const int now =
+            lds_volatile(turn_at) + lds_volatile(turn_at + 16) + lds_volatile(search_at);
         if (now != steps) t0 = globaltimer_ns();
         steps = now;
       }
@@ -455,6 +460,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
     if (threadIdx.x == 128) {
       sts_volatile(zero_at, 0);
       sts_volatile(abort_at, 0);
+      if (kLong) sts_volatile(search_at, 0);
       dealt = 0;
       unpublished.nq = -1;
     }
@@ -534,7 +540,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
         loaded = base_b;
       };
       int block = blockIdx.x, issued = 0, q_loads = 0;
-      int asked = 0;
+      int asked = 0, searched = 0;
       bool ok = true;
       // (not cut short by an abort: a block that was handed over will not start)
       auto answered = [&]() {
@@ -565,6 +571,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           u.hu = block - tile * p.head_units;
           if (tile < base_tile) base_b = base_tile = 0;  // blocks come in order, as a rule
           while (base_b < p.B) {
+            if (kLong && lane == 0) sts_volatile(search_at, ++searched);
             if (loaded != base_b) load_group();
             const unsigned behind = __ballot_sync(0xffffffffu, tile < base_tile + g_incl);
             if (behind) {
@@ -584,6 +591,7 @@ attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant
           if (u.nq >= 0) break;
           // behind the last tile (the grid is an upper bound): take the rest of the
           // blocks off the queue, so that none starts only to find nothing
+          if (kLong && lane == 0) sts_volatile(search_at, ++searched);
           ask();
           ok = answered();
         }

@@ -3063,7 +3063,7 @@ template <bool kBf16, int kDP>
 static void prompt_launch(const PromptParams& p, unsigned grid, const CUtensorMap& q,
                           const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   const size_t sm = AttnShape<kDP>::kSmem;
-  if (p.Tk > kAttnShortKeys)
+  if (p.Tk > kAttnShortKeys || p.B > kAttnFewSeqs || grid > kAttnFewUnits)
     attn_prompt_kernel<kBf16, kDP, true><<<grid, kAttnThreads, sm, s>>>(p, q, k, v);
   else
     attn_prompt_kernel<kBf16, kDP, false><<<grid, kAttnThreads, sm, s>>>(p, q, k, v);

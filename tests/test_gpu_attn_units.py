@@ -170,6 +170,20 @@ def test_unit_longer_than_the_wait_limit():
     assert abs(float(lse) - math.log(n)) <= math.log(n) * 2.0 ** -22 + 2.0 ** -20
 
 
+def test_search_longer_than_the_wait_limit():
+    """13 million sequences of which the last has rows: the search for its unit, and past the
+    blocks of the others, lasts longer than a wait may without anything done."""
+    B, n = 13_000_000, 130
+    g = torch.Generator("cuda").manual_seed(31)
+    q, k, v = (normal(g, (n, h, 64), BF) for h in (2, 1, 1))
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[-1] = n
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    out = rnn.attn_prompt(q, k, v, cu, workspace=ws)
+    rnn.workspace_status(ws)
+    assert torch.equal(out, rnn.attn_prompt(q, k, v, ints([0, n])))
+
+
 # ------------------------------------------------------------------- long sums
 def held(ref, segment):
     """The oracle's results with the number of keys that meet in one accumulator: `segment`
