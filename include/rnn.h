@@ -477,16 +477,16 @@ rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream);
  *   - A row that sees no key gets zeros, and -infinity as its log-sum.
  *   - Queries, and the keys and values of a sequence, must be finite.  A row
  *     that sees a NaN or +infinite score becomes NaN, its log-sum too (a log-sum
- *     beyond fp32 is infinite); a value
- *     that is not finite may reach earlier rows of its sequence as well.  What
- *     lies outside the sequences may hold anything.
+ *     beyond fp32 is infinite); a value that is not finite may reach earlier
+ *     rows of its sequence as well.  What lies outside the sequences may hold
+ *     anything.
  *   - Arguments come in a structure, which is only read during the call;
  *     dtype is an rnn_dtype.
  *   - Softmax statistics and sums are fp32; each product's probabilities are
  *     rounded to the 16-bit type once, outputs once.  The tensor cores cut sums
  *     off at fp32's last bits instead of rounding them; no more than 65536 keys
- *     of a row meet in one of their accumulators, which is a relative 2^-11 at
- *     most.
+ *     of a row meet in one of their accumulators, which costs up to 2^-11 of
+ *     the sum of the weighted |values|.
  */
 #define RNN_ATTN_MAX_DIM 128
 #define RNN_ATTN_MAX_HEADS 1024
@@ -553,9 +553,9 @@ rnn_status rnn_kv_append(const rnn_kv_append_args *args, rnn_stream_t stream);
  *   lse      [Tq][Hq] float, log sum exp of the scaled scores; may be NULL.
  * d <= RNN_ATTN_MAX_DIM.  The kernel's waits are bounded (those that last as
  * long as a sequence has keys, or as the search for one with rows, count from
- * the last step done); with a workspace (it
- * may be NULL) rnn_workspace_status tells whether one ran out.  The rows that
- * were then not computed are NaN, their log-sums too.
+ * the last step done); with a workspace (it may be NULL) rnn_workspace_status
+ * tells whether one ran out.  The rows that were then not computed are NaN,
+ * their log-sums too.
  */
 typedef struct rnn_attn_prompt_args {
   rnn_rows q, k, v, out;
