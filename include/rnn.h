@@ -594,6 +594,88 @@ size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
 rnn_status rnn_attn_decode(const rnn_attn_decode_args *args, rnn_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The paged cache in 8-bit codes.
+ *
+ * The conventions are those of the attention entry points above.  A row is one
+ * token's d channels x of one head: the key as rotated, in fp32, or the value.
+ * It is held as d codes of one byte, rows and strides as in rnn_pages (strides
+ * in codes), and one fp32 scale
+ *     s = max(max |x| / top, 2^-126)
+ * with top = 448 (RNN_CODES_E4M3: sign, 4 bits of exponent with bias 7, 3 of
+ * mantissa, no infinity) or 127 (RNN_CODES_INT8: two's complement); the codes
+ * are x * (1 / s), both quotients and the codes rounded to nearest even.  Code
+ * times s is the value that a row holds.  A row with a channel that is not
+ * finite gets a NaN for its scale.
+ * The cache is two rnn_pages of codes and one rnn_scales, whose page and head
+ * hold page_size pairs of the key's and the value's scale of a token, in order.
+ */
+typedef enum rnn_codes { RNN_CODES_E4M3 = 0, RNN_CODES_INT8 = 1 } rnn_codes;
+
+/* [pages][heads][page_size][2]; strides in floats, even and at least
+ * 2 * page_size (a dimension of size 1 may have any), data 8-byte aligned */
+typedef struct rnn_scales {
+  float *data;
+  int64_t page_stride, head_stride;
+} rnn_scales;
+
+/*
+ * rnn_kv_append into a cache of codes: arguments, rotation, places and errors
+ * are those of rnn_kv_append, with `codes` an rnn_codes.  q_out and k_out are
+ * 16-bit rows, rounded once (k_out: the rotated keys as they are, not as the
+ * cache holds them).  d <= 256.  No workspace.
+ */
+typedef struct rnn_kv_append_q8_args {
+  rnn_rows q, k, v, q_out, k_out;
+  rnn_pages k_cache, v_cache;
+  rnn_scales scales;
+  const int32_t *page_table, *start, *cu, *positions;
+  const double *inv_freq;
+  int64_t T, num_pages, table_stride, position_stride;
+  int32_t Hq, Hkv, d, dtype, codes, page_size, max_pages, B, pairs, axes, paired;
+} rnn_kv_append_q8_args;
+rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args *args, rnn_stream_t stream);
+
+/*
+ * Cached rows as packed 16-bit rows k, v [T][Hkv][d]: packed token t of sequence
+ * b (cu[b] <= t < cu[b+1]) is number start[b] + t - cu[b] of it (start may be
+ * NULL: 0), placed as in rnn_kv_append; code times scale, rounded once to dtype.
+ * A token whose number or page does not exist gives zeros.  Rows outside the
+ * sequences are not written.  d <= 256.  No workspace.
+ */
+typedef struct rnn_kv_read_q8_args {
+  rnn_rows k, v;
+  rnn_pages k_cache, v_cache;
+  rnn_scales scales;
+  const int32_t *page_table, *start, *cu;
+  int64_t T, num_pages, table_stride;
+  int32_t Hkv, d, dtype, codes, page_size, max_pages, B;
+} rnn_kv_read_q8_args;
+rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args *args, rnn_stream_t stream);
+
+/*
+ * rnn_attn_decode over a cache of codes, which attends to code times scale:
+ * arguments, results and errors are those of rnn_attn_decode.  The scores take
+ * the products as they are; a value's weight (probability times the value's
+ * scale, with a power of two for each query head) is rounded to fp16 once.
+ * Queries are held as fp16 times a power of two for each head: what is 2^-39 of
+ * a row's largest channel and less may be lost.
+ */
+typedef struct rnn_attn_decode_q8_args {
+  rnn_rows q, out;
+  rnn_pages k_cache, v_cache;
+  rnn_scales scales;
+  const int32_t *page_table, *lens;
+  float *lse;
+  void *workspace;
+  uint64_t ws_bytes;
+  int64_t num_pages, table_stride;
+  int32_t page_size, max_pages, B, Hq, Hkv, d, dtype, codes;
+  float scale;
+} rnn_attn_decode_q8_args;
+size_t rnn_attn_decode_q8_workspace_size(int B, int Hq, int Hkv, int d);
+rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args *args, rnn_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics for benchmarking (no effect on results).
  *
  * rnn_launch_count: number of kernels this library has launched in this

@@ -31,6 +31,9 @@ contiguous fp16/bf16 CUDA tensors; pixel index ``p = y*W + x``.
   network in front of the matching (image tokens, and the memory of earlier
   frames): softmax-weighted sums over the rows of Q K^T instead of their
   argmax, for packed sequences and over a paged cache.
+* ``kv_append_q8`` / ``kv_read_q8`` / ``attn_decode_q8``: that cache in 8-bit
+  codes (e4m3 or int8, a scale for each token and head): written, read back
+  and attended to.
 
 Results stay on the device; pair lists come back as ``(pairs, count)`` with
 ``pairs`` a ``[cap, 2]`` int32 buffer and ``count`` a device int32 tensor;
@@ -52,7 +55,7 @@ __all__ = [
     "frm_max_pairs", "workspace_status", "trim", "MNNResult", "FRMResult", "RNNError",
     "RNNLibraryError", "FRMPlan", "frm_match_ex", "frm_refine", "pts_nn", "pts_mnn",
     "pts_frm_match", "c2f_match", "C2FResult", "mnn_mutual", "FRMGraph", "kv_append",
-    "attn_prompt", "attn_decode",
+    "attn_prompt", "attn_decode", "kv_append_q8", "kv_read_q8", "attn_decode_q8",
 ]
 
 _DT = {torch.float16: _lib.RNN_F16, torch.bfloat16: _lib.RNN_BF16}
@@ -600,3 +603,4 @@ def c2f_match(C1: torch.Tensor, C2: torch.Tensor, F1: torch.Tensor, F2: torch.Te
 
 
 from .attn import attn_decode, attn_prompt, kv_append  # noqa: E402
+from .cache_q8 import attn_decode_q8, kv_append_q8, kv_read_q8  # noqa: E402

@@ -56,6 +56,10 @@ EXPORTS = (
     "rnn_attn_prompt",
     "rnn_attn_decode_workspace_size",
     "rnn_attn_decode",
+    "rnn_kv_append_q8",
+    "rnn_kv_read_q8",
+    "rnn_attn_decode_q8_workspace_size",
+    "rnn_attn_decode_q8",
 )
 
 STATUS = {
@@ -64,6 +68,7 @@ STATUS = {
 }
 RNN_F16, RNN_BF16 = 0, 1
 RNN_DOT, RNN_L2 = 0, 1
+RNN_CODES_E4M3, RNN_CODES_INT8 = 0, 1
 METRICS = {"dot": RNN_DOT, "l2": RNN_L2}
 RNN_MAX_BATCH = 1024
 RNN_NN_NOALLOC_MAX_QUERIES = 65536
@@ -83,9 +88,15 @@ class Pages(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class Scales(ctypes.Structure):
+    """``rnn_scales``: [pages][heads][page_size][2], page and head strides in floats."""
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 def _fields(**groups):
     """Structure fields from ``type="names"`` groups in order."""
-    types = {"rows": Rows, "pages": Pages, "ptr": ctypes.c_void_p, "u64": ctypes.c_uint64,
+    types = {"rows": Rows, "pages": Pages, "scales": Scales, "ptr": ctypes.c_void_p, "u64": ctypes.c_uint64,
              "i64": ctypes.c_int64, "i32": ctypes.c_int32, "f32": ctypes.c_float}
     return [(n, types[t.rstrip("_")]) for t, names in groups.items() for n in names.split()]
 
@@ -109,6 +120,29 @@ class AttnDecodeArgs(ctypes.Structure):
     _fields_ = _fields(rows="q out", pages="k_cache v_cache", ptr="page_table lens lse workspace",
                        u64="ws_bytes", i64="num_pages table_stride",
                        i32="page_size max_pages B Hq Hkv d dtype", f32="scale")
+
+
+class KvAppendQ8Args(ctypes.Structure):
+    """``rnn_kv_append_q8_args``"""
+    _fields_ = _fields(rows="q k v q_out k_out", pages="k_cache v_cache", scales="scales",
+                       ptr="page_table start cu positions inv_freq",
+                       i64="T num_pages table_stride position_stride",
+                       i32="Hq Hkv d dtype codes page_size max_pages B pairs axes paired")
+
+
+class KvReadQ8Args(ctypes.Structure):
+    """``rnn_kv_read_q8_args``"""
+    _fields_ = _fields(rows="k v", pages="k_cache v_cache", scales="scales",
+                       ptr="page_table start cu", i64="T num_pages table_stride",
+                       i32="Hkv d dtype codes page_size max_pages B")
+
+
+class AttnDecodeQ8Args(ctypes.Structure):
+    """``rnn_attn_decode_q8_args``"""
+    _fields_ = _fields(rows="q out", pages="k_cache v_cache", scales="scales",
+                       ptr="page_table lens lse workspace", u64="ws_bytes",
+                       i64="num_pages table_stride",
+                       i32="page_size max_pages B Hq Hkv d dtype codes", f32="scale")
 
 
 class RNNLibraryError(RuntimeError):
@@ -189,6 +223,10 @@ def load():
         "rnn_attn_prompt": (I, [P, P]),
         "rnn_attn_decode_workspace_size": (SZ, [I, I, I, I]),
         "rnn_attn_decode": (I, [P, P]),
+        "rnn_kv_append_q8": (I, [P, P]),
+        "rnn_kv_read_q8": (I, [P, P]),
+        "rnn_attn_decode_q8_workspace_size": (SZ, [I, I, I, I]),
+        "rnn_attn_decode_q8": (I, [P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -189,6 +189,72 @@ def _call(fn, name: str, t: torch.Tensor, args: bytes) -> None:
         _lib.check(code, name)
 
 
+def _new_rows(k, v, q, q_out, inv_freq):
+    """Type, device and sizes of the rows that an append takes."""
+    kind = _value_dtype(k, "k")
+    dev = k.device
+    _all(kind, dev, 3, k, "k", v, "v")
+    T, hkv, d = shape = k.shape
+    if v.shape != shape:
+        raise ValueError(f"v must have the shape of k, got {tuple(v.shape)}")
+    hq = 0
+    if q is not None:
+        _all(kind, dev, 3, q, "q")
+        tq, hq, dq = q.shape
+        if tq != T or dq != d or hq < 1:
+            raise ValueError(f"q must have shape [{T}, heads, {d}], got {tuple(q.shape)}")
+        if inv_freq is None:
+            raise ValueError("q is only rotated: it needs inv_freq")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if hkv < 1:
+        raise ValueError("k and v have no heads")
+    if d < 8 or d % 8 or d > 256:
+        raise ValueError(f"channels per head must be a multiple of 8 up to 256, got {d}")
+    if max(hq, hkv) > _lib.RNN_ATTN_MAX_HEADS:
+        raise ValueError(f"at most {_lib.RNN_ATTN_MAX_HEADS} heads")
+    return kind, dev, T, hq, hkv, d
+
+
+def _turns(inv_freq, positions, T: int, d: int, dev):
+    """Channel pairs an axis, axes, and the stride of the positions' rows."""
+    pairs = axes = pos_stride = 0
+    if inv_freq is not None:
+        _all(torch.float64, dev, 1, inv_freq, "inv_freq")
+        pairs, axes = inv_freq.shape[0], 1
+        if pairs < 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous and not empty")
+    if positions is not None:
+        if inv_freq is None:
+            raise ValueError("positions need inv_freq")
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+            raise ValueError("positions must be a [T] or [T, 2] tensor")
+        _check(positions, "positions", positions.dim(), torch.int32, dev)
+        axes = positions.shape[1] if positions.dim() == 2 else 1
+        if positions.shape[0] != T or axes not in (1, 2):
+            raise ValueError(f"positions must have shape [{T}] or [{T}, 2], got "
+                             f"{tuple(positions.shape)}")
+        if positions.dim() == 2 and axes > 1 and positions.stride(1) != 1:
+            raise ValueError("rows of positions must be contiguous")
+        pos_stride = positions.stride(0) if T > 1 else axes
+        if pos_stride < axes:
+            raise ValueError("rows of positions must not overlap")
+    if 2 * pairs * axes > d:
+        raise ValueError(f"{2 * pairs * axes} rotated channels do not fit into {d}")
+    return pairs, axes, pos_stride
+
+
+def _rotated(q, k, q_out, k_out, with_k: bool):
+    """The outputs of an append: the caller's, or new ones."""
+    if q is not None:
+        q_out = _packed(q) if q_out is None else _given(q_out, q.shape, k.dtype, k.device, "q_out")
+    if k_out is not None:
+        _given(k_out, k.shape, k.dtype, k.device, "k_out")
+    elif with_k:
+        k_out = _packed(k)
+    return q_out, k_out
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               page_table: torch.Tensor, start: torch.Tensor, cu: torch.Tensor, *,
               q: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
@@ -213,61 +279,13 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     Rows outside the sequences are not written; a token whose page does not
     exist is not stored.
     """
-    kind = _value_dtype(k, "k")
-    dev = k.device
-    _all(kind, dev, 3, k, "k", v, "v")
-    T, hkv, d = shape = k.shape
-    if v.shape != shape:
-        raise ValueError(f"v must have the shape of k, got {tuple(v.shape)}")
-    hq = 0
-    if q is not None:
-        _all(kind, dev, 3, q, "q")
-        tq, hq, dq = q.shape
-        if tq != T or dq != d or hq < 1:
-            raise ValueError(f"q must have shape [{T}, heads, {d}], got {tuple(q.shape)}")
-        if inv_freq is None:
-            raise ValueError("q is only rotated: it needs inv_freq")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    if hkv < 1:
-        raise ValueError("k and v have no heads")
-    if d < 8 or d % 8 or d > 256:
-        raise ValueError(f"channels per head must be a multiple of 8 up to 256, got {d}")
-    if max(hq, hkv) > _lib.RNN_ATTN_MAX_HEADS:
-        raise ValueError(f"at most {_lib.RNN_ATTN_MAX_HEADS} heads")
+    kind, dev, T, hq, hkv, d = _new_rows(k, v, q, q_out, inv_freq)
     num_pages, size = _cache(k_cache, v_cache, kind, dev, hkv, d)
     B = _cu(cu, "cu", dev)
     _ints(start, "start", dev, B)
     table_stride, max_pages = _table(page_table, dev, B)
-    pairs = axes = pos_stride = 0
-    if inv_freq is not None:
-        _all(torch.float64, dev, 1, inv_freq, "inv_freq")
-        pairs, axes = inv_freq.shape[0], 1
-        if pairs < 1 or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous and not empty")
-    if positions is not None:
-        if inv_freq is None:
-            raise ValueError("positions need inv_freq")
-        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
-            raise ValueError("positions must be a [T] or [T, 2] tensor")
-        _check(positions, "positions", positions.dim(), torch.int32, dev)
-        axes = positions.shape[1] if positions.dim() == 2 else 1
-        if positions.shape[0] != T or axes not in (1, 2):
-            raise ValueError(f"positions must have shape [{T}] or [{T}, 2], got "
-                             f"{tuple(positions.shape)}")
-        if positions.dim() == 2 and axes > 1 and positions.stride(1) != 1:
-            raise ValueError("rows of positions must be contiguous")
-        pos_stride = positions.stride(0) if T > 1 else axes
-        if pos_stride < axes:
-            raise ValueError("rows of positions must not overlap")
-    if 2 * pairs * axes > d:
-        raise ValueError(f"{2 * pairs * axes} rotated channels do not fit into {d}")
-    if q is not None:
-        q_out = _packed(q) if q_out is None else _given(q_out, q.shape, kind, dev, "q_out")
-    if k_out is not None:
-        _given(k_out, k.shape, kind, dev, "k_out")
-    elif with_k:
-        k_out = _packed(k)
+    pairs, axes, pos_stride = _turns(inv_freq, positions, T, d, dev)
+    q_out, k_out = _rotated(q, k, q_out, k_out, with_k)
     _call(_lib.load().rnn_kv_append, "rnn_kv_append", k, _APPEND.pack(
         *(_NO_ROWS if q is None else _rows(q, "q", d)), *_rows(k, "k", d), *_rows(v, "v", d),
         *(_NO_ROWS if q is None else _rows(q_out, "q_out", d)),

@@ -84,6 +84,11 @@ struct DecodeParams {
   float2* part_ml;                 // [grid][2][16] maximum, total
   int* err;                        // status word, cleared: no wait here can run out
   int2* span;                      // [B][Hkv * hblocks] first and last CTA of a pair
+  // caches of codes (attn_decode_q8_kernel), whose strides are in bytes
+  const uint8_t *kc8, *vc8;
+  const float* scales;             // [page][head][row][key, value]
+  int64_t s_ps, s_hs;
+  int wide;                        // rows start on 16 bytes and have whole 16-byte chunks
 };
 
 __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
@@ -107,6 +112,83 @@ __device__ __forceinline__ int dec_owner(int64_t w, int64_t total, int64_t grid)
   while (c + 1 < grid && dec_share(c + 1, total, grid) <= w) ++c;
   while (c > 0 && dec_share(c, total, grid) > w) --c;
   return static_cast<int>(c);
+}
+
+// Where a walk along the tile list is.
+struct DecCursor {
+  int b, h, j, n, len;  // sequence, head unit, tile, tiles, keys
+  int64_t at;           // place of the tile in the list
+};
+
+// This CTA's share of the list: its first tile and the place behind its last; all
+// places, and the CTAs with a share.  False where there is none.  By the whole block.
+template <int kTile>
+__device__ __forceinline__ bool dec_begin(const DecodeParams& p, int warp, int lane, DecCursor& ld,
+                                          int64_t& hi, int64_t& total, int64_t& grid) {
+  const int Hv = p.Hkv * p.hblocks;
+  __shared__ int64_t scan[kDecWarps];
+  __shared__ int64_t sh_before;
+  __shared__ int sh_b;
+  const int per = (p.B + kDecWarps * 32 - 1) / (kDecWarps * 32);
+  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += dec_places<kTile>(p, b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  if (threadIdx.x == 0) sh_b = p.B;
+  __syncthreads();
+  int64_t before = incl - mine, places = 0;
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += scan[w];
+    places += scan[w];
+  }
+  total = places * Hv;
+  // CTAs with a share: no more than places, so that none inside a pair's span is empty
+  grid = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= grid) return false;
+  const int64_t lo = dec_share(blockIdx.x, total, grid);
+  hi = dec_share(blockIdx.x + 1, total, grid);
+  if (lo >= before * Hv && lo < (before + mine) * Hv) {
+    int64_t at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int64_t n = dec_places<kTile>(p, b);
+      if (lo < (at + n) * Hv) {
+        sh_b = b;
+        sh_before = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  ld.b = sh_b;
+  ld.len = dec_len(p, ld.b);
+  ld.n = (ld.len + kTile - 1) / kTile;
+  // the share's first place is a tile, or stands for its pair's cost
+  const int64_t r = lo - sh_before * Hv, per_pair = ld.n + kDecPairCost;
+  ld.h = static_cast<int>(r / per_pair);
+  ld.j = max(0, static_cast<int>(r - ld.h * per_pair) - kDecPairCost);
+  ld.at = sh_before * Hv + ld.h * per_pair + kDecPairCost + ld.j;
+  return true;
+}
+template <int kTile>
+__device__ __forceinline__ void dec_advance(const DecodeParams& p, int Hv, DecCursor& k) {
+  ++k.at;
+  if (++k.j < k.n) return;
+  k.j = 0;
+  k.at += kDecPairCost;
+  if (++k.h < Hv) return;
+  k.h = 0;
+  do {
+    if (++k.b >= p.B) return;
+    k.len = dec_len(p, k.b);
+    k.n = (k.len + kTile - 1) / kTile;
+  } while (k.n == 0);
 }
 
 // kLong: page tables with room for more than kDecShortKeys keys.  The matrix instruction
@@ -137,78 +219,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 
   const int Hv = p.Hkv * p.hblocks;
   // ---- this CTA's share of the tile list, and the pair it starts in
-  __shared__ int64_t scan[kDecWarps];
-  __shared__ int64_t sh_before;
-  __shared__ int sh_b;
-  const int per = (p.B + kDecWarps * 32 - 1) / (kDecWarps * 32);
-  const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += dec_places<S::kTile>(p, b);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) scan[warp] = incl;
-  if (threadIdx.x == 0) sh_b = p.B;
-  __syncthreads();
-  int64_t before = incl - mine, places = 0;
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += scan[w];
-    places += scan[w];
-  }
-  const int64_t total = places * Hv;
-  // CTAs with a share: no more than places, so that none inside a pair's span is empty
-  const int64_t grid = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= grid) return;
-  const int64_t lo = dec_share(blockIdx.x, total, grid);
-  const int64_t hi = dec_share(blockIdx.x + 1, total, grid);
-  if (lo >= before * Hv && lo < (before + mine) * Hv) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t n = dec_places<S::kTile>(p, b);
-      if (lo < (at + n) * Hv) {
-        sh_b = b;
-        sh_before = at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-
-  struct Cursor {
-    int b, h, j, n, len;  // sequence, head unit, tile, tiles, keys
-    int64_t at;           // place of the tile in the list
-  } ld, cur;
-  ld.b = sh_b;
-  ld.len = dec_len(p, ld.b);
-  ld.n = (ld.len + S::kTile - 1) / S::kTile;
-  {
-    // the share's first place is a tile, or stands for its pair's cost
-    const int64_t r = lo - sh_before * Hv, per_pair = ld.n + kDecPairCost;
-    ld.h = static_cast<int>(r / per_pair);
-    ld.j = max(0, static_cast<int>(r - ld.h * per_pair) - kDecPairCost);
-    ld.at = sh_before * Hv + ld.h * per_pair + kDecPairCost + ld.j;
-  }
+  DecCursor ld, cur;
+  int64_t hi, total, grid;
+  if (!dec_begin<S::kTile>(p, warp, lane, ld, hi, total, grid)) return;
   cur = ld;
-  auto advance = [&](Cursor& k) {
-    ++k.at;
-    if (++k.j < k.n) return;
-    k.j = 0;
-    k.at += kDecPairCost;
-    if (++k.h < Hv) return;
-    k.h = 0;
-    do {
-      if (++k.b >= p.B) return;
-      k.len = dec_len(p, k.b);
-      k.n = (k.len + S::kTile - 1) / S::kTile;
-    } while (k.n == 0);
-  };
+  auto advance = [&](DecCursor& k) { dec_advance<S::kTile>(p, Hv, k); };
   // Page of key (lane % kKeys) of a tile, -1 where there is none.
   const int my_row = lane & (kKeys - 1);
-  auto page_of = [&](const Cursor& k) -> int {
+  auto page_of = [&](const DecCursor& k) -> int {
     const int t = k.j * S::kTile + warp * kKeys + my_row;
     if (t >= k.len) return -1;
     const int id = __ldg(p.table + k.b * p.table_bs + fdiv(t, p.page));
@@ -216,7 +234,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   };
   const int ch = lane % kChunks, sub = lane / kChunks;
   const bool ch_live = ch * 8 < p.d;
-  auto issue = [&](int stage, const Cursor& k, int id) {
+  auto issue = [&](int stage, const DecCursor& k, int id) {
     const int t0 = k.j * S::kTile + warp * kKeys;
     const int hk = p.hblocks == 1 ? k.h : k.h / p.hblocks;
     const unsigned valid = __ballot_sync(0xffffffffu, id >= 0) &
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   int next_id = page_of(ld);
   auto issue_next = [&]() {
     if (ld.at < hi) {
-      const Cursor now = ld;
+      const DecCursor now = ld;
       const int id = next_id;
       advance(ld);
       if (ld.at < hi) next_id = page_of(ld);  // the next tile's pages are looked up a tile ahead
@@ -565,10 +583,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
 // Joins the parts of the pairs that several CTAs shared, and writes the rows
 // of sequences without a key.  One block per (sequence, query head); its four
 // warps take the parts in turn and their sums meet in a fixed order.
-template <bool kBf16, int kDP>
+// kBias: log2 of the factor that the weights' totals carry.
+template <bool kBf16, int kDP, int kBias>
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const DecodeParams p) {
   constexpr int kVals = kDP / 32;  // channels per lane
-  constexpr float kBias = kBf16 ? 0.f : 7.f;
   using VecT = std::conditional_t<kVals == 4, float4, float2>;
   __shared__ float acc[4][kDP];
   __shared__ float2 tot[4];

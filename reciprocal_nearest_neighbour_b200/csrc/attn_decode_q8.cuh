@@ -1,0 +1,525 @@
+// attn_decode over a cache of 8-bit codes (kv_q8.cuh):
+//   out = sum_t softmax_t(scale ks_t q.kc_t) vs_t vc_t
+// with the codes kc_t, vc_t and scales ks_t, vs_t of cached row t.
+//
+// Bound by memory as attn_decode is, by half its bytes.  The split of the cache into
+// tiles and of their list into the CTAs' shares, the four warps with a softmax state
+// each, the ring of asynchronous copies, the parts and their join are attn_decode's; a
+// tile has 4 x 32 keys here.  Codes stay codes on their way through shared memory and
+// become fp16 in registers, exactly: e4m3 by the conversion instruction (two codes, 64
+// lanes a cycle and SM), int8 by planting the byte into the mantissa of 1024 and taking
+// 1152 off.  The matrix instruction adds its 16 depth steps in any order, so a lane reads
+// 16 neighbouring codes of a key row and takes them as its share of four steps; the
+// queries' fragments follow the same order.  The values' fragments pair neighbouring
+// keys of one channel: the byte permutation that gathers the codes for the conversion
+// also transposes them.
+//
+// Range.  Queries are scaled by a power of two to below 2^15 for fp16, and their scores
+// back together with ks_t, in fp32.  A value's weight is p_t vs_t with any size of vs_t,
+// but its fp16 operand holds 2^-24 to 2^16 only: it carries a factor f, a power of two for
+// each head that puts the largest weight so far at 2^6 when it is chosen, and is chosen
+// again, the sums following, when the softmax reference moves or a weight passes 2^15.
+// The totals are of p_t alone, in fp32.
+#pragma once
+#include <cstdint>
+#include "attn_decode.cuh"
+#include "attn_prompt.cuh"
+#include "kv_q8.cuh"
+
+namespace rnn {
+
+constexpr int kQ8Keys = 32;  // keys per warp and tile, the lanes of a warp
+template <int kDP>
+struct DecQ8Shape {
+  static constexpr int kTile = kDecWarps * kQ8Keys;
+  static constexpr int kStageBytes = 2 * kQ8Keys * kDP + kQ8Keys * 8;  // K, V, scales
+  static constexpr int kStages = 384 / kDP;                            // 25 KB a warp
+  static constexpr int kMergeRow = kDP + 4;
+  static constexpr int kMergeBytes = 2 * 8 * kMergeRow * 4;
+  static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes + kMergeBytes +
+                                  kDecWarps * kDecRows * 8 + kDecWarps * kStages * 4;
+};
+
+// 8 bytes to shared memory; with `live` false they are zeroed and nothing is read.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+// The two codes of a half word as fp16; kHigh: of the upper half.  int8 codes come with
+// their sign bits flipped (q8_raw).
+template <int kFmt>
+__device__ __forceinline__ uint32_t q8_raw(uint32_t w) {
+  return kFmt == kInt8 ? w ^ 0x80808080u : w;
+}
+template <int kFmt, bool kHigh>
+__device__ __forceinline__ uint32_t q8_halves(uint32_t w) {
+  uint32_t r;
+  if constexpr (kFmt == kE4m3) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(kHigh ? w >> 16 : w)));
+  } else {
+    const uint32_t m = __byte_perm(w, 0x64646464u, kHigh ? 0x4342 : 0x4140);  // 1024 + byte
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64806480u));      // 1024 + 128
+  }
+  return r;
+}
+
+template <bool kBf16, int kFmt, int kDP, int kNT, bool kLong>
+__global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const DecodeParams p) {
+  using S = DecQ8Shape<kDP>;
+  constexpr int kStages = S::kStages;
+  constexpr int kMT = kQ8Keys / 16;      // 16-key groups
+  constexpr int kSteps = kDP / 16;       // depth steps of K Q^T, channel pairs of V^T P^T
+  constexpr int kChunks = kDP / 16;      // 16-byte chunks of a row
+  constexpr int kRowsPer = 32 / kChunks; // rows moved by one warp-wide copy
+  constexpr int kLaneCh = kDP / 8;       // a lane's channels of a value row
+  constexpr float kWeightTop = 32768.f, kWeightAim = 64.f;
+  extern __shared__ __align__(128) uint8_t dec_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = smem_u32(dec_smem) + warp * kStages * S::kStageBytes;
+  float* merge = reinterpret_cast<float*>(dec_smem + kDecWarps * kStages * S::kStageBytes);
+  float2* ml = reinterpret_cast<float2*>(merge + 2 * 8 * S::kMergeRow);  // [warp][16]
+  uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
+
+  const int Hv = p.Hkv * p.hblocks;
+  DecCursor ld, cur;
+  int64_t hi, total, grid;
+  if (!dec_begin<S::kTile>(p, warp, lane, ld, hi, total, grid)) return;
+  cur = ld;
+  auto advance = [&](DecCursor& k) { dec_advance<S::kTile>(p, Hv, k); };
+  // Page of key `lane` of a tile, -1 where there is none.
+  auto page_of = [&](const DecCursor& k) -> int {
+    const int t = k.j * S::kTile + warp * kQ8Keys + lane;
+    if (t >= k.len) return -1;
+    const int id = __ldg(p.table + k.b * p.table_bs + fdiv(t, p.page));
+    return (id >= 0 && id < p.num_pages) ? id : -1;
+  };
+  // Where chunk ch of row r lies, so that eight lanes that read together (two key rows,
+  // or two chunks of every second value row) meet no bank twice.
+  auto k_at = [](int r, int ch) {
+    return r * kDP + ((kDP == 128 ? ch ^ ((r & 1) << 2) : ch) << 4);
+  };
+  auto v_at = [](int r, int ch) {
+    return r * kDP + ((kDP == 128 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ (((r >> 2) & 1) << 1)) << 4);
+  };
+  const int ch = lane % kChunks, sub = lane / kChunks;
+  const int ch_bytes = p.d - ch * 16;  // live bytes of this lane's chunk
+  auto copy = [&](uint32_t dst, const uint8_t* src, const uint8_t* none, bool live) {
+    if (p.wide) {
+      live = live && ch_bytes > 0;
+      cp_async16(dst, live ? src : none, live);
+    } else {
+      const bool a = live && ch_bytes > 0, b = live && ch_bytes > 8;
+      cp_async8(dst, a ? src : none, a);
+      cp_async8(dst + 8, b ? src + 8 : none, b);
+    }
+  };
+  auto issue = [&](int stage, const DecCursor& k, int id) {
+    const int t0 = k.j * S::kTile + warp * kQ8Keys;
+    const int hk = p.hblocks == 1 ? k.h : k.h / p.hblocks;
+    const unsigned valid = __ballot_sync(0xffffffffu, id >= 0);
+    if (lane == 0) masks[stage] = valid;
+    const uint32_t dst = ring + stage * S::kStageBytes, vdst = dst + kQ8Keys * kDP;
+    const int t = t0 + lane;
+    const int my_row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
+    const float* sc = p.scales + (id * p.s_ps + hk * p.s_hs + 2 * my_row);
+    cp_async8(vdst + kQ8Keys * kDP + lane * 8, id >= 0 ? sc : p.scales, id >= 0);
+    if (p.page16) {
+      // pages are whole 16-key groups: one base per group, no shuffles per row
+#pragma unroll
+      for (int g = 0; g < kMT; ++g) {
+        const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
+        const int row = __shfl_sync(0xffffffffu, my_row, g * 16) + sub;
+        const uint8_t* ks = p.kc8 + (page * p.k_ps + hk * p.k_hs + row * p.k_ts + ch * 16);
+        const uint8_t* vs = p.vc8 + (page * p.v_ps + hk * p.v_hs + row * p.v_ts + ch * 16);
+#pragma unroll
+        for (int i = 0; i < 16 / kRowsPer; ++i) {
+          const int r = g * 16 + i * kRowsPer + sub;
+          const bool live = (valid >> r) & 1u;
+          copy(dst + k_at(r, ch), ks, p.kc8, live);
+          copy(vdst + v_at(r, ch), vs, p.vc8, live);
+          ks += kRowsPer * p.k_ts;
+          vs += kRowsPer * p.v_ts;
+        }
+      }
+      return;
+    }
+    const int64_t ko = id * p.k_ps + my_row * p.k_ts + hk * p.k_hs;
+    const int64_t vo = id * p.v_ps + my_row * p.v_ts + hk * p.v_hs;
+#pragma unroll
+    for (int i = 0; i < kQ8Keys / kRowsPer; ++i) {
+      const int r = i * kRowsPer + sub;
+      const int64_t k_off = __shfl_sync(0xffffffffu, ko, r);
+      const int64_t v_off = __shfl_sync(0xffffffffu, vo, r);
+      const bool live = (valid >> r) & 1u;
+      copy(dst + k_at(r, ch), p.kc8 + k_off + ch * 16, p.kc8, live);
+      copy(vdst + v_at(r, ch), p.vc8 + v_off + ch * 16, p.vc8, live);
+    }
+  };
+
+  int fill = 0, stage = 0;  // ring places of the next load and of the current tile
+  int next_id = page_of(ld);
+  auto issue_next = [&]() {
+    if (ld.at < hi) {
+      const DecCursor now = ld;
+      const int id = next_id;
+      advance(ld);
+      if (ld.at < hi) next_id = page_of(ld);  // the next tile's pages are looked up a tile ahead
+      issue(fill, now, id);
+    }
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages - 1; ++s) issue_next();
+
+  const int g = lane >> 2, q = lane & 3, q2 = q * 2;
+  uint32_t qf[kNT][kSteps][2];
+  float o[kNT][kSteps][4];   // channel kLaneCh g + 2 c (+ 1 in 2, 3), head 8 n + 2 q (+ 1 in 1, 3)
+  float ch_scale[kNT][2];    // of those heads: scale * log2(e) / the queries' factor
+  float m[kNT][2], l[kNT][2], f[kNT][2];
+  constexpr int kSums = kNT * kSteps * 4, kHoldTiles = kDecHoldKeys / kQ8Keys;
+  volatile float held[kSums + 6 * kNT];  // sums taken out, their totals, references, factors
+  bool any_held = false;
+  int until = kHoldTiles;
+  auto add_held = [&]() {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = held[kSums + 2 * kNT + 2 * n + e];
+        const float a = ref == kNegInf ? 0.f : exp2_approx(ref - m[n][e]);
+        const float b = a * f[n][e] / held[kSums + 4 * kNT + 2 * n + e];
+        l[n][e] = fmaf(held[kSums + 2 * n + e], a, l[n][e]);
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+          for (int h = e; h < 4; h += 2)
+            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], b, o[n][c][h]);
+      }
+  };
+  bool fresh = true;
+  bool whole = cur.j == 0;   // the pair started in this share
+#pragma unroll 1
+  while (cur.at < hi) {
+    const int hk = p.hblocks == 1 ? cur.h : cur.h / p.hblocks, hb = cur.h - hk * p.hblocks;
+    const int rows = min(kDecRows, p.group - hb * kDecRows);
+    const int head0 = hk * p.group + hb * kDecRows;
+    if (fresh) {  // under the wait for the first tile
+      const uint16_t* qb = p.q + cur.b * p.q_bs;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const bool row_live = n * 8 + g < rows;
+        const uint16_t* qr = qb + (head0 + (row_live ? n * 8 + g : 0)) * p.q_hs;
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const int c = (s >> 2) * 64 + 16 * q + (s & 3) * 4;
+          const uint2 w = row_live && c < p.d ? *reinterpret_cast<const uint2*>(qr + c)
+                                              : make_uint2(0u, 0u);
+          qf[n][s][0] = w.x, qf[n][s][1] = w.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack2<kBf16>(qf[n][s][e]);
+            top = max(top, max(__float_as_uint(x.x) & 0x7FFFFFFFu,
+                               __float_as_uint(x.y) & 0x7FFFFFFFu));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest magnitude to [2^14, 2^15); below 2^-112 to what 2^126 makes of it
+        const int k = min(126, 14 + 127 - static_cast<int>(top >> 23));
+        const float to = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack2<kBf16>(qf[n][s][e]);
+            qf[n][s][e] = pack2<false>(x.x * to, x.y * to);
+          }
+        const float back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ch_scale[n][e] = __shfl_sync(0xffffffffu, back, (q2 + e) * 4) * p.c;
+          m[n][e] = kNegInf;
+          l[n][e] = 0.f;
+          f[n][e] = 1.f;
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][s][e] = 0.f;
+      }
+      fresh = false;
+    }
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    issue_next();
+    const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + kQ8Keys * kDP;
+    const uint32_t sb = vb + kQ8Keys * kDP;
+    const uint32_t valid = masks[stage];
+    if (valid) {
+      float s[kMT][kNT][4];
+      float vscale[kMT][2];
+#pragma unroll
+      for (int t = 0; t < kMT; ++t) {
+        // two chains of products per score tile, added at the end
+        float s1[kNT][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][n][e] = s1[n][e] = 0.f;
+        const int ra = t * 16 + g, rb = ra + 8;
+#pragma unroll
+        for (int hh = 0; hh < kDP / 64; ++hh) {
+          const uint4 wa = lds_v4(kb + k_at(ra, hh * 4 + q)), wb = lds_v4(kb + k_at(rb, hh * 4 + q));
+          const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            const uint32_t x = q8_raw<kFmt>(a[st]), y = q8_raw<kFmt>(b[st]);
+            const uint32_t frag[4] = {q8_halves<kFmt, false>(x), q8_halves<kFmt, false>(y),
+                                      q8_halves<kFmt, true>(x), q8_halves<kFmt, true>(y)};
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              mma_16816<false>(st & 1 ? s1[n] : s[t][n], frag, qf[n][hh * 4 + st][0],
+                               qf[n][hh * 4 + st][1]);
+          }
+        }
+        const float2 sa = lds_f2(sb + ra * 8), sc = lds_f2(sb + rb * 8);
+        vscale[t][0] = sa.y, vscale[t][1] = sc.y;
+        const bool in_a = (valid >> ra) & 1u, in_b = (valid >> rb) & 1u;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[t][n][e] = in_a ? (s[t][n][e] + s1[n][e]) * (sa.x * ch_scale[n][e]) : kNegInf;
+            s[t][n][e + 2] =
+                in_b ? (s[t][n][e + 2] + s1[n][e + 2]) * (sc.x * ch_scale[n][e]) : kNegInf;
+          }
+      }
+      // ---- the softmax's reference, and p = 2^(score - reference)
+      float x[kNT][2], shrink[kNT][2];
+      bool up = false;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+          for (int t = 1; t < kMT; ++t) x[n][e] = fmax3(x[n][e], s[t][n][e], s[t][n][e + 2]);
+          up = up || x[n][e] - m[n][e] > kDecSlack;  // also from -inf to a number
+          shrink[n][e] = 1.f;
+        }
+      const bool moved = __any_sync(0xffffffffu, up);
+      if (moved) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = x[n][e];
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            y = fmaxf(y, m[n][e]);
+            shrink[n][e] = m[n][e] == kNegInf ? 0.f : exp2_approx(m[n][e] - y);
+            m[n][e] = y;
+            l[n][e] *= shrink[n][e];
+          }
+      }
+      bool over = moved;
+      float top[kNT][2];  // largest weight p vs
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float z = m[n][e] == kNegInf ? 0.f : m[n][e];
+          top[n][e] = 0.f;
+#pragma unroll
+          for (int t = 0; t < kMT; ++t) {
+            const float a = exp2_approx(s[t][n][e] - z), b = exp2_approx(s[t][n][e + 2] - z);
+            l[n][e] += a + b;
+            s[t][n][e] = a * vscale[t][0];
+            s[t][n][e + 2] = b * vscale[t][1];
+            top[n][e] = fmax3(top[n][e], s[t][n][e], s[t][n][e + 2]);
+          }
+          over = over || top[n][e] * f[n][e] > kWeightTop;
+        }
+      // ---- the weights' factor
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = top[n][e];
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            // the largest weight before is kWeightAim * shrink / f
+            y = fminf(kWeightAim / y, f[n][e] / shrink[n][e]);
+            y = fminf(fmaxf(y, kQ8MinScale), 1.329227996e36f);  // 2^-126 to 2^120
+            y = __uint_as_float(__float_as_uint(y) & 0x7F800000u);
+            const float a = shrink[n][e] * y / f[n][e];
+            f[n][e] = y;
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c) {
+              o[n][c][e] *= a;
+              o[n][c][e + 2] *= a;
+            }
+          }
+      }
+      uint32_t pf[kMT][kNT][2];
+#pragma unroll
+      for (int t = 0; t < kMT; ++t)
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          // weights round to fp16 for the second product (half a step: 2^-12)
+          pf[t][n][0] = movmatrix_t(pack2<false>(s[t][n][0] * f[n][0], s[t][n][1] * f[n][1]));
+          pf[t][n][1] = movmatrix_t(pack2<false>(s[t][n][2] * f[n][0], s[t][n][3] * f[n][1]));
+        }
+#pragma unroll
+      for (int t = 0; t < kMT; ++t) {
+        const int r = t * 16 + q2;
+        constexpr int kWords = kLaneCh / 4;
+        uint32_t w[4][kWords];  // rows r, r + 1, r + 8, r + 9
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = r + (i & 1) + (i >> 1) * 8;
+          if constexpr (kDP == 128) {
+            const uint4 v = lds_v4(vb + v_at(row, g));
+            w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+          } else {
+            const float2 v = lds_f2(vb + v_at(row, g >> 1) + (g & 1) * 8);
+            w[i][0] = __float_as_uint(v.x), w[i][1] = __float_as_uint(v.y);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // codes of channels 2 h, 2 h + 1 of a word, key by key
+            const uint32_t x = q8_raw<kFmt>(__byte_perm(w[0][j], w[1][j], h ? 0x7362 : 0x5140));
+            const uint32_t y = q8_raw<kFmt>(__byte_perm(w[2][j], w[3][j], h ? 0x7362 : 0x5140));
+            const uint32_t frag[4] = {q8_halves<kFmt, false>(x), q8_halves<kFmt, true>(x),
+                                      q8_halves<kFmt, false>(y), q8_halves<kFmt, true>(y)};
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              mma_16816<false>(o[n][2 * j + h], frag, pf[t][n][0], pf[t][n][1]);
+          }
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    const bool last = cur.j == cur.n - 1;
+    if (kLong && --until == 0) {
+      if (any_held) add_held();
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          held[kSums + 2 * n + e] = l[n][e];
+          held[kSums + 2 * kNT + 2 * n + e] = m[n][e];
+          held[kSums + 4 * kNT + 2 * n + e] = f[n][e];
+          l[n][e] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+            for (int h = e; h < 4; h += 2) {
+              held[(n * kSteps + c) * 4 + h] = o[n][c][h];
+              o[n][c][h] = 0.f;
+            }
+        }
+      any_held = true;
+      until = kHoldTiles;
+    }
+    if (last || cur.at + 1 >= hi) {
+      if (kLong) {
+        if (any_held) add_held();
+        any_held = false;
+        until = kHoldTiles;
+      }
+      // ---- the pair ends here, or goes on in the next share
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = l[n][e];
+          y += __shfl_xor_sync(0xffffffffu, y, 4);
+          y += __shfl_xor_sync(0xffffffffu, y, 8);
+          y += __shfl_xor_sync(0xffffffffu, y, 16);
+          if (g == 0) ml[warp * kDecRows + n * 8 + q2 + e] = make_float2(m[n][e], y);
+        }
+      __syncthreads();
+      const bool done = whole && last;
+      // a pair that began in an earlier share fills slot 0, one that goes on slot 1
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (whole ? 1 : 0);
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        if (n * 8 >= rows) break;
+        float r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float M = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + n * 8 + q2 + e].x);
+          r[e] = m[n][e] == kNegInf ? 0.f : exp2_approx(m[n][e] - M) / f[n][e];
+        }
+        float* buf = merge + (warp & 1) * 8 * S::kMergeRow;
+        auto each = [&](auto&& op) {
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              op(buf[(q2 + (e & 1)) * S::kMergeRow + kLaneCh * g + 2 * c + (e >> 1)], o[n][c][e],
+                 r[e & 1]);
+        };
+        if (warp >= 2) each([](float& to, float a, float b) { to = a * b; });
+        __syncthreads();
+        if (warp < 2) each([](float& to, float a, float b) { to = fmaf(a, b, to); });
+        __syncthreads();
+        for (int i = warp; i < 8 && n * 8 + i < rows; i += kDecWarps) {
+          const int row = n * 8 + i;
+          float M = kNegInf, L = 0.f;
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + row].x);
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float2 a = ml[w * kDecRows + row];
+            // without a reference the total is 0, or NaN if its scores were
+            L += a.x == kNegInf ? a.y : a.y * exp2_approx(a.x - M);
+          }
+          const float inv = L != 0.f ? 1.f / L : 0.f;
+          const float* b0 = merge + i * S::kMergeRow;
+          const float* b1 = b0 + 8 * S::kMergeRow;
+          if (done) {
+            uint16_t* ob = p.out + cur.b * p.o_bs + (head0 + row) * p.o_hs;
+            for (int c = lane * 2; c < p.d; c += 64)
+              *reinterpret_cast<uint32_t*>(ob + c) =
+                  pack2<kBf16>((b0[c] + b1[c]) * inv, (b0[c + 1] + b1[c + 1]) * inv);
+            if (p.lse && lane == 0)
+              p.lse[static_cast<int64_t>(cur.b) * p.Hq + head0 + row] =
+                  L != 0.f ? (M + log2f(L)) * 0.69314718f : kNegInf;
+          } else {
+            float* pb = p.part + (slot * kDecRows + row) * kDP;
+            for (int c = lane * 2; c < kDP; c += 64)
+              *reinterpret_cast<float2*>(pb + c) =
+                  make_float2(b0[c] + b1[c], b0[c + 1] + b1[c + 1]);
+            if (lane == 0) p.part_ml[slot * kDecRows + row] = make_float2(M, L);
+          }
+        }
+        if (n + 1 < kNT) __syncthreads();  // the next heads reuse the buffer
+      }
+      if (whole && threadIdx.x == 0) {
+        int c1 = blockIdx.x;
+        if (!last) c1 = dec_owner(cur.at + (cur.n - 1 - cur.j), total, grid);
+        p.span[static_cast<int64_t>(cur.b) * Hv + cur.h] = make_int2(blockIdx.x, c1);
+      }
+      __syncthreads();  // the next pair's totals and sums come behind these reads
+      fresh = true;
+      whole = true;
+    }
+    advance(cur);
+  }
+  cp_async_wait<0>();
+}
+
+}  // namespace rnn

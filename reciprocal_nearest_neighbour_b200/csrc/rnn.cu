@@ -63,7 +63,7 @@ struct DeviceInfo {
   bool sm100 = false;
   bool smem_set = false;
   bool op_smem_set = false;  // one-pass exhaustive-set kernels
-  bool attn_smem_set = false;
+  bool attn_smem_set = false, attn_q8_smem_set = false;
 };
 
 static std::mutex g_mu;
@@ -1466,6 +1466,8 @@ __global__ void frm_emit_kernel(FrmState st, int32_t* pairs, int64_t cap, int32_
 #include "attn_decode.cuh"
 #include "attn_prompt.cuh"
 #include "kv_append.cuh"
+#include "kv_q8.cuh"
+#include "attn_decode_q8.cuh"
 
 namespace rnn {
 
@@ -3178,7 +3180,7 @@ static rnn_status decode_launch(const DecodeParams& p, dim3 grid, cudaStream_t s
          : attn_decode_kernel<kBf16, kDP, 2, false><<<grid, block, sm, s>>>(p);
   const rnn_status r = launched();
   if (r != RNN_OK) return r;
-  launch_k(attn_decode_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
+  launch_k(attn_decode_join_kernel<kBf16, kDP, kBf16 ? 0 : 7>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
            0, s, true, p);
   return launched();
 }
@@ -3404,6 +3406,330 @@ rnn_status rnn_kv_append(const rnn_kv_append_args* args, rnn_stream_t stream) {
   if (dtype == RNN_BF16) kv_append_launch<true>(p, vec, grid, smem, s);
   else kv_append_launch<false>(p, vec, grid, smem, s);
   return launched();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the cache in 8-bit codes
+static rnn_status check_scales(rnn_scales* c, int64_t num_pages, int page_size, int heads) {
+  const int64_t row = 2 * static_cast<int64_t>(page_size);
+  if (!c->data || (reinterpret_cast<uintptr_t>(c->data) & 7u)) return RNN_EINVAL;
+  c->head_stride = stride_or(heads, c->head_stride, row);
+  c->page_stride = stride_or(num_pages, c->page_stride, row);
+  if (c->head_stride < row || c->page_stride < row) return RNN_EINVAL;
+  return c->head_stride % 2 || c->page_stride % 2 ? RNN_EALIGN : RNN_OK;
+}
+static bool valid_codes(int codes) { return codes == RNN_CODES_E4M3 || codes == RNN_CODES_INT8; }
+
+// What appends and reads share: sizes, and that what a call needs is there.
+static rnn_status check_cache_call(int64_t T, int B, int Hkv, int d, int dtype, int64_t num_pages,
+                                   int page_size, int max_pages, int64_t table_stride,
+                                   const int32_t* page_table, const int32_t* cu) {
+  if (T < 0 || T > INT32_MAX || B < 0 || B == INT32_MAX || Hkv < 1 || num_pages < 1 ||
+      num_pages > INT32_MAX || page_size < 1 || max_pages < 1 || table_stride < 0 || d < 1 ||
+      !valid_dtype(static_cast<rnn_dtype>(dtype)))
+    return RNN_EINVAL;
+  if (d % 8) return RNN_EALIGN;
+  if (d > 256 || Hkv > RNN_ATTN_MAX_HEADS || B > INT32_MAX - 1024 || T > INT32_MAX - 1024)
+    return RNN_EUNSUPPORTED;
+  if ((B > 0 && (!page_table || !cu)) || !aligned4(page_table) || !aligned4(cu)) return RNN_EINVAL;
+  return RNN_OK;
+}
+
+// Warps that share a token, log2: up to 8, while all of them fit on the GPU at once.
+static int token_share(int64_t T, int sms) {
+  int share = 0;
+  while (share < 3 && (T << (share + 1)) <= 16 * sms) ++share;
+  return share;
+}
+
+template <bool kBf16, int kFmt>
+static void append_q8_launch(const AppendQ8Params& p, int vec, dim3 grid, size_t smem, cudaStream_t s) {
+  const dim3 block(kQ8Warps * 32);
+  if (vec == 8) kv_append_q8_kernel<kBf16, kFmt, 8><<<grid, block, smem, s>>>(p);
+  else if (vec == 4) kv_append_q8_kernel<kBf16, kFmt, 4><<<grid, block, smem, s>>>(p);
+  else if (vec == 2) kv_append_q8_kernel<kBf16, kFmt, 2><<<grid, block, smem, s>>>(p);
+  else kv_append_q8_kernel<kBf16, kFmt, 1><<<grid, block, smem, s>>>(p);
+}
+
+template <bool kBf16, int kFmt, int kDP>
+static rnn_status decode_q8_launch(const DecodeParams& p, dim3 grid, cudaStream_t s) {
+  const dim3 block(kDecWarps * 32);
+  const size_t sm = DecQ8Shape<kDP>::kSmem;
+  const bool many = static_cast<int64_t>(p.max_pages) * p.page.div > kDecShortKeys;
+  if (p.group <= 8)
+    many ? attn_decode_q8_kernel<kBf16, kFmt, kDP, 1, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_q8_kernel<kBf16, kFmt, kDP, 1, false><<<grid, block, sm, s>>>(p);
+  else
+    many ? attn_decode_q8_kernel<kBf16, kFmt, kDP, 2, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_q8_kernel<kBf16, kFmt, kDP, 2, false><<<grid, block, sm, s>>>(p);
+  const rnn_status r = launched();
+  if (r != RNN_OK) return r;
+  DecodeParams j = p;   // these parts' maxima are scaled already, in log2
+  j.c = 1.f;
+  j.scale = 0.69314718f;
+  launch_k(attn_decode_join_kernel<kBf16, kDP, 0>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
+           0, s, true, j);
+  return launched();
+}
+template <int kDP>
+static rnn_status decode_q8_dispatch(const DecodeParams& p, bool bf, bool int8, dim3 grid,
+                                     cudaStream_t s) {
+  if (int8)
+    return bf ? decode_q8_launch<true, kInt8, kDP>(p, grid, s)
+              : decode_q8_launch<false, kInt8, kDP>(p, grid, s);
+  return bf ? decode_q8_launch<true, kE4m3, kDP>(p, grid, s)
+            : decode_q8_launch<false, kE4m3, kDP>(p, grid, s);
+}
+template <int kDP>
+static bool decode_q8_smem() {
+  const auto set = [](auto... kernels) {
+    return ((cudaFuncSetAttribute(kernels, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(DecQ8Shape<kDP>::kSmem)) == cudaSuccess) && ...);
+  };
+  return set(attn_decode_q8_kernel<true, kE4m3, kDP, 1, false>, attn_decode_q8_kernel<true, kE4m3, kDP, 1, true>,
+             attn_decode_q8_kernel<true, kE4m3, kDP, 2, false>, attn_decode_q8_kernel<true, kE4m3, kDP, 2, true>,
+             attn_decode_q8_kernel<false, kE4m3, kDP, 1, false>, attn_decode_q8_kernel<false, kE4m3, kDP, 1, true>,
+             attn_decode_q8_kernel<false, kE4m3, kDP, 2, false>, attn_decode_q8_kernel<false, kE4m3, kDP, 2, true>,
+             attn_decode_q8_kernel<true, kInt8, kDP, 1, false>, attn_decode_q8_kernel<true, kInt8, kDP, 1, true>,
+             attn_decode_q8_kernel<true, kInt8, kDP, 2, false>, attn_decode_q8_kernel<true, kInt8, kDP, 2, true>,
+             attn_decode_q8_kernel<false, kInt8, kDP, 1, false>, attn_decode_q8_kernel<false, kInt8, kDP, 1, true>,
+             attn_decode_q8_kernel<false, kInt8, kDP, 2, false>, attn_decode_q8_kernel<false, kInt8, kDP, 2, true>);
+}
+static rnn_status decode_q8_setup(DeviceInfo* di) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (di->attn_q8_smem_set) return RNN_OK;
+  if (!decode_q8_smem<64>() || !decode_q8_smem<128>()) return RNN_ECUDA;
+  di->attn_q8_smem_set = true;
+  return RNN_OK;
+}
+
+extern "C" {
+
+rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_kv_append_q8");
+  if (!args) return RNN_EINVAL;
+  rnn_kv_append_q8_args a = *args;
+  const int64_t T = a.T;
+  const int Hq = a.Hq, Hkv = a.Hkv, d = a.d, pairs = a.pairs, axes = a.axes;
+  if (Hq < 0 || !valid_codes(a.codes)) return RNN_EINVAL;
+  rnn_status r = check_cache_call(T, a.B, Hkv, d, a.dtype, a.num_pages, a.page_size, a.max_pages,
+                                  a.table_stride, a.page_table, a.cu);
+  if (r != RNN_OK) return r;
+  if (Hq > RNN_ATTN_MAX_HEADS) return RNN_EUNSUPPORTED;
+  if (pairs < 0 || axes < 0 || axes > 2 || (pairs == 0) != (axes == 0) || 2 * pairs * axes > d ||
+      (pairs > 0 && !a.inv_freq) || (axes == 2 && !a.positions) ||
+      (a.positions && T > 1 && a.position_stride < axes))
+    return RNN_EINVAL;
+  if ((a.B > 0 && !a.start) || !aligned4(a.start) || !aligned4(a.positions) ||
+      (reinterpret_cast<uintptr_t>(a.inv_freq) & 7u))
+    return RNN_EINVAL;
+  if ((r = check_rows(&a.k, T, Hkv, d)) != RNN_OK || (r = check_rows(&a.v, T, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&a.k_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&a.v_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK ||
+      (r = check_scales(&a.scales, a.num_pages, a.page_size, Hkv)) != RNN_OK)
+    return r;
+  if (Hq > 0 && ((r = check_rows(&a.q, T, Hq, d)) != RNN_OK ||
+                 (r = check_written_rows(&a.q_out, T, Hq, d)) != RNN_OK))
+    return r;
+  if (a.k_out.data && (r = check_written_rows(&a.k_out, T, Hkv, d)) != RNN_OK) return r;
+  // in place only as q in q and k in k: other rows are read while these are written
+  if (T > 0 && ((Hq > 0 && (a.q_out.data == a.k.data || a.q_out.data == a.v.data)) ||
+                (a.k_out.data && (a.k_out.data == a.v.data ||
+                                  (Hq > 0 && (a.k_out.data == a.q.data || a.k_out.data == a.q_out.data))))))
+    return RNN_EINVAL;
+  // rows rotated in place are read where they are written
+  const auto moved = [&](const rnn_rows& x, const rnn_rows& y) {
+    return x.data == y.data && (x.token_stride != y.token_stride || x.head_stride != y.head_stride);
+  };
+  if (T > 0 && ((Hq > 0 && moved(a.q, a.q_out)) || (a.k_out.data && moved(a.k, a.k_out))))
+    return RNN_EINVAL;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK) return r;
+  if (T == 0 || a.B == 0) return RNN_OK;
+  AppendQ8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(a.q.data);
+  p.k = static_cast<const uint16_t*>(a.k.data);
+  p.v = static_cast<const uint16_t*>(a.v.data);
+  p.q_out = static_cast<uint16_t*>(a.q_out.data);
+  p.k_out = static_cast<uint16_t*>(a.k_out.data);
+  p.kc = static_cast<uint8_t*>(a.k_cache.data);
+  p.vc = static_cast<uint8_t*>(a.v_cache.data);
+  p.scales = a.scales.data;
+  p.q_ts = a.q.token_stride, p.q_hs = a.q.head_stride;
+  p.k_ts = a.k.token_stride, p.k_hs = a.k.head_stride;
+  p.v_ts = a.v.token_stride, p.v_hs = a.v.head_stride;
+  p.qo_ts = a.q_out.token_stride, p.qo_hs = a.q_out.head_stride;
+  p.ko_ts = a.k_out.token_stride, p.ko_hs = a.k_out.head_stride;
+  p.kc_ps = a.k_cache.page_stride, p.kc_ts = a.k_cache.token_stride, p.kc_hs = a.k_cache.head_stride;
+  p.vc_ps = a.v_cache.page_stride, p.vc_ts = a.v_cache.token_stride, p.vc_hs = a.v_cache.head_stride;
+  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
+  p.table = a.page_table;
+  p.start = a.start;
+  p.cu = a.cu;
+  p.positions = a.positions;
+  p.table_bs = a.table_stride;
+  p.pos_ts = a.position_stride;
+  p.num_pages = a.num_pages;
+  p.inv_freq = a.inv_freq;
+  p.T = static_cast<int>(T);
+  p.B = a.B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.pairs = pairs;
+  p.axes = axes;
+  p.paired = a.paired != 0;
+  p.share = token_share(T, di->sms);
+  while ((8 << p.row_lanes) < d) ++p.row_lanes;
+  const int vec = p.paired || pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
+  const dim3 grid(static_cast<unsigned>(((T << p.share) + kQ8Warps - 1) / kQ8Warps));
+  // (each warp's turns start on 16 bytes)
+  const size_t smem = static_cast<size_t>(kQ8Warps) * ((axes * pairs + 1) & ~1) * sizeof(float2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = a.dtype == RNN_BF16;
+  if (a.codes == RNN_CODES_INT8)
+    bf ? append_q8_launch<true, kInt8>(p, vec, grid, smem, s) : append_q8_launch<false, kInt8>(p, vec, grid, smem, s);
+  else
+    bf ? append_q8_launch<true, kE4m3>(p, vec, grid, smem, s) : append_q8_launch<false, kE4m3>(p, vec, grid, smem, s);
+  return launched();
+}
+
+rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args* args, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_kv_read_q8");
+  if (!args) return RNN_EINVAL;
+  rnn_kv_read_q8_args a = *args;
+  if (!valid_codes(a.codes)) return RNN_EINVAL;
+  rnn_status r = check_cache_call(a.T, a.B, a.Hkv, a.d, a.dtype, a.num_pages, a.page_size, a.max_pages,
+                                  a.table_stride, a.page_table, a.cu);
+  if (r != RNN_OK) return r;
+  if (!aligned4(a.start)) return RNN_EINVAL;
+  if ((r = check_written_rows(&a.k, a.T, a.Hkv, a.d)) != RNN_OK ||
+      (r = check_written_rows(&a.v, a.T, a.Hkv, a.d)) != RNN_OK ||
+      (r = check_pages(&a.k_cache, a.num_pages, a.page_size, a.Hkv, a.d)) != RNN_OK ||
+      (r = check_pages(&a.v_cache, a.num_pages, a.page_size, a.Hkv, a.d)) != RNN_OK ||
+      (r = check_scales(&a.scales, a.num_pages, a.page_size, a.Hkv)) != RNN_OK)
+    return r;
+  if (a.T > 0 && a.k.data == a.v.data) return RNN_EINVAL;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK) return r;
+  if (a.T == 0 || a.B == 0) return RNN_OK;
+  ReadQ8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.kc = static_cast<const uint8_t*>(a.k_cache.data);
+  p.vc = static_cast<const uint8_t*>(a.v_cache.data);
+  p.scales = a.scales.data;
+  p.k = static_cast<uint16_t*>(a.k.data);
+  p.v = static_cast<uint16_t*>(a.v.data);
+  p.kc_ps = a.k_cache.page_stride, p.kc_ts = a.k_cache.token_stride, p.kc_hs = a.k_cache.head_stride;
+  p.vc_ps = a.v_cache.page_stride, p.vc_ts = a.v_cache.token_stride, p.vc_hs = a.v_cache.head_stride;
+  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
+  p.k_ts = a.k.token_stride, p.k_hs = a.k.head_stride;
+  p.v_ts = a.v.token_stride, p.v_hs = a.v.head_stride;
+  p.table = a.page_table;
+  p.start = a.start;
+  p.cu = a.cu;
+  p.table_bs = a.table_stride;
+  p.num_pages = a.num_pages;
+  p.T = static_cast<int>(a.T);
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.d = a.d;
+  p.max_pages = a.max_pages;
+  p.page_size = a.page_size;
+  p.share = token_share(a.T, di->sms);
+  p.by_row = make_fastdiv(a.d / 8);
+  const dim3 grid(static_cast<unsigned>(((a.T << p.share) + kQ8Warps - 1) / kQ8Warps)), block(kQ8Warps * 32);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = a.dtype == RNN_BF16;
+  if (a.codes == RNN_CODES_INT8)
+    bf ? kv_read_q8_kernel<true, kInt8><<<grid, block, 0, s>>>(p) : kv_read_q8_kernel<false, kInt8><<<grid, block, 0, s>>>(p);
+  else
+    bf ? kv_read_q8_kernel<true, kE4m3><<<grid, block, 0, s>>>(p) : kv_read_q8_kernel<false, kE4m3><<<grid, block, 0, s>>>(p);
+  return launched();
+}
+
+size_t rnn_attn_decode_q8_workspace_size(int B, int Hq, int Hkv, int d) {
+  return rnn_attn_decode_workspace_size(B, Hq, Hkv, d);
+}
+
+rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_attn_decode_q8");
+  if (!args) return RNN_EINVAL;
+  rnn_attn_decode_q8_args a = *args;
+  const int B = a.B, Hq = a.Hq, Hkv = a.Hkv, d = a.d;
+  if (B < 0 || a.num_pages < 1 || a.num_pages > INT32_MAX || a.page_size < 1 || a.max_pages < 1 ||
+      a.table_stride < 0 || !valid_codes(a.codes))
+    return RNN_EINVAL;
+  rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, static_cast<rnn_dtype>(a.dtype));
+  if (r != RNN_OK) return r;
+  if (!(a.scale > 0.f) || !(a.scale < 2e38f)) return RNN_EINVAL;
+  if ((B > 0 && (!a.page_table || !a.lens)) || !aligned4(a.page_table) || !aligned4(a.lens) ||
+      !aligned4(a.lse))
+    return RNN_EINVAL;
+  if ((r = check_rows(&a.q, B, Hq, d)) != RNN_OK || (r = check_written_rows(&a.out, B, Hq, d)) != RNN_OK ||
+      (r = check_pages(&a.k_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&a.v_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK ||
+      (r = check_scales(&a.scales, a.num_pages, a.page_size, Hkv)) != RNN_OK)
+    return r;
+  if (B > INT32_MAX - 1024 || static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
+  if (!a.workspace || !aligned256(a.workspace) ||
+      a.ws_bytes < rnn_attn_decode_q8_workspace_size(B, Hq, Hkv, d))
+    return RNN_EWORKSPACE;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK || (r = decode_q8_setup(di)) != RNN_OK) return r;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0) {
+    zero_words_kernel<<<1, 32, 0, s>>>(static_cast<int*>(a.workspace), 1);
+    return launched();
+  }
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  DecWs w;
+  dec_layout(a.workspace, B, Hkv, Hq / Hkv, d, &w);
+  p.q = static_cast<const uint16_t*>(a.q.data);
+  p.kc8 = static_cast<const uint8_t*>(a.k_cache.data);
+  p.vc8 = static_cast<const uint8_t*>(a.v_cache.data);
+  p.scales = a.scales.data;
+  p.out = static_cast<uint16_t*>(a.out.data);
+  p.lse = a.lse;
+  p.q_bs = a.q.token_stride, p.q_hs = a.q.head_stride;
+  p.o_bs = a.out.token_stride, p.o_hs = a.out.head_stride;
+  p.k_ps = a.k_cache.page_stride, p.k_ts = a.k_cache.token_stride, p.k_hs = a.k_cache.head_stride;
+  p.v_ps = a.v_cache.page_stride, p.v_ts = a.v_cache.token_stride, p.v_hs = a.v_cache.head_stride;
+  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
+  p.wide = d % 16 == 0 && (p.k_ps | p.k_ts | p.k_hs | p.v_ps | p.v_ts | p.v_hs) % 16 == 0;
+  p.table = a.page_table;
+  p.lens = a.lens;
+  p.table_bs = a.table_stride;
+  p.num_pages = a.num_pages;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.hblocks = (p.group + kDecRows - 1) / kDecRows;
+  p.d = d;
+  p.max_pages = a.max_pages;
+  p.page = make_fastdiv(a.page_size);
+  p.page16 = a.page_size % 16 == 0;
+  p.scale = a.scale;
+  p.c = a.scale * 1.44269504f;
+  p.part = w.part;
+  p.part_ml = w.ml;
+  p.span = w.span;
+  p.err = w.err;
+  const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
+  const int per_tile = DecQ8Shape<128>::kTile;
+  static_assert(DecQ8Shape<64>::kTile == DecQ8Shape<128>::kTile, "");
+  const int64_t tiles = (keys + per_tile - 1) / per_tile * B * Hkv * p.hblocks;
+  const int most = std::min(2 * di->sms, kDecMaxGrid);
+  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
+  const bool bf = a.dtype == RNN_BF16, int8 = a.codes == RNN_CODES_INT8;
+  return d <= 64 ? decode_q8_dispatch<64>(p, bf, int8, grid, s) : decode_q8_dispatch<128>(p, bf, int8, grid, s);
 }
 
 }  // extern "C"
