@@ -593,6 +593,37 @@ typedef struct rnn_attn_decode_args {
 size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
 rnn_status rnn_attn_decode(const rnn_attn_decode_args *args, rnn_stream_t stream);
 
+/*
+ * rnn_attn_decode for a batch whose sequences all start with the same cached
+ * tokens: each query sees the prefix's rows and the rows of its own sequence
+ * behind them.  The prefix is read once for the batch.
+ *   prefix_pages  [prefix_pages_count] int32, the pages of the prefix;
+ *   prefix_len    one int32 on the device: its tokens (values below 0 count as
+ *                 0, values beyond prefix_pages_count * page_size as that).
+ *   page_table, lens  each sequence's own tokens, the new one included, which
+ *                 start on a page of their own (0: it sees the prefix only).
+ * The rest is as in rnn_attn_decode: keys whose page is outside [0, num_pages)
+ * count as absent, a row without a key gets zeros and -infinity.  Where keys
+ * stand in the sequence (for a rotation) was settled when they were appended.
+ * workspace: rnn_attn_decode_shared_workspace_size bytes with prefix_room =
+ * prefix_pages_count * page_size.  The kernels' waits are bounded;
+ * rnn_workspace_status tells whether one ran out, and the rows concerned are
+ * NaN.  3 kernel launches.
+ */
+typedef struct rnn_attn_decode_shared_args {
+  rnn_rows q, out;
+  rnn_pages k_cache, v_cache;
+  const int32_t *prefix_pages, *prefix_len, *page_table, *lens;
+  float *lse;
+  void *workspace;
+  uint64_t ws_bytes;
+  int64_t num_pages, table_stride;
+  int32_t page_size, prefix_pages_count, max_pages, B, Hq, Hkv, d, dtype;
+  float scale;
+} rnn_attn_decode_shared_args;
+size_t rnn_attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int64_t prefix_room);
+rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args *args, rnn_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * The paged cache in 8-bit codes.
  *

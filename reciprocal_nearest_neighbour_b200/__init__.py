@@ -30,7 +30,8 @@ contiguous fp16/bf16 CUDA tensors; pixel index ``p = y*W + x``.
 * ``kv_append`` / ``attn_prompt`` / ``attn_decode``: the attention steps of the
   network in front of the matching (image tokens, and the memory of earlier
   frames): softmax-weighted sums over the rows of Q K^T instead of their
-  argmax, for packed sequences and over a paged cache.
+  argmax, for packed sequences and over a paged cache.  ``attn_decode_shared``:
+  the latter for a batch whose sequences start with the same cached tokens.
 * ``kv_append_q8`` / ``kv_read_q8`` / ``attn_decode_q8``: that cache in 8-bit
   codes (e4m3 or int8, a scale for each token and head): written, read back
   and attended to.
@@ -56,6 +57,7 @@ __all__ = [
     "RNNLibraryError", "FRMPlan", "frm_match_ex", "frm_refine", "pts_nn", "pts_mnn",
     "pts_frm_match", "c2f_match", "C2FResult", "mnn_mutual", "FRMGraph", "kv_append",
     "attn_prompt", "attn_decode", "kv_append_q8", "kv_read_q8", "attn_decode_q8",
+    "attn_decode_shared",
 ]
 
 _DT = {torch.float16: _lib.RNN_F16, torch.bfloat16: _lib.RNN_BF16}
@@ -602,5 +604,5 @@ def c2f_match(C1: torch.Tensor, C2: torch.Tensor, F1: torch.Tensor, F2: torch.Te
     return out
 
 
-from .attn import attn_decode, attn_prompt, kv_append  # noqa: E402
+from .attn import attn_decode, attn_decode_shared, attn_prompt, kv_append  # noqa: E402
 from .cache_q8 import attn_decode_q8, kv_append_q8, kv_read_q8  # noqa: E402

@@ -60,6 +60,8 @@ EXPORTS = (
     "rnn_kv_read_q8",
     "rnn_attn_decode_q8_workspace_size",
     "rnn_attn_decode_q8",
+    "rnn_attn_decode_shared_workspace_size",
+    "rnn_attn_decode_shared",
 )
 
 STATUS = {
@@ -120,6 +122,14 @@ class AttnDecodeArgs(ctypes.Structure):
     _fields_ = _fields(rows="q out", pages="k_cache v_cache", ptr="page_table lens lse workspace",
                        u64="ws_bytes", i64="num_pages table_stride",
                        i32="page_size max_pages B Hq Hkv d dtype", f32="scale")
+
+
+class AttnDecodeSharedArgs(ctypes.Structure):
+    """``rnn_attn_decode_shared_args``"""
+    _fields_ = _fields(rows="q out", pages="k_cache v_cache",
+                       ptr="prefix_pages prefix_len page_table lens lse workspace", u64="ws_bytes",
+                       i64="num_pages table_stride",
+                       i32="page_size prefix_pages_count max_pages B Hq Hkv d dtype", f32="scale")
 
 
 class KvAppendQ8Args(ctypes.Structure):
@@ -227,6 +237,8 @@ def load():
         "rnn_kv_read_q8": (I, [P, P]),
         "rnn_attn_decode_q8_workspace_size": (SZ, [I, I, I, I]),
         "rnn_attn_decode_q8": (I, [P, P]),
+        "rnn_attn_decode_shared_workspace_size": (SZ, [I, I, I, I, I64]),
+        "rnn_attn_decode_shared": (I, [P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)

@@ -3,7 +3,8 @@
 ``kv_append`` puts new tokens' keys and values into a paged cache (rotating
 keys and queries by their positions), ``attn_prompt`` attends within packed
 sequences, ``attn_decode`` attends from one new token per sequence over the
-cache.  Tensors are fp16 or bf16 CUDA tensors whose last dimension (the
+cache, and ``attn_decode_shared`` also over a prefix that all sequences share.
+Tensors are fp16 or bf16 CUDA tensors whose last dimension (the
 channels of a head) is contiguous; the other dimensions may have any strides
 that are multiples of 8 elements, so slices of a fused projection's output
 pass as they are (no two rows of an output may overlap).  Calls run on the
@@ -28,6 +29,7 @@ _ROWS, _PAGES = "Qqq", "Qqqq"
 _APPEND = struct.Struct("=" + 5 * _ROWS + 2 * _PAGES + "5Q4q10i")
 _PROMPT = struct.Struct("=" + 4 * _ROWS + "4QQ2q6if4x")
 _DECODE = struct.Struct("=" + 2 * _ROWS + 2 * _PAGES + "4QQ2q7if")
+_SHARED = struct.Struct("=" + 2 * _ROWS + 2 * _PAGES + "6QQ2q8if4x")
 
 
 def _check(t, name: str, ndim: int, dtype, device=None) -> None:
@@ -375,4 +377,56 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         *_pages(v_cache, "v_cache", d), page_table.data_ptr(), lens.data_ptr(),
         0 if lse is None else lse.data_ptr(), ws, ws_bytes, num_pages, table_stride, size,
         max_pages, B, hq, hkv, d, _DT[kind], scale))
+    return (out, lse) if with_lse else out
+
+
+@functools.lru_cache(maxsize=256)
+def _shared_need(B: int, hq: int, hkv: int, d: int, room: int) -> int:
+    return _lib.load().rnn_attn_decode_shared_workspace_size(B, hq, hkv, d, room)
+
+
+def attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       prefix_pages: torch.Tensor, prefix_len: torch.Tensor,
+                       page_table: torch.Tensor, lens: torch.Tensor, *,
+                       scale: Optional[float] = None, with_lse: bool = False,
+                       out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """``attn_decode`` for sequences that all start with the same cached tokens.
+
+    The first ``prefix_len`` tokens (int32 ``[1]``) of every sequence are on the
+    pages ``prefix_pages`` (int32 ``[pages]``), and are read once for the batch;
+    behind them sequence ``b`` has ``lens[b]`` tokens of its own (the new one
+    included, or 0) on the pages ``page_table[b]``.  All else is as in
+    ``attn_decode``; a row that sees no key is 0.  ``kv_append`` takes a
+    sequence's own tokens with ``start`` counted behind the prefix, and their
+    numbers in the whole sequence as ``positions``.  Should a wait of the kernels
+    run out, the rows concerned are NaN, and ``workspace_status`` tells.
+    """
+    kind = _value_dtype(q, "q")
+    dev = q.device
+    _all(kind, dev, 3, q, "q")
+    B, hq, d = q.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
+    hkv = k_cache.shape[2]
+    _heads(hq, hkv, d, _lib.RNN_ATTN_MAX_DIM)
+    num_pages, size = _cache(k_cache, v_cache, kind, dev, hkv, d)
+    prefix = _cu(prefix_pages, "prefix_pages", dev, 0) + 1
+    if prefix < 1:
+        raise ValueError("prefix_pages must name at least one page")
+    _ints(prefix_len, "prefix_len", dev, 1)
+    _ints(lens, "lens", dev, B)
+    table_stride, max_pages = _table(page_table, dev, B)
+    scale = _scale(scale, d)
+    out = _packed(q) if out is None else _given(out, q.shape, kind, dev, "out")
+    lse = torch.empty((B, hq), dtype=torch.float32, device=dev) if with_lse else None
+    if workspace is None:
+        workspace = torch.empty(_shared_need(B, hq, hkv, d, prefix * size), dtype=torch.uint8,
+                                device=dev)
+    ws, ws_bytes = _given_scratch(workspace, dev)
+    _call(_lib.load().rnn_attn_decode_shared, "rnn_attn_decode_shared", q, _SHARED.pack(
+        *_rows(q, "q", d), *_rows(out, "out", d), *_pages(k_cache, "k_cache", d),
+        *_pages(v_cache, "v_cache", d), prefix_pages.data_ptr(), prefix_len.data_ptr(),
+        page_table.data_ptr(), lens.data_ptr(), 0 if lse is None else lse.data_ptr(), ws, ws_bytes,
+        num_pages, table_stride, size, prefix, max_pages, B, hq, hkv, d, _DT[kind], scale))
     return (out, lse) if with_lse else out

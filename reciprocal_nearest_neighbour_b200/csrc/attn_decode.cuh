@@ -84,6 +84,8 @@ struct DecodeParams {
   float2* part_ml;                 // [grid][2][16] maximum, total
   int* err;                        // status word, cleared: no wait here can run out
   int2* span;                      // [B][Hkv * hblocks] first and last CTA of a pair
+  float* row_part;                 // [B][Hq][kDP] and [B][Hq]: parts of pairs in one share
+  float2* row_ml;
   // caches of codes (attn_decode_q8_kernel), whose strides are in bytes
   const uint8_t *kc8, *vc8;
   const float* scales;             // [page][head][row][key, value]
@@ -196,7 +198,9 @@ __device__ __forceinline__ void dec_advance(const DecodeParams& p, int Hv, DecCu
 // of n weights of one size loses about n 2^-27 (65536 keys: less than 2^-11, half a step
 // of fp16; 2^22 in one warp: 2.7 %).  There a warp takes its sums out of the accumulator
 // every kDecHoldKeys keys and adds them up itself, rounded to nearest, in local memory.
-template <bool kBf16, int kDP, int kNT, bool kLong>
+// kRows: every row's unnormalised sums and totals go to the workspace, for a join with
+// other parts, also those of a pair that lies in one share.
+template <bool kBf16, int kDP, int kNT, bool kLong, bool kRows = false>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const DecodeParams p) {
   using S = DecShape<kDP>;
   constexpr int kKeys = S::kKeys, kStages = S::kStages;
@@ -217,6 +221,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   float2* ml = reinterpret_cast<float2*>(merge + 2 * 8 * S::kMergeRow);  // [warp][16]
   uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
 
+  if (kRows && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
   const int Hv = p.Hkv * p.hblocks;
   // ---- this CTA's share of the tile list, and the pair it starts in
   DecCursor ld, cur;
@@ -548,7 +553,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
           const float inv = L != 0.f ? 1.f / L : 0.f;
           const float* b0 = merge + r * S::kMergeRow;
           const float* b1 = b0 + 8 * S::kMergeRow;
-          if (done) {
+          if (kRows && done) {
+            const int64_t at = static_cast<int64_t>(cur.b) * p.Hq + head0 + row;
+            for (int c = lane * 2; c < kDP; c += 64)
+              *reinterpret_cast<float2*>(p.row_part + at * kDP + c) =
+                  make_float2(b0[c] + b1[c], b0[c + 1] + b1[c + 1]);
+            if (lane == 0) p.row_ml[at] = make_float2(M, L);
+          } else if (done) {
             uint16_t* ob = p.out + cur.b * p.o_bs + (head0 + row) * p.o_hs;
             for (int c = lane * 2; c < p.d; c += 64)
               *reinterpret_cast<uint32_t*>(ob + c) =

@@ -1,0 +1,543 @@
+// Attention of one new token per sequence where all sequences of the batch start with
+// the same cached tokens:
+//   out = sum_t softmax_t(scale q.k_t) v_t over the prefix's rows t and the sequence's own.
+// Softmax parts over disjoint keys join exactly: with maximum m, total l and sum o of
+// each part, out = sum o 2^(m - M) / sum l 2^(m - M), M the largest m.  So the prefix is
+// attended to once for the whole batch (attn_prefix_kernel), each sequence's own rows as
+// in attn_decode (its kernel, with parts in place of outputs), and a last kernel joins.
+//
+// The prefix's rows are read once per 256 query rows in place of once per sequence: the
+// B * group queries of a key head are the rows of one matrix, 128 to a tile of the
+// tensor cores.  Up to about 100 rows its 512 bytes a key and head (128 channels) bound
+// the kernel, beyond that 4 * 128 * 128 d flops a row tile and 128 keys.
+//
+// attn_prefix_kernel: a CTA takes up to 256 rows of one key head and a range of the
+// prefix's 128-key tiles.  With more than 128 rows (wide) its two row tiles go over the
+// same keys, with up to 128 (narrow) the one row tile is there twice, for every other key
+// tile, so that in either case one tile's softmax runs under the other's products:
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row (as in attn_prompt): scores
+//                   from tensor memory, probabilities back over them as the 16-bit A
+//                   operand of the second product; in the end the row's part
+//   warps 8, 9      issue S = Q K^T and O += P V of tile 0 and 1
+//   warps 12-15     fetch the queries, then a ring of alternating K and V tiles, by
+//                   16-byte asynchronous copies: pages of any size and stride
+//                   lie in shared memory as the tensor cores' 128-byte swizzle wants them
+// Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
+#pragma once
+#include <cstdint>
+#include "attn_decode.cuh"
+#include "attn_prompt.cuh"
+
+namespace rnn {
+
+constexpr int kPreThreads = 512;   // warps 10 and 11 only complete their warpgroup
+constexpr int kPreMmaWarp = 8, kPreLoadWarp = 12;
+constexpr int kPreUnit = 2 * kAttnM;        // query rows of a unit
+// Key tiles of a row tile in one accumulator: 65536 keys (see attn_prompt).
+constexpr int kPreMostTiles = 512;
+
+template <int kDP>
+struct PreShape {
+  static constexpr int kTileBytes = kAttnM * kDP * 2;
+  static constexpr int kBlockBytes = kAttnM * 128;
+  static constexpr int kStages = kDP == 128 ? 4 : 8;
+  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 512;
+};
+
+struct PrefixParams {
+  const uint16_t *q, *kc, *vc;
+  int64_t q_bs, q_hs;                  // strides in elements
+  int64_t k_ps, k_ts, k_hs, v_ps, v_ts, v_hs;
+  const int32_t *pages, *len;          // the prefix: its pages, and its length on the device
+  int64_t num_pages;
+  int max_pages, page16;
+  FastDiv page, by_group;
+  int rows, group, d;                  // rows: B * group
+  int wide, narrow;                    // units of a key head: wide ones, and 0 or 1 narrow one
+  int wide_splits, narrow_splits;      // CTAs that share a unit's keys
+  int Hkv;
+  float c;                             // scale * log2(e)
+  uint32_t idesc_s, idesc_o;
+  float* part;                         // [slot][128][kDP] unnormalised parts
+  float2* part_ml;                     // [slot][128] maximum, total
+  int* err;
+  unsigned long long wait_limit_ns;
+  int stall_loads;
+};
+
+// Slots of the parts of a unit: its splits times its two tiles.
+__device__ __forceinline__ int pre_slot0(const PrefixParams& p, int hk, int unit) {
+  const int per_head = 2 * (p.wide * p.wide_splits + p.narrow * p.narrow_splits);
+  return hk * per_head + 2 * min(unit, p.wide) * p.wide_splits;
+}
+
+template <bool kBf16, int kDP>
+__global__ void __launch_bounds__(kPreThreads, 1)
+attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using S = PreShape<kDP>;
+  constexpr int kStages = S::kStages, kCols = 512;
+  constexpr int kOutCol = 2 * kAttnN;
+  constexpr float kBias = kBf16 ? 0.f : 7.f;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_tiles = smem;
+  const uint32_t ring = smem + 2 * S::kTileBytes;
+  const uint32_t bars = ring + kStages * S::kTileBytes;
+  const uint32_t full_bar = bars;
+  const uint32_t empty_bar = full_bar + 8 * kStages;
+  const uint32_t qfull_bar = empty_bar + 8 * kStages;
+  const uint32_t s_bar = qfull_bar + 8;     // scores of tile i are in tensor memory
+  const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
+  const uint32_t o_bar = p_bar + 32;        // its output is complete so far
+  const uint32_t drain_bar = o_bar + 16;
+  const uint32_t tmem_slot = drain_bar + 16;
+  const uint32_t abort_at = tmem_slot + 4;
+  // Keys that exist, 4 words for each of 8 tiles: when a tile's words are written, the
+  // values six tiles and more before it have been given back by both row tiles, so the
+  // softmax has read their words.
+  const uint32_t mask_at = tmem_slot + 8;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // ---- this CTA's unit and key tiles
+  const int wide_ctas = p.Hkv * p.wide * p.wide_splits;
+  const bool wide = static_cast<int>(blockIdx.x) < wide_ctas;
+  const int splits = wide ? p.wide_splits : p.narrow_splits, units = wide ? p.wide : 1;
+  int x = static_cast<int>(blockIdx.x) - (wide ? 0 : wide_ctas);
+  const int unit = wide ? x % units : p.wide;
+  x /= units;
+  const int split = x % splits, hk = x / splits;
+  const int rows = min(kPreUnit, p.rows - unit * kPreUnit);
+  const int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
+  const int64_t given = __ldg(p.len);
+  const int keys = static_cast<int>(
+      given < 0 ? 0 : min(given, min(room, static_cast<int64_t>(kDecMaxKeys))));
+  const int all = (keys + kAttnN - 1) / kAttnN;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
+  const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
+
+  auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
+  auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (true) {
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+      if (aborted()) return false;
+      if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+        sts_volatile(abort_at, 1);
+        atomicOr(p.err, code);
+        return false;
+      }
+    }
+  };
+  if (threadIdx.x < kStages) {
+    mbar_init(full_bar + 8 * threadIdx.x, 4);
+    mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
+    fence_barrier_init();
+  } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
+    const int i = threadIdx.x - 32;
+    mbar_init(s_bar + 8 * i, 1);
+    mbar_init(p_bar + 8 * i, 4);
+    mbar_init(p_bar + 8 * (2 + i), 4);
+    mbar_init(o_bar + 8 * i, 1);
+    mbar_init(drain_bar + 8 * i, 1);
+    if (i == 0) mbar_init(qfull_bar, 4);
+    fence_barrier_init();
+  } else if (threadIdx.x == 64) {
+    sts_volatile(abort_at, 0);
+  }
+  if (warp == kPreMmaWarp) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = lds_volatile(tmem_slot);
+  // steps of tile i, and the CTA's key tile of its step k
+  const int n_of[2] = {wide ? n : (n + 1) / 2, wide ? n : n / 2};
+  auto tile_of = [&](int i, int k) { return wide ? k : 2 * k + i; };
+
+  if (warp >= kPreMmaWarp) {
+    regs_give<kAttnRegsOther>();
+    if (warp >= kPreLoadWarp) {
+      // ------------------------------------------------------------- loads
+      constexpr int kChunks = kDP / 8, kRowsPer = 32 / kChunks;
+      const int w = warp - kPreLoadWarp;
+      const int ch = lane % kChunks, sub = lane / kChunks;
+      const bool ch_live = ch * 8 < p.d;
+      // chunk `ch` of row r in the 128-byte swizzle of its 64-channel block
+      auto at = [&](int r) {
+        return (ch >> 3) * S::kBlockBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+      };
+      // (a unit without keys fetches nothing, a narrow one its one row tile)
+      if (n > 0 && !p.stall_loads) {
+        for (int i = 0; i < (wide ? 2 : 1); ++i) {
+          for (int r = w * 32 + sub; r < w * 32 + 32; r += kRowsPer) {
+            const bool live = i * kAttnM + r < rows && ch_live;
+            const int row = unit * kPreUnit + i * kAttnM + r;
+            const int b = live ? fdiv(row, p.by_group) : 0;
+            const uint16_t* src = p.q + b * p.q_bs +
+                                  (hk * p.group + (live ? row - b * p.group : 0)) * p.q_hs + ch * 8;
+            cp_async16(q_tiles + i * S::kTileBytes + at(r), live ? src : p.q, live);
+          }
+        }
+      }
+      cp_async_commit();
+      // Copies are told to the tensor cores' proxy by the thread that made them, when
+      // they are complete: groups in their order, the queries' first.
+      int issued = 0, told = 0;  // groups, the queries' among them
+      auto tell = [&]() {
+        switch (issued - told) {
+          case 0: break;
+          case 1: cp_async_wait<0>(); break;
+          case 2: cp_async_wait<1>(); break;
+          case 3: cp_async_wait<2>(); break;
+          default: cp_async_wait<3>(); break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * ((told - 1) % kStages));
+        ++told;
+      };
+      issued = 1;
+      const int loads = p.stall_loads ? 0 : 2 * n;
+      bool ok = true;
+      int id = -1;
+      for (int l = 0; l < loads; ++l) {
+        const int slot = l % kStages;
+        const uint32_t eb = empty_bar + 8 * slot, parity = ((l / kStages) & 1) ^ 1u;
+        while (!__all_sync(0xffffffffu, mbar_test_wait(eb, parity))) {
+          if (told < issued) {
+            tell();
+          } else {
+            ok = __all_sync(0xffffffffu, wait(eb, parity, kErrWaitProducer));
+            break;
+          }
+        }
+        if (!ok) break;
+        const int t0 = (tile0 + (l >> 1)) * kAttnN + w * 32, t = t0 + lane;
+        if (!(l & 1)) {  // a tile's keys: their pages, for its values too
+          id = -1;
+          if (t < keys) {
+            id = __ldg(p.pages + fdiv(t, p.page));
+            if (id < 0 || id >= p.num_pages) id = -1;
+          }
+          const unsigned there = __ballot_sync(0xffffffffu, id >= 0);
+          if (lane == 0) sts_volatile(mask_at + 16 * ((l >> 1) & 7) + 4 * w, static_cast<int>(there));
+        }
+        const unsigned valid = __ballot_sync(0xffffffffu, id >= 0);
+        const uint16_t* base = l & 1 ? p.vc : p.kc;
+        const int64_t ps = l & 1 ? p.v_ps : p.k_ps, ts = l & 1 ? p.v_ts : p.k_ts;
+        const uint16_t* head = base + hk * (l & 1 ? p.v_hs : p.k_hs) + ch * 8;
+        const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
+        const uint32_t dst = ring + slot * S::kTileBytes;
+        if (p.page16) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
+            const int r0 = __shfl_sync(0xffffffffu, row, g * 16) + sub;
+            const uint16_t* src = head + page * ps + r0 * ts;
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsPer; ++i) {
+              const int r = g * 16 + i * kRowsPer + sub;
+              const bool live = ((valid >> r) & 1u) && ch_live;
+              cp_async16(dst + at(w * 32 + r), live ? src : base, live);
+              src += kRowsPer * ts;
+            }
+          }
+        } else {
+          const int64_t off = id * ps + row * ts;
+#pragma unroll 4
+          for (int i = 0; i < 32 / kRowsPer; ++i) {
+            const int r = i * kRowsPer + sub;
+            const int64_t o = __shfl_sync(0xffffffffu, off, r);
+            const bool live = ((valid >> r) & 1u) && ch_live;
+            cp_async16(dst + at(w * 32 + r), live ? head + o : base, live);
+          }
+        }
+        cp_async_commit();
+        ++issued;
+        if (issued - told > 4) tell();
+      }
+      while (told < issued) tell();
+      if (w == 0 && !aborted()) {
+        // no arrival of a product's completion is under way when the CTA exits
+        const int l = max(0, loads - kStages) + lane;
+        if (lane < kStages && l < loads)
+          settle_phase(empty_bar + 8 * (l % kStages), (l / kStages) & 1, p.wait_limit_ns, p.err);
+        __syncwarp();
+      }
+    } else if (warp < kPreMmaWarp + 2) {
+      // ---------------------------------------------------------- products
+      const int i = warp - kPreMmaWarp;
+      const int dsteps = (p.d + 15) / 16;
+      const uint64_t q_desc = make_sdesc(q_tiles + (wide ? i : 0) * S::kTileBytes, 64);
+      const uint64_t k_desc = make_sdesc(ring, 64);
+      const uint64_t v_desc = make_vdesc(ring);
+      bool ok = true, any = false;
+      auto wait_mma = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, wait(bar, parity, kErrWaitMma));
+        return ok;
+      };
+      if (n_of[i] > 0) wait_mma(qfull_bar, 0);
+      for (int k = 0; ok && k < n_of[i]; ++k) {
+        const int kx = 2 * tile_of(i, k), vx = kx + 1;
+        const int ks = kx % kStages, vs = vx % kStages;
+        if (!wait_mma(full_bar + 8 * ks, (kx / kStages) & 1)) break;
+        // the probabilities lie over the scores: the product that reads them first
+        if (k > 0 && !wait_mma(o_bar + 8 * i, (k - 1) & 1)) break;
+        tc_fence_after();
+        const uint64_t k_at = k_desc + static_cast<uint64_t>(ks * (S::kTileBytes >> 4));
+        const int whole = dsteps >> 2;
+#pragma unroll
+        for (int c = 0; c < kDP / 64; ++c) {
+          const uint32_t blk = c * (S::kBlockBytes >> 4);
+          if (c < whole) {
+            umma_ss_x4(tmem + i * kAttnN, q_desc + blk, k_at + blk, p.idesc_s, c > 0);
+          } else {
+            for (int s = 0; s < dsteps - 4 * c; ++s)
+              umma_f16_warp(tmem + i * kAttnN, q_desc + blk + 2 * s, k_at + blk + 2 * s, p.idesc_s,
+                            c > 0 || s > 0);
+          }
+        }
+        umma_commit_warp(s_bar + 8 * i);
+        umma_commit_warp(empty_bar + 8 * ks);
+        any = true;
+        if (!wait_mma(full_bar + 8 * vs, (vx / kStages) & 1)) break;
+        const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_mma(p_bar + 8 * (2 * h + i), k & 1)) break;
+          tc_fence_after();
+          umma_ts_x4(tmem + kOutCol + i * kDP, tmem + i * kAttnN + h * 32,
+                     v_at + static_cast<uint64_t>(h * (8192 >> 4)), p.idesc_o,
+                     (k > 0 || h > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        umma_commit_warp(o_bar + 8 * i);
+        umma_commit_warp(empty_bar + 8 * vs);
+        __syncwarp();
+      }
+      if (aborted() && any) {
+        // let every product issued finish before tensor memory is released
+        umma_commit_warp(drain_bar + 8 * i);
+        __syncwarp();
+        settle_phase(drain_bar + 8 * i, 0, p.wait_limit_ns, p.err);
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax
+    regs_take<kAttnRegsSoftmax>();
+    const int i = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;     // row of the tile
+    const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lane_at + i * kAttnN;
+    const uint32_t o_at = tmem + lane_at + kOutCol + i * kDP;
+    const int steps = i ? n_of[1] : n_of[0];
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+      ok = wait(s_bar + 8 * i, k & 1, kErrWaitEpilogue);
+      __syncwarp();
+      tc_fence_after();
+      float s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s[c]);
+      const uint4 there = lds_v4(mask_at + 16 * (tile_of(i, k) & 7));
+      tmem_wait_ld_regs(s[0]);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) reg_fence(s[c]);
+      if ((there.x & there.y & there.z & there.w) != 0xffffffffu) {
+        const uint32_t has[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((has[c] >> e) & 1u)) s[c][e] = kNegInf;
+      }
+      const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+      if (k == 0) m = top;
+      const bool grow = (top - m) * p.c > kAttnSlack;  // also from -inf to a number
+      float mc = m * p.c;
+      // one vote for all: a lane whose wait gave up takes the warp with it
+      if (__any_sync(0xffffffffu, grow || !ok || fabsf(mc) > kAttnFar)) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float f = grow ? exp2_approx((m - top) * p.c) : 1.f;
+        if (grow) m = top;
+        mc = m == kNegInf ? 0.f : m * p.c;
+        const bool before = fabsf(mc) > kAttnFar && fabsf(m) < -kNegInf;
+        if (__any_sync(0xffffffffu, before)) {
+          const float ref = before ? m : 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c][e] -= ref;
+          if (before) mc = 0.f;
+        }
+        l *= f;
+        if (__any_sync(0xffffffffu, grow)) {  // (only behind a first step: its product is done)
+#pragma unroll
+          for (int c = 0; c < kDP / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_at + c * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[h * 16 + e] * f);
+              tmem_st16(o_at + c * 32 + h * 16, w);
+            }
+          }
+        }
+      }
+      const float z = mc - kBias;
+      const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float a, b;
+          f2_get(f2_fma(f2_make(s[c][2 * e], s[c][2 * e + 1]), c2, z2), a, b);
+          a = exp2_approx(a);
+          b = exp2_approx(b);
+          sum[e & 1] = f2_add(sum[e & 1], f2_make(a, b));
+          // the second product takes the probabilities in the value type (half a step:
+          // 2^-9 of bf16, 2^-12 of fp16, of each weight); the total keeps them in fp32
+          w[e] = pack2<kBf16>(a, b);
+        }
+        tmem_st16(s_at + c * 16, w);
+        if (c & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_bar + 8 * (2 * (c >> 1) + i));
+        }
+      }
+      float a, b;
+      f2_get(f2_add(sum[0], sum[1]), a, b);
+      l += a + b;
+    }
+    if (steps > 0) {
+      ok = ok && wait(o_bar + 8 * i, (steps - 1) & 1, kErrWaitEpilogue);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    // ---- the row's part
+    const int slot = pre_slot0(p, hk, unit) + 2 * split + i;
+    const bool mine = (wide ? i * kAttnM : 0) + r < rows;
+    const int64_t at = static_cast<int64_t>(slot) * kAttnM + r;
+    if (!ok) m = l = __uint_as_float(0x7FC00000u);  // given up: its row becomes NaN
+    if (mine) p.part_ml[at] = make_float2(m, l);
+    if (steps > 0) {
+#pragma unroll 1
+      for (int c = 0; c < kDP; c += 32) {
+        float o[32];
+        tmem_ld32(o_at + c, o);
+        tmem_wait_ld_regs(o);
+        if (mine) {
+          float4* to = reinterpret_cast<float4*>(p.part + at * kDP + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPreMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// Joins a row's parts: the prefix's, one from each of its unit's splits (and tiles), and
+// its sequence's own.  One block per (sequence, query head); its four warps take the
+// parts in turn and their sums meet in a fixed order.
+template <bool kBf16, int kDP>
+__global__ void __launch_bounds__(128)
+attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixParams pre) {
+  constexpr int kVals = kDP / 32;  // channels per lane
+  constexpr float kBias = kBf16 ? 0.f : 7.f;
+  using VecT = std::conditional_t<kVals == 4, float4, float2>;
+  __shared__ float acc[4][kDP];
+  __shared__ float2 tot[4];
+  pdl_wait();
+  const int b = blockIdx.x / p.Hq, head = blockIdx.x - b * p.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = head / p.group, in = head - hk * p.group;
+  const int hb = in / kDecRows, dec_row = in - hb * kDecRows;
+  const int row = b * p.group + in, unit = row / kPreUnit, at = row - unit * kPreUnit;
+  const bool wide = unit < pre.wide;
+  const int slot0 = pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0);
+  const int pre_row = wide ? at % kAttnM : at;
+  const int n_pre = wide ? pre.wide_splits : 2 * pre.narrow_splits;
+  int2 sp = make_int2(0, -1);
+  if (dec_len(p, b) > 0)
+    sp = p.span[static_cast<int64_t>(b) * (p.Hkv * p.hblocks) + hk * p.hblocks + hb];
+  const int parts = n_pre + sp.y - sp.x + 1;
+  float v[kVals] = {}, M = kNegInf, L = 0.f;
+#pragma unroll 2
+  for (int i = warp; i < parts; i += 4) {
+    float2 a;
+    const float* from;
+    if (i < n_pre) {
+      const int64_t slot = slot0 + (wide ? 2 : 1) * i;
+      a = pre.part_ml[slot * kAttnM + pre_row];
+      from = pre.part + (slot * kAttnM + pre_row) * kDP;
+    } else if (sp.x == sp.y) {
+      const int64_t own = static_cast<int64_t>(b) * p.Hq + head;
+      a = p.row_ml[own];
+      from = p.row_part + own * kDP;
+    } else {
+      const int c = sp.x + i - n_pre;
+      const int64_t own = (static_cast<int64_t>(c) * 2 + (c == sp.x ? 1 : 0)) * kDecRows + dec_row;
+      a = p.part_ml[own];
+      from = p.part + own * kDP;
+    }
+    if (a.x == kNegInf && a.y == 0.f) continue;  // no key: its sums were not written
+    const VecT x = *reinterpret_cast<const VecT*>(from + lane * kVals);
+    const float* xs = reinterpret_cast<const float*>(&x);
+    const float top = fmaxf(M, a.x);
+    // (a NaN maximum is a part that was given up: its factor is NaN too)
+    const float f = a.x == kNegInf ? 1.f : exp2_approx((a.x - top) * p.c);
+    const float h = M == kNegInf ? 0.f : exp2_approx((M - top) * p.c);
+    M = top;
+    L = L * h + a.y * f;
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) v[e] = v[e] * h + xs[e] * f;
+  }
+#pragma unroll
+  for (int e = 0; e < kVals; ++e) acc[warp][lane * kVals + e] = v[e];
+  if (lane == 0) tot[warp] = make_float2(M, L);
+  __syncthreads();
+  M = fmaxf(fmaxf(tot[0].x, tot[1].x), fmaxf(tot[2].x, tot[3].x));
+  float f[4];
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    // without a reference the total is 0, or NaN if its scores were
+    f[w] = tot[w].x == kNegInf ? 1.f : exp2_approx((tot[w].x - M) * p.c);
+    L += tot[w].y * f[w];
+  }
+  uint16_t* ob = p.out + b * p.o_bs + head * p.o_hs;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+    const float y =
+        ((acc[0][c] * f[0] + acc[1][c] * f[1]) + (acc[2][c] * f[2] + acc[3][c] * f[3])) * inv;
+    ob[c] = kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y))
+                  : __half_as_ushort(__float2half_rn(y));
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[static_cast<int64_t>(b) * p.Hq + head] =
+        L != 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
+}
+
+}  // namespace rnn

@@ -63,7 +63,7 @@ struct DeviceInfo {
   bool sm100 = false;
   bool smem_set = false;
   bool op_smem_set = false;  // one-pass exhaustive-set kernels
-  bool attn_smem_set = false, attn_q8_smem_set = false;
+  bool attn_smem_set = false, attn_q8_smem_set = false, attn_shared_smem_set = false;
 };
 
 static std::mutex g_mu;
@@ -1468,6 +1468,7 @@ __global__ void frm_emit_kernel(FrmState st, int32_t* pairs, int64_t cap, int32_
 #include "kv_append.cuh"
 #include "kv_q8.cuh"
 #include "attn_decode_q8.cuh"
+#include "attn_shared.cuh"
 
 namespace rnn {
 
@@ -3205,6 +3206,42 @@ static size_t dec_layout(void* ws, int64_t B, int Hkv, int group, int d, DecWs* 
   return c.off;
 }
 
+// What the decode kernels' calls have alike; the caller sets the rest.
+static DecodeParams decode_params(const rnn_rows& q, const rnn_rows& out, const rnn_pages& k,
+                                  const rnn_pages& v, const DecWs& w, int page_size, int Hkv,
+                                  int group, int d, float scale) {
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q.data);
+  p.out = static_cast<uint16_t*>(out.data);
+  p.q_bs = q.token_stride, p.q_hs = q.head_stride;
+  p.o_bs = out.token_stride, p.o_hs = out.head_stride;
+  p.k_ps = k.page_stride, p.k_ts = k.token_stride, p.k_hs = k.head_stride;
+  p.v_ps = v.page_stride, p.v_ts = v.token_stride, p.v_hs = v.head_stride;
+  p.Hq = Hkv * group;
+  p.Hkv = Hkv;
+  p.group = group;
+  p.hblocks = (group + kDecRows - 1) / kDecRows;
+  p.d = d;
+  p.page = make_fastdiv(page_size);
+  // one page look-up and no shuffles per 16 keys: 96 streams 108 us, 110 row by row
+  p.page16 = page_size % 16 == 0;
+  p.scale = scale;
+  p.c = scale * 1.44269504f;
+  p.part = w.part;
+  p.part_ml = w.ml;
+  p.span = w.span;
+  p.err = w.err;
+  return p;
+}
+static dim3 decode_grid(const DecodeParams& p, int per_tile, int sms) {
+  const int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
+  const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
+  const int64_t tiles = (keys + per_tile - 1) / per_tile * p.B * p.Hkv * p.hblocks;
+  const int most = std::min(2 * sms, kDecMaxGrid);
+  return dim3(static_cast<unsigned>(tiles < most ? tiles : most));
+}
+
 size_t rnn_attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
   if (B < 0 || check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, RNN_F16) != RNN_OK) return 0;
   DecWs w;
@@ -3248,51 +3285,19 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
     zero_words_kernel<<<1, 32, 0, s>>>(static_cast<int*>(workspace), 1);
     return launched();
   }
-  DecodeParams p;
-  std::memset(&p, 0, sizeof(p));
   DecWs w;
   dec_layout(workspace, B, Hkv, Hq / Hkv, d, &w);
-  p.q = static_cast<const uint16_t*>(q.data);
+  DecodeParams p = decode_params(q, out, k_cache, v_cache, w, page_size, Hkv, Hq / Hkv, d, scale);
   p.kc = static_cast<const uint16_t*>(k_cache.data);
   p.vc = static_cast<const uint16_t*>(v_cache.data);
-  p.out = static_cast<uint16_t*>(out.data);
   p.lse = lse;
-  p.q_bs = q.token_stride;
-  p.q_hs = q.head_stride;
-  p.o_bs = out.token_stride;
-  p.o_hs = out.head_stride;
-  p.k_ps = k_cache.page_stride;
-  p.k_ts = k_cache.token_stride;
-  p.k_hs = k_cache.head_stride;
-  p.v_ps = v_cache.page_stride;
-  p.v_ts = v_cache.token_stride;
-  p.v_hs = v_cache.head_stride;
   p.table = page_table;
   p.lens = lens;
   p.table_bs = table_stride;
   p.num_pages = num_pages;
   p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.group = Hq / Hkv;
-  p.hblocks = (p.group + kDecRows - 1) / kDecRows;
-  p.d = d;
   p.max_pages = max_pages;
-  p.page = make_fastdiv(page_size);
-  // one page look-up and no shuffles per 16 keys: 96 streams 108 us, 110 row by row
-  p.page16 = page_size % 16 == 0;
-  p.scale = scale;
-  p.c = scale * 1.44269504f;
-  p.part = w.part;
-  p.part_ml = w.ml;
-  p.span = w.span;
-  p.err = w.err;
-  const int64_t room = static_cast<int64_t>(max_pages) * page_size;
-  const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
-  const int per_tile = d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile;
-  const int64_t tiles = (keys + per_tile - 1) / per_tile * B * Hkv * p.hblocks;
-  const int most = std::min(2 * di->sms, kDecMaxGrid);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
+  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile, di->sms);
   const bool bf = dtype == RNN_BF16;
   if (d <= 64)
     return bf ? decode_launch<true, 64>(p, grid, s) : decode_launch<false, 64>(p, grid, s);
@@ -3686,50 +3691,222 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
     zero_words_kernel<<<1, 32, 0, s>>>(static_cast<int*>(a.workspace), 1);
     return launched();
   }
-  DecodeParams p;
-  std::memset(&p, 0, sizeof(p));
   DecWs w;
   dec_layout(a.workspace, B, Hkv, Hq / Hkv, d, &w);
-  p.q = static_cast<const uint16_t*>(a.q.data);
+  DecodeParams p =
+      decode_params(a.q, a.out, a.k_cache, a.v_cache, w, a.page_size, Hkv, Hq / Hkv, d, a.scale);
   p.kc8 = static_cast<const uint8_t*>(a.k_cache.data);
   p.vc8 = static_cast<const uint8_t*>(a.v_cache.data);
   p.scales = a.scales.data;
-  p.out = static_cast<uint16_t*>(a.out.data);
-  p.lse = a.lse;
-  p.q_bs = a.q.token_stride, p.q_hs = a.q.head_stride;
-  p.o_bs = a.out.token_stride, p.o_hs = a.out.head_stride;
-  p.k_ps = a.k_cache.page_stride, p.k_ts = a.k_cache.token_stride, p.k_hs = a.k_cache.head_stride;
-  p.v_ps = a.v_cache.page_stride, p.v_ts = a.v_cache.token_stride, p.v_hs = a.v_cache.head_stride;
   p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
   p.wide = d % 16 == 0 && (p.k_ps | p.k_ts | p.k_hs | p.v_ps | p.v_ts | p.v_hs) % 16 == 0;
+  p.lse = a.lse;
   p.table = a.page_table;
   p.lens = a.lens;
   p.table_bs = a.table_stride;
   p.num_pages = a.num_pages;
   p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.group = Hq / Hkv;
-  p.hblocks = (p.group + kDecRows - 1) / kDecRows;
-  p.d = d;
   p.max_pages = a.max_pages;
-  p.page = make_fastdiv(a.page_size);
-  p.page16 = a.page_size % 16 == 0;
-  p.scale = a.scale;
-  p.c = a.scale * 1.44269504f;
-  p.part = w.part;
-  p.part_ml = w.ml;
-  p.span = w.span;
-  p.err = w.err;
-  const int64_t room = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
-  const int per_tile = DecQ8Shape<128>::kTile;
   static_assert(DecQ8Shape<64>::kTile == DecQ8Shape<128>::kTile, "");
-  const int64_t tiles = (keys + per_tile - 1) / per_tile * B * Hkv * p.hblocks;
-  const int most = std::min(2 * di->sms, kDecMaxGrid);
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most));
+  const dim3 grid = decode_grid(p, DecQ8Shape<128>::kTile, di->sms);
   const bool bf = a.dtype == RNN_BF16, int8 = a.codes == RNN_CODES_INT8;
   return d <= 64 ? decode_q8_dispatch<64>(p, bf, int8, grid, s) : decode_q8_dispatch<128>(p, bf, int8, grid, s);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ a prefix shared by the batch
+// How the prefix's work is cut: units of 256 query rows of a key head, the last of them
+// narrow where it has up to 128, and the CTAs that share a unit's keys.
+struct PrefixPlan {
+  int wide, narrow, wide_splits, narrow_splits;
+  int64_t ctas;
+};
+static PrefixPlan prefix_plan(int64_t rows, int Hkv, int64_t room) {
+  PrefixPlan best{};
+  const int64_t units = (rows + kPreUnit - 1) / kPreUnit;
+  best.narrow = rows - (units - 1) * kPreUnit <= kAttnM;
+  best.wide = static_cast<int>(units - best.narrow);
+  const int64_t keys = std::min<int64_t>(room, kDecMaxKeys);
+  const int64_t tiles = std::max<int64_t>(1, (keys + kAttnN - 1) / kAttnN);
+  // The time of a wave, in the time of a row tile's products with 128 keys: 2 for a wide
+  // unit's key tile, 1.4 for a narrow one's (its loads), 4 to begin and to end, and 1/1000
+  // for each row's part, which the join reads.
+  constexpr int kSms = 148;
+  double least = 0;
+  // (from what one accumulator takes; a narrow unit has two)
+  const int64_t from = (tiles + kPreMostTiles - 1) / kPreMostTiles;
+  for (int64_t sw = from; sw <= std::max(from, std::min<int64_t>(tiles, 2 * kSms)); ++sw) {
+    const int64_t sn = best.wide ? (sw * 7 + 5) / 10 : sw;
+    const int64_t ctas = Hkv * (best.wide * sw + best.narrow * sn);
+    const int64_t waves = (ctas + kSms - 1) / kSms;
+    const double steps = std::max(best.wide ? 2.0 * ((tiles + sw - 1) / sw) : 0.0,
+                                  best.narrow ? 1.4 * ((tiles + sn - 1) / sn) : 0.0);
+    const double parts = static_cast<double>(Hkv) * kAttnM * 2 * (best.wide * sw + best.narrow * sn);
+    const double time = waves * (steps + 4) + 1e-3 * parts / 16;
+    if (best.ctas == 0 || time < least) {
+      least = time;
+      best.wide_splits = static_cast<int>(sw);
+      best.narrow_splits = static_cast<int>(sn);
+      best.ctas = ctas;
+    }
+    if (ctas > 8 * kSms && best.ctas) break;
+  }
+  return best;
+}
+
+struct SharedWs {
+  DecWs dec;
+  float *row_part, *part;
+  float2 *row_ml, *part_ml;
+};
+static size_t shared_layout(void* ws, int64_t B, int Hkv, int group, int d, const PrefixPlan& plan,
+                            SharedWs* w) {
+  Carve c(ws);
+  c.off = dec_layout(ws, B, Hkv, group, d, &w->dec);
+  const int64_t dp = d <= 64 ? 64 : 128;
+  w->row_ml = c.take<float2>(B * Hkv * group);
+  w->row_part = c.take<float>(B * Hkv * group * dp);
+  w->part_ml = c.take<float2>(plan.ctas * 2 * kAttnM);
+  w->part = c.take<float>(plan.ctas * 2 * kAttnM * dp);
+  return c.off;
+}
+
+template <bool kBf16, int kDP>
+static rnn_status shared_launch(const DecodeParams& p, dim3 grid, const PrefixParams& pre, unsigned ctas,
+                                cudaStream_t s) {
+  const dim3 block(kDecWarps * 32);
+  const size_t sm = DecShape<kDP>::kSmem;
+  const bool many = static_cast<int64_t>(p.max_pages) * p.page.div > kDecShortKeys;
+  if (p.group <= 8)
+    many ? attn_decode_kernel<kBf16, kDP, 1, true, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_kernel<kBf16, kDP, 1, false, true><<<grid, block, sm, s>>>(p);
+  else
+    many ? attn_decode_kernel<kBf16, kDP, 2, true, true><<<grid, block, sm, s>>>(p)
+         : attn_decode_kernel<kBf16, kDP, 2, false, true><<<grid, block, sm, s>>>(p);
+  rnn_status r = launched();
+  if (r != RNN_OK) return r;
+  attn_prefix_kernel<kBf16, kDP><<<ctas, kPreThreads, PreShape<kDP>::kSmem, s>>>(pre);
+  if ((r = launched()) != RNN_OK) return r;
+  launch_k(attn_shared_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
+           0, s, true, p, pre);
+  return launched();
+}
+template <bool kBf16, int kDP>
+static bool shared_smem() {
+  const auto set = [](size_t bytes, auto... kernels) {
+    return ((cudaFuncSetAttribute(kernels, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(bytes)) == cudaSuccess) && ...);
+  };
+  return set(DecShape<kDP>::kSmem, attn_decode_kernel<kBf16, kDP, 1, false, true>,
+             attn_decode_kernel<kBf16, kDP, 1, true, true>, attn_decode_kernel<kBf16, kDP, 2, false, true>,
+             attn_decode_kernel<kBf16, kDP, 2, true, true>) &&
+         set(PreShape<kDP>::kSmem, attn_prefix_kernel<kBf16, kDP>);
+}
+static rnn_status shared_setup(DeviceInfo* di) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (di->attn_shared_smem_set) return RNN_OK;
+  if (!shared_smem<true, 64>() || !shared_smem<false, 64>() || !shared_smem<true, 128>() ||
+      !shared_smem<false, 128>())
+    return RNN_ECUDA;
+  di->attn_shared_smem_set = true;
+  return RNN_OK;
+}
+
+extern "C" {
+
+size_t rnn_attn_decode_shared_workspace_size(int B, int Hq, int Hkv, int d, int64_t prefix_room) {
+  if (B < 0 || prefix_room < 1 || check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, RNN_F16) != RNN_OK) return 0;
+  SharedWs w;
+  const int group = Hq / Hkv;
+  return shared_layout(nullptr, B, Hkv, group, d,
+                       prefix_plan(std::max<int64_t>(1, int64_t{B} * group), Hkv, prefix_room), &w);
+}
+
+rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args* args, rnn_stream_t stream) {
+  NvtxRange nvtx_range("rnn_attn_decode_shared");
+  if (!args) return RNN_EINVAL;
+  rnn_attn_decode_shared_args a = *args;
+  const int B = a.B, Hq = a.Hq, Hkv = a.Hkv, d = a.d;
+  const rnn_dtype dtype = static_cast<rnn_dtype>(a.dtype);
+  if (B < 0 || a.num_pages < 1 || a.num_pages > INT32_MAX || a.page_size < 1 || a.max_pages < 1 ||
+      a.prefix_pages_count < 1 || a.table_stride < 0)
+    return RNN_EINVAL;
+  rnn_status r = check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, dtype);
+  if (r != RNN_OK) return r;
+  if (!(a.scale > 0.f) || !(a.scale < 2e38f)) return RNN_EINVAL;
+  if ((B > 0 && (!a.page_table || !a.lens || !a.prefix_pages || !a.prefix_len)) ||
+      !aligned4(a.page_table) || !aligned4(a.lens) || !aligned4(a.prefix_pages) ||
+      !aligned4(a.prefix_len) || !aligned4(a.lse))
+    return RNN_EINVAL;
+  if ((r = check_rows(&a.q, B, Hq, d)) != RNN_OK || (r = check_written_rows(&a.out, B, Hq, d)) != RNN_OK ||
+      (r = check_pages(&a.k_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK ||
+      (r = check_pages(&a.v_cache, a.num_pages, a.page_size, Hkv, d)) != RNN_OK)
+    return r;
+  if (B > INT32_MAX - 1024 || static_cast<int64_t>(B) * Hq > INT32_MAX - 1024) return RNN_EUNSUPPORTED;
+  const int64_t room = int64_t{a.prefix_pages_count} * a.page_size;
+  if (!a.workspace || !aligned256(a.workspace) ||
+      a.ws_bytes < rnn_attn_decode_shared_workspace_size(B, Hq, Hkv, d, room))
+    return RNN_EWORKSPACE;
+  const int group = Hq / Hkv;
+  const PrefixPlan plan = prefix_plan(std::max<int64_t>(1, int64_t{B} * group), Hkv, room);
+  if (plan.ctas * 2 > INT32_MAX) return RNN_EUNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK || (r = shared_setup(di)) != RNN_OK) return r;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0) {
+    zero_words_kernel<<<1, 32, 0, s>>>(static_cast<int*>(a.workspace), 1);
+    return launched();
+  }
+  SharedWs w;
+  shared_layout(a.workspace, B, Hkv, group, d, plan, &w);
+  DecodeParams p =
+      decode_params(a.q, a.out, a.k_cache, a.v_cache, w.dec, a.page_size, Hkv, group, d, a.scale);
+  p.kc = static_cast<const uint16_t*>(a.k_cache.data);
+  p.vc = static_cast<const uint16_t*>(a.v_cache.data);
+  p.lse = a.lse;
+  p.table = a.page_table;
+  p.lens = a.lens;
+  p.table_bs = a.table_stride;
+  p.num_pages = a.num_pages;
+  p.B = B;
+  p.max_pages = a.max_pages;
+  p.row_part = w.row_part;
+  p.row_ml = w.row_ml;
+  PrefixParams pre;
+  std::memset(&pre, 0, sizeof(pre));
+  pre.q = p.q, pre.kc = p.kc, pre.vc = p.vc;
+  pre.q_bs = p.q_bs, pre.q_hs = p.q_hs;
+  pre.k_ps = p.k_ps, pre.k_ts = p.k_ts, pre.k_hs = p.k_hs;
+  pre.v_ps = p.v_ps, pre.v_ts = p.v_ts, pre.v_hs = p.v_hs;
+  pre.pages = a.prefix_pages;
+  pre.len = a.prefix_len;
+  pre.num_pages = a.num_pages;
+  pre.max_pages = a.prefix_pages_count;
+  pre.page16 = p.page16;
+  pre.page = p.page;
+  pre.by_group = make_fastdiv(group);
+  pre.rows = B * group;
+  pre.group = group;
+  pre.d = d;
+  pre.wide = plan.wide, pre.narrow = plan.narrow;
+  pre.wide_splits = plan.wide_splits, pre.narrow_splits = plan.narrow_splits;
+  pre.Hkv = Hkv;
+  pre.c = p.c;
+  pre.idesc_s = make_idesc(dtype, kAttnN);
+  pre.idesc_o = make_idesc(dtype, (d + 15) / 16 * 16) | (1u << 16);  // B with its channels contiguous
+  pre.part = w.part;
+  pre.part_ml = w.part_ml;
+  pre.err = w.dec.err;
+  pre.stall_loads = g_stall_loads.load(std::memory_order_relaxed);
+  pre.wait_limit_ns = pre.stall_loads ? g_stall_limit_ns.load(std::memory_order_relaxed)
+                                      : kWaitLimitNs;
+  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile, di->sms);
+  const unsigned ctas = static_cast<unsigned>(plan.ctas);
+  const bool bf = dtype == RNN_BF16;
+  if (d <= 64)
+    return bf ? shared_launch<true, 64>(p, grid, pre, ctas, s) : shared_launch<false, 64>(p, grid, pre, ctas, s);
+  return bf ? shared_launch<true, 128>(p, grid, pre, ctas, s) : shared_launch<false, 128>(p, grid, pre, ctas, s);
 }
 
 }  // extern "C"
