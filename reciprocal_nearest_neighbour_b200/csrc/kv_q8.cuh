@@ -22,7 +22,7 @@ namespace rnn {
 
 constexpr int kQ8Warps = 4;
 // Rows in flight a lane.
-constexpr int kQ8Batch = 3;
+constexpr int kQ8Batch = 2;
 constexpr float kQ8MinScale = 1.1754943508222875e-38f;  // 2^-126
 
 enum CodeFormat : int { kE4m3 = 0, kInt8 = 1 };
@@ -40,14 +40,13 @@ struct AppendQ8Params {
   int T, B, Hq, Hkv, d;             // Hq = 0 without queries
   int max_pages, page_size;
   int pairs, axes;                  // channel pairs per axis, axes (0: no rotation)
-  int paired;                       // pairs side by side instead of half a block apart
   int share;                        // log2 of the warps that share a token
-  int row_lanes;                    // log2 of the lanes of a row, 8 channels each
+  int row_lanes;                    // log2 of the lanes of a row, up to 16 channels each
 };
 
 // Codes of 8 channels, 4 a word.
 template <int kFmt>
-__device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float inv) {
+__device__ __forceinline__ uint2 q8_codes(const float* x, float inv) {
   uint2 r;
   uint32_t* w = &r.x;
 #pragma unroll
@@ -56,10 +55,12 @@ __device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float inv) {
     const float a = __fmul_rn(x[4 * h], inv), b = __fmul_rn(x[4 * h + 1], inv);
     const float c = __fmul_rn(x[4 * h + 2], inv), e = __fmul_rn(x[4 * h + 3], inv);
     if constexpr (kFmt == kE4m3) {
-      uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(e), "f"(c));
-      w[h] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+      asm("{\n\t.reg .b16 lo, hi;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+          "mov.b32 %0, {lo, hi};\n\t}"
+          : "=r"(w[h])
+          : "f"(a), "f"(b), "f"(c), "f"(e));
     } else {
       // added to 1.5 * 2^23, a number of up to 2^22 rounds to the integer that its
       // lowest bits then hold
@@ -69,6 +70,18 @@ __device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float inv) {
       w[h] = __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
     }
   }
+  return r;
+}
+
+// The largest magnitude, NaN if one of them is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -105,13 +118,42 @@ __device__ __forceinline__ CachePlace cache_place(int64_t place, const int32_t* 
   return at;
 }
 
-// A lane holds 8 neighbouring channels of a row and fetches their partners of the
-// rotation again beside them (from the first-level cache, in pieces of kVec channels,
-// the widest that divides the pairs), so that rows of every layout are read, reduced to
-// their maximum and written in their natural order, by 1 to 32 lanes each.
+// A lane's channels of a row: two vectors of 8 (cb < 0: one).  Where channels i and
+// pairs + i of an axis form a pair and 8 divides the pairs (kVec = 8), a lane of the
+// rotated channels has 8 pairs; else they are 16 neighbours.
+struct Q8Place {
+  int ca, cb, turn;  // turn: the first pair, < 0 behind the rotated channels
+};
+template <int kVec>
+__device__ __forceinline__ Q8Place q8_place(int unit, const AppendQ8Params& p) {
+  Q8Place at{unit * 16, unit * 16 + 8, -1};
+  if (kVec == 8) {
+    const int per_axis = p.pairs >> 3, rot = p.axes * per_axis;
+    if (unit < rot) {
+      const int axis = unit >= per_axis ? 1 : 0, i0 = (unit - axis * per_axis) * 8;
+      at.ca = 2 * axis * p.pairs + i0;
+      at.cb = at.ca + p.pairs;
+      at.turn = axis * p.pairs + i0;
+      return at;
+    }
+    at.ca = 2 * p.axes * p.pairs + (unit - rot) * 16;
+    at.cb = at.ca + 8;
+  }
+  if (at.cb >= p.d) at.cb = -1;
+  return at;
+}
+
+constexpr int kNeighbours = 16;
+
+// A row takes 1 to 16 lanes with up to 16 channels each, and is reduced to its maximum
+// between them.  Pairs that do not come in eights (kVec < 8) have their partners fetched a
+// second time beside them, in pieces of kVec channels; pairs of neighbours (kNeighbours)
+// are in a lane in any case.
 template <bool kBf16, int kFmt, int kVec>
-__global__ void __launch_bounds__(kQ8Warps * 32, 8) kv_append_q8_kernel(const AppendQ8Params p) {
-  using V = typename VecOf<kVec>::T;
+__global__ void __launch_bounds__(kQ8Warps * 32, kVec >= 8 ? 6 : 4)
+kv_append_q8_kernel(const AppendQ8Params p) {
+  constexpr int kPiece = kVec >= 8 ? 8 : kVec, kAgain = kVec >= 8 ? 1 : 2;
+  using V = typename VecOf<kPiece>::T;
   constexpr float kTop = kFmt == kE4m3 ? 448.f : 127.f;
   extern __shared__ __align__(16) float2 app_turns[];  // [warp][axes * pairs] cos, sin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -121,31 +163,40 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 8) kv_append_q8_kernel(const Ap
   const int part = static_cast<int>(gw) & ((1 << p.share) - 1);
   const int angles = p.axes * p.pairs, rotated = 2 * angles;
   float2* turn = app_turns + warp * ((angles + 1) & ~1);
-  const int c0 = (lane & ((1 << p.row_lanes) - 1)) * 8;  // this lane's channels
-  const bool live = c0 < p.d;
+  const int sub = lane >> p.row_lanes;                   // row of the pass
   const int per_pass = 32 >> p.row_lanes;                // rows of a pass over the warp
+  const int unit = lane & ((1 << p.row_lanes) - 1);
+  const Q8Place at = q8_place<kVec>(unit, p);
+  const bool live = at.ca < p.d, both = at.cb >= 0;
   const int n_rows = p.Hq + 2 * p.Hkv;                   // queries, keys, values
-  const int first = part * per_pass + (lane >> p.row_lanes), step = per_pass << p.share;
+  const int first = part * per_pass, step = per_pass << p.share;
+  const uint16_t* q_row = p.q + t * p.q_ts;  // never read without queries
+  const uint16_t* k_row = p.k + t * p.k_ts - p.Hq * p.k_hs;
+  const uint16_t* v_row = p.v + t * p.v_ts - (p.Hq + p.Hkv) * p.v_hs;
 
-  uint4 x[kQ8Batch];
-  union Partner { uint4 v; V part[8 / kVec]; } y[kQ8Batch];
-  auto fetch = [&](int r0) {
+  uint4 x[kQ8Batch][2];
+  union Partner { uint4 v; V part[8 / kPiece]; } y[kQ8Batch][kAgain];
+  auto fetch = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kQ8Batch; ++i) {
-      const int r = r0 + i * step;
-      if (r >= n_rows || !live) break;
-      const uint16_t* src = r < p.Hq             ? p.q + t * p.q_ts + r * p.q_hs
-                            : r < p.Hq + p.Hkv   ? p.k + t * p.k_ts + (r - p.Hq) * p.k_hs
-                                                 : p.v + t * p.v_ts + (r - p.Hq - p.Hkv) * p.v_hs;
-      x[i] = *reinterpret_cast<const uint4*>(src + c0);
-      if (p.paired || r >= p.Hq + p.Hkv) continue;
+      const int r = base + i * step + sub;
+      const bool is_v = r >= p.Hq + p.Hkv;
+      if (r >= n_rows || !live) continue;
+      const uint16_t* src = r < p.Hq ? q_row + r * p.q_hs : is_v ? v_row + r * p.v_hs : k_row + r * p.k_hs;
+      x[i][0] = *reinterpret_cast<const uint4*>(src + at.ca);
+      if (both) x[i][1] = *reinterpret_cast<const uint4*>(src + at.cb);
+      if constexpr (kVec < 8) {
+        if (is_v) continue;
 #pragma unroll
-      for (int s = 0; s < 8 / kVec; ++s) {
-        const int c = c0 + s * kVec;
-        if (c >= rotated) break;
-        const int in = c >= 2 * p.pairs ? c - 2 * p.pairs : c;  // within its axis
-        y[i].part[s] =
-            *reinterpret_cast<const V*>(src + (in < p.pairs ? c + p.pairs : c - p.pairs));
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < 8 / kPiece; ++s) {
+            const int c = at.ca + 8 * h + s * kPiece;
+            if (c >= rotated) break;
+            const int in = c >= 2 * p.pairs ? c - 2 * p.pairs : c;  // within its axis
+            y[i][h].part[s] =
+                *reinterpret_cast<const V*>(src + (in < p.pairs ? c + p.pairs : c - p.pairs));
+          }
       }
     }
   };
@@ -154,8 +205,11 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 8) kv_append_q8_kernel(const Ap
   const int b = find_sequence(p.cu, p.B, t, lane);
   if (b < 0 || b >= p.B) return;
   const int64_t place = static_cast<int64_t>(__ldg(p.start + b)) + t - __ldg(p.cu + b);
-  const CachePlace at =
+  const CachePlace to =
       cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page_size, p.num_pages);
+  uint8_t* const k_to = p.kc + to.page * p.kc_ps + to.row * p.kc_ts;
+  uint8_t* const v_to = p.vc + to.page * p.vc_ps + to.row * p.vc_ts;
+  float* const s_to = p.scales + to.page * p.s_ps + 2 * to.row;
   for (int a = lane; a < angles; a += 32) {
     const int axis = a >= p.pairs ? 1 : 0;
     const double pos = p.positions ? static_cast<double>(__ldg(p.positions + t * p.pos_ts + axis))
@@ -168,79 +222,99 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 8) kv_append_q8_kernel(const Ap
   }
   __syncwarp();
   // (the bound is the warp's, so that all its lanes reach the reductions)
-  for (int r0 = first; r0 - (lane >> p.row_lanes) < n_rows; r0 += kQ8Batch * step) {
-    if (r0 != first) fetch(r0);
+#pragma unroll 1
+  for (int base = first; base < n_rows; base += kQ8Batch * step) {
+    if (base != first) fetch(base);
     __syncwarp();  // rows rotated in place are written behind every lane's reads
 #pragma unroll
     for (int i = 0; i < kQ8Batch; ++i) {
-      const int r = r0 + i * step;
-      if (r - (lane >> p.row_lanes) >= n_rows) break;
-      const bool here = live && r < n_rows;
-      const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
-      float f[8];
-      const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      const int r = base + i * step + sub;
+      if (r - sub >= n_rows) break;
+      const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
+      const bool here = r < n_rows && live, two = here && both;
+      float f[16];
+      const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                             x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 u = here ? unpack2<kBf16>(xw[e]) : make_float2(0.f, 0.f);
+      for (int e = 0; e < 8; ++e) {
+        const float2 u = unpack2<kBf16>((e < 4 ? here : two) ? w[e] : 0u);
         f[2 * e] = u.x, f[2 * e + 1] = u.y;
       }
-      if (here && (is_q || is_k) && c0 < rotated) {
-        if (p.paired) {
+      if (!is_v && here) {
+        if constexpr (kVec == kNeighbours) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (c0 + 2 * e >= rotated) break;
-            const float2 cs = turn[c0 / 2 + e];
-            const float one = f[2 * e], two = f[2 * e + 1];
-            f[2 * e] = one * cs.x - two * cs.y;
-            f[2 * e + 1] = two * cs.x + one * cs.y;
+          for (int e = 0; e < 8; ++e) {
+            if (at.ca + 2 * e >= rotated) break;
+            const float2 cs = turn[at.ca / 2 + e];
+            const float one = f[2 * e], other = f[2 * e + 1];
+            f[2 * e] = one * cs.x - other * cs.y;
+            f[2 * e + 1] = other * cs.x + one * cs.y;
+          }
+        } else if constexpr (kVec == 8) {
+          if (at.turn >= 0) {
+            const float4* cs = reinterpret_cast<const float4*>(turn + at.turn);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 z = cs[e];
+              const float a0 = f[2 * e], a1 = f[2 * e + 1], b0 = f[8 + 2 * e], b1 = f[9 + 2 * e];
+              f[2 * e] = a0 * z.x - b0 * z.y;
+              f[2 * e + 1] = a1 * z.z - b1 * z.w;
+              f[8 + 2 * e] = b0 * z.x + a0 * z.y;
+              f[9 + 2 * e] = b1 * z.z + a1 * z.w;
+            }
           }
         } else {
-          const uint32_t yw[4] = {y[i].v.x, y[i].v.y, y[i].v.z, y[i].v.w};
-          float g[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack2<kBf16>(yw[e]);
-            g[2 * e] = u.x, g[2 * e + 1] = u.y;
-          }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t yw[4] = {y[i][h].v.x, y[i][h].v.y, y[i][h].v.z, y[i][h].v.w};
+            float g[8];
 #pragma unroll
-          for (int s = 0; s < 8 / kVec; ++s) {
-            const int c = c0 + s * kVec;
-            if (c >= rotated) break;
-            const int axis = c >= 2 * p.pairs ? 1 : 0, in = c - 2 * axis * p.pairs;
-            const bool second = in >= p.pairs;
-            const float2* cs = turn + axis * p.pairs + (second ? in - p.pairs : in);
+            for (int e = 0; e < 4; ++e) {
+              const float2 u = unpack2<kBf16>(yw[e]);
+              g[2 * e] = u.x, g[2 * e + 1] = u.y;
+            }
 #pragma unroll
-            for (int e = s * kVec; e < (s + 1) * kVec; ++e) {
-              const float2 z = cs[e - s * kVec];
-              f[e] = f[e] * z.x + g[e] * (second ? z.y : -z.y);
+            for (int s = 0; s < 8 / kPiece; ++s) {
+              const int c = at.ca + 8 * h + s * kPiece;
+              if (c >= rotated) break;
+              const int axis = c >= 2 * p.pairs ? 1 : 0, in = c - 2 * axis * p.pairs;
+              const bool second = in >= p.pairs;
+              const float2* cs = turn + axis * p.pairs + (second ? in - p.pairs : in);
+#pragma unroll
+              for (int e = s * kPiece; e < (s + 1) * kPiece; ++e) {
+                const float2 z = cs[e - s * kPiece];
+                f[8 * h + e] = f[8 * h + e] * z.x + g[e] * (second ? z.y : -z.y);
+              }
             }
           }
         }
       }
-      if (here && (is_q || (is_k && p.k_out))) {
+      if (here && (is_q || (!is_v && p.k_out))) {
         uint16_t* dst = is_q ? p.q_out + t * p.qo_ts + r * p.qo_hs
                              : p.k_out + t * p.ko_ts + (r - p.Hq) * p.ko_hs;
-        *reinterpret_cast<uint4*>(dst + c0) =
+        *reinterpret_cast<uint4*>(dst + at.ca) =
             make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]),
                        pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
+        if (two)
+          *reinterpret_cast<uint4*>(dst + at.cb) =
+              make_uint4(pack2<kBf16>(f[8], f[9]), pack2<kBf16>(f[10], f[11]),
+                         pack2<kBf16>(f[12], f[13]), pack2<kBf16>(f[14], f[15]));
       }
-      if (r - (lane >> p.row_lanes) + per_pass <= p.Hq) continue;  // queries only
-      // the largest magnitude by its bits: a NaN's are above infinity's
-      uint32_t top = 0;
+      if (r - sub + per_pass <= p.Hq) continue;  // queries only
+      float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 8; ++e) top = max_abs(top, f[2 * e], f[2 * e + 1]);
       for (int o = 1; o < (1 << p.row_lanes); o <<= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!here || is_q || at.page < 0) continue;
-      float scale = fmaxf(__fdiv_rn(__uint_as_float(top), kTop), kQ8MinScale);
-      if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);
-      const uint2 codes = q8_codes<kFmt>(f, __fdiv_rn(1.f, scale));
-      const int h = is_k ? r - p.Hq : r - p.Hq - p.Hkv;
-      uint8_t* dst = is_k ? p.kc + at.page * p.kc_ps + at.row * p.kc_ts + h * p.kc_hs
-                          : p.vc + at.page * p.vc_ps + at.row * p.vc_ts + h * p.vc_hs;
-      *reinterpret_cast<uint2*>(dst + c0) = codes;
-      if (c0 == 0)
-        p.scales[at.page * p.s_ps + h * p.s_hs + 2 * at.row + (is_k ? 0 : 1)] = scale;
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (!here || is_q || to.page < 0) continue;
+      const float scale = top < -kNegInf ? fmaxf(__fdiv_rn(top, kTop), kQ8MinScale)
+                                         : __uint_as_float(0x7FC00000u);
+      const float inv = __fdiv_rn(1.f, scale);
+      const int h = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
+      uint8_t* dst = is_v ? v_to + h * p.vc_hs : k_to + h * p.kc_hs;
+      *reinterpret_cast<uint2*>(dst + at.ca) = q8_codes<kFmt>(f, inv);
+      if (two) *reinterpret_cast<uint2*>(dst + at.cb) = q8_codes<kFmt>(f + 8, inv);
+      if (unit == 0) s_to[h * p.s_hs + (is_v ? 1 : 0)] = scale;
     }
   }
 }
@@ -258,7 +332,7 @@ struct ReadQ8Params {
   FastDiv by_row;                   // 8-channel units of a row
 };
 
-constexpr int kReadBatch = 4;
+constexpr int kReadBatch = 8;
 
 // One warp a token (for few tokens up to 8); a unit is 8 channels of a head, the keys'
 // units first.

@@ -3451,7 +3451,8 @@ static int token_share(int64_t T, int sms) {
 template <bool kBf16, int kFmt>
 static void append_q8_launch(const AppendQ8Params& p, int vec, dim3 grid, size_t smem, cudaStream_t s) {
   const dim3 block(kQ8Warps * 32);
-  if (vec == 8) kv_append_q8_kernel<kBf16, kFmt, 8><<<grid, block, smem, s>>>(p);
+  if (vec == kNeighbours) kv_append_q8_kernel<kBf16, kFmt, kNeighbours><<<grid, block, smem, s>>>(p);
+  else if (vec == 8) kv_append_q8_kernel<kBf16, kFmt, 8><<<grid, block, smem, s>>>(p);
   else if (vec == 4) kv_append_q8_kernel<kBf16, kFmt, 4><<<grid, block, smem, s>>>(p);
   else if (vec == 2) kv_append_q8_kernel<kBf16, kFmt, 2><<<grid, block, smem, s>>>(p);
   else kv_append_q8_kernel<kBf16, kFmt, 1><<<grid, block, smem, s>>>(p);
@@ -3587,10 +3588,15 @@ rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stre
   p.page_size = a.page_size;
   p.pairs = pairs;
   p.axes = axes;
-  p.paired = a.paired != 0;
   p.share = token_share(T, di->sms);
-  while ((8 << p.row_lanes) < d) ++p.row_lanes;
-  const int vec = p.paired || pairs % 8 == 0 ? 8 : pairs % 4 == 0 ? 4 : pairs % 2 == 0 ? 2 : 1;
+  const int vec = a.paired && pairs      ? kNeighbours
+                  : pairs % 8 == 0 ? 8
+                  : pairs % 4 == 0 ? 4
+                  : pairs % 2 == 0 ? 2
+                                   : 1;
+  // lanes of a row: those of the rotated pairs, then of what is left
+  const int rotated = vec == 8 ? 2 * pairs * axes : 0;
+  while ((1 << p.row_lanes) < rotated / 16 + (d - rotated + 15) / 16) ++p.row_lanes;
   const dim3 grid(static_cast<unsigned>(((T << p.share) + kQ8Warps - 1) / kQ8Warps));
   // (each warp's turns start on 16 bytes)
   const size_t smem = static_cast<size_t>(kQ8Warps) * ((axes * pairs + 1) & ~1) * sizeof(float2);
