@@ -29,17 +29,23 @@
 namespace rnn {
 
 constexpr int kQ8Keys = 32;  // keys per warp and tile, the lanes of a warp
+// Three CTAs per SM for up to 8 query heads a key head, with two tiles each a warp.
 template <int kDP>
 struct DecQ8Shape {
   static constexpr int kTile = kDecWarps * kQ8Keys;
   static constexpr int kStageBytes = 2 * kQ8Keys * kDP + kQ8Keys * 8;  // K, V, scales
-  static constexpr int kStages = 384 / kDP;                            // 25 KB a warp
-  static constexpr int kMergeRow = kDP + 4;
-  static constexpr int kMergeBytes = 2 * 8 * kMergeRow * 4;
-  static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes + kMergeBytes +
+  static constexpr int kStages = 256 / kDP;                            // 17 KB a warp
+  static constexpr int kMergeRow = kDP + 4;                            // floats
+  // a warp's sums of two times 8 heads take the place of the tile it has just used
+  static_assert(2 * 8 * kMergeRow * 4 <= kStageBytes, "");
+  static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes +
                                   kDecWarps * kDecRows * 8 + kDecWarps * kStages * 4;
 };
 
+// 16 bytes to shared memory.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 8 bytes to shared memory; with `live` false they are zeroed and nothing is read.
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
   const int n = live ? 8 : 0;
@@ -66,7 +72,8 @@ __device__ __forceinline__ uint32_t q8_halves(uint32_t w) {
 }
 
 template <bool kBf16, int kFmt, int kDP, int kNT, bool kLong>
-__global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecWarps * 32, kNT == 1 ? 3 : 2)
+attn_decode_q8_kernel(const DecodeParams p) {
   using S = DecQ8Shape<kDP>;
   constexpr int kStages = S::kStages;
   constexpr int kMT = kQ8Keys / 16;      // 16-key groups
@@ -77,9 +84,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
   constexpr float kWeightTop = 32768.f, kWeightAim = 64.f;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_u32(dec_smem) + warp * kStages * S::kStageBytes;
-  float* merge = reinterpret_cast<float*>(dec_smem + kDecWarps * kStages * S::kStageBytes);
-  float2* ml = reinterpret_cast<float2*>(merge + 2 * 8 * S::kMergeRow);  // [warp][16]
+  uint8_t* const tiles = dec_smem + warp * kStages * S::kStageBytes;
+  const uint32_t ring = smem_u32(tiles);
+  float2* ml = reinterpret_cast<float2*>(dec_smem + kDecWarps * kStages * S::kStageBytes);  // [warp][16]
   uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
 
   const int Hv = p.Hkv * p.hblocks;
@@ -127,12 +134,24 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
     cp_async8(vdst + kQ8Keys * kDP + lane * 8, id >= 0 ? sc : p.scales, id >= 0);
     if (p.page16) {
       // pages are whole 16-key groups: one base per group, no shuffles per row
+      const bool all = p.wide && valid == 0xffffffffu && kChunks * 16 == p.d;
 #pragma unroll
       for (int g = 0; g < kMT; ++g) {
         const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
         const int row = __shfl_sync(0xffffffffu, my_row, g * 16) + sub;
         const uint8_t* ks = p.kc8 + (page * p.k_ps + hk * p.k_hs + row * p.k_ts + ch * 16);
         const uint8_t* vs = p.vc8 + (page * p.v_ps + hk * p.v_hs + row * p.v_ts + ch * 16);
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsPer; ++i) {
+            const int r = g * 16 + i * kRowsPer + sub;
+            cp_async16(dst + k_at(r, ch), ks);
+            cp_async16(vdst + v_at(r, ch), vs);
+            ks += kRowsPer * p.k_ts;
+            vs += kRowsPer * p.v_ts;
+          }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 16 / kRowsPer; ++i) {
           const int r = g * 16 + i * kRowsPer + sub;
@@ -256,8 +275,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
     cp_async_wait<kStages - 2>();
     __syncwarp();
     issue_next();
-    const uint32_t kb = ring + stage * S::kStageBytes, vb = kb + kQ8Keys * kDP;
-    const uint32_t sb = vb + kQ8Keys * kDP;
+    const uint8_t* const kb = tiles + stage * S::kStageBytes;
+    const uint8_t* const vb = kb + kQ8Keys * kDP;
+    const float2* const sb = reinterpret_cast<const float2*>(vb + kQ8Keys * kDP);
     const uint32_t valid = masks[stage];
     if (valid) {
       float s[kMT][kNT][4];
@@ -273,7 +293,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
         const int ra = t * 16 + g, rb = ra + 8;
 #pragma unroll
         for (int hh = 0; hh < kDP / 64; ++hh) {
-          const uint4 wa = lds_v4(kb + k_at(ra, hh * 4 + q)), wb = lds_v4(kb + k_at(rb, hh * 4 + q));
+          const uint4 wa = *reinterpret_cast<const uint4*>(kb + k_at(ra, hh * 4 + q));
+          const uint4 wb = *reinterpret_cast<const uint4*>(kb + k_at(rb, hh * 4 + q));
           const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
@@ -286,17 +307,24 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
                                qf[n][hh * 4 + st][1]);
           }
         }
-        const float2 sa = lds_f2(sb + ra * 8), sc = lds_f2(sb + rb * 8);
+        const float2 sa = sb[ra], sc = sb[rb];
         vscale[t][0] = sa.y, vscale[t][1] = sc.y;
-        const bool in_a = (valid >> ra) & 1u, in_b = (valid >> rb) & 1u;
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[t][n][e] = in_a ? (s[t][n][e] + s1[n][e]) * (sa.x * ch_scale[n][e]) : kNegInf;
-            s[t][n][e + 2] =
-                in_b ? (s[t][n][e + 2] + s1[n][e + 2]) * (sc.x * ch_scale[n][e]) : kNegInf;
+            s[t][n][e] = (s[t][n][e] + s1[n][e]) * (sa.x * ch_scale[n][e]);
+            s[t][n][e + 2] = (s[t][n][e + 2] + s1[n][e + 2]) * (sc.x * ch_scale[n][e]);
           }
+      }
+      if (valid != 0xffffffffu) {
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((valid >> (t * 16 + g + (e >> 1) * 8)) & 1u))
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) s[t][n][e] = kNegInf;
       }
       // ---- the softmax's reference, and p = 2^(score - reference)
       float x[kNT][2], shrink[kNT][2];
@@ -386,11 +414,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
         for (int i = 0; i < 4; ++i) {
           const int row = r + (i & 1) + (i >> 1) * 8;
           if constexpr (kDP == 128) {
-            const uint4 v = lds_v4(vb + v_at(row, g));
+            const uint4 v = *reinterpret_cast<const uint4*>(vb + v_at(row, g));
             w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
           } else {
-            const float2 v = lds_f2(vb + v_at(row, g >> 1) + (g & 1) * 8);
-            w[i][0] = __float_as_uint(v.x), w[i][1] = __float_as_uint(v.y);
+            const uint2 v = *reinterpret_cast<const uint2*>(vb + v_at(row, g >> 1) + (g & 1) * 8);
+            w[i][0] = v.x, w[i][1] = v.y;
           }
         }
 #pragma unroll
@@ -408,6 +436,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
           }
       }
     }
+    const int used = stage;
     stage = stage + 1 == kStages ? 0 : stage + 1;
     const bool last = cur.j == cur.n - 1;
     if (kLong && --until == 0) {
@@ -452,6 +481,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
       const bool done = whole && last;
       // a pair that began in an earlier share fills slot 0, one that goes on slot 1
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (whole ? 1 : 0);
+      // the warps' sums, at the pair's reference, in the places of the tiles they used
+      float* const mine = reinterpret_cast<float*>(tiles + used * S::kStageBytes);
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         if (n * 8 >= rows) break;
@@ -463,21 +494,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
           for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + n * 8 + q2 + e].x);
           r[e] = m[n][e] == kNegInf ? 0.f : exp2_approx(m[n][e] - M) / f[n][e];
         }
-        float* buf = merge + (warp & 1) * 8 * S::kMergeRow;
-        auto each = [&](auto&& op) {
 #pragma unroll
-          for (int c = 0; c < kSteps; ++c)
+        for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              op(buf[(q2 + (e & 1)) * S::kMergeRow + kLaneCh * g + 2 * c + (e >> 1)], o[n][c][e],
-                 r[e & 1]);
-        };
-        if (warp >= 2) each([](float& to, float a, float b) { to = a * b; });
-        __syncthreads();
-        if (warp < 2) each([](float& to, float a, float b) { to = fmaf(a, b, to); });
-        __syncthreads();
-        for (int i = warp; i < 8 && n * 8 + i < rows; i += kDecWarps) {
-          const int row = n * 8 + i;
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(mine + (n * 8 + q2 + e) * S::kMergeRow + kLaneCh * g + 2 * c) =
+                make_float2(o[n][c][e] * r[e], o[n][c][e + 2] * r[e]);
+      }
+      __syncthreads();
+      {
+        const int used_all = used * S::kStageBytes;  // (the same in every warp)
+        for (int row = warp; row < rows; row += kDecWarps) {
           float M = kNegInf, L = 0.f;
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + row].x);
@@ -488,25 +515,28 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_q8_kernel(const
             L += a.x == kNegInf ? a.y : a.y * exp2_approx(a.x - M);
           }
           const float inv = L != 0.f ? 1.f / L : 0.f;
-          const float* b0 = merge + i * S::kMergeRow;
-          const float* b1 = b0 + 8 * S::kMergeRow;
-          if (done) {
-            uint16_t* ob = p.out + cur.b * p.o_bs + (head0 + row) * p.o_hs;
-            for (int c = lane * 2; c < p.d; c += 64)
-              *reinterpret_cast<uint32_t*>(ob + c) =
-                  pack2<kBf16>((b0[c] + b1[c]) * inv, (b0[c + 1] + b1[c + 1]) * inv);
-            if (p.lse && lane == 0)
+          for (int c = lane * 2; c < kDP; c += 64) {
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+              const float2 a = *reinterpret_cast<const float2*>(
+                  dec_smem + w * kStages * S::kStageBytes + used_all + (row * S::kMergeRow + c) * 4);
+              sum.x += a.x, sum.y += a.y;
+            }
+            if (!done)
+              *reinterpret_cast<float2*>(p.part + (slot * kDecRows + row) * kDP + c) = sum;
+            else if (c < p.d)
+              *reinterpret_cast<uint32_t*>(p.out + cur.b * p.o_bs + (head0 + row) * p.o_hs + c) =
+                  pack2<kBf16>(sum.x * inv, sum.y * inv);
+          }
+          if (lane == 0) {
+            if (!done)
+              p.part_ml[slot * kDecRows + row] = make_float2(M, L);
+            else if (p.lse)
               p.lse[static_cast<int64_t>(cur.b) * p.Hq + head0 + row] =
                   L != 0.f ? (M + log2f(L)) * 0.69314718f : kNegInf;
-          } else {
-            float* pb = p.part + (slot * kDecRows + row) * kDP;
-            for (int c = lane * 2; c < kDP; c += 64)
-              *reinterpret_cast<float2*>(pb + c) =
-                  make_float2(b0[c] + b1[c], b0[c + 1] + b1[c + 1]);
-            if (lane == 0) p.part_ml[slot * kDecRows + row] = make_float2(M, L);
           }
         }
-        if (n + 1 < kNT) __syncthreads();  // the next heads reuse the buffer
       }
       if (whole && threadIdx.x == 0) {
         int c1 = blockIdx.x;

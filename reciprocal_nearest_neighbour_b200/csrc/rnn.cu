@@ -3189,20 +3189,22 @@ static rnn_status decode_launch(const DecodeParams& p, dim3 grid, cudaStream_t s
 extern "C" {
 
 // Grid of the decode kernel: two CTAs per SM, or one per tile when there are fewer.
-constexpr int kDecMaxGrid = 2 * 160;
+constexpr int kDecMaxGrid = 2 * 160, kDecQ8MaxGrid = 3 * 160;
 struct DecWs {
   int* err;
   float* part;
   float2* ml;
   int2* span;
 };
-static size_t dec_layout(void* ws, int64_t B, int Hkv, int group, int d, DecWs* w) {
+// most: CTAs that may leave parts.
+static size_t dec_layout(void* ws, int64_t B, int Hkv, int group, int d, DecWs* w,
+                         int64_t most = kDecMaxGrid) {
   Carve c(ws);
   w->err = c.take<int>(64);
   const int64_t dp = d <= 64 ? 64 : 128;
   w->span = c.take<int2>(B * Hkv * ((group + kDecRows - 1) / kDecRows));
-  w->ml = c.take<float2>(int64_t{kDecMaxGrid} * 2 * kDecRows);
-  w->part = c.take<float>(int64_t{kDecMaxGrid} * 2 * kDecRows * dp);
+  w->ml = c.take<float2>(most * 2 * kDecRows);
+  w->part = c.take<float>(most * 2 * kDecRows * dp);
   return c.off;
 }
 
@@ -3234,11 +3236,10 @@ static DecodeParams decode_params(const rnn_rows& q, const rnn_rows& out, const 
   p.err = w.err;
   return p;
 }
-static dim3 decode_grid(const DecodeParams& p, int per_tile, int sms) {
+static dim3 decode_grid(const DecodeParams& p, int per_tile, int most) {
   const int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
   const int64_t keys = room < INT32_MAX ? room : INT32_MAX;
   const int64_t tiles = (keys + per_tile - 1) / per_tile * p.B * p.Hkv * p.hblocks;
-  const int most = std::min(2 * sms, kDecMaxGrid);
   return dim3(static_cast<unsigned>(tiles < most ? tiles : most));
 }
 
@@ -3297,7 +3298,8 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args* args, rnn_stream_t stream
   p.num_pages = num_pages;
   p.B = B;
   p.max_pages = max_pages;
-  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile, di->sms);
+  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile,
+                                std::min(2 * di->sms, kDecMaxGrid));
   const bool bf = dtype == RNN_BF16;
   if (d <= 64)
     return bf ? decode_launch<true, 64>(p, grid, s) : decode_launch<false, 64>(p, grid, s);
@@ -3664,7 +3666,9 @@ rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args* args, rnn_stream_t stream) 
 }
 
 size_t rnn_attn_decode_q8_workspace_size(int B, int Hq, int Hkv, int d) {
-  return rnn_attn_decode_workspace_size(B, Hq, Hkv, d);
+  if (B < 0 || check_heads(Hq, Hkv, d, RNN_ATTN_MAX_DIM, RNN_F16) != RNN_OK) return 0;
+  DecWs w;
+  return dec_layout(nullptr, B, Hkv, Hq / Hkv, d, &w, kDecQ8MaxGrid);
 }
 
 rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t stream) {
@@ -3698,7 +3702,7 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
     return launched();
   }
   DecWs w;
-  dec_layout(a.workspace, B, Hkv, Hq / Hkv, d, &w);
+  dec_layout(a.workspace, B, Hkv, Hq / Hkv, d, &w, kDecQ8MaxGrid);
   DecodeParams p =
       decode_params(a.q, a.out, a.k_cache, a.v_cache, w, a.page_size, Hkv, Hq / Hkv, d, a.scale);
   p.kc8 = static_cast<const uint8_t*>(a.k_cache.data);
@@ -3714,7 +3718,10 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
   p.B = B;
   p.max_pages = a.max_pages;
   static_assert(DecQ8Shape<64>::kTile == DecQ8Shape<128>::kTile, "");
-  const dim3 grid = decode_grid(p, DecQ8Shape<128>::kTile, di->sms);
+  // as many CTAs as run at once
+  const int per_sm = p.group <= 8 ? 3 : 2;
+  const dim3 grid =
+      decode_grid(p, DecQ8Shape<128>::kTile, std::min(per_sm * di->sms, kDecQ8MaxGrid));
   const bool bf = a.dtype == RNN_BF16, int8 = a.codes == RNN_CODES_INT8;
   return d <= 64 ? decode_q8_dispatch<64>(p, bf, int8, grid, s) : decode_q8_dispatch<128>(p, bf, int8, grid, s);
 }
@@ -3907,7 +3914,8 @@ rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args* args, rnn_s
   pre.stall_loads = g_stall_loads.load(std::memory_order_relaxed);
   pre.wait_limit_ns = pre.stall_loads ? g_stall_limit_ns.load(std::memory_order_relaxed)
                                       : kWaitLimitNs;
-  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile, di->sms);
+  const dim3 grid = decode_grid(p, d <= 64 ? DecShape<64>::kTile : DecShape<128>::kTile,
+                                std::min(2 * di->sms, kDecMaxGrid));
   const unsigned ctas = static_cast<unsigned>(plan.ctas);
   const bool bf = dtype == RNN_BF16;
   if (d <= 64)
