@@ -86,10 +86,10 @@ struct DecodeParams {
   int2* span;                      // [B][Hkv * hblocks] first and last CTA of a pair
   float* row_part;                 // [B][Hq][kDP] and [B][Hq]: parts of pairs in one share
   float2* row_ml;
-  // caches of codes (attn_decode_q8_kernel), whose strides are in bytes
+  // caches of codes (attn_decode_q8_kernel)
   const uint8_t *kc8, *vc8;
   const float* scales;             // [page][head][row][key, value]
-  int64_t s_ps, s_hs;
+  int k_s8[3], v_s8[3], s_s8[3];   // strides of page, row and head in units of 8 bytes
   int wide;                        // rows start on 16 bytes and have whole 16-byte chunks
 };
 

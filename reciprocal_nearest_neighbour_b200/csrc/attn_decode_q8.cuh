@@ -15,11 +15,12 @@
 // also transposes them.
 //
 // Range.  Queries are scaled by a power of two to below 2^15 for fp16, and their scores
-// back together with ks_t, in fp32.  A value's weight is p_t vs_t with any size of vs_t,
-// but its fp16 operand holds 2^-24 to 2^16 only: it carries a factor f, a power of two for
-// each head that puts the largest weight so far at 2^6 when it is chosen, and is chosen
-// again, the sums following, when the softmax reference moves or a weight passes 2^15.
-// The totals are of p_t alone, in fp32.
+// back together with ks_t, in fp32.  The second product's operand is the weight
+// p_t vs_t with any size of vs_t, as fp16, which holds 2^-24 to 2^16.  So the running
+// reference z of a head is that of score + log2 vs, not of the score: with p_t =
+// 2^(score - z) the largest weight is put at 2^6 when z is chosen, and z is chosen again,
+// the sums following, when a weight passes 2^15.  The totals sum p_t in fp32, which z
+// keeps below 2^100, and whose least 2^-126 a value beyond about 2^100 would come near.
 #pragma once
 #include <cstdint>
 #include "attn_decode.cuh"
@@ -39,7 +40,7 @@ struct DecQ8Shape {
   // a warp's sums of two times 8 heads take the place of the tile it has just used
   static_assert(2 * 8 * kMergeRow * 4 <= kStageBytes, "");
   static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes +
-                                  kDecWarps * kDecRows * 8 + kDecWarps * kStages * 4;
+                                  kDecWarps * kDecRows * 8;
 };
 
 // 16 bytes to shared memory.
@@ -81,13 +82,13 @@ attn_decode_q8_kernel(const DecodeParams p) {
   constexpr int kChunks = kDP / 16;      // 16-byte chunks of a row
   constexpr int kRowsPer = 32 / kChunks; // rows moved by one warp-wide copy
   constexpr int kLaneCh = kDP / 8;       // a lane's channels of a value row
-  constexpr float kWeightTop = 32768.f, kWeightAim = 64.f;
+  constexpr float kWeightTop = 32768.f, kTotalTop = 1.2676506e30f;  // 2^15, 2^100
+  constexpr float kAim = 6.f, kTotalAim = 60.f;                      // log2
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* const tiles = dec_smem + warp * kStages * S::kStageBytes;
   const uint32_t ring = smem_u32(tiles);
   float2* ml = reinterpret_cast<float2*>(dec_smem + kDecWarps * kStages * S::kStageBytes);  // [warp][16]
-  uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
 
   const int Hv = p.Hkv * p.hblocks;
   DecCursor ld, cur;
@@ -101,6 +102,12 @@ attn_decode_q8_kernel(const DecodeParams p) {
     if (t >= k.len) return -1;
     const int id = __ldg(p.table + k.b * p.table_bs + fdiv(t, p.page));
     return (id >= 0 && id < p.num_pages) ? id : -1;
+  };
+  // Offsets of a row, from strides in units of 8 bytes.
+  auto row_at = [](int page, int row, int hk, const int (&stride)[3]) {
+    const int64_t units = static_cast<int64_t>(page) * stride[0] +
+                          static_cast<int64_t>(row) * stride[1] + static_cast<int64_t>(hk) * stride[2];
+    return units * 8;
   };
   // Where chunk ch of row r lies, so that eight lanes that read together (two key rows,
   // or two chunks of every second value row) meet no bank twice.
@@ -122,33 +129,34 @@ attn_decode_q8_kernel(const DecodeParams p) {
       cp_async8(dst + 8, b ? src + 8 : none, b);
     }
   };
-  auto issue = [&](int stage, const DecCursor& k, int id) {
+  auto issue = [&](int stage, const DecCursor& k, int id) -> unsigned {
     const int t0 = k.j * S::kTile + warp * kQ8Keys;
     const int hk = p.hblocks == 1 ? k.h : k.h / p.hblocks;
     const unsigned valid = __ballot_sync(0xffffffffu, id >= 0);
-    if (lane == 0) masks[stage] = valid;
     const uint32_t dst = ring + stage * S::kStageBytes, vdst = dst + kQ8Keys * kDP;
     const int t = t0 + lane;
     const int my_row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
-    const float* sc = p.scales + (id * p.s_ps + hk * p.s_hs + 2 * my_row);
-    cp_async8(vdst + kQ8Keys * kDP + lane * 8, id >= 0 ? sc : p.scales, id >= 0);
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(p.scales);
+    if (id >= 0) sc += row_at(id, my_row, hk, p.s_s8);
+    cp_async8(vdst + kQ8Keys * kDP + lane * 8, sc, id >= 0);
     if (p.page16) {
       // pages are whole 16-key groups: one base per group, no shuffles per row
       const bool all = p.wide && valid == 0xffffffffu && kChunks * 16 == p.d;
+      const int64_t k_step = int64_t{kRowsPer * 8} * p.k_s8[1], v_step = int64_t{kRowsPer * 8} * p.v_s8[1];
 #pragma unroll
       for (int g = 0; g < kMT; ++g) {
-        const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
+        const int page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
         const int row = __shfl_sync(0xffffffffu, my_row, g * 16) + sub;
-        const uint8_t* ks = p.kc8 + (page * p.k_ps + hk * p.k_hs + row * p.k_ts + ch * 16);
-        const uint8_t* vs = p.vc8 + (page * p.v_ps + hk * p.v_hs + row * p.v_ts + ch * 16);
+        const uint8_t* ks = p.kc8 + row_at(page, row, hk, p.k_s8) + ch * 16;
+        const uint8_t* vs = p.vc8 + row_at(page, row, hk, p.v_s8) + ch * 16;
         if (all) {
 #pragma unroll
           for (int i = 0; i < 16 / kRowsPer; ++i) {
             const int r = g * 16 + i * kRowsPer + sub;
             cp_async16(dst + k_at(r, ch), ks);
             cp_async16(vdst + v_at(r, ch), vs);
-            ks += kRowsPer * p.k_ts;
-            vs += kRowsPer * p.v_ts;
+            ks += k_step;
+            vs += v_step;
           }
           continue;
         }
@@ -158,14 +166,13 @@ attn_decode_q8_kernel(const DecodeParams p) {
           const bool live = (valid >> r) & 1u;
           copy(dst + k_at(r, ch), ks, p.kc8, live);
           copy(vdst + v_at(r, ch), vs, p.vc8, live);
-          ks += kRowsPer * p.k_ts;
-          vs += kRowsPer * p.v_ts;
+          ks += k_step;
+          vs += v_step;
         }
       }
-      return;
+      return valid;
     }
-    const int64_t ko = id * p.k_ps + my_row * p.k_ts + hk * p.k_hs;
-    const int64_t vo = id * p.v_ps + my_row * p.v_ts + hk * p.v_hs;
+    const int64_t ko = row_at(id, my_row, hk, p.k_s8), vo = row_at(id, my_row, hk, p.v_s8);
 #pragma unroll
     for (int i = 0; i < kQ8Keys / kRowsPer; ++i) {
       const int r = i * kRowsPer + sub;
@@ -175,17 +182,21 @@ attn_decode_q8_kernel(const DecodeParams p) {
       copy(dst + k_at(r, ch), p.kc8 + k_off + ch * 16, p.kc8, live);
       copy(vdst + v_at(r, ch), p.vc8 + v_off + ch * 16, p.vc8, live);
     }
+    return valid;
   };
 
   int fill = 0, stage = 0;  // ring places of the next load and of the current tile
   int next_id = page_of(ld);
+  unsigned there[kStages];  // keys of the tiles in the ring, the current one's first
   auto issue_next = [&]() {
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) there[i] = there[i + 1];
     if (ld.at < hi) {
       const DecCursor now = ld;
       const int id = next_id;
       advance(ld);
       if (ld.at < hi) next_id = page_of(ld);  // the next tile's pages are looked up a tile ahead
-      issue(fill, now, id);
+      there[kStages - 1] = issue(fill, now, id);
     }
     fill = fill + 1 == kStages ? 0 : fill + 1;
     cp_async_commit();
@@ -197,9 +208,9 @@ attn_decode_q8_kernel(const DecodeParams p) {
   uint32_t qf[kNT][kSteps][2];
   float o[kNT][kSteps][4];   // channel kLaneCh g + 2 c (+ 1 in 2, 3), head 8 n + 2 q (+ 1 in 1, 3)
   float ch_scale[kNT][2];    // of those heads: scale * log2(e) / the queries' factor
-  float m[kNT][2], l[kNT][2], f[kNT][2];
+  float z[kNT][2], l[kNT][2];
   constexpr int kSums = kNT * kSteps * 4, kHoldTiles = kDecHoldKeys / kQ8Keys;
-  volatile float held[kSums + 6 * kNT];  // sums taken out, their totals, references, factors
+  volatile float held[kSums + 4 * kNT];  // sums taken out, their totals and references
   bool any_held = false;
   int until = kHoldTiles;
   auto add_held = [&]() {
@@ -208,14 +219,13 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float ref = held[kSums + 2 * kNT + 2 * n + e];
-        const float a = ref == kNegInf ? 0.f : exp2_approx(ref - m[n][e]);
-        const float b = a * f[n][e] / held[kSums + 4 * kNT + 2 * n + e];
+        const float a = ref == kNegInf ? 0.f : exp2_approx(ref - z[n][e]);
         l[n][e] = fmaf(held[kSums + 2 * n + e], a, l[n][e]);
 #pragma unroll
         for (int c = 0; c < kSteps; ++c)
 #pragma unroll
           for (int h = e; h < 4; h += 2)
-            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], b, o[n][c][h]);
+            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], a, o[n][c][h]);
       }
   };
   bool fresh = true;
@@ -261,9 +271,8 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           ch_scale[n][e] = __shfl_sync(0xffffffffu, back, (q2 + e) * 4) * p.c;
-          m[n][e] = kNegInf;
+          z[n][e] = kNegInf;
           l[n][e] = 0.f;
-          f[n][e] = 1.f;
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -278,18 +287,16 @@ attn_decode_q8_kernel(const DecodeParams p) {
     const uint8_t* const kb = tiles + stage * S::kStageBytes;
     const uint8_t* const vb = kb + kQ8Keys * kDP;
     const float2* const sb = reinterpret_cast<const float2*>(vb + kQ8Keys * kDP);
-    const uint32_t valid = masks[stage];
+    const unsigned valid = there[0];  // (after the next tile's issue the current one is first)
     if (valid) {
       float s[kMT][kNT][4];
       float vscale[kMT][2];
 #pragma unroll
       for (int t = 0; t < kMT; ++t) {
-        // two chains of products per score tile, added at the end
-        float s1[kNT][4];
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][n][e] = s1[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[t][n][e] = 0.f;
         const int ra = t * 16 + g, rb = ra + 8;
 #pragma unroll
         for (int hh = 0; hh < kDP / 64; ++hh) {
@@ -303,7 +310,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
                                       q8_halves<kFmt, true>(x), q8_halves<kFmt, true>(y)};
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              mma_16816<false>(st & 1 ? s1[n] : s[t][n], frag, qf[n][hh * 4 + st][0],
+              mma_16816<false>(s[t][n], frag, qf[n][hh * 4 + st][0],
                                qf[n][hh * 4 + st][1]);
           }
         }
@@ -313,8 +320,8 @@ attn_decode_q8_kernel(const DecodeParams p) {
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[t][n][e] = (s[t][n][e] + s1[n][e]) * (sa.x * ch_scale[n][e]);
-            s[t][n][e + 2] = (s[t][n][e + 2] + s1[n][e + 2]) * (sc.x * ch_scale[n][e]);
+            s[t][n][e] *= sa.x * ch_scale[n][e];
+            s[t][n][e + 2] *= sc.x * ch_scale[n][e];
           }
       }
       if (valid != 0xffffffffu) {
@@ -326,74 +333,58 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
               for (int n = 0; n < kNT; ++n) s[t][n][e] = kNegInf;
       }
-      // ---- the softmax's reference, and p = 2^(score - reference)
-      float x[kNT][2], shrink[kNT][2];
-      bool up = false;
+      // ---- p = 2^(score - z), and the weights p vs
+      float pr[kMT][kNT][4], w[kMT][kNT][4];
+      auto weigh = [&](int n, int e) {
+        const float zz = z[n][e] == kNegInf ? 0.f : z[n][e];
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pr[t][n][e + 2 * h] = exp2_approx(s[t][n][e + 2 * h] - zz);
+            w[t][n][e + 2 * h] = pr[t][n][e + 2 * h] * vscale[t][h];
+          }
+      };
+      bool over = false;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
+          weigh(n, e);
+          float tw = fmaxf(w[0][n][e], w[0][n][e + 2]), tp = fmaxf(pr[0][n][e], pr[0][n][e + 2]);
 #pragma unroll
-          for (int t = 1; t < kMT; ++t) x[n][e] = fmax3(x[n][e], s[t][n][e], s[t][n][e + 2]);
-          up = up || x[n][e] - m[n][e] > kDecSlack;  // also from -inf to a number
-          shrink[n][e] = 1.f;
-        }
-      const bool moved = __any_sync(0xffffffffu, up);
-      if (moved) {
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = x[n][e];
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-            y = fmaxf(y, m[n][e]);
-            shrink[n][e] = m[n][e] == kNegInf ? 0.f : exp2_approx(m[n][e] - y);
-            m[n][e] = y;
-            l[n][e] *= shrink[n][e];
+          for (int t = 1; t < kMT; ++t) {
+            tw = fmax3(tw, w[t][n][e], w[t][n][e + 2]);
+            tp = fmax3(tp, pr[t][n][e], pr[t][n][e + 2]);
           }
-      }
-      bool over = moved;
-      float top[kNT][2];  // largest weight p vs
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float z = m[n][e] == kNegInf ? 0.f : m[n][e];
-          top[n][e] = 0.f;
-#pragma unroll
-          for (int t = 0; t < kMT; ++t) {
-            const float a = exp2_approx(s[t][n][e] - z), b = exp2_approx(s[t][n][e + 2] - z);
-            l[n][e] += a + b;
-            s[t][n][e] = a * vscale[t][0];
-            s[t][n][e + 2] = b * vscale[t][1];
-            top[n][e] = fmax3(top[n][e], s[t][n][e], s[t][n][e + 2]);
-          }
-          over = over || top[n][e] * f[n][e] > kWeightTop;
+          over = over || tw > kWeightTop || tp > kTotalTop || z[n][e] == kNegInf;
         }
-      // ---- the weights' factor
+      // ---- the reference
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y = top[n][e];
+            float y = z[n][e];
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float x = s[t][n][e + 2 * h];
+                y = fmax3(y, x + (log2f(vscale[t][h]) - kAim), x - kTotalAim);
+              }
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-            // the largest weight before is kWeightAim * shrink / f
-            y = fminf(kWeightAim / y, f[n][e] / shrink[n][e]);
-            y = fminf(fmaxf(y, kQ8MinScale), 1.329227996e36f);  // 2^-126 to 2^120
-            y = __uint_as_float(__float_as_uint(y) & 0x7F800000u);
-            const float a = shrink[n][e] * y / f[n][e];
-            f[n][e] = y;
+            const float a = z[n][e] == kNegInf ? 0.f : exp2_approx(z[n][e] - y);
+            z[n][e] = y;
+            l[n][e] *= a;
 #pragma unroll
             for (int c = 0; c < kSteps; ++c) {
               o[n][c][e] *= a;
               o[n][c][e + 2] *= a;
             }
+            weigh(n, e);
           }
       }
       uint32_t pf[kMT][kNT][2];
@@ -401,24 +392,26 @@ attn_decode_q8_kernel(const DecodeParams p) {
       for (int t = 0; t < kMT; ++t)
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
+          l[n][0] += pr[t][n][0] + pr[t][n][2];
+          l[n][1] += pr[t][n][1] + pr[t][n][3];
           // weights round to fp16 for the second product (half a step: 2^-12)
-          pf[t][n][0] = movmatrix_t(pack2<false>(s[t][n][0] * f[n][0], s[t][n][1] * f[n][1]));
-          pf[t][n][1] = movmatrix_t(pack2<false>(s[t][n][2] * f[n][0], s[t][n][3] * f[n][1]));
+          pf[t][n][0] = movmatrix_t(pack2<false>(w[t][n][0], w[t][n][1]));
+          pf[t][n][1] = movmatrix_t(pack2<false>(w[t][n][2], w[t][n][3]));
         }
 #pragma unroll
       for (int t = 0; t < kMT; ++t) {
         const int r = t * 16 + q2;
         constexpr int kWords = kLaneCh / 4;
-        uint32_t w[4][kWords];  // rows r, r + 1, r + 8, r + 9
+        uint32_t v4[4][kWords];  // rows r, r + 1, r + 8, r + 9
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = r + (i & 1) + (i >> 1) * 8;
           if constexpr (kDP == 128) {
             const uint4 v = *reinterpret_cast<const uint4*>(vb + v_at(row, g));
-            w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+            v4[i][0] = v.x, v4[i][1] = v.y, v4[i][2] = v.z, v4[i][3] = v.w;
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(vb + v_at(row, g >> 1) + (g & 1) * 8);
-            w[i][0] = v.x, w[i][1] = v.y;
+            v4[i][0] = v.x, v4[i][1] = v.y;
           }
         }
 #pragma unroll
@@ -426,8 +419,8 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // codes of channels 2 h, 2 h + 1 of a word, key by key
-            const uint32_t x = q8_raw<kFmt>(__byte_perm(w[0][j], w[1][j], h ? 0x7362 : 0x5140));
-            const uint32_t y = q8_raw<kFmt>(__byte_perm(w[2][j], w[3][j], h ? 0x7362 : 0x5140));
+            const uint32_t x = q8_raw<kFmt>(__byte_perm(v4[0][j], v4[1][j], h ? 0x7362 : 0x5140));
+            const uint32_t y = q8_raw<kFmt>(__byte_perm(v4[2][j], v4[3][j], h ? 0x7362 : 0x5140));
             const uint32_t frag[4] = {q8_halves<kFmt, false>(x), q8_halves<kFmt, true>(x),
                                       q8_halves<kFmt, false>(y), q8_halves<kFmt, true>(y)};
 #pragma unroll
@@ -446,8 +439,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           held[kSums + 2 * n + e] = l[n][e];
-          held[kSums + 2 * kNT + 2 * n + e] = m[n][e];
-          held[kSums + 4 * kNT + 2 * n + e] = f[n][e];
+          held[kSums + 2 * kNT + 2 * n + e] = z[n][e];
           l[n][e] = 0.f;
 #pragma unroll
           for (int c = 0; c < kSteps; ++c)
@@ -475,7 +467,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
           y += __shfl_xor_sync(0xffffffffu, y, 4);
           y += __shfl_xor_sync(0xffffffffu, y, 8);
           y += __shfl_xor_sync(0xffffffffu, y, 16);
-          if (g == 0) ml[warp * kDecRows + n * 8 + q2 + e] = make_float2(m[n][e], y);
+          if (g == 0) ml[warp * kDecRows + n * 8 + q2 + e] = make_float2(z[n][e], y);
         }
       __syncthreads();
       const bool done = whole && last;
@@ -492,7 +484,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
           float M = kNegInf;
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + n * 8 + q2 + e].x);
-          r[e] = m[n][e] == kNegInf ? 0.f : exp2_approx(m[n][e] - M) / f[n][e];
+          r[e] = z[n][e] == kNegInf ? 0.f : exp2_approx(z[n][e] - M);
         }
 #pragma unroll
         for (int c = 0; c < kSteps; ++c)

@@ -3691,6 +3691,11 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
       (r = check_scales(&a.scales, a.num_pages, a.page_size, Hkv)) != RNN_OK)
     return r;
   if (B > INT32_MAX - 1024 || static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
+  // the kernel's strides are 32-bit numbers of 8 bytes
+  for (const rnn_pages* c : {&a.k_cache, &a.v_cache})
+    for (int64_t x : {c->page_stride, c->token_stride, c->head_stride})
+      if (x / 8 > INT32_MAX) return RNN_EUNSUPPORTED;
+  if (a.scales.page_stride / 2 > INT32_MAX || a.scales.head_stride / 2 > INT32_MAX) return RNN_EUNSUPPORTED;
   if (!a.workspace || !aligned256(a.workspace) ||
       a.ws_bytes < rnn_attn_decode_q8_workspace_size(B, Hq, Hkv, d))
     return RNN_EWORKSPACE;
@@ -3708,7 +3713,12 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
   p.kc8 = static_cast<const uint8_t*>(a.k_cache.data);
   p.vc8 = static_cast<const uint8_t*>(a.v_cache.data);
   p.scales = a.scales.data;
-  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
+  const auto units = [](int (&to)[3], int64_t page, int64_t row, int64_t head) {
+    to[0] = static_cast<int>(page), to[1] = static_cast<int>(row), to[2] = static_cast<int>(head);
+  };
+  units(p.k_s8, p.k_ps / 8, p.k_ts / 8, p.k_hs / 8);
+  units(p.v_s8, p.v_ps / 8, p.v_ts / 8, p.v_hs / 8);
+  units(p.s_s8, a.scales.page_stride / 2, 1, a.scales.head_stride / 2);
   p.wide = d % 16 == 0 && (p.k_ps | p.k_ts | p.k_hs | p.v_ps | p.v_ts | p.v_hs) % 16 == 0;
   p.lse = a.lse;
   p.table = a.page_table;
