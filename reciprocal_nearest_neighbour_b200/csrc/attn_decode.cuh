@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) attn_decode_kernel(const De
   float2* ml = reinterpret_cast<float2*>(merge + 2 * 8 * S::kMergeRow);  // [warp][16]
   uint32_t* masks = reinterpret_cast<uint32_t*>(ml + kDecWarps * kDecRows) + warp * kStages;
 
-  if (kRows && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+  if (kRows) {
+    pdl_trigger();  // the kernel behind this one needs nothing of it before its end
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
+  }
   const int Hv = p.Hkv * p.hblocks;
   // ---- this CTA's share of the tile list, and the pair it starts in
   DecCursor ld, cur;

@@ -40,7 +40,7 @@ template <int kDP>
 struct PreShape {
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
-  static constexpr int kStages = kDP == 128 ? 4 : 8;
+  static constexpr int kStages = kDP == 128 ? 4 : 8;  // one more in a narrow unit: it has one Q
   static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 512;
 };
 
@@ -80,12 +80,11 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_tiles = smem;
-  const uint32_t ring = smem + 2 * S::kTileBytes;
-  const uint32_t bars = ring + kStages * S::kTileBytes;
+  constexpr int kSlots = kStages + 1;
+  const uint32_t bars = smem + (2 + kStages) * S::kTileBytes;
   const uint32_t full_bar = bars;
-  const uint32_t empty_bar = full_bar + 8 * kStages;
-  const uint32_t qfull_bar = empty_bar + 8 * kStages;
+  const uint32_t empty_bar = full_bar + 8 * kSlots;
+  const uint32_t qfull_bar = empty_bar + 8 * kSlots;
   const uint32_t s_bar = qfull_bar + 8;     // scores of tile i are in tensor memory
   const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
   const uint32_t o_bar = p_bar + 32;        // its output is complete so far
@@ -95,7 +94,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   // Keys that exist, 4 words for each of 8 tiles: when a tile's words are written, the
   // values six tiles and more before it have been given back by both row tiles, so the
   // softmax has read their words.
-  const uint32_t mask_at = tmem_slot + 8;
+  const uint32_t mask_at = (tmem_slot + 8 + 15) & ~15u;
+  const uint32_t turn_at = mask_at + 128;   // per softmax warp: steps whose exponentials are out
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- this CTA's unit and key tiles
@@ -115,6 +115,11 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
   const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
 
+  // shared memory: the row tiles, then the ring, load x in slot x % slots
+  const uint32_t q_tiles = smem, ring = smem + (wide ? 2 : 1) * S::kTileBytes;
+  auto slot_of = [&](int load) { return wide ? load % kStages : load % kSlots; };
+  auto turn_of = [&](int load) { return (wide ? load / kStages : load / kSlots) & 1; };
+
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto wait = [&](uint32_t bar, uint32_t parity, int code) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
@@ -130,7 +135,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
     }
   };
-  if (threadIdx.x < kStages) {
+  if (threadIdx.x < kSlots) {
     mbar_init(full_bar + 8 * threadIdx.x, 4);
     mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
     fence_barrier_init();
@@ -143,8 +148,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     mbar_init(drain_bar + 8 * i, 1);
     if (i == 0) mbar_init(qfull_bar, 4);
     fence_barrier_init();
-  } else if (threadIdx.x == 64) {
-    sts_volatile(abort_at, 0);
+  } else if (threadIdx.x >= 64 && threadIdx.x < 72) {
+    sts_volatile(turn_at + 4 * (threadIdx.x - 64), 0);
+    if (threadIdx.x == 64) sts_volatile(abort_at, 0);
   }
   if (warp == kPreMmaWarp) {
     tmem_alloc(tmem_slot, kCols);
@@ -197,7 +203,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * ((told - 1) % kStages));
+        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * slot_of(told - 1));
         ++told;
       };
       issued = 1;
@@ -205,8 +211,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       bool ok = true;
       int id = -1;
       for (int l = 0; l < loads; ++l) {
-        const int slot = l % kStages;
-        const uint32_t eb = empty_bar + 8 * slot, parity = ((l / kStages) & 1) ^ 1u;
+        const int slot = slot_of(l);
+        const uint32_t eb = empty_bar + 8 * slot, parity = turn_of(l) ^ 1u;
         while (!__all_sync(0xffffffffu, mbar_test_wait(eb, parity))) {
           if (told < issued) {
             tell();
@@ -263,9 +269,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       while (told < issued) tell();
       if (w == 0 && !aborted()) {
         // no arrival of a product's completion is under way when the CTA exits
-        const int l = max(0, loads - kStages) + lane;
-        if (lane < kStages && l < loads)
-          settle_phase(empty_bar + 8 * (l % kStages), (l / kStages) & 1, p.wait_limit_ns, p.err);
+        const int slots = wide ? kStages : kSlots, l = max(0, loads - slots) + lane;
+        if (lane < slots && l < loads)
+          settle_phase(empty_bar + 8 * slot_of(l), turn_of(l), p.wait_limit_ns, p.err);
         __syncwarp();
       }
     } else if (warp < kPreMmaWarp + 2) {
@@ -283,8 +289,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       if (n_of[i] > 0) wait_mma(qfull_bar, 0);
       for (int k = 0; ok && k < n_of[i]; ++k) {
         const int kx = 2 * tile_of(i, k), vx = kx + 1;
-        const int ks = kx % kStages, vs = vx % kStages;
-        if (!wait_mma(full_bar + 8 * ks, (kx / kStages) & 1)) break;
+        const int ks = slot_of(kx), vs = slot_of(vx);
+        if (!wait_mma(full_bar + 8 * ks, turn_of(kx))) break;
         // the probabilities lie over the scores: the product that reads them first
         if (k > 0 && !wait_mma(o_bar + 8 * i, (k - 1) & 1)) break;
         tc_fence_after();
@@ -304,7 +310,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         umma_commit_warp(s_bar + 8 * i);
         umma_commit_warp(empty_bar + 8 * ks);
         any = true;
-        if (!wait_mma(full_bar + 8 * vs, (vx / kStages) & 1)) break;
+        if (!wait_mma(full_bar + 8 * vs, turn_of(vx))) break;
         const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -334,7 +340,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     const uint32_t lane_at = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lane_at + i * kAttnN;
     const uint32_t o_at = tmem + lane_at + kOutCol + i * kDP;
-    const int steps = i ? n_of[1] : n_of[0];
+    const int steps = i ? n_of[1] : n_of[0], steps_o = i ? n_of[0] : n_of[1];
     float m = kNegInf, l = 0.f;
     bool ok = true;
 #pragma unroll 1
@@ -396,6 +402,15 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
       const float z = mc - kBias;
       const uint64_t c2 = f2_make(p.c, p.c), z2 = f2_make(-z, -z);
+      // the two warps of a scheduler take turns at the exponential unit, as in attn_prompt
+      const int k_o = i ? k : k - 1;  // the other's step to wait for
+      if (k_o >= 0 && k_o < steps_o) {
+#pragma unroll 1
+        for (int look = 0; look < kTurnPolls; ++look) {
+          if (lds_volatile(turn_at + 4 * (warp ^ 4)) > k_o) break;
+          __nanosleep(40);
+        }
+      }
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -411,6 +426,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
           // 2^-9 of bf16, 2^-12 of fp16, of each weight); the total keeps them in fp32
           w[e] = pack2<kBf16>(a, b);
         }
+        if (c == kTurnChunk && lane == 0) sts_volatile(turn_at + 4 * warp, k + 1);
         tmem_st16(s_at + c * 16, w);
         if (c & 1) {
           tmem_wait_st();
@@ -456,11 +472,16 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
+  // This kernel starts while the one that attends to the sequences' own rows still runs,
+  // and reads nothing of it; the join behind both may only wait for this one's end.
+  pdl_wait();
 }
 
 // Joins a row's parts: the prefix's, one from each of its unit's splits (and tiles), and
-// its sequence's own.  One block per (sequence, query head); its four warps take the
-// parts in turn and their sums meet in a fixed order.
+// its sequence's own.  One block per (sequence, query head): the threads fetch the parts'
+// maxima and totals at once, then its four warps take the sums in turn, several in flight,
+// and meet in a fixed order.
+constexpr int kJoinParts = 128;  // of them in a pass
 template <bool kBf16, int kDP>
 __global__ void __launch_bounds__(128)
 attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixParams pre) {
@@ -468,8 +489,9 @@ attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixPara
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   using VecT = std::conditional_t<kVals == 4, float4, float2>;
   __shared__ float acc[4][kDP];
-  __shared__ float2 tot[4];
-  pdl_wait();
+  __shared__ float factor[kJoinParts];
+  __shared__ const float* source[kJoinParts];
+  __shared__ float tops[4], sums[4];
   const int b = blockIdx.x / p.Hq, head = blockIdx.x - b * p.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = head / p.group, in = head - hk * p.group;
@@ -479,59 +501,75 @@ attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixPara
   const int slot0 = pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0);
   const int pre_row = wide ? at % kAttnM : at;
   const int n_pre = wide ? pre.wide_splits : 2 * pre.narrow_splits;
+  const bool own = dec_len(p, b) > 0;
+  pdl_wait();
   int2 sp = make_int2(0, -1);
-  if (dec_len(p, b) > 0)
-    sp = p.span[static_cast<int64_t>(b) * (p.Hkv * p.hblocks) + hk * p.hblocks + hb];
+  if (own) sp = p.span[static_cast<int64_t>(b) * (p.Hkv * p.hblocks) + hk * p.hblocks + hb];
   const int parts = n_pre + sp.y - sp.x + 1;
   float v[kVals] = {}, M = kNegInf, L = 0.f;
-#pragma unroll 2
-  for (int i = warp; i < parts; i += 4) {
-    float2 a;
-    const float* from;
+  for (int base = 0; base < parts; base += kJoinParts) {
+    const int i = base + static_cast<int>(threadIdx.x);
+    float2 a = make_float2(kNegInf, 0.f);
+    const float* from = nullptr;
     if (i < n_pre) {
       const int64_t slot = slot0 + (wide ? 2 : 1) * i;
       a = pre.part_ml[slot * kAttnM + pre_row];
       from = pre.part + (slot * kAttnM + pre_row) * kDP;
-    } else if (sp.x == sp.y) {
-      const int64_t own = static_cast<int64_t>(b) * p.Hq + head;
-      a = p.row_ml[own];
-      from = p.row_part + own * kDP;
-    } else {
+    } else if (i < parts && sp.x == sp.y) {
+      const int64_t mine = static_cast<int64_t>(b) * p.Hq + head;
+      a = p.row_ml[mine];
+      from = p.row_part + mine * kDP;
+    } else if (i < parts) {
       const int c = sp.x + i - n_pre;
-      const int64_t own = (static_cast<int64_t>(c) * 2 + (c == sp.x ? 1 : 0)) * kDecRows + dec_row;
-      a = p.part_ml[own];
-      from = p.part + own * kDP;
+      const int64_t mine = (static_cast<int64_t>(c) * 2 + (c == sp.x ? 1 : 0)) * kDecRows + dec_row;
+      a = p.part_ml[mine];
+      from = p.part + mine * kDP;
     }
-    if (a.x == kNegInf && a.y == 0.f) continue;  // no key: its sums were not written
-    const VecT x = *reinterpret_cast<const VecT*>(from + lane * kVals);
-    const float* xs = reinterpret_cast<const float*>(&x);
-    const float top = fmaxf(M, a.x);
-    // (a NaN maximum is a part that was given up: its factor is NaN too)
-    const float f = a.x == kNegInf ? 1.f : exp2_approx((a.x - top) * p.c);
-    const float h = M == kNegInf ? 0.f : exp2_approx((M - top) * p.c);
-    M = top;
-    L = L * h + a.y * f;
+    if (a.x == kNegInf && a.y == 0.f) from = nullptr;  // no key: its sums were not written
+    float top = a.x;
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) v[e] = v[e] * h + xs[e] * f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    const float m = fmaxf(M, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+    // (a NaN maximum is a part that was given up: its factor is NaN too; without a
+    // reference a part's total is 0, or NaN if its scores were)
+    const float f = a.x == kNegInf ? 1.f : exp2_approx((a.x - m) * p.c);
+    factor[threadIdx.x] = f;
+    source[threadIdx.x] = from;
+    float l = a.y * f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) sums[warp] = l;
+    __syncthreads();
+    if (base) {
+      const float h = M == kNegInf ? 1.f : exp2_approx((M - m) * p.c);
+      L *= h;
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) v[e] *= h;
+    }
+    M = m;
+    L += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    const int here = min(kJoinParts, parts - base);
+#pragma unroll 8
+    for (int j = warp; j < here; j += 4) {
+      const float* src = source[j];
+      if (!src) continue;
+      const VecT x = *reinterpret_cast<const VecT*>(src + lane * kVals);
+      const float* xs = reinterpret_cast<const float*>(&x);
+      const float g = factor[j];
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) v[e] = fmaf(xs[e], g, v[e]);
+    }
+    __syncthreads();  // the next pass writes the factors anew
   }
 #pragma unroll
   for (int e = 0; e < kVals; ++e) acc[warp][lane * kVals + e] = v[e];
-  if (lane == 0) tot[warp] = make_float2(M, L);
   __syncthreads();
-  M = fmaxf(fmaxf(tot[0].x, tot[1].x), fmaxf(tot[2].x, tot[3].x));
-  float f[4];
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    // without a reference the total is 0, or NaN if its scores were
-    f[w] = tot[w].x == kNegInf ? 1.f : exp2_approx((tot[w].x - M) * p.c);
-    L += tot[w].y * f[w];
-  }
   uint16_t* ob = p.out + b * p.o_bs + head * p.o_hs;
   const float inv = L != 0.f ? 1.f / L : 0.f;
   for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-    const float y =
-        ((acc[0][c] * f[0] + acc[1][c] * f[1]) + (acc[2][c] * f[2] + acc[3][c] * f[3])) * inv;
+    const float y = ((acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c])) * inv;
     ob[c] = kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y))
                   : __half_as_ushort(__float2half_rn(y));
   }

@@ -3753,27 +3753,36 @@ static PrefixPlan prefix_plan(int64_t rows, int Hkv, int64_t room) {
   const int64_t keys = std::min<int64_t>(room, kDecMaxKeys);
   const int64_t tiles = std::max<int64_t>(1, (keys + kAttnN - 1) / kAttnN);
   // The time of a wave, in the time of a row tile's products with 128 keys: 2 for a wide
-  // unit's key tile, 1.4 for a narrow one's (its loads), 4 to begin and to end, and 1/1000
+  // unit's key tile, 1.3 for a narrow one's (its loads), 6 to begin and to end, and 1/16000
   // for each row's part, which the join reads.
   constexpr int kSms = 148;
   double least = 0;
   // (from what one accumulator takes; a narrow unit has two)
   const int64_t from = (tiles + kPreMostTiles - 1) / kPreMostTiles;
-  for (int64_t sw = from; sw <= std::max(from, std::min<int64_t>(tiles, 2 * kSms)); ++sw) {
-    const int64_t sn = best.wide ? (sw * 7 + 5) / 10 : sw;
+  const int64_t to = std::max(from, std::min<int64_t>(tiles, 2 * kSms));
+  const auto look = [&](int64_t sw, int64_t sn) {
     const int64_t ctas = Hkv * (best.wide * sw + best.narrow * sn);
     const int64_t waves = (ctas + kSms - 1) / kSms;
     const double steps = std::max(best.wide ? 2.0 * ((tiles + sw - 1) / sw) : 0.0,
-                                  best.narrow ? 1.4 * ((tiles + sn - 1) / sn) : 0.0);
-    const double parts = static_cast<double>(Hkv) * kAttnM * 2 * (best.wide * sw + best.narrow * sn);
-    const double time = waves * (steps + 4) + 1e-3 * parts / 16;
+                                  best.narrow ? 1.3 * ((tiles + sn - 1) / sn) : 0.0);
+    const double time = waves * (steps + 6) + static_cast<double>(ctas) * 2 * kAttnM / 16000;
     if (best.ctas == 0 || time < least) {
       least = time;
       best.wide_splits = static_cast<int>(sw);
       best.narrow_splits = static_cast<int>(sn);
       best.ctas = ctas;
     }
-    if (ctas > 8 * kSms && best.ctas) break;
+    return ctas <= 8 * kSms;
+  };
+  for (int64_t sw = from; sw <= to; ++sw) {
+    // a narrow unit's share of CTAs beside wide ones: its share of the time, or one off
+    const int64_t sn = best.wide ? (sw * 13 + 10) / 20 : sw;
+    const bool more = look(sw, sn);
+    if (best.wide && best.narrow) {
+      look(sw, sn + 1);
+      if (sn > 1) look(sw, sn - 1);
+    }
+    if (!more) break;
   }
   return best;
 }
@@ -3809,7 +3818,7 @@ static rnn_status shared_launch(const DecodeParams& p, dim3 grid, const PrefixPa
          : attn_decode_kernel<kBf16, kDP, 2, false, true><<<grid, block, sm, s>>>(p);
   rnn_status r = launched();
   if (r != RNN_OK) return r;
-  attn_prefix_kernel<kBf16, kDP><<<ctas, kPreThreads, PreShape<kDP>::kSmem, s>>>(pre);
+  launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads), PreShape<kDP>::kSmem, s, true, pre);
   if ((r = launched()) != RNN_OK) return r;
   launch_k(attn_shared_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
            0, s, true, p, pre);
