@@ -169,6 +169,39 @@ class RNNError(RuntimeError):
 _lib = None
 
 
+class _Python:
+    """In the place of the extension module: no call is served, so the Python forms are."""
+
+    @staticmethod
+    def _none(*_):
+        return None
+
+    kv_append_q8 = kv_read_q8 = attn_decode_q8 = attn_decode_shared = _none
+
+
+# The extension module ``_fast`` once it is loaded.  Its functions serve the usual calls
+# of their namesakes, or return None.
+fast = None
+
+
+def load_fast():
+    """Load the library and the extension module beside it (not built: the Python forms)."""
+    global fast
+    if fast is None:
+        lib = load()
+        try:
+            from . import _fast as module
+        except ImportError:
+            fast = _Python
+            return fast
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "rnn_kv_read_q8", "rnn_attn_decode_q8", "rnn_attn_decode_q8_workspace_size",
+            "rnn_attn_decode_shared", "rnn_attn_decode_shared_workspace_size",
+            "rnn_kv_append_q8")))
+        fast = module
+    return fast
+
+
 def load():
     """Load librnn.so once and declare its signatures."""
     global _lib

@@ -402,6 +402,11 @@ def attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     numbers in the whole sequence as ``positions``.  Should a wait of the kernels
     run out, the rows concerned are NaN, and ``workspace_status`` tells.
     """
+    done = (_lib.fast or _lib.load_fast()).attn_decode_shared(
+        q, k_cache, v_cache, prefix_pages, prefix_len, page_table, lens, scale, with_lse, out,
+        workspace)
+    if done is not None:
+        return done
     kind = _value_dtype(q, "q")
     dev = q.device
     _all(kind, dev, 3, q, "q")

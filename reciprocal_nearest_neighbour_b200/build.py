@@ -1,23 +1,30 @@
-"""Build ``librnn.so`` in-tree with nvcc for sm_100a.
+"""Build ``librnn.so`` and ``_fast.so`` in-tree, the first with nvcc for sm_100a.
 
 ``python -m reciprocal_nearest_neighbour_b200.build`` (or ``build()``) compiles
 ``csrc/*.cu`` into ``reciprocal_nearest_neighbour_b200/librnn.so`` next to this
 file.  The CUDA runtime is linked statically and the driver's tensor-map
 encoder is looked up at run time, so the library loads on a machine without
-a GPU (its entry points then fail with RNN_ECUDA).
+a GPU (its entry points then fail with RNN_ECUDA).  ``csrc/fast.cpp`` becomes
+the extension module ``_fast.so`` (g++, against torch's headers): the short way
+from tensors to some of the library's calls.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librnn.so")
+FAST = os.path.join(PKG, "_fast.so")
+FAST_SOURCE = os.path.join(CSRC, "fast.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -39,7 +46,32 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _older(path: str, deps) -> bool:
+    return not os.path.exists(path) or \
+        any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+
+def build_fast(force: bool = False) -> str:
+    """The extension module of csrc/fast.cpp."""
+    if not force and not _older(FAST, [FAST_SOURCE, os.path.join(INCLUDE, "rnn.h")]):
+        return FAST
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
+    cuda = os.path.join(os.environ.get("CUDA_HOME") or os.path.dirname(os.path.dirname(nvcc)), "include")
+    system = [os.path.join(torch_dir, "include"),
+              os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], cuda, "/usr/local/cuda/include"]
+    tmp = FAST + f".tmp{os.getpid()}"
+    subprocess.check_call(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+         *(f"-isystem{p}" for p in system), FAST_SOURCE, "-L", os.path.join(torch_dir, "lib"),
+         "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp])
+    os.replace(tmp, FAST)
+    return FAST
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_fast(force)
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

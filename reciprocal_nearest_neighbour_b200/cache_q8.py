@@ -75,6 +75,11 @@ def kv_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     channel that is not finite reads back as NaN.  Outputs given in place of
     ``q`` and ``k`` have their strides.  All else is as in ``kv_append``.
     """
+    done = (_lib.fast or _lib.load_fast()).kv_append_q8(
+        k, v, k_cache, v_cache, scales, page_table, start, cu, q, inv_freq, positions, paired,
+        with_k, q_out, k_out)
+    if done is not None:
+        return done
     kind, dev, T, hq, hkv, d = _new_rows(k, v, q, q_out, inv_freq)
     codes, _, num_pages, size, scale_at = _coded(k_cache, v_cache, scales, dev, hkv, d)
     B = _cu(cu, "cu", dev)
@@ -107,6 +112,10 @@ def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tenso
     """
     if dtype not in _DT:
         raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+    done = (_lib.fast or _lib.load_fast()).kv_read_q8(
+        k_cache, v_cache, scales, page_table, cu, tokens, dtype is torch.bfloat16, start, k_out, v_out)
+    if done is not None:
+        return done
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
     dev, d, tokens = k_cache.device, k_cache.shape[3], int(tokens)
@@ -145,6 +154,10 @@ def attn_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
     ``q [B, Hq, d]`` fp16 or bf16; all else is as in ``attn_decode``.
     """
+    done = (_lib.fast or _lib.load_fast()).attn_decode_q8(
+        q, k_cache, v_cache, scales, page_table, lens, scale, with_lse, out, workspace)
+    if done is not None:
+        return done
     kind = _value_dtype(q, "q")
     dev = q.device
     _all(kind, dev, 3, q, "q")

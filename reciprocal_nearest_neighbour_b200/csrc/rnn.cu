@@ -3745,7 +3745,7 @@ struct PrefixPlan {
   int wide, narrow, wide_splits, narrow_splits;
   int64_t ctas;
 };
-static PrefixPlan prefix_plan(int64_t rows, int Hkv, int64_t room) {
+static PrefixPlan make_prefix_plan(int64_t rows, int Hkv, int64_t room) {
   PrefixPlan best{};
   const int64_t units = (rows + kPreUnit - 1) / kPreUnit;
   best.narrow = rows - (units - 1) * kPreUnit <= kAttnM;
@@ -3785,6 +3785,18 @@ static PrefixPlan prefix_plan(int64_t rows, int Hkv, int64_t room) {
     if (!more) break;
   }
   return best;
+}
+// (sizes repeat from call to call: the last ones' plan is kept)
+static PrefixPlan prefix_plan(int64_t rows, int Hkv, int64_t room) {
+  struct Last {
+    int64_t rows, room;
+    int Hkv;
+    PrefixPlan plan;
+  };
+  thread_local Last last{-1, -1, -1, {}};
+  if (last.rows != rows || last.Hkv != Hkv || last.room != room)
+    last = Last{rows, room, Hkv, make_prefix_plan(rows, Hkv, room)};
+  return last.plan;
 }
 
 struct SharedWs {

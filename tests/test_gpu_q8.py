@@ -562,3 +562,36 @@ def test_nothing_to_do():
     out = rnn.kv_read_q8(kc, vc, scales, none, ints([0]), 3, BF, k_out=x)[0]
     assert (out == 1).all()
     assert (raw(kc) == 0x5A).all() and (scales == 7).all()
+
+
+def test_python_forms_give_the_same(monkeypatch):
+    """The calls' way through the extension module and the one through Python."""
+    g = gen_of(6)
+    lens, size, d = [37, 100], 16, 64
+    table, pages = deal(g, [n + 1 for n in lens], size)
+    kc, vc, scales, _, _ = filled(g, "e4m3", pages, size, 2, d)
+    q, k, v = (normal(g, (2, h, d), HF) for h in (4, 2, 2))
+    inv = torch.ones(32, dtype=torch.float64, device="cuda")
+    tab, now, cu = ints(table), ints(lens), ints([0, 1, 2])
+
+    def everything():
+        a = rnn.kv_append_q8(k, v, kc, vc, scales, tab, now, cu, q=q, inv_freq=inv, with_k=True)
+        b = rnn.kv_read_q8(kc, vc, scales, tab, ints(cum(lens)), sum(lens), HF)
+        c = rnn.attn_decode_q8(a[0], kc, vc, scales, tab, now, with_lse=True, scale=0.25)
+        return *a, *b, *c, kc.view(torch.uint8).clone(), scales.clone()
+
+    assert rnn._lib.load_fast().__name__.endswith("_fast")
+    mine = everything()
+    monkeypatch.setattr(rnn._lib, "fast", rnn._lib._Python)
+    for x, y in zip(mine, everything()):
+        assert torch.equal(x, y) and x.dtype == y.dtype and x.stride() == y.stride()
+
+
+def test_a_size_of_one_may_have_any_stride():
+    g = gen_of(6)
+    kc, vc, scales, kv, vv = filled(g, "int8", 3, 16, 1, 64)
+    kc, vc = (x.as_strided((3, 16, 1, 64), (1024, 64, 3, 1)) for x in (kc, vc))
+    q = normal(g, (1, 2, 64), HF).as_strided((1, 2, 64), (5, 64, 1))
+    out, lse = rnn.attn_decode_q8(q, kc, vc, scales, ints([[2, 0]]), ints([20]), with_lse=True)
+    ref = oa.decode(f64(q), kv, vv, np.array([[2, 0]]), [20], 1 / 8)
+    check_attention_q8(out, lse, ref, HF, 64, np.abs(vv).max())

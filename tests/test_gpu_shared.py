@@ -317,3 +317,13 @@ def test_a_long_prefix():
     # each sum leaves its accumulator after 65536 keys at most: 2^-11 of it may be cut off
     ref.spread *= 1 + 2.0 ** -11 / 2.0 ** -11
     check_attention(out, lse, ref, HF, d, float(vc.max()))
+
+
+def test_python_form_gives_the_same(monkeypatch):
+    """The call's way through the extension module and the one through Python."""
+    q, kc, vc, names, table = setting(BF, 300, [20, 3], 4, 2, 64, 16)
+    args = (q, kc, vc, ints(names), ints([300]), ints(table), ints([20, 3]))
+    mine = rnn.attn_decode_shared(*args, with_lse=True, scale=0.2)
+    monkeypatch.setattr(rnn._lib, "fast", rnn._lib._Python)
+    for x, y in zip(mine, rnn.attn_decode_shared(*args, with_lse=True, scale=0.2)):
+        assert torch.equal(x, y)
