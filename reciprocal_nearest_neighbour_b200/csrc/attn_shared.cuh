@@ -40,8 +40,12 @@ template <int kDP>
 struct PreShape {
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
-  static constexpr int kStages = kDP == 128 ? 4 : 8;  // one more in a narrow unit: it has one Q
-  static constexpr size_t kSmem = 1024 + size_t(2 + kStages) * kTileBytes + 512;
+  static constexpr int kStages = kDP == 128 ? 4 : 8;  // at most; a power of two
+  // with `slots` of the ring, and one row tile where every unit is narrow
+  static constexpr size_t smem(int slots, bool any_wide) {
+    return 1024 + size_t((any_wide ? 2 : 1) + slots) * kTileBytes + 512;
+  }
+  static constexpr size_t kSmem = smem(kStages, true);
 };
 
 struct PrefixParams {
@@ -56,6 +60,7 @@ struct PrefixParams {
   int wide, narrow;                    // units of a key head: wide ones, and 0 or 1 narrow one
   int wide_splits, narrow_splits;      // CTAs that share a unit's keys
   int Hkv;
+  int slots, slot_bits;                // of the ring, and its log2
   float c;                             // scale * log2(e)
   uint32_t idesc_s, idesc_o;
   float* part;                         // [slot][128][kDP] unnormalised parts
@@ -80,11 +85,11 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  constexpr int kSlots = kStages + 1;
-  const uint32_t bars = smem + (2 + kStages) * S::kTileBytes;
+  const uint32_t q_tiles = smem, ring = smem + (p.wide ? 2 : 1) * S::kTileBytes;
+  const uint32_t bars = ring + p.slots * S::kTileBytes;
   const uint32_t full_bar = bars;
-  const uint32_t empty_bar = full_bar + 8 * kSlots;
-  const uint32_t qfull_bar = empty_bar + 8 * kSlots;
+  const uint32_t empty_bar = full_bar + 8 * kStages;
+  const uint32_t qfull_bar = empty_bar + 8 * kStages;
   const uint32_t s_bar = qfull_bar + 8;     // scores of tile i are in tensor memory
   const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
   const uint32_t o_bar = p_bar + 32;        // its output is complete so far
@@ -115,10 +120,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
   const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
 
-  // shared memory: the row tiles, then the ring, load x in slot x % slots
-  const uint32_t q_tiles = smem, ring = smem + (wide ? 2 : 1) * S::kTileBytes;
-  auto slot_of = [&](int load) { return wide ? load % kStages : load % kSlots; };
-  auto turn_of = [&](int load) { return (wide ? load / kStages : load / kSlots) & 1; };
+  // the ring: load x in slot x % slots
+  auto slot_of = [&](int load) { return load & (p.slots - 1); };
+  auto turn_of = [&](int load) { return (load >> p.slot_bits) & 1; };
 
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto wait = [&](uint32_t bar, uint32_t parity, int code) {
@@ -135,7 +139,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
     }
   };
-  if (threadIdx.x < kSlots) {
+  if (threadIdx.x < p.slots) {
     mbar_init(full_bar + 8 * threadIdx.x, 4);
     mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
     fence_barrier_init();
@@ -269,8 +273,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       while (told < issued) tell();
       if (w == 0 && !aborted()) {
         // no arrival of a product's completion is under way when the CTA exits
-        const int slots = wide ? kStages : kSlots, l = max(0, loads - slots) + lane;
-        if (lane < slots && l < loads)
+        const int l = max(0, loads - p.slots) + lane;
+        if (lane < p.slots && l < loads)
           settle_phase(empty_bar + 8 * slot_of(l), turn_of(l), p.wait_limit_ns, p.err);
         __syncwarp();
       }

@@ -12,7 +12,8 @@
 // infinity gets a NaN for its scale and reads back as NaN.
 //
 // Bound by memory: a 16-bit channel is read, a code and d-th of a scale written (append),
-// or the other way round (read).
+// or the other way round (read).  What it takes is enough reads under way: an append's
+// warp has three passes over its rows on their way to shared memory.
 #pragma once
 #include <cstdint>
 #include "kv_append.cuh"
@@ -21,8 +22,9 @@
 namespace rnn {
 
 constexpr int kQ8Warps = 4;
-// Rows in flight a lane.
-constexpr int kQ8Batch = 2;
+// Passes of a warp (32 lanes of up to 16 channels) in its ring, all but one of them on
+// their way while one is worked on.
+constexpr int kQ8Ring = 4, kQ8PassBytes = 1024;
 constexpr float kQ8MinScale = 1.1754943508222875e-38f;  // 2^-126
 
 enum CodeFormat : int { kE4m3 = 0, kInt8 = 1 };
@@ -146,70 +148,61 @@ __device__ __forceinline__ Q8Place q8_place(int unit, const AppendQ8Params& p) {
 constexpr int kNeighbours = 16;
 
 // A row takes 1 to 16 lanes with up to 16 channels each, and is reduced to its maximum
-// between them.  Pairs that do not come in eights (kVec < 8) have their partners fetched a
-// second time beside them, in pieces of kVec channels; pairs of neighbours (kNeighbours)
-// are in a lane in any case.
+// between them; a pass takes the rows that fit the warp, of queries, keys or values.  A
+// lane fetches its own channels ahead, into a place of its own, so that a row rotated in
+// place is written behind its reads.  Partners of pairs that do not come in eights
+// (kVec < 8) are read from the other lanes' places, in pieces of kVec channels.
 template <bool kBf16, int kFmt, int kVec>
-__global__ void __launch_bounds__(kQ8Warps * 32, kVec >= 8 ? 6 : 4)
+__global__ void __launch_bounds__(kQ8Warps * 32, kVec >= 8 ? 8 : 6)
 kv_append_q8_kernel(const AppendQ8Params p) {
-  constexpr int kPiece = kVec >= 8 ? 8 : kVec, kAgain = kVec >= 8 ? 1 : 2;
+  constexpr int kPiece = kVec >= 8 ? 8 : kVec;
   using V = typename VecOf<kPiece>::T;
   constexpr float kTop = kFmt == kE4m3 ? 448.f : 127.f;
-  extern __shared__ __align__(16) float2 app_turns[];  // [warp][axes * pairs] cos, sin
+  extern __shared__ __align__(16) uint8_t app_smem[];  // rings, then [warp][axes * pairs] cos, sin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp;
   if ((gw >> p.share) >= p.T) return;
   const int t = static_cast<int>(gw >> p.share);
   const int part = static_cast<int>(gw) & ((1 << p.share) - 1);
   const int angles = p.axes * p.pairs, rotated = 2 * angles;
-  float2* turn = app_turns + warp * ((angles + 1) & ~1);
+  uint8_t* const ring = app_smem + warp * (kQ8Ring * kQ8PassBytes);
+  float2* const turn = reinterpret_cast<float2*>(app_smem + kQ8Warps * kQ8Ring * kQ8PassBytes) +
+                       warp * ((angles + 1) & ~1);
   const int sub = lane >> p.row_lanes;                   // row of the pass
-  const int per_pass = 32 >> p.row_lanes;                // rows of a pass over the warp
   const int unit = lane & ((1 << p.row_lanes) - 1);
   const Q8Place at = q8_place<kVec>(unit, p);
   const bool live = at.ca < p.d, both = at.cb >= 0;
-  const int n_rows = p.Hq + 2 * p.Hkv;                   // queries, keys, values
-  const int first = part * per_pass, step = per_pass << p.share;
-  const uint16_t* q_row = p.q + t * p.q_ts;  // never read without queries
-  const uint16_t* k_row = p.k + t * p.k_ts - p.Hq * p.k_hs;
-  const uint16_t* v_row = p.v + t * p.v_ts - (p.Hq + p.Hkv) * p.v_hs;
-
-  uint4 x[kQ8Batch][2];
-  union Partner { uint4 v; V part[8 / kPiece]; } y[kQ8Batch][kAgain];
-  auto fetch = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kQ8Batch; ++i) {
-      const int r = base + i * step + sub;
-      const bool is_v = r >= p.Hq + p.Hkv;
-      if (r >= n_rows || !live) continue;
-      const uint16_t* src = r < p.Hq ? q_row + r * p.q_hs : is_v ? v_row + r * p.v_hs : k_row + r * p.k_hs;
-      x[i][0] = *reinterpret_cast<const uint4*>(src + at.ca);
-      if (both) x[i][1] = *reinterpret_cast<const uint4*>(src + at.cb);
-      if constexpr (kVec < 8) {
-        if (is_v) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int s = 0; s < 8 / kPiece; ++s) {
-            const int c = at.ca + 8 * h + s * kPiece;
-            if (c >= rotated) break;
-            const int in = c >= 2 * p.pairs ? c - 2 * p.pairs : c;  // within its axis
-            y[i][h].part[s] =
-                *reinterpret_cast<const V*>(src + (in < p.pairs ? c + p.pairs : c - p.pairs));
-          }
+  // passes: the queries', the keys', the values'
+  const int rows_log = 5 - p.row_lanes, fill = (1 << rows_log) - 1;
+  const int q_passes = (p.Hq + fill) >> rows_log, k_passes = (p.Hkv + fill) >> rows_log;
+  const int passes = q_passes + 2 * k_passes, step = 1 << p.share;
+  const uint32_t mine = smem_u32(ring) + lane * 16;
+  auto fetch = [&](int pass, int slot) {
+    if (pass < passes) {
+      const int in = pass < q_passes ? pass : pass - q_passes;
+      const bool is_q = pass < q_passes, is_v = !is_q && in >= k_passes;
+      const int r = ((is_v ? in - k_passes : in) << rows_log) + sub;
+      const uint16_t* src = is_q ? p.q + t * p.q_ts : is_v ? p.v + t * p.v_ts : p.k + t * p.k_ts;
+      src += r * (is_q ? p.q_hs : is_v ? p.v_hs : p.k_hs);
+      if (live && r < (is_q ? p.Hq : p.Hkv)) {
+        const uint32_t to = mine + slot * kQ8PassBytes;
+        cp_async16(to, src + at.ca, true);
+        if (both) cp_async16(to + 512, src + at.cb, true);
       }
     }
+    cp_async_commit();
   };
-  fetch(first);
+#pragma unroll
+  for (int i = 0; i < kQ8Ring - 1; ++i) fetch(part + i * step, i);
   // ---- the token's sequence, cache row and angles
   const int b = find_sequence(p.cu, p.B, t, lane);
-  if (b < 0 || b >= p.B) return;
+  if (b < 0 || b >= p.B) {
+    cp_async_wait<0>();
+    return;
+  }
   const int64_t place = static_cast<int64_t>(__ldg(p.start + b)) + t - __ldg(p.cu + b);
   const CachePlace to =
       cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page_size, p.num_pages);
-  uint8_t* const k_to = p.kc + to.page * p.kc_ps + to.row * p.kc_ts;
-  uint8_t* const v_to = p.vc + to.page * p.vc_ps + to.row * p.vc_ts;
-  float* const s_to = p.scales + to.page * p.s_ps + 2 * to.row;
   for (int a = lane; a < angles; a += 32) {
     const int axis = a >= p.pairs ? 1 : 0;
     const double pos = p.positions ? static_cast<double>(__ldg(p.positions + t * p.pos_ts + axis))
@@ -220,103 +213,105 @@ kv_append_q8_kernel(const AppendQ8Params p) {
     sincospif(2.0f * static_cast<float>(turns), &s, &c);
     turn[a] = make_float2(c, s);
   }
-  __syncwarp();
-  // (the bound is the warp's, so that all its lanes reach the reductions)
+  int slot = 0;
 #pragma unroll 1
-  for (int base = first; base < n_rows; base += kQ8Batch * step) {
-    if (base != first) fetch(base);
-    __syncwarp();  // rows rotated in place are written behind every lane's reads
-#pragma unroll
-    for (int i = 0; i < kQ8Batch; ++i) {
-      const int r = base + i * step + sub;
-      if (r - sub >= n_rows) break;
-      const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-      const bool here = r < n_rows && live, two = here && both;
-      float f[16];
-      const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                             x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+  for (int pass = part; pass < passes; pass += step) {
+    cp_async_wait<kQ8Ring - 2>();
+    __syncwarp();  // others' channels and the angles are there, and the last pass's are read
+    fetch(pass + (kQ8Ring - 1) * step, slot == 0 ? kQ8Ring - 1 : slot - 1);
+    const bool is_q = pass < q_passes;
+    const int in = is_q ? pass : pass - q_passes;
+    const bool is_v = !is_q && in >= k_passes;
+    const int r = ((is_v ? in - k_passes : in) << rows_log) + sub;
+    const bool here = live && r < (is_q ? p.Hq : p.Hkv), two = here && both;
+    const uint8_t* const from = ring + slot * kQ8PassBytes;
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+    if (here) x0 = *reinterpret_cast<const uint4*>(from + lane * 16);
+    if (two) x1 = *reinterpret_cast<const uint4*>(from + 512 + lane * 16);
+    float f[16];
+    {
+      const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 u = unpack2<kBf16>((e < 4 ? here : two) ? w[e] : 0u);
+        const float2 u = unpack2<kBf16>(w[e]);
         f[2 * e] = u.x, f[2 * e + 1] = u.y;
       }
-      if (!is_v && here) {
-        if constexpr (kVec == kNeighbours) {
+    }
+    if (!is_v && here) {
+      if constexpr (kVec == kNeighbours) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (at.ca + 2 * e >= rotated) break;
-            const float2 cs = turn[at.ca / 2 + e];
-            const float one = f[2 * e], other = f[2 * e + 1];
-            f[2 * e] = one * cs.x - other * cs.y;
-            f[2 * e + 1] = other * cs.x + one * cs.y;
-          }
-        } else if constexpr (kVec == 8) {
-          if (at.turn >= 0) {
-            const float4* cs = reinterpret_cast<const float4*>(turn + at.turn);
+        for (int e = 0; e < 8; ++e) {
+          if (at.ca + 2 * e >= rotated) break;
+          const float2 cs = turn[at.ca / 2 + e];
+          const float one = f[2 * e], other = f[2 * e + 1];
+          f[2 * e] = one * cs.x - other * cs.y;
+          f[2 * e + 1] = other * cs.x + one * cs.y;
+        }
+      } else if constexpr (kVec == 8) {
+        if (at.turn >= 0) {
+          const float4* cs = reinterpret_cast<const float4*>(turn + at.turn);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 z = cs[e];
-              const float a0 = f[2 * e], a1 = f[2 * e + 1], b0 = f[8 + 2 * e], b1 = f[9 + 2 * e];
-              f[2 * e] = a0 * z.x - b0 * z.y;
-              f[2 * e + 1] = a1 * z.z - b1 * z.w;
-              f[8 + 2 * e] = b0 * z.x + a0 * z.y;
-              f[9 + 2 * e] = b1 * z.z + a1 * z.w;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t yw[4] = {y[i][h].v.x, y[i][h].v.y, y[i][h].v.z, y[i][h].v.w};
-            float g[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 u = unpack2<kBf16>(yw[e]);
-              g[2 * e] = u.x, g[2 * e + 1] = u.y;
-            }
-#pragma unroll
-            for (int s = 0; s < 8 / kPiece; ++s) {
-              const int c = at.ca + 8 * h + s * kPiece;
-              if (c >= rotated) break;
-              const int axis = c >= 2 * p.pairs ? 1 : 0, in = c - 2 * axis * p.pairs;
-              const bool second = in >= p.pairs;
-              const float2* cs = turn + axis * p.pairs + (second ? in - p.pairs : in);
-#pragma unroll
-              for (int e = s * kPiece; e < (s + 1) * kPiece; ++e) {
-                const float2 z = cs[e - s * kPiece];
-                f[8 * h + e] = f[8 * h + e] * z.x + g[e] * (second ? z.y : -z.y);
-              }
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float4 z = cs[e];
+            const float a0 = f[2 * e], a1 = f[2 * e + 1], b0 = f[8 + 2 * e], b1 = f[9 + 2 * e];
+            f[2 * e] = a0 * z.x - b0 * z.y;
+            f[2 * e + 1] = a1 * z.z - b1 * z.w;
+            f[8 + 2 * e] = b0 * z.x + a0 * z.y;
+            f[9 + 2 * e] = b1 * z.z + a1 * z.w;
           }
         }
-      }
-      if (here && (is_q || (!is_v && p.k_out))) {
-        uint16_t* dst = is_q ? p.q_out + t * p.qo_ts + r * p.qo_hs
-                             : p.k_out + t * p.ko_ts + (r - p.Hq) * p.ko_hs;
-        *reinterpret_cast<uint4*>(dst + at.ca) =
-            make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]),
-                       pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
-        if (two)
-          *reinterpret_cast<uint4*>(dst + at.cb) =
-              make_uint4(pack2<kBf16>(f[8], f[9]), pack2<kBf16>(f[10], f[11]),
-                         pack2<kBf16>(f[12], f[13]), pack2<kBf16>(f[14], f[15]));
-      }
-      if (r - sub + per_pass <= p.Hq) continue;  // queries only
-      float top = 0.f;
+      } else {
+        const uint8_t* row = from + (sub << p.row_lanes) * 16;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max_abs(top, f[2 * e], f[2 * e + 1]);
-      for (int o = 1; o < (1 << p.row_lanes); o <<= 1)
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!here || is_q || to.page < 0) continue;
-      const float scale = top < -kNegInf ? fmaxf(__fdiv_rn(top, kTop), kQ8MinScale)
-                                         : __uint_as_float(0x7FC00000u);
-      const float inv = __fdiv_rn(1.f, scale);
-      const int h = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-      uint8_t* dst = is_v ? v_to + h * p.vc_hs : k_to + h * p.kc_hs;
-      *reinterpret_cast<uint2*>(dst + at.ca) = q8_codes<kFmt>(f, inv);
-      if (two) *reinterpret_cast<uint2*>(dst + at.cb) = q8_codes<kFmt>(f + 8, inv);
-      if (unit == 0) s_to[h * p.s_hs + (is_v ? 1 : 0)] = scale;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < 8 / kPiece; ++s) {
+            const int c = at.ca + 8 * h + s * kPiece;
+            if (c >= rotated) break;
+            const int axis = c >= 2 * p.pairs ? 1 : 0, in_axis = c - 2 * axis * p.pairs;
+            const bool second = in_axis >= p.pairs;
+            const int o = second ? c - p.pairs : c + p.pairs;  // the partners
+            union { V v; uint16_t e[kPiece]; } g;
+            g.v = *reinterpret_cast<const V*>(row + ((o >> 3) & 1) * 512 + (o >> 4) * 16 + (o & 7) * 2);
+            const float2* cs = turn + axis * p.pairs + (second ? in_axis - p.pairs : in_axis);
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+              const float2 z = cs[e];
+              float& y = f[8 * h + s * kPiece + e];
+              y = y * z.x + app_float<kBf16>(g.e[e]) * (second ? z.y : -z.y);
+            }
+          }
+      }
     }
+    slot = slot + 1 == kQ8Ring ? 0 : slot + 1;
+    if (here && (is_q || (!is_v && p.k_out))) {
+      uint16_t* dst = is_q ? p.q_out + t * p.qo_ts + r * p.qo_hs : p.k_out + t * p.ko_ts + r * p.ko_hs;
+      *reinterpret_cast<uint4*>(dst + at.ca) =
+          make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]),
+                     pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
+      if (two)
+        *reinterpret_cast<uint4*>(dst + at.cb) =
+            make_uint4(pack2<kBf16>(f[8], f[9]), pack2<kBf16>(f[10], f[11]),
+                       pack2<kBf16>(f[12], f[13]), pack2<kBf16>(f[14], f[15]));
+    }
+    if (is_q || to.page < 0) continue;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max_abs(top, f[2 * e], f[2 * e + 1]);
+    for (int o = 1; o < (1 << p.row_lanes); o <<= 1)
+      top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!here) continue;
+    const float scale = top < -kNegInf ? fmaxf(__fdiv_rn(top, kTop), kQ8MinScale)
+                                       : __uint_as_float(0x7FC00000u);
+    const float inv = __fdiv_rn(1.f, scale);
+    uint8_t* dst = is_v ? p.vc + to.page * p.vc_ps + to.row * p.vc_ts + r * p.vc_hs
+                        : p.kc + to.page * p.kc_ps + to.row * p.kc_ts + r * p.kc_hs;
+    *reinterpret_cast<uint2*>(dst + at.ca) = q8_codes<kFmt>(f, inv);
+    if (two) *reinterpret_cast<uint2*>(dst + at.cb) = q8_codes<kFmt>(f + 8, inv);
+    if (unit == 0)
+      p.scales[to.page * p.s_ps + r * p.s_hs + 2 * to.row + (is_v ? 1 : 0)] = scale;
   }
+  cp_async_wait<0>();
 }
 
 struct ReadQ8Params {
@@ -332,12 +327,12 @@ struct ReadQ8Params {
   FastDiv by_row;                   // 8-channel units of a row
 };
 
-constexpr int kReadBatch = 8;
+constexpr int kReadBatch = 4;
 
 // One warp a token (for few tokens up to 8); a unit is 8 channels of a head, the keys'
 // units first.
 template <bool kBf16, int kFmt>
-__global__ void __launch_bounds__(kQ8Warps * 32) kv_read_q8_kernel(const ReadQ8Params p) {
+__global__ void __launch_bounds__(kQ8Warps * 32, 12) kv_read_q8_kernel(const ReadQ8Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp;
   if ((gw >> p.share) >= p.T) return;

@@ -3600,8 +3600,9 @@ rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stre
   const int rotated = vec == 8 ? 2 * pairs * axes : 0;
   while ((1 << p.row_lanes) < rotated / 16 + (d - rotated + 15) / 16) ++p.row_lanes;
   const dim3 grid(static_cast<unsigned>(((T << p.share) + kQ8Warps - 1) / kQ8Warps));
-  // (each warp's turns start on 16 bytes)
-  const size_t smem = static_cast<size_t>(kQ8Warps) * ((axes * pairs + 1) & ~1) * sizeof(float2);
+  // (each warp's turns start on 16 bytes; 20 KB at most)
+  const size_t smem = static_cast<size_t>(kQ8Warps) *
+                      (kQ8Ring * kQ8PassBytes + ((axes * pairs + 1) & ~1) * sizeof(float2));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == RNN_BF16;
   if (a.codes == RNN_CODES_INT8)
@@ -3830,7 +3831,8 @@ static rnn_status shared_launch(const DecodeParams& p, dim3 grid, const PrefixPa
          : attn_decode_kernel<kBf16, kDP, 2, false, true><<<grid, block, sm, s>>>(p);
   rnn_status r = launched();
   if (r != RNN_OK) return r;
-  launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads), PreShape<kDP>::kSmem, s, true, pre);
+  launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads),
+           PreShape<kDP>::smem(pre.slots, pre.wide > 0), s, true, pre);
   if ((r = launched()) != RNN_OK) return r;
   launch_k(attn_shared_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
            0, s, true, p, pre);
@@ -3936,6 +3938,16 @@ rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args* args, rnn_s
   pre.wide = plan.wide, pre.narrow = plan.narrow;
   pre.wide_splits = plan.wide_splits, pre.narrow_splits = plan.narrow_splits;
   pre.Hkv = Hkv;
+  // no more of the ring than a CTA's loads fill: what is left of the SM's shared memory
+  // goes to the kernel before this one, which then still runs
+  const int64_t most = (std::min<int64_t>(room, kDecMaxKeys) + kAttnN - 1) / kAttnN;
+  const int64_t each = std::max<int64_t>(plan.wide ? (most + plan.wide_splits - 1) / plan.wide_splits : 1,
+                                         plan.narrow ? (most + plan.narrow_splits - 1) / plan.narrow_splits : 1);
+  pre.slot_bits = 1;
+  while ((1 << pre.slot_bits) < (d <= 64 ? PreShape<64>::kStages : PreShape<128>::kStages) &&
+         (1 << pre.slot_bits) < 2 * each)
+    ++pre.slot_bits;
+  pre.slots = 1 << pre.slot_bits;
   pre.c = p.c;
   pre.idesc_s = make_idesc(dtype, kAttnN);
   pre.idesc_o = make_idesc(dtype, (d + 15) / 16 * 16) | (1u << 16);  // B with its channels contiguous
