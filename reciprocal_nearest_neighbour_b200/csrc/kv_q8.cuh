@@ -33,14 +33,16 @@ struct AppendQ8Params {
   const uint16_t *q, *k, *v;        // q may be null
   uint16_t *q_out, *k_out;          // k_out may be null
   uint8_t *kc, *vc;
-  float* scales;                    // [page][head][row][key, value]
-  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;  // elements
-  int64_t kc_ps, kc_ts, kc_hs, vc_ps, vc_ts, vc_hs, s_ps, s_hs;
+  float2* scales;                   // [page][head][row] of key, value
+  // strides in units of 8 elements, of scales in pairs
+  int q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+  int kc_ps, kc_ts, kc_hs, vc_ps, vc_ts, vc_hs, s_ps, s_hs;
   const int32_t *table, *start, *cu, *positions;  // positions may be null
   int64_t table_bs, pos_ts, num_pages;
   const double* inv_freq;
   int T, B, Hq, Hkv, d;             // Hq = 0 without queries
-  int max_pages, page_size;
+  int max_pages;
+  FastDiv page;
   int pairs, axes;                  // channel pairs per axis, axes (0: no rotation)
   int share;                        // log2 of the warps that share a token
   int row_lanes;                    // log2 of the lanes of a row, up to 16 channels each
@@ -97,27 +99,36 @@ __device__ __forceinline__ void q8_floats(uint32_t w, float (&x)[4]) {
     const float2 a = unpack2<false>(lo), b = unpack2<false>(hi);
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
   } else {
+    // a byte with its sign bit flipped, planted into 2^23: 128 + 2^23 above its value
+    const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      x[e] = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
+      x[e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + e)) - 8388736.f;
   }
 }
 
 // Row of a token in the caches, or nothing.
 struct CachePlace {
-  int64_t page;  // -1: not there
+  int page;  // -1: not there
   int row;
 };
 __device__ __forceinline__ CachePlace cache_place(int64_t place, const int32_t* table, int max_pages,
-                                                  int page_size, int64_t num_pages) {
+                                                  const FastDiv& page, int64_t num_pages) {
   CachePlace at{-1, 0};
-  if (place >= 0 && place < static_cast<int64_t>(max_pages) * page_size) {
-    const int pg = static_cast<int>(place / page_size);
-    at.row = static_cast<int>(place - static_cast<int64_t>(pg) * page_size);
-    const int64_t id = __ldg(table + pg);
+  if (place >= 0 && place < static_cast<int64_t>(max_pages) * page.div) {
+    // (a division of 64 bits costs a hundred instructions)
+    const int pg = static_cast<int>(place < 0x7FFFFFFF ? fdiv(static_cast<uint32_t>(place), page)
+                                                       : place / page.div);
+    at.row = static_cast<int>(place - static_cast<int64_t>(pg) * page.div);
+    const int id = __ldg(table + pg);
     if (id >= 0 && id < num_pages) at.page = id;
   }
   return at;
+}
+
+// x * stride in 64 bits, with strides in units of 8 elements (of 2 for scales).
+__device__ __forceinline__ int64_t times(int x, int stride) {
+  return static_cast<int64_t>(x) * stride;
 }
 
 // A lane's channels of a row: two vectors of 8 (cb < 0: one).  Where channels i and
@@ -177,13 +188,16 @@ kv_append_q8_kernel(const AppendQ8Params p) {
   const int q_passes = (p.Hq + fill) >> rows_log, k_passes = (p.Hkv + fill) >> rows_log;
   const int passes = q_passes + 2 * k_passes, step = 1 << p.share;
   const uint32_t mine = smem_u32(ring) + lane * 16;
+  const uint16_t* const q_row = p.q + 8 * times(t, p.q_ts);  // never read without queries
+  const uint16_t* const k_row = p.k + 8 * times(t, p.k_ts);
+  const uint16_t* const v_row = p.v + 8 * times(t, p.v_ts);
   auto fetch = [&](int pass, int slot) {
     if (pass < passes) {
       const int in = pass < q_passes ? pass : pass - q_passes;
       const bool is_q = pass < q_passes, is_v = !is_q && in >= k_passes;
       const int r = ((is_v ? in - k_passes : in) << rows_log) + sub;
-      const uint16_t* src = is_q ? p.q + t * p.q_ts : is_v ? p.v + t * p.v_ts : p.k + t * p.k_ts;
-      src += r * (is_q ? p.q_hs : is_v ? p.v_hs : p.k_hs);
+      const uint16_t* src = is_q ? q_row : is_v ? v_row : k_row;
+      src += 8 * times(r, is_q ? p.q_hs : is_v ? p.v_hs : p.k_hs);
       if (live && r < (is_q ? p.Hq : p.Hkv)) {
         const uint32_t to = mine + slot * kQ8PassBytes;
         cp_async16(to, src + at.ca, true);
@@ -202,7 +216,7 @@ kv_append_q8_kernel(const AppendQ8Params p) {
   }
   const int64_t place = static_cast<int64_t>(__ldg(p.start + b)) + t - __ldg(p.cu + b);
   const CachePlace to =
-      cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page_size, p.num_pages);
+      cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page, p.num_pages);
   for (int a = lane; a < angles; a += 32) {
     const int axis = a >= p.pairs ? 1 : 0;
     const double pos = p.positions ? static_cast<double>(__ldg(p.positions + t * p.pos_ts + axis))
@@ -213,6 +227,9 @@ kv_append_q8_kernel(const AppendQ8Params p) {
     sincospif(2.0f * static_cast<float>(turns), &s, &c);
     turn[a] = make_float2(c, s);
   }
+  uint8_t* const k_to = p.kc + 8 * (times(to.page, p.kc_ps) + times(to.row, p.kc_ts));
+  uint8_t* const v_to = p.vc + 8 * (times(to.page, p.vc_ps) + times(to.row, p.vc_ts));
+  float2* const s_to = p.scales + times(to.page, p.s_ps) + to.row;
   int slot = 0;
 #pragma unroll 1
   for (int pass = part; pass < passes; pass += step) {
@@ -285,7 +302,8 @@ kv_append_q8_kernel(const AppendQ8Params p) {
     }
     slot = slot + 1 == kQ8Ring ? 0 : slot + 1;
     if (here && (is_q || (!is_v && p.k_out))) {
-      uint16_t* dst = is_q ? p.q_out + t * p.qo_ts + r * p.qo_hs : p.k_out + t * p.ko_ts + r * p.ko_hs;
+      uint16_t* dst = is_q ? p.q_out + 8 * (times(t, p.qo_ts) + times(r, p.qo_hs))
+                           : p.k_out + 8 * (times(t, p.ko_ts) + times(r, p.ko_hs));
       *reinterpret_cast<uint4*>(dst + at.ca) =
           make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]),
                      pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
@@ -304,79 +322,97 @@ kv_append_q8_kernel(const AppendQ8Params p) {
     const float scale = top < -kNegInf ? fmaxf(__fdiv_rn(top, kTop), kQ8MinScale)
                                        : __uint_as_float(0x7FC00000u);
     const float inv = __fdiv_rn(1.f, scale);
-    uint8_t* dst = is_v ? p.vc + to.page * p.vc_ps + to.row * p.vc_ts + r * p.vc_hs
-                        : p.kc + to.page * p.kc_ps + to.row * p.kc_ts + r * p.kc_hs;
+    uint8_t* dst = (is_v ? v_to : k_to) + 8 * times(r, is_v ? p.vc_hs : p.kc_hs);
     *reinterpret_cast<uint2*>(dst + at.ca) = q8_codes<kFmt>(f, inv);
     if (two) *reinterpret_cast<uint2*>(dst + at.cb) = q8_codes<kFmt>(f + 8, inv);
-    if (unit == 0)
-      p.scales[to.page * p.s_ps + r * p.s_hs + 2 * to.row + (is_v ? 1 : 0)] = scale;
+    if (unit == 0) reinterpret_cast<float*>(s_to + times(r, p.s_hs))[is_v ? 1 : 0] = scale;
   }
   cp_async_wait<0>();
 }
 
 struct ReadQ8Params {
   const uint8_t *kc, *vc;
-  const float* scales;
+  const float2* scales;
   uint16_t *k, *v;
-  int64_t kc_ps, kc_ts, kc_hs, vc_ps, vc_ts, vc_hs, s_ps, s_hs;
-  int64_t k_ts, k_hs, v_ts, v_hs;
+  // strides in units of 8 elements, of scales in pairs
+  int kc_ps, kc_ts, kc_hs, vc_ps, vc_ts, vc_hs, s_ps, s_hs;
+  int k_ts, k_hs, v_ts, v_hs;
   const int32_t *table, *start, *cu;  // start may be null
   int64_t table_bs, num_pages;
-  int T, B, Hkv, d, max_pages, page_size;
-  int share;
+  int T, B, Hkv, d, max_pages;
+  FastDiv page;
+  int share;                        // log2 of the warps that share a token
+  int tokens;                       // of a warp
   FastDiv by_row;                   // 8-channel units of a row
 };
 
-constexpr int kReadBatch = 4;
+constexpr int kReadBatch = 4, kReadTokens = 4;
 
-// One warp a token (for few tokens up to 8); a unit is 8 channels of a head, the keys'
-// units first.
+// One warp per `tokens` tokens, whose places its lanes look up together (for few
+// tokens up to 8 warps share one); a unit is 8 channels of a head.
 template <bool kBf16, int kFmt>
-__global__ void __launch_bounds__(kQ8Warps * 32, 12) kv_read_q8_kernel(const ReadQ8Params p) {
+__global__ void __launch_bounds__(kQ8Warps * 32) kv_read_q8_kernel(const ReadQ8Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kQ8Warps + warp;
-  if ((gw >> p.share) >= p.T) return;
-  const int t = static_cast<int>(gw >> p.share);
+  const int64_t t0 = (gw >> p.share) * p.tokens;
+  if (t0 >= p.T) return;
   const int part = static_cast<int>(gw) & ((1 << p.share) - 1);
-  const int b = find_sequence(p.cu, p.B, t, lane);
-  if (b < 0 || b >= p.B) return;
-  const int64_t place =
-      static_cast<int64_t>(p.start ? __ldg(p.start + b) : 0) + t - __ldg(p.cu + b);
-  const CachePlace at =
-      cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page_size, p.num_pages);
-  const int row_units = p.by_row.div, half = p.Hkv * row_units;
-  const int step = 32 << p.share;
-  for (int u0 = part * 32 + lane; u0 < 2 * half; u0 += kReadBatch * step) {
-    uint2 w[kReadBatch];
-    float s[kReadBatch];
-#pragma unroll
-    for (int i = 0; i < kReadBatch; ++i) {
-      const int u = u0 + i * step;
-      if (u >= 2 * half) break;
-      const bool is_v = u >= half;
-      const int in = is_v ? u - half : u, h = fdiv(in, p.by_row), c = (in - h * row_units) * 8;
-      w[i] = make_uint2(0u, 0u);
-      s[i] = 0.f;
-      if (at.page >= 0) {
-        const uint8_t* src = is_v ? p.vc + at.page * p.vc_ps + at.row * p.vc_ts + h * p.vc_hs
-                                  : p.kc + at.page * p.kc_ps + at.row * p.kc_ts + h * p.kc_hs;
-        w[i] = __ldg(reinterpret_cast<const uint2*>(src + c));
-        s[i] = __ldg(p.scales + at.page * p.s_ps + h * p.s_hs + 2 * at.row + (is_v ? 1 : 0));
-      }
+  const int first = find_sequence(p.cu, p.B, static_cast<int>(t0), lane);
+  // lane i: token t0 + i, page -2: not in a sequence
+  CachePlace mine{-2, 0};
+  if (lane < p.tokens && t0 + lane < p.T) {
+    const int t = static_cast<int>(t0) + lane;
+    int b = first;
+    while (b < p.B && __ldg(p.cu + b + 1) <= t) ++b;
+    if (b >= 0 && b < p.B) {
+      const int64_t place =
+          static_cast<int64_t>(p.start ? __ldg(p.start + b) : 0) + t - __ldg(p.cu + b);
+      mine = cache_place(place, p.table + b * p.table_bs, p.max_pages, p.page, p.num_pages);
     }
+  }
+  const int row_units = p.by_row.div, units = p.Hkv * row_units;
+  const int step = 32 << p.share;
+#pragma unroll 1
+  for (int i = 0; i < p.tokens; ++i) {
+    const int page = __shfl_sync(0xffffffffu, mine.page, i);
+    const int row = __shfl_sync(0xffffffffu, mine.row, i);
+    if (page == -2) continue;
+    const int t = static_cast<int>(t0) + i;
+    const float2* const sc = p.scales + times(page, p.s_ps) + row;
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+      const uint8_t* const from =
+          kind ? p.vc + 8 * (times(page, p.vc_ps) + times(row, p.vc_ts))
+               : p.kc + 8 * (times(page, p.kc_ps) + times(row, p.kc_ts));
+      uint16_t* const to = kind ? p.v + 8 * times(t, p.v_ts) : p.k + 8 * times(t, p.k_ts);
+      const int from_hs = kind ? p.vc_hs : p.kc_hs, to_hs = kind ? p.v_hs : p.k_hs;
+      for (int u0 = part * 32 + lane; u0 < units; u0 += kReadBatch * step) {
+        uint2 w[kReadBatch];
+        float s[kReadBatch];
+        int h[kReadBatch], c[kReadBatch];  // head, and unit of its row
 #pragma unroll
-    for (int i = 0; i < kReadBatch; ++i) {
-      const int u = u0 + i * step;
-      if (u >= 2 * half) break;
-      const bool is_v = u >= half;
-      const int in = is_v ? u - half : u, h = fdiv(in, p.by_row), c = (in - h * row_units) * 8;
-      float a[4], e[4];
-      q8_floats<kFmt>(w[i].x, a);
-      q8_floats<kFmt>(w[i].y, e);
-      uint16_t* dst = is_v ? p.v + t * p.v_ts + h * p.v_hs : p.k + t * p.k_ts + h * p.k_hs;
-      *reinterpret_cast<uint4*>(dst + c) = make_uint4(
-          pack2<kBf16>(a[0] * s[i], a[1] * s[i]), pack2<kBf16>(a[2] * s[i], a[3] * s[i]),
-          pack2<kBf16>(e[0] * s[i], e[1] * s[i]), pack2<kBf16>(e[2] * s[i], e[3] * s[i]));
+        for (int j = 0; j < kReadBatch; ++j) {
+          const int u = u0 + j * step;
+          if (u >= units) break;
+          h[j] = fdiv(u, p.by_row), c[j] = u - h[j] * row_units;
+          w[j] = make_uint2(0u, 0u);
+          s[j] = 0.f;
+          if (page >= 0) {
+            w[j] = __ldg(reinterpret_cast<const uint2*>(from) + (times(h[j], from_hs) + c[j]));
+            s[j] = __ldg(reinterpret_cast<const float*>(sc + times(h[j], p.s_hs)) + kind);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kReadBatch; ++j) {
+          if (u0 + j * step >= units) break;
+          float a[4], e[4];
+          q8_floats<kFmt>(w[j].x, a);
+          q8_floats<kFmt>(w[j].y, e);
+          reinterpret_cast<uint4*>(to)[times(h[j], to_hs) + c[j]] = make_uint4(
+              pack2<kBf16>(a[0] * s[j], a[1] * s[j]), pack2<kBf16>(a[2] * s[j], a[3] * s[j]),
+              pack2<kBf16>(e[0] * s[j], e[1] * s[j]), pack2<kBf16>(e[2] * s[j], e[3] * s[j]));
+        }
+      }
     }
   }
 }

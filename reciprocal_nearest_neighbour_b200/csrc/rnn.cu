@@ -3443,6 +3443,22 @@ static rnn_status check_cache_call(int64_t T, int B, int Hkv, int d, int dtype, 
   return RNN_OK;
 }
 
+// Strides as the kernels take them, 32-bit numbers of 8 elements (of pairs for scales).
+static bool unit_stride(int64_t stride, int unit, int* to) {
+  *to = static_cast<int>(stride / unit);
+  return stride / unit <= INT32_MAX;
+}
+static bool in_units(const rnn_rows& r, int* token, int* head) {
+  return unit_stride(r.token_stride, 8, token) && unit_stride(r.head_stride, 8, head);
+}
+static bool in_units(const rnn_pages& c, int* page, int* token, int* head) {
+  return unit_stride(c.page_stride, 8, page) && unit_stride(c.token_stride, 8, token) &&
+         unit_stride(c.head_stride, 8, head);
+}
+static bool in_units(const rnn_scales& s, int* page, int* head) {
+  return unit_stride(s.page_stride, 2, page) && unit_stride(s.head_stride, 2, head);
+}
+
 // Warps that share a token, log2: up to 8, while all of them fit on the GPU at once.
 static int token_share(int64_t T, int sms) {
   int share = 0;
@@ -3552,9 +3568,6 @@ rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stre
   };
   if (T > 0 && ((Hq > 0 && moved(a.q, a.q_out)) || (a.k_out.data && moved(a.k, a.k_out))))
     return RNN_EINVAL;
-  DeviceInfo* di = nullptr;
-  if ((r = device_info(&di)) != RNN_OK) return r;
-  if (T == 0 || a.B == 0) return RNN_OK;
   AppendQ8Params p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const uint16_t*>(a.q.data);
@@ -3564,15 +3577,16 @@ rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stre
   p.k_out = static_cast<uint16_t*>(a.k_out.data);
   p.kc = static_cast<uint8_t*>(a.k_cache.data);
   p.vc = static_cast<uint8_t*>(a.v_cache.data);
-  p.scales = a.scales.data;
-  p.q_ts = a.q.token_stride, p.q_hs = a.q.head_stride;
-  p.k_ts = a.k.token_stride, p.k_hs = a.k.head_stride;
-  p.v_ts = a.v.token_stride, p.v_hs = a.v.head_stride;
-  p.qo_ts = a.q_out.token_stride, p.qo_hs = a.q_out.head_stride;
-  p.ko_ts = a.k_out.token_stride, p.ko_hs = a.k_out.head_stride;
-  p.kc_ps = a.k_cache.page_stride, p.kc_ts = a.k_cache.token_stride, p.kc_hs = a.k_cache.head_stride;
-  p.vc_ps = a.v_cache.page_stride, p.vc_ts = a.v_cache.token_stride, p.vc_hs = a.v_cache.head_stride;
-  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
+  p.scales = reinterpret_cast<float2*>(a.scales.data);
+  if (!(Hq == 0 || (in_units(a.q, &p.q_ts, &p.q_hs) && in_units(a.q_out, &p.qo_ts, &p.qo_hs))) ||
+      !in_units(a.k, &p.k_ts, &p.k_hs) || !in_units(a.v, &p.v_ts, &p.v_hs) ||
+      !(!a.k_out.data || in_units(a.k_out, &p.ko_ts, &p.ko_hs)) ||
+      !in_units(a.k_cache, &p.kc_ps, &p.kc_ts, &p.kc_hs) ||
+      !in_units(a.v_cache, &p.vc_ps, &p.vc_ts, &p.vc_hs) || !in_units(a.scales, &p.s_ps, &p.s_hs))
+    return RNN_EUNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK) return r;
+  if (T == 0 || a.B == 0) return RNN_OK;
   p.table = a.page_table;
   p.start = a.start;
   p.cu = a.cu;
@@ -3587,7 +3601,7 @@ rnn_status rnn_kv_append_q8(const rnn_kv_append_q8_args* args, rnn_stream_t stre
   p.Hkv = Hkv;
   p.d = d;
   p.max_pages = a.max_pages;
-  p.page_size = a.page_size;
+  p.page = make_fastdiv(a.page_size);
   p.pairs = pairs;
   p.axes = axes;
   p.share = token_share(T, di->sms);
@@ -3628,21 +3642,20 @@ rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args* args, rnn_stream_t stream) 
       (r = check_scales(&a.scales, a.num_pages, a.page_size, a.Hkv)) != RNN_OK)
     return r;
   if (a.T > 0 && a.k.data == a.v.data) return RNN_EINVAL;
-  DeviceInfo* di = nullptr;
-  if ((r = device_info(&di)) != RNN_OK) return r;
-  if (a.T == 0 || a.B == 0) return RNN_OK;
   ReadQ8Params p;
   std::memset(&p, 0, sizeof(p));
   p.kc = static_cast<const uint8_t*>(a.k_cache.data);
   p.vc = static_cast<const uint8_t*>(a.v_cache.data);
-  p.scales = a.scales.data;
+  p.scales = reinterpret_cast<const float2*>(a.scales.data);
   p.k = static_cast<uint16_t*>(a.k.data);
   p.v = static_cast<uint16_t*>(a.v.data);
-  p.kc_ps = a.k_cache.page_stride, p.kc_ts = a.k_cache.token_stride, p.kc_hs = a.k_cache.head_stride;
-  p.vc_ps = a.v_cache.page_stride, p.vc_ts = a.v_cache.token_stride, p.vc_hs = a.v_cache.head_stride;
-  p.s_ps = a.scales.page_stride, p.s_hs = a.scales.head_stride;
-  p.k_ts = a.k.token_stride, p.k_hs = a.k.head_stride;
-  p.v_ts = a.v.token_stride, p.v_hs = a.v.head_stride;
+  if (!in_units(a.k, &p.k_ts, &p.k_hs) || !in_units(a.v, &p.v_ts, &p.v_hs) ||
+      !in_units(a.k_cache, &p.kc_ps, &p.kc_ts, &p.kc_hs) ||
+      !in_units(a.v_cache, &p.vc_ps, &p.vc_ts, &p.vc_hs) || !in_units(a.scales, &p.s_ps, &p.s_hs))
+    return RNN_EUNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  if ((r = device_info(&di)) != RNN_OK) return r;
+  if (a.T == 0 || a.B == 0) return RNN_OK;
   p.table = a.page_table;
   p.start = a.start;
   p.cu = a.cu;
@@ -3653,10 +3666,13 @@ rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args* args, rnn_stream_t stream) 
   p.Hkv = a.Hkv;
   p.d = a.d;
   p.max_pages = a.max_pages;
-  p.page_size = a.page_size;
+  p.page = make_fastdiv(a.page_size);
   p.share = token_share(a.T, di->sms);
+  // several tokens a warp once there are more than run at once
+  p.tokens = a.T >= int64_t{256} * di->sms ? kReadTokens : 1;
   p.by_row = make_fastdiv(a.d / 8);
-  const dim3 grid(static_cast<unsigned>(((a.T << p.share) + kQ8Warps - 1) / kQ8Warps)), block(kQ8Warps * 32);
+  const int64_t warps = ((a.T + p.tokens - 1) / p.tokens) << p.share;
+  const dim3 grid(static_cast<unsigned>((warps + kQ8Warps - 1) / kQ8Warps)), block(kQ8Warps * 32);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == RNN_BF16;
   if (a.codes == RNN_CODES_INT8)
@@ -3692,11 +3708,11 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
       (r = check_scales(&a.scales, a.num_pages, a.page_size, Hkv)) != RNN_OK)
     return r;
   if (B > INT32_MAX - 1024 || static_cast<int64_t>(B) * Hq > INT32_MAX) return RNN_EUNSUPPORTED;
-  // the kernel's strides are 32-bit numbers of 8 bytes
-  for (const rnn_pages* c : {&a.k_cache, &a.v_cache})
-    for (int64_t x : {c->page_stride, c->token_stride, c->head_stride})
-      if (x / 8 > INT32_MAX) return RNN_EUNSUPPORTED;
-  if (a.scales.page_stride / 2 > INT32_MAX || a.scales.head_stride / 2 > INT32_MAX) return RNN_EUNSUPPORTED;
+  int k_s8[3], v_s8[3], s_s8[3];
+  s_s8[1] = 1;
+  if (!in_units(a.k_cache, &k_s8[0], &k_s8[1], &k_s8[2]) || !in_units(a.v_cache, &v_s8[0], &v_s8[1], &v_s8[2]) ||
+      !in_units(a.scales, &s_s8[0], &s_s8[2]))
+    return RNN_EUNSUPPORTED;
   if (!a.workspace || !aligned256(a.workspace) ||
       a.ws_bytes < rnn_attn_decode_q8_workspace_size(B, Hq, Hkv, d))
     return RNN_EWORKSPACE;
@@ -3714,12 +3730,9 @@ rnn_status rnn_attn_decode_q8(const rnn_attn_decode_q8_args* args, rnn_stream_t 
   p.kc8 = static_cast<const uint8_t*>(a.k_cache.data);
   p.vc8 = static_cast<const uint8_t*>(a.v_cache.data);
   p.scales = a.scales.data;
-  const auto units = [](int (&to)[3], int64_t page, int64_t row, int64_t head) {
-    to[0] = static_cast<int>(page), to[1] = static_cast<int>(row), to[2] = static_cast<int>(head);
-  };
-  units(p.k_s8, p.k_ps / 8, p.k_ts / 8, p.k_hs / 8);
-  units(p.v_s8, p.v_ps / 8, p.v_ts / 8, p.v_hs / 8);
-  units(p.s_s8, a.scales.page_stride / 2, 1, a.scales.head_stride / 2);
+  std::copy(k_s8, k_s8 + 3, p.k_s8);
+  std::copy(v_s8, v_s8 + 3, p.v_s8);
+  std::copy(s_s8, s_s8 + 3, p.s_s8);
   p.wide = d % 16 == 0 && (p.k_ps | p.k_ts | p.k_hs | p.v_ps | p.v_ts | p.v_hs) % 16 == 0;
   p.lse = a.lse;
   p.table = a.page_table;

@@ -49,6 +49,11 @@ def cache_errors(call):
     assert call(sc=scales(p=None)) == EINVAL and call(sc=scales(p=FAKE + 4)) == EINVAL
     assert call(sc=scales(head=30)) == EINVAL and call(sc=scales(page=2)) == EINVAL
     assert call(sc=scales(head=33)) == EALIGN and call(sc=scales(page=131)) == EALIGN
+    # strides beyond 32-bit numbers of 8 codes, or of pairs of scales
+    for name in ("kc", "vc"):
+        assert call(**{name: pages(page=1 << 34)}) == EUNSUP
+        assert call(**{name: pages(head=1 << 34)}) == EUNSUP
+    assert call(sc=scales(page=1 << 32)) == EUNSUP and call(sc=scales(head=1 << 32)) == EUNSUP
 
 
 def test_append_errors(lib):
