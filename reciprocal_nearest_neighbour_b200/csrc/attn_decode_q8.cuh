@@ -43,10 +43,6 @@ struct DecQ8Shape {
                                   kDecWarps * kDecRows * 8;
 };
 
-// 16 bytes to shared memory.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // 8 bytes to shared memory; with `live` false they are zeroed and nothing is read.
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
   const int n = live ? 8 : 0;
