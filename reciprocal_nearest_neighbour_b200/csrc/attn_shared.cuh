@@ -19,8 +19,8 @@
 //                   from tensor memory, probabilities back over them as the 16-bit A
 //                   operand of the second product; in the end the row's part
 //   warps 8, 9      issue S = Q K^T and O += P V of tile 0 and 1
-//   warps 12-15     fetch the queries, then a ring of alternating K and V tiles, by
-//                   16-byte asynchronous copies: pages of any size and stride
+//   warps 12-15     fetch the queries, then K tiles (two warps) and V tiles (two) into a
+//                   ring each, by 16-byte asynchronous copies: pages of any size and stride
 //                   lie in shared memory as the tensor cores' 128-byte swizzle wants them
 // Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
 #pragma once
@@ -40,10 +40,10 @@ template <int kDP>
 struct PreShape {
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
-  static constexpr int kStages = kDP == 128 ? 4 : 8;  // at most; a power of two
-  // with `slots` of the ring, and one row tile where every unit is narrow
+  static constexpr int kStages = kDP == 128 ? 2 : 4;  // of each ring, at most; a power of two
+  // with `slots` of each ring, and one row tile where every unit is narrow
   static constexpr size_t smem(int slots, bool any_wide) {
-    return 1024 + size_t((any_wide ? 2 : 1) + slots) * kTileBytes + 512;
+    return 1024 + size_t((any_wide ? 2 : 1) + 2 * slots) * kTileBytes + 512;
   }
   static constexpr size_t kSmem = smem(kStages, true);
 };
@@ -60,7 +60,7 @@ struct PrefixParams {
   int wide, narrow;                    // units of a key head: wide ones, and 0 or 1 narrow one
   int wide_splits, narrow_splits;      // CTAs that share a unit's keys
   int Hkv;
-  int slots, slot_bits;                // of the ring, and its log2
+  int slots, slot_bits;                // of each ring, and its log2
   float c;                             // scale * log2(e)
   uint32_t idesc_s, idesc_o;
   float* part;                         // [slot][128][kDP] unnormalised parts
@@ -86,10 +86,10 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_tiles = smem, ring = smem + (p.wide ? 2 : 1) * S::kTileBytes;
-  const uint32_t bars = ring + p.slots * S::kTileBytes;
+  const uint32_t bars = ring + 2 * p.slots * S::kTileBytes;
   const uint32_t full_bar = bars;
-  const uint32_t empty_bar = full_bar + 8 * kStages;
-  const uint32_t qfull_bar = empty_bar + 8 * kStages;
+  const uint32_t empty_bar = full_bar + 16 * kStages;
+  const uint32_t qfull_bar = empty_bar + 16 * kStages;
   const uint32_t s_bar = qfull_bar + 8;     // scores of tile i are in tensor memory
   const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
   const uint32_t o_bar = p_bar + 32;        // its output is complete so far
@@ -97,8 +97,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const uint32_t tmem_slot = drain_bar + 16;
   const uint32_t abort_at = tmem_slot + 4;
   // Keys that exist, 4 words for each of 8 tiles: when a tile's words are written, the
-  // values six tiles and more before it have been given back by both row tiles, so the
-  // softmax has read their words.
+  // scores of the tile four before it are done, so the softmax has read the words of the
+  // one eight before it.
   const uint32_t mask_at = (tmem_slot + 8 + 15) & ~15u;
   const uint32_t turn_at = mask_at + 128;   // per softmax warp: steps whose exponentials are out
 
@@ -120,9 +120,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
   const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
 
-  // the ring: load x in slot x % slots
-  auto slot_of = [&](int load) { return load & (p.slots - 1); };
-  auto turn_of = [&](int load) { return (load >> p.slot_bits) & 1; };
+  // the rings: K of key tile j in slot j % slots, V behind the K slots
+  auto slot_of = [&](int j) { return j & (p.slots - 1); };
+  auto turn_of = [&](int j) { return (j >> p.slot_bits) & 1; };
 
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto wait = [&](uint32_t bar, uint32_t parity, int code) {
@@ -139,8 +139,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
     }
   };
-  if (threadIdx.x < p.slots) {
-    mbar_init(full_bar + 8 * threadIdx.x, 4);
+  if (threadIdx.x < 2 * p.slots) {
+    mbar_init(full_bar + 8 * threadIdx.x, 2);
     mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
     fence_barrier_init();
   } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
@@ -174,6 +174,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       // ------------------------------------------------------------- loads
       constexpr int kChunks = kDP / 8, kRowsPer = 32 / kChunks;
       const int w = warp - kPreLoadWarp;
+      const bool is_v = w >= 2;               // of the rings
+      const int first = is_v ? p.slots : 0, rows0 = (w & 1) * 64;
       const int ch = lane % kChunks, sub = lane / kChunks;
       const bool ch_live = ch * 8 < p.d;
       // chunk `ch` of row r in the 128-byte swizzle of its 64-channel block
@@ -207,16 +209,18 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * slot_of(told - 1));
+        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * (first + slot_of(told - 1)));
         ++told;
       };
       issued = 1;
-      const int loads = p.stall_loads ? 0 : 2 * n;
+      const int loads = p.stall_loads ? 0 : n;
+      const uint16_t* const base = is_v ? p.vc : p.kc;
+      const int64_t ps = is_v ? p.v_ps : p.k_ps, ts = is_v ? p.v_ts : p.k_ts;
+      const uint16_t* const head = base + hk * (is_v ? p.v_hs : p.k_hs) + ch * 8;
       bool ok = true;
-      int id = -1;
-      for (int l = 0; l < loads; ++l) {
-        const int slot = slot_of(l);
-        const uint32_t eb = empty_bar + 8 * slot, parity = turn_of(l) ^ 1u;
+      for (int j = 0; j < loads; ++j) {
+        const int slot = first + slot_of(j);
+        const uint32_t eb = empty_bar + 8 * slot, parity = turn_of(j) ^ 1u;
         while (!__all_sync(0xffffffffu, mbar_test_wait(eb, parity))) {
           if (told < issued) {
             tell();
@@ -226,44 +230,42 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
           }
         }
         if (!ok) break;
-        const int t0 = (tile0 + (l >> 1)) * kAttnN + w * 32, t = t0 + lane;
-        if (!(l & 1)) {  // a tile's keys: their pages, for its values too
-          id = -1;
+        const uint32_t dst = ring + slot * S::kTileBytes;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // 32 rows, a lane's page for each
+          const int r0 = rows0 + half * 32, t = (tile0 + j) * kAttnN + r0 + lane;
+          int id = -1;
           if (t < keys) {
             id = __ldg(p.pages + fdiv(t, p.page));
             if (id < 0 || id >= p.num_pages) id = -1;
           }
-          const unsigned there = __ballot_sync(0xffffffffu, id >= 0);
-          if (lane == 0) sts_volatile(mask_at + 16 * ((l >> 1) & 7) + 4 * w, static_cast<int>(there));
-        }
-        const unsigned valid = __ballot_sync(0xffffffffu, id >= 0);
-        const uint16_t* base = l & 1 ? p.vc : p.kc;
-        const int64_t ps = l & 1 ? p.v_ps : p.k_ps, ts = l & 1 ? p.v_ts : p.k_ts;
-        const uint16_t* head = base + hk * (l & 1 ? p.v_hs : p.k_hs) + ch * 8;
-        const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
-        const uint32_t dst = ring + slot * S::kTileBytes;
-        if (p.page16) {
+          const unsigned valid = __ballot_sync(0xffffffffu, id >= 0);
+          if (!is_v && lane == 0)
+            sts_volatile(mask_at + 16 * (j & 7) + (r0 >> 3), static_cast<int>(valid));
+          const int row = t - static_cast<int>(fdiv(t, p.page)) * static_cast<int>(p.page.div);
+          if (p.page16) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
-            const int r0 = __shfl_sync(0xffffffffu, row, g * 16) + sub;
-            const uint16_t* src = head + page * ps + r0 * ts;
+            for (int g = 0; g < 2; ++g) {
+              const int64_t page = max(0, __shfl_sync(0xffffffffu, id, g * 16));
+              const int row0 = __shfl_sync(0xffffffffu, row, g * 16) + sub;
+              const uint16_t* src = head + page * ps + row0 * ts;
 #pragma unroll
-            for (int i = 0; i < 16 / kRowsPer; ++i) {
-              const int r = g * 16 + i * kRowsPer + sub;
-              const bool live = ((valid >> r) & 1u) && ch_live;
-              cp_async16(dst + at(w * 32 + r), live ? src : base, live);
-              src += kRowsPer * ts;
+              for (int i = 0; i < 16 / kRowsPer; ++i) {
+                const int r = g * 16 + i * kRowsPer + sub;
+                const bool live = ((valid >> r) & 1u) && ch_live;
+                cp_async16(dst + at(r0 + r), live ? src : base, live);
+                src += kRowsPer * ts;
+              }
             }
-          }
-        } else {
-          const int64_t off = id * ps + row * ts;
+          } else {
+            const int64_t off = id * ps + row * ts;
 #pragma unroll 4
-          for (int i = 0; i < 32 / kRowsPer; ++i) {
-            const int r = i * kRowsPer + sub;
-            const int64_t o = __shfl_sync(0xffffffffu, off, r);
-            const bool live = ((valid >> r) & 1u) && ch_live;
-            cp_async16(dst + at(w * 32 + r), live ? head + o : base, live);
+            for (int i = 0; i < 32 / kRowsPer; ++i) {
+              const int r = i * kRowsPer + sub;
+              const int64_t o = __shfl_sync(0xffffffffu, off, r);
+              const bool live = ((valid >> r) & 1u) && ch_live;
+              cp_async16(dst + at(r0 + r), live ? head + o : base, live);
+            }
           }
         }
         cp_async_commit();
@@ -271,11 +273,11 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         if (issued - told > 4) tell();
       }
       while (told < issued) tell();
-      if (w == 0 && !aborted()) {
+      if (!(w & 1) && !aborted()) {
         // no arrival of a product's completion is under way when the CTA exits
-        const int l = max(0, loads - p.slots) + lane;
-        if (lane < p.slots && l < loads)
-          settle_phase(empty_bar + 8 * slot_of(l), turn_of(l), p.wait_limit_ns, p.err);
+        const int j = max(0, loads - p.slots) + lane;
+        if (lane < p.slots && j < loads)
+          settle_phase(empty_bar + 8 * (first + slot_of(j)), turn_of(j), p.wait_limit_ns, p.err);
         __syncwarp();
       }
     } else if (warp < kPreMmaWarp + 2) {
@@ -292,9 +294,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       };
       if (n_of[i] > 0) wait_mma(qfull_bar, 0);
       for (int k = 0; ok && k < n_of[i]; ++k) {
-        const int kx = 2 * tile_of(i, k), vx = kx + 1;
-        const int ks = slot_of(kx), vs = slot_of(vx);
-        if (!wait_mma(full_bar + 8 * ks, turn_of(kx))) break;
+        const int j = tile_of(i, k), ks = slot_of(j), vs = p.slots + ks;
+        if (!wait_mma(full_bar + 8 * ks, turn_of(j))) break;
         // the probabilities lie over the scores: the product that reads them first
         if (k > 0 && !wait_mma(o_bar + 8 * i, (k - 1) & 1)) break;
         tc_fence_after();
@@ -314,7 +315,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         umma_commit_warp(s_bar + 8 * i);
         umma_commit_warp(empty_bar + 8 * ks);
         any = true;
-        if (!wait_mma(full_bar + 8 * vs, turn_of(vx))) break;
+        if (!wait_mma(full_bar + 8 * vs, turn_of(j))) break;
         const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -3951,14 +3951,13 @@ rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args* args, rnn_s
   pre.wide = plan.wide, pre.narrow = plan.narrow;
   pre.wide_splits = plan.wide_splits, pre.narrow_splits = plan.narrow_splits;
   pre.Hkv = Hkv;
-  // no more of the ring than a CTA's loads fill: what is left of the SM's shared memory
+  // no more of the rings than a CTA's loads fill: what is left of the SM's shared memory
   // goes to the kernel before this one, which then still runs
   const int64_t most = (std::min<int64_t>(room, kDecMaxKeys) + kAttnN - 1) / kAttnN;
   const int64_t each = std::max<int64_t>(plan.wide ? (most + plan.wide_splits - 1) / plan.wide_splits : 1,
                                          plan.narrow ? (most + plan.narrow_splits - 1) / plan.narrow_splits : 1);
-  pre.slot_bits = 1;
   while ((1 << pre.slot_bits) < (d <= 64 ? PreShape<64>::kStages : PreShape<128>::kStages) &&
-         (1 << pre.slot_bits) < 2 * each)
+         (1 << pre.slot_bits) < each)
     ++pre.slot_bits;
   pre.slots = 1 << pre.slot_bits;
   pre.c = p.c;
