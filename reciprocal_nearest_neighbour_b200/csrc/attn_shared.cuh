@@ -15,12 +15,12 @@
 // prefix's 128-key tiles.  With more than 128 rows (wide) its two row tiles go over the
 // same keys, with up to 128 (narrow) the one row tile is there twice, for every other key
 // tile, so that in either case one tile's softmax runs under the other's products:
-//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row (as in attn_prompt): scores
-//                   from tensor memory, probabilities back over them as the 16-bit A
-//                   operand of the second product; in the end the row's part
+//   warps 0-3, 4-7  fetch the queries of tile 0 and 1; then the softmax, one thread a row
+//                   (as in attn_prompt): scores from tensor memory, probabilities back over
+//                   them as the 16-bit A operand of the second product; in the end the
+//                   rows' parts
 //   warps 8, 9      issue S = Q K^T and O += P V of tile 0 and 1
-//   warps 12-15     fetch the queries, then K tiles (two warps) and V tiles (two) into a
-//                   ring each, by 16-byte asynchronous copies: pages of any size and stride
+//   warps 12-15     fetch K tiles (two warps) and V tiles (two) into a ring each, by 16-byte asynchronous copies: pages of any size and stride
 //                   lie in shared memory as the tensor cores' 128-byte swizzle wants them
 // Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
 #pragma once
@@ -150,7 +150,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     mbar_init(p_bar + 8 * (2 + i), 4);
     mbar_init(o_bar + 8 * i, 1);
     mbar_init(drain_bar + 8 * i, 1);
-    if (i == 0) mbar_init(qfull_bar, 4);
+    if (i == 0) mbar_init(qfull_bar, wide ? 8 : 4);
     fence_barrier_init();
   } else if (threadIdx.x >= 64 && threadIdx.x < 72) {
     sts_volatile(turn_at + 4 * (threadIdx.x - 64), 0);
@@ -168,6 +168,11 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int n_of[2] = {wide ? n : (n + 1) / 2, wide ? n : n / 2};
   auto tile_of = [&](int i, int k) { return wide ? k : 2 * k + i; };
 
+  // 16-byte chunk `ch` of row r of a tile, in the 128-byte swizzle of its 64-channel block
+  auto chunk_at = [](int r, int ch) {
+    return (ch >> 3) * S::kBlockBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  };
+
   if (warp >= kPreMmaWarp) {
     regs_give<kAttnRegsOther>();
     if (warp >= kPreLoadWarp) {
@@ -178,27 +183,10 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       const int first = is_v ? p.slots : 0, rows0 = (w & 1) * 64;
       const int ch = lane % kChunks, sub = lane / kChunks;
       const bool ch_live = ch * 8 < p.d;
-      // chunk `ch` of row r in the 128-byte swizzle of its 64-channel block
-      auto at = [&](int r) {
-        return (ch >> 3) * S::kBlockBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-      };
-      // (a unit without keys fetches nothing, a narrow one its one row tile)
-      if (n > 0 && !p.stall_loads) {
-        for (int i = 0; i < (wide ? 2 : 1); ++i) {
-          for (int r = w * 32 + sub; r < w * 32 + 32; r += kRowsPer) {
-            const bool live = i * kAttnM + r < rows && ch_live;
-            const int row = unit * kPreUnit + i * kAttnM + r;
-            const int b = live ? fdiv(row, p.by_group) : 0;
-            const uint16_t* src = p.q + b * p.q_bs +
-                                  (hk * p.group + (live ? row - b * p.group : 0)) * p.q_hs + ch * 8;
-            cp_async16(q_tiles + i * S::kTileBytes + at(r), live ? src : p.q, live);
-          }
-        }
-      }
-      cp_async_commit();
+      auto at = [&](int r) { return chunk_at(r, ch); };
       // Copies are told to the tensor cores' proxy by the thread that made them, when
-      // they are complete: groups in their order, the queries' first.
-      int issued = 0, told = 0;  // groups, the queries' among them
+      // they are complete, in their order.
+      int issued = 0, told = 0;
       auto tell = [&]() {
         switch (issued - told) {
           case 0: break;
@@ -209,10 +197,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(told == 0 ? qfull_bar : full_bar + 8 * (first + slot_of(told - 1)));
+        if (lane == 0) mbar_arrive(full_bar + 8 * (first + slot_of(told)));
         ++told;
       };
-      issued = 1;
       const int loads = p.stall_loads ? 0 : n;
       const uint16_t* const base = is_v ? p.vc : p.kc;
       const int64_t ps = is_v ? p.v_ps : p.k_ps, ts = is_v ? p.v_ts : p.k_ts;
@@ -346,6 +333,27 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     const uint32_t s_at = tmem + lane_at + i * kAttnN;
     const uint32_t o_at = tmem + lane_at + kOutCol + i * kDP;
     const int steps = i ? n_of[1] : n_of[0], steps_o = i ? n_of[0] : n_of[1];
+    const int base = unit * kPreUnit + (wide ? i * kAttnM : 0);  // the tile's first row
+    if (n > 0 && (wide || i == 0)) {  // (a narrow unit has its row tile once)
+      constexpr int kChunks = kDP / 8, kRowsPer = 32 / kChunks;
+      const int ch = lane % kChunks, sub = lane / kChunks;
+      const bool row_live = base + r < p.rows;
+      const int b = row_live ? fdiv(base + r, p.by_group) : 0;
+      const int64_t off = b * p.q_bs + (hk * p.group + (row_live ? base + r - b * p.group : 0)) * p.q_hs;
+      const unsigned rows_there = __ballot_sync(0xffffffffu, row_live);
+#pragma unroll 4
+      for (int x = sub; x < 32; x += kRowsPer) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, x);
+        const bool live = ((rows_there >> x) & 1u) && ch * 8 < p.d;
+        cp_async16(q_tiles + i * S::kTileBytes + chunk_at((warp & 3) * 32 + x, ch),
+                   live ? p.q + o + ch * 8 : p.q, live);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull_bar);
+    }
     float m = kNegInf, l = 0.f;
     bool ok = true;
 #pragma unroll 1
@@ -444,29 +452,40 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       f2_get(f2_add(sum[0], sum[1]), a, b);
       l += a + b;
     }
-    if (steps > 0) {
-      ok = ok && wait(o_bar + 8 * i, (steps - 1) & 1, kErrWaitEpilogue);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    // ---- the row's part
-    const int slot = pre_slot0(p, hk, unit) + 2 * split + i;
-    const bool mine = (wide ? i * kAttnM : 0) + r < rows;
-    const int64_t at = static_cast<int64_t>(slot) * kAttnM + r;
+    // every product is complete: the rings are free for the way out
+    ok = ok && (n_of[0] == 0 || wait(o_bar, (n_of[0] - 1) & 1, kErrWaitEpilogue)) &&
+         (n_of[1] == 0 || wait(o_bar + 8, (n_of[1] - 1) & 1, kErrWaitEpilogue));
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    // ---- the rows' parts
+    const int64_t at = static_cast<int64_t>(pre_slot0(p, hk, unit) + 2 * split + i) * kAttnM;
+    const int mine = min(kAttnM, p.rows - base);   // rows of the tile
     if (!ok) m = l = __uint_as_float(0x7FC00000u);  // given up: its row becomes NaN
-    if (mine) p.part_ml[at] = make_float2(m, l);
-    if (steps > 0) {
+    if (r < mine) p.part_ml[at + r] = make_float2(m, l);
+    if (steps > 0 && ok) {
+      // 32 channels at a time through shared memory, so that a store covers whole lines
+      // (straight from its row each thread would write 16 bytes of 32 lines: 5000 cycles)
+      const uint32_t stage = ring + warp * 4096;
+      const int ch = lane & 7;
+      float* const to = p.part + at * kDP + ch * 4;
 #pragma unroll 1
       for (int c = 0; c < kDP; c += 32) {
         float o[32];
         tmem_ld32(o_at + c, o);
         tmem_wait_ld_regs(o);
-        if (mine) {
-          float4* to = reinterpret_cast<float4*>(p.part + at * kDP + c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 8; ++e)
+          sts_v4(stage + lane * 128 + ((e ^ (lane & 7)) << 4),
+                 make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                            __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = e * 4 + (lane >> 3), row = (warp & 3) * 32 + x;
+          if (row < mine)
+            *reinterpret_cast<uint4*>(to + row * kDP + c) = lds_v4(stage + x * 128 + ((ch ^ (x & 7)) << 4));
         }
+        __syncwarp();
       }
     }
   }
