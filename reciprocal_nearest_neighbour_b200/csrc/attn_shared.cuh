@@ -502,43 +502,46 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
 }
 
 // Joins a row's parts: the prefix's, one from each of its unit's splits (and tiles), and
-// its sequence's own.  One block per (sequence, query head): the threads fetch the parts'
-// maxima and totals at once, then its four warps take the sums in turn, several in flight,
-// and meet in a fixed order.
-constexpr int kJoinParts = 128;  // of them in a pass
-template <bool kBf16, int kDP>
+// its sequence's own.  A team of kTeam warps (4, or 1 with many rows) takes a (sequence,
+// query head): its lanes fetch the parts' maxima and totals at once, then its warps the
+// sums in turn, several in flight, in a fixed order.
+constexpr int kJoinPass = 32;  // parts whose totals a warp has at a time
+template <bool kBf16, int kDP, int kTeam>
 __global__ void __launch_bounds__(128)
 attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixParams pre) {
   constexpr int kVals = kDP / 32;  // channels per lane
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   using VecT = std::conditional_t<kVals == 4, float4, float2>;
   __shared__ float acc[4][kDP];
-  __shared__ float factor[kJoinParts];
-  __shared__ const float* source[kJoinParts];
-  __shared__ float tops[4], sums[4];
-  const int b = blockIdx.x / p.Hq, head = blockIdx.x - b * p.Hq;
+  __shared__ float2 tot[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int member = warp % kTeam;
+  const int64_t at_row = static_cast<int64_t>(blockIdx.x) * (4 / kTeam) + warp / kTeam;
+  if (at_row >= static_cast<int64_t>(p.B) * p.Hq) return;  // (never with a team of 4)
+  const int b = static_cast<int>(at_row / p.Hq), head = static_cast<int>(at_row - static_cast<int64_t>(b) * p.Hq);
   const int hk = head / p.group, in = head - hk * p.group;
   const int hb = in / kDecRows, dec_row = in - hb * kDecRows;
   const int row = b * p.group + in, unit = row / kPreUnit, at = row - unit * kPreUnit;
   const bool wide = unit < pre.wide;
-  const int slot0 = pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0);
-  const int pre_row = wide ? at % kAttnM : at;
+  const int64_t pre0 = static_cast<int64_t>(pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0)) * kAttnM +
+                       (wide ? at % kAttnM : at);
   const int n_pre = wide ? pre.wide_splits : 2 * pre.narrow_splits;
+  const int pre_step = (wide ? 2 : 1) * kAttnM;
   const bool own = dec_len(p, b) > 0;
   pdl_wait();
   int2 sp = make_int2(0, -1);
   if (own) sp = p.span[static_cast<int64_t>(b) * (p.Hkv * p.hblocks) + hk * p.hblocks + hb];
   const int parts = n_pre + sp.y - sp.x + 1;
   float v[kVals] = {}, M = kNegInf, L = 0.f;
-  for (int base = 0; base < parts; base += kJoinParts) {
-    const int i = base + static_cast<int>(threadIdx.x);
+  // this warp's parts: member, member + kTeam, ...
+  for (int base = member; base < parts; base += kJoinPass * kTeam) {
+    const int i = base + lane * kTeam;
     float2 a = make_float2(kNegInf, 0.f);
     const float* from = nullptr;
     if (i < n_pre) {
-      const int64_t slot = slot0 + (wide ? 2 : 1) * i;
-      a = pre.part_ml[slot * kAttnM + pre_row];
-      from = pre.part + (slot * kAttnM + pre_row) * kDP;
+      const int64_t mine = pre0 + static_cast<int64_t>(i) * pre_step;
+      a = pre.part_ml[mine];
+      from = pre.part + mine * kDP;
     } else if (i < parts && sp.x == sp.y) {
       const int64_t mine = static_cast<int64_t>(b) * p.Hq + head;
       a = p.row_ml[mine];
@@ -549,57 +552,66 @@ attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixPara
       a = p.part_ml[mine];
       from = p.part + mine * kDP;
     }
-    if (a.x == kNegInf && a.y == 0.f) from = nullptr;  // no key: its sums were not written
-    float top = a.x;
+    // no key: its sums were not written
+    const unsigned there = __ballot_sync(0xffffffffu, !(a.x == kNegInf && a.y == 0.f));
+    float m = fmaxf(M, a.x);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    const float m = fmaxf(M, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     // (a NaN maximum is a part that was given up: its factor is NaN too; without a
     // reference a part's total is 0, or NaN if its scores were)
     const float f = a.x == kNegInf ? 1.f : exp2_approx((a.x - m) * p.c);
-    factor[threadIdx.x] = f;
-    source[threadIdx.x] = from;
     float l = a.y * f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) sums[warp] = l;
-    __syncthreads();
-    if (base) {
-      const float h = M == kNegInf ? 1.f : exp2_approx((M - m) * p.c);
-      L *= h;
-#pragma unroll
-      for (int e = 0; e < kVals; ++e) v[e] *= h;
-    }
+    const float h = M == kNegInf ? 1.f : exp2_approx((M - m) * p.c);
+    L = L * h + l;
     M = m;
-    L += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    const int here = min(kJoinParts, parts - base);
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) v[e] *= h;
+    const int here = min(kJoinPass, (parts - base + kTeam - 1) / kTeam);
+    const uint64_t at64 = reinterpret_cast<uint64_t>(from);
 #pragma unroll 8
-    for (int j = warp; j < here; j += 4) {
-      const float* src = source[j];
-      if (!src) continue;
+    for (int j = 0; j < here; ++j) {
+      const float g = __shfl_sync(0xffffffffu, f, j);
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, at64, j));
+      if (!((there >> j) & 1u)) continue;
       const VecT x = *reinterpret_cast<const VecT*>(src + lane * kVals);
       const float* xs = reinterpret_cast<const float*>(&x);
-      const float g = factor[j];
 #pragma unroll
       for (int e = 0; e < kVals; ++e) v[e] = fmaf(xs[e], g, v[e]);
     }
-    __syncthreads();  // the next pass writes the factors anew
   }
+  if constexpr (kTeam > 1) {
 #pragma unroll
-  for (int e = 0; e < kVals; ++e) acc[warp][lane * kVals + e] = v[e];
-  __syncthreads();
-  uint16_t* ob = p.out + b * p.o_bs + head * p.o_hs;
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-    const float y = ((acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c])) * inv;
-    ob[c] = kBf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y))
-                  : __half_as_ushort(__float2half_rn(y));
+    for (int e = 0; e < kVals; ++e) acc[warp][lane * kVals + e] = v[e];
+    if (lane == 0) tot[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp != 0) return;
+    M = fmaxf(fmaxf(tot[0].x, tot[1].x), fmaxf(tot[2].x, tot[3].x));
+    float f[4];
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[w] = tot[w].x == kNegInf ? 1.f : exp2_approx((tot[w].x - M) * p.c);
+      L += tot[w].y * f[w];
+    }
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) {
+      const int c = lane * kVals + e;
+      v[e] = (acc[0][c] * f[0] + acc[1][c] * f[1]) + (acc[2][c] * f[2] + acc[3][c] * f[3]);
+    }
   }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[static_cast<int64_t>(b) * p.Hq + head] =
-        L != 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  uint16_t* ob = p.out + b * p.o_bs + head * p.o_hs + lane * kVals;
+  if (lane * kVals < p.d) {  // (kVals divides d)
+    if constexpr (kVals == 4)
+      *reinterpret_cast<uint2*>(ob) =
+          make_uint2(pack2<kBf16>(v[0] * inv, v[1] * inv), pack2<kBf16>(v[2] * inv, v[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(ob) = pack2<kBf16>(v[0] * inv, v[1] * inv);
+  }
+  if (p.lse && lane == 0)
+    p.lse[at_row] = L != 0.f ? M * p.scale + (log2f(L) - kBias) * 0.69314718f : kNegInf;
 }
 
 }  // namespace rnn

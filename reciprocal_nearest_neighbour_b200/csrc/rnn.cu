@@ -3847,8 +3847,12 @@ static rnn_status shared_launch(const DecodeParams& p, dim3 grid, const PrefixPa
   launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads),
            PreShape<kDP>::smem(pre.slots, pre.wide > 0), s, true, pre);
   if ((r = launched()) != RNN_OK) return r;
-  launch_k(attn_shared_join_kernel<kBf16, kDP>, dim3(static_cast<unsigned>(p.B) * p.Hq), dim3(128),
-           0, s, true, p, pre);
+  const unsigned out_rows = static_cast<unsigned>(p.B) * p.Hq;
+  // a warp a row once there are enough rows to fill the GPU with them
+  if (out_rows >= 148u * 16u)
+    launch_k(attn_shared_join_kernel<kBf16, kDP, 1>, dim3((out_rows + 3) / 4), dim3(128), 0, s, true, p, pre);
+  else
+    launch_k(attn_shared_join_kernel<kBf16, kDP, 4>, dim3(out_rows), dim3(128), 0, s, true, p, pre);
   return launched();
 }
 template <bool kBf16, int kDP>
