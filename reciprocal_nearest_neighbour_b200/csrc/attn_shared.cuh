@@ -94,7 +94,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
   const uint32_t o_bar = p_bar + 32;        // its output is complete so far
   const uint32_t drain_bar = o_bar + 16;
-  const uint32_t tmem_slot = drain_bar + 16;
+  const uint32_t last_bar = drain_bar + 16; // tile i's last product is complete
+  const uint32_t tmem_slot = last_bar + 16;
   const uint32_t abort_at = tmem_slot + 4;
   // Keys that exist, 4 words for each of 8 tiles: when a tile's words are written, the
   // scores of the tile four before it are done, so the softmax has read the words of the
@@ -150,6 +151,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     mbar_init(p_bar + 8 * (2 + i), 4);
     mbar_init(o_bar + 8 * i, 1);
     mbar_init(drain_bar + 8 * i, 1);
+    mbar_init(last_bar + 8 * i, 1);
     if (i == 0) mbar_init(qfull_bar, wide ? 8 : 4);
     fence_barrier_init();
   } else if (threadIdx.x >= 64 && threadIdx.x < 72) {
@@ -315,6 +317,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         if (!ok) break;
         umma_commit_warp(o_bar + 8 * i);
         umma_commit_warp(empty_bar + 8 * vs);
+        if (k + 1 == n_of[i]) umma_commit_warp(last_bar + 8 * i);
         __syncwarp();
       }
       if (aborted() && any) {
@@ -453,8 +456,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       l += a + b;
     }
     // every product is complete: the rings are free for the way out
-    ok = ok && (n_of[0] == 0 || wait(o_bar, (n_of[0] - 1) & 1, kErrWaitEpilogue)) &&
-         (n_of[1] == 0 || wait(o_bar + 8, (n_of[1] - 1) & 1, kErrWaitEpilogue));
+    // (told by a barrier that has one phase: the other tile may be any number of steps behind)
+    ok = ok && (n_of[0] == 0 || wait(last_bar, 0, kErrWaitEpilogue)) &&
+         (n_of[1] == 0 || wait(last_bar + 8, 0, kErrWaitEpilogue));
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     // ---- the rows' parts
