@@ -41,9 +41,14 @@ struct PreShape {
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
   static constexpr int kStages = kDP == 128 ? 2 : 4;  // of each ring, at most; a power of two
-  // with `slots` of each ring, and one row tile where every unit is narrow
+  // Tiles of shared memory with `slots` of each ring: a narrow unit has one row tile less
+  // and, where the rings are full, one V slot more (144 streams behind 30011 tokens: its V
+  // tiles were waited for a thousand cycles a step).
+  static __host__ __device__ constexpr int tiles(int slots, bool any_wide) {
+    return 2 * slots + (any_wide || slots == kStages ? 2 : 1);
+  }
   static constexpr size_t smem(int slots, bool any_wide) {
-    return 1024 + size_t((any_wide ? 2 : 1) + 2 * slots) * kTileBytes + 512;
+    return 1024 + size_t(tiles(slots, any_wide)) * kTileBytes + 512;
   }
   static constexpr size_t kSmem = smem(kStages, true);
 };
@@ -85,11 +90,10 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_tiles = smem, ring = smem + (p.wide ? 2 : 1) * S::kTileBytes;
-  const uint32_t bars = ring + 2 * p.slots * S::kTileBytes;
+  const uint32_t bars = smem + S::tiles(p.slots, p.wide > 0) * S::kTileBytes;
   const uint32_t full_bar = bars;
-  const uint32_t empty_bar = full_bar + 16 * kStages;
-  const uint32_t qfull_bar = empty_bar + 16 * kStages;
+  const uint32_t empty_bar = full_bar + 8 * (2 * kStages + 1);
+  const uint32_t qfull_bar = empty_bar + 8 * (2 * kStages + 1);
   const uint32_t s_bar = qfull_bar + 8;     // scores of tile i are in tensor memory
   const uint32_t p_bar = s_bar + 16;        // its probabilities are there, by halves
   const uint32_t o_bar = p_bar + 32;        // its output is complete so far
@@ -121,9 +125,13 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
   const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
 
-  // the rings: K of key tile j in slot j % slots, V behind the K slots
+  // the row tiles, then the rings: K of key tile j in slot j % slots, V behind the K slots
+  const uint32_t q_tiles = smem, ring = smem + (wide ? 2 : 1) * S::kTileBytes;
+  const bool more_v = !wide && p.slots == kStages;
   auto slot_of = [&](int j) { return j & (p.slots - 1); };
   auto turn_of = [&](int j) { return (j >> p.slot_bits) & 1; };
+  auto v_slot_of = [&](int j) { return p.slots + (more_v ? j % (kStages + 1) : slot_of(j)); };
+  auto v_turn_of = [&](int j) { return more_v ? j / (kStages + 1) & 1 : turn_of(j); };
 
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto wait = [&](uint32_t bar, uint32_t parity, int code) {
@@ -140,7 +148,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
     }
   };
-  if (threadIdx.x < 2 * p.slots) {
+  if (threadIdx.x < 2 * p.slots + 1) {
     mbar_init(full_bar + 8 * threadIdx.x, 2);
     mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
     fence_barrier_init();
@@ -182,7 +190,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       constexpr int kChunks = kDP / 8, kRowsPer = 32 / kChunks;
       const int w = warp - kPreLoadWarp;
       const bool is_v = w >= 2;               // of the rings
-      const int first = is_v ? p.slots : 0, rows0 = (w & 1) * 64;
+      const int rows0 = (w & 1) * 64;
+      auto place_of = [&](int j) { return is_v ? v_slot_of(j) : slot_of(j); };
+      auto phase_of = [&](int j) { return is_v ? v_turn_of(j) : turn_of(j); };
       const int ch = lane % kChunks, sub = lane / kChunks;
       const bool ch_live = ch * 8 < p.d;
       auto at = [&](int r) { return chunk_at(r, ch); };
@@ -199,7 +209,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar + 8 * (first + slot_of(told)));
+        if (lane == 0) mbar_arrive(full_bar + 8 * place_of(told));
         ++told;
       };
       const int loads = p.stall_loads ? 0 : n;
@@ -208,8 +218,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       const uint16_t* const head = base + hk * (is_v ? p.v_hs : p.k_hs) + ch * 8;
       bool ok = true;
       for (int j = 0; j < loads; ++j) {
-        const int slot = first + slot_of(j);
-        const uint32_t eb = empty_bar + 8 * slot, parity = turn_of(j) ^ 1u;
+        const int slot = place_of(j);
+        const uint32_t eb = empty_bar + 8 * slot, parity = phase_of(j) ^ 1u;
         while (!__all_sync(0xffffffffu, mbar_test_wait(eb, parity))) {
           if (told < issued) {
             tell();
@@ -264,9 +274,9 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       while (told < issued) tell();
       if (!(w & 1) && !aborted()) {
         // no arrival of a product's completion is under way when the CTA exits
-        const int j = max(0, loads - p.slots) + lane;
-        if (lane < p.slots && j < loads)
-          settle_phase(empty_bar + 8 * (first + slot_of(j)), turn_of(j), p.wait_limit_ns, p.err);
+        const int slots = p.slots + (is_v && more_v), j = max(0, loads - slots) + lane;
+        if (lane < slots && j < loads)
+          settle_phase(empty_bar + 8 * place_of(j), phase_of(j), p.wait_limit_ns, p.err);
         __syncwarp();
       }
     } else if (warp < kPreMmaWarp + 2) {
@@ -283,7 +293,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       };
       if (n_of[i] > 0) wait_mma(qfull_bar, 0);
       for (int k = 0; ok && k < n_of[i]; ++k) {
-        const int j = tile_of(i, k), ks = slot_of(j), vs = p.slots + ks;
+        const int j = tile_of(i, k), ks = slot_of(j), vs = v_slot_of(j);
         if (!wait_mma(full_bar + 8 * ks, turn_of(j))) break;
         // the probabilities lie over the scores: the product that reads them first
         if (k > 0 && !wait_mma(o_bar + 8 * i, (k - 1) & 1)) break;
@@ -304,7 +314,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         umma_commit_warp(s_bar + 8 * i);
         umma_commit_warp(empty_bar + 8 * ks);
         any = true;
-        if (!wait_mma(full_bar + 8 * vs, turn_of(j))) break;
+        if (!wait_mma(full_bar + 8 * vs, v_turn_of(j))) break;
         const uint64_t v_at = v_desc + static_cast<uint64_t>(vs * (S::kTileBytes >> 4));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
