@@ -40,17 +40,10 @@ template <int kDP>
 struct PreShape {
   static constexpr int kTileBytes = kAttnM * kDP * 2;
   static constexpr int kBlockBytes = kAttnM * 128;
-  static constexpr int kStages = kDP == 128 ? 2 : 4;  // of each ring, at most; a power of two
-  // Tiles of shared memory with `slots` of each ring: a narrow unit has one row tile less
-  // and, where the rings are full, one V slot more (144 streams behind 30011 tokens: its V
-  // tiles were waited for a thousand cycles a step).
-  static __host__ __device__ constexpr int tiles(int slots, bool any_wide) {
-    return 2 * slots + (any_wide || slots == kStages ? 2 : 1);
-  }
-  static constexpr size_t smem(int slots, bool any_wide) {
-    return 1024 + size_t(tiles(slots, any_wide)) * kTileBytes + 512;
-  }
-  static constexpr size_t kSmem = smem(kStages, true);
+  static constexpr int kStages = kDP == 128 ? 2 : 4;  // of each ring; a power of two
+  // (narrow units have one row tile less and one V slot more: 144 streams behind 30011
+  // tokens waited a thousand cycles a step for their V tiles)
+  static constexpr size_t kSmem = 1024 + size_t(2 + 2 * kStages) * kTileBytes + 512;
 };
 
 struct PrefixParams {
@@ -65,7 +58,6 @@ struct PrefixParams {
   int wide, narrow;                    // units of a key head: wide ones, and 0 or 1 narrow one
   int wide_splits, narrow_splits;      // CTAs that share a unit's keys
   int Hkv;
-  int slots, slot_bits;                // of each ring, and its log2
   float c;                             // scale * log2(e)
   uint32_t idesc_s, idesc_o;
   float* part;                         // [slot][128][kDP] unnormalised parts
@@ -90,7 +82,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   constexpr float kBias = kBf16 ? 0.f : 7.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bars = smem + S::tiles(p.slots, p.wide > 0) * S::kTileBytes;
+  const uint32_t bars = smem + (2 + 2 * kStages) * S::kTileBytes;
   const uint32_t full_bar = bars;
   const uint32_t empty_bar = full_bar + 8 * (2 * kStages + 1);
   const uint32_t qfull_bar = empty_bar + 8 * (2 * kStages + 1);
@@ -125,13 +117,12 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int tile0 = static_cast<int>(static_cast<int64_t>(all) * split / splits);
   const int n = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - tile0;
 
-  // the row tiles, then the rings: K of key tile j in slot j % slots, V behind the K slots
+  // the row tiles, then the rings: K of key tile j in slot j % kStages, V behind the K slots
   const uint32_t q_tiles = smem, ring = smem + (wide ? 2 : 1) * S::kTileBytes;
-  const bool more_v = !wide && p.slots == kStages;
-  auto slot_of = [&](int j) { return j & (p.slots - 1); };
-  auto turn_of = [&](int j) { return (j >> p.slot_bits) & 1; };
-  auto v_slot_of = [&](int j) { return p.slots + (more_v ? j % (kStages + 1) : slot_of(j)); };
-  auto v_turn_of = [&](int j) { return more_v ? j / (kStages + 1) & 1 : turn_of(j); };
+  auto slot_of = [&](int j) { return j % kStages; };
+  auto turn_of = [&](int j) { return j / kStages & 1; };
+  auto v_slot_of = [&](int j) { return kStages + (wide ? j % kStages : j % (kStages + 1)); };
+  auto v_turn_of = [&](int j) { return (wide ? j / kStages : j / (kStages + 1)) & 1; };
 
   auto aborted = [&]() { return lds_volatile(abort_at) != 0; };
   auto wait = [&](uint32_t bar, uint32_t parity, int code) {
@@ -148,7 +139,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       }
     }
   };
-  if (threadIdx.x < 2 * p.slots + 1) {
+  if (threadIdx.x < 2 * kStages + 1) {
     mbar_init(full_bar + 8 * threadIdx.x, 2);
     mbar_init(empty_bar + 8 * threadIdx.x, wide ? 2 : 1);
     fence_barrier_init();
@@ -274,7 +265,7 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
       while (told < issued) tell();
       if (!(w & 1) && !aborted()) {
         // no arrival of a product's completion is under way when the CTA exits
-        const int slots = p.slots + (is_v && more_v), j = max(0, loads - slots) + lane;
+        const int slots = kStages + (is_v && !wide), j = max(0, loads - slots) + lane;
         if (lane < slots && j < loads)
           settle_phase(empty_bar + 8 * place_of(j), phase_of(j), p.wait_limit_ns, p.err);
         __syncwarp();

@@ -3773,6 +3773,7 @@ static PrefixPlan make_prefix_plan(int64_t rows, int Hkv, int64_t room) {
   double least = 0;
   // (from what one accumulator takes; a narrow unit has two)
   const int64_t from = (tiles + kPreMostTiles - 1) / kPreMostTiles;
+  const int64_t from_n = (tiles + 2 * kPreMostTiles - 1) / (2 * kPreMostTiles);
   const int64_t to = std::max(from, std::min<int64_t>(tiles, 2 * kSms));
   const auto look = [&](int64_t sw, int64_t sn) {
     const int64_t ctas = Hkv * (best.wide * sw + best.narrow * sn);
@@ -3790,11 +3791,11 @@ static PrefixPlan make_prefix_plan(int64_t rows, int Hkv, int64_t room) {
   };
   for (int64_t sw = from; sw <= to; ++sw) {
     // a narrow unit's share of CTAs beside wide ones: its share of the time, or one off
-    const int64_t sn = best.wide ? (sw * 13 + 10) / 20 : sw;
+    const int64_t sn = best.wide ? std::max(from_n, (sw * 13 + 10) / 20) : sw;
     const bool more = look(sw, sn);
     if (best.wide && best.narrow) {
       look(sw, sn + 1);
-      if (sn > 1) look(sw, sn - 1);
+      if (sn > from_n) look(sw, sn - 1);
     }
     if (!more) break;
   }
@@ -3844,8 +3845,8 @@ static rnn_status shared_launch(const DecodeParams& p, dim3 grid, const PrefixPa
          : attn_decode_kernel<kBf16, kDP, 2, false, true><<<grid, block, sm, s>>>(p);
   rnn_status r = launched();
   if (r != RNN_OK) return r;
-  launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads),
-           PreShape<kDP>::smem(pre.slots, pre.wide > 0), s, true, pre);
+  launch_k(attn_prefix_kernel<kBf16, kDP>, dim3(ctas), dim3(kPreThreads), PreShape<kDP>::kSmem, s,
+           true, pre);
   if ((r = launched()) != RNN_OK) return r;
   const unsigned out_rows = static_cast<unsigned>(p.B) * p.Hq;
   // a warp a row once there are enough rows to fill the GPU with them
@@ -3955,15 +3956,6 @@ rnn_status rnn_attn_decode_shared(const rnn_attn_decode_shared_args* args, rnn_s
   pre.wide = plan.wide, pre.narrow = plan.narrow;
   pre.wide_splits = plan.wide_splits, pre.narrow_splits = plan.narrow_splits;
   pre.Hkv = Hkv;
-  // no more of the rings than a CTA's loads fill: what is left of the SM's shared memory
-  // goes to the kernel before this one, which then still runs
-  const int64_t most = (std::min<int64_t>(room, kDecMaxKeys) + kAttnN - 1) / kAttnN;
-  const int64_t each = std::max<int64_t>(plan.wide ? (most + plan.wide_splits - 1) / plan.wide_splits : 1,
-                                         plan.narrow ? (most + plan.narrow_splits - 1) / plan.narrow_splits : 1);
-  while ((1 << pre.slot_bits) < (d <= 64 ? PreShape<64>::kStages : PreShape<128>::kStages) &&
-         (1 << pre.slot_bits) < each)
-    ++pre.slot_bits;
-  pre.slots = 1 << pre.slot_bits;
   pre.c = p.c;
   pre.idesc_s = make_idesc(dtype, kAttnN);
   pre.idesc_o = make_idesc(dtype, (d + 15) / 16 * 16) | (1u << 16);  // B with its channels contiguous

@@ -595,3 +595,94 @@ def test_a_size_of_one_may_have_any_stride():
     out, lse = rnn.attn_decode_q8(q, kc, vc, scales, ints([[2, 0]]), ints([20]), with_lse=True)
     ref = oa.decode(f64(q), kv, vv, np.array([[2, 0]]), [20], 1 / 8)
     check_attention_q8(out, lse, ref, HF, 64, np.abs(vv).max())
+
+
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+def test_offsets_beyond_32_bits(codes):
+    """Pages 1.5 10^9 codes apart, and scales 6 10^8 floats."""
+    g = gen_of(1)
+    d, size, hkv, gap = 64, 16, 2, 1500000000 // 16 * 16
+    store = torch.zeros(4 * gap, dtype=torch.uint8, device="cuda")
+    shape, strides = (4, size, hkv, d), (gap, hkv * d, d, 1)
+    kc, vc = (store[o:].as_strided(shape, strides).view(CODES[codes]) for o in (0, gap // 2 // 16 * 16))
+    scale_gap = 600000000
+    scales = torch.zeros(4 * scale_gap, device="cuda").as_strided((4, hkv, size, 2), (scale_gap, 2 * size, 2, 1))
+    lens = [40, 16]
+    table = np.array([[3, 0, 2], [1, -1, -1]])
+    k, v = (normal(g, (56, hkv, d), HF) for _ in range(2))
+    args = (kc, vc, scales, ints(table))
+    rnn.kv_append_q8(k, v, *args, ints([0, 0]), ints([0, 40, 56]))
+    values = []
+    for x in (k, v):
+        c, s = oq.quantise32(x.float().cpu().numpy(), codes)
+        values.append(c * s[..., None].astype(np.float64))
+    got = rnn.kv_read_q8(*args, ints([0, 40, 56]), 56, HF)
+    for x, y in zip(got, values):
+        assert np.all(np.abs(f64(x) - y) <= 2.0 ** -11 * np.abs(y) + 2.0 ** -25)
+    q = normal(g, (2, 4, d), HF)
+    out, lse = rnn.attn_decode_q8(q, *args, ints(lens), with_lse=True)
+    packed = [np.zeros((4, size, hkv, d)) for _ in range(2)]
+    for b, n in enumerate(lens):
+        for t in range(n):
+            for to, x in zip(packed, values):
+                to[table[b, t // size], t % size] = x[(0, 40)[b] + t]
+    ref = oa.decode(f64(q), *packed, table, lens, 1 / 8)
+    check_attention_q8(out, lse, ref, HF, d, np.abs(packed[1]).max())
+
+
+def test_many_empty_sequences_and_the_same_page_twice():
+    g = gen_of(7)
+    lens = [0] * 300 + [5] + [0] * 400 + [33, 0, 1]
+    table, pages = deal(g, lens, 16)
+    table[-1, 0] = table[300, 0]                  # two sequences on one page
+    kc, vc, scales, kv, vv = filled(g, "int8", pages, 16, 2, 64)
+    cu = cum(lens)
+    got = rnn.kv_read_q8(kc, vc, scales, ints(table), ints(cu), cu[-1], HF)
+    where, _ = oa.slots(cu, [0] * len(lens), table, 16, pages, cu[-1])
+    for x, y in zip(got, (kv, vv)):
+        want = np.stack([y[w] for w in where])
+        assert np.all(np.abs(f64(x) - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -25)
+    q = normal(g, (len(lens), 4, 64), HF)
+    out, lse = rnn.attn_decode_q8(q, kc, vc, scales, ints(table), ints(lens), with_lse=True)
+    ref = oa.decode(f64(q), kv, vv, table, lens, 1 / 8)
+    check_attention_q8(out, lse, ref, HF, 64, np.abs(vv).max())
+
+
+def test_many_tokens_read():
+    """Enough of them that a warp takes several."""
+    g = gen_of(8)
+    lens = [25000, 1, 0, 14000, 3]
+    table, pages = deal(g, lens, 64)
+    kc, vc, scales, _, _ = filled(g, "e4m3", pages, 64, 1, 16)
+    cu = cum(lens)
+    k, v = rnn.kv_read_q8(kc, vc, scales, ints(table), ints(cu), cu[-1] + 5, BF,
+                          k_out=torch.full((cu[-1] + 5, 1, 16), 3.0, dtype=BF, device="cuda"))
+    assert (k[cu[-1]:] == 3).all()
+    number = np.concatenate([np.arange(n) for n in lens])
+    seq = np.repeat(np.arange(len(lens)), lens)
+    page, row = torch.from_numpy(table[seq, number // 64]).cuda(), torch.from_numpy(number % 64).cuda()
+    for which, (out, cache) in enumerate(((k, kc), (v, vc))):
+        want = cache.view(torch.uint8)[page, row].view(CODES["e4m3"]).float() * \
+            scales[..., which].transpose(1, 2)[page, row][..., None]
+        assert torch.equal(out[:cu[-1]], want.to(BF))
+
+
+def test_two_calls_at_once():
+    g = gen_of(4)
+    lens = [700, 3, 90, 2000]
+    table, pages = deal(g, lens, 16)
+    sets = []
+    for s in (1, 2):
+        kc, vc, scales, _, _ = filled(gen_of(s), "e4m3", pages, 16, 2, 128)
+        sets.append((normal(g, (4, 8, 128), BF), kc, vc, scales, ints(table), ints(lens)))
+    want = [rnn.attn_decode_q8(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(rnn.attn_decode_q8(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])

@@ -327,3 +327,56 @@ def test_python_form_gives_the_same(monkeypatch):
     monkeypatch.setattr(rnn._lib, "fast", rnn._lib._Python)
     for x, y in zip(mine, rnn.attn_decode_shared(*args, with_lse=True, scale=0.2)):
         assert torch.equal(x, y)
+
+
+def test_more_rows_than_a_wave():
+    rng = np.random.default_rng(0)
+    run_shared(BF, 150, rng.integers(0, 4, 3000).tolist(), 2, 2, 32, 16)
+
+
+def test_pages_may_repeat():
+    def change(q, kc, vc, names, table):
+        names[2], names[4], table[1] = names[0], names[0], table[0]
+
+    run_shared(HF, 200, [30, 30], 4, 2, 64, 16, change=change)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_beyond_32_bits(d):
+    """Pages 1.3 10^9 elements apart."""
+    g = gen_of(1)
+    size, hkv, gap = 16, 2, 1300000000 // 8 * 8
+    store = torch.empty(3 * gap, dtype=HF, device="cuda")
+    shape, strides = (4, size, hkv, d), (gap // 2 // 8 * 8, hkv * d, d, 1)
+    kc = store.as_strided(shape, strides)
+    vc = store[gap // 4 // 8 * 8:].as_strided(shape, strides)
+    for c in (kc, vc):
+        c.copy_(normal(g, shape, HF))
+    q = normal(g, (2, 4, d), HF)
+    names, table, lens = np.array([3, 0]), np.array([[2], [1]]), [16, 5]
+    out, lse = rnn.attn_decode_shared(q, kc, vc, ints(names), ints([30]), ints(table), ints(lens), with_lse=True)
+    ref = decode_shared(f64(q), f64(kc), f64(vc), names, 30, table, lens, d ** -0.5)
+    check_attention(out, lse, ref, HF, d, float(vc.abs().max()))
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, and a prompt beside them."""
+    sets = [setting(BF, 2000, [40] * 60, 4, 1, 128, 16, seed=s) for s in (1, 2)]
+    args = [(q, kc, vc, ints(names), ints([2000]), ints(table), ints([40] * 60)) for q, kc, vc, names, table in sets]
+    want = [rnn.attn_decode_shared(*a) for a in args]
+    x = normal(gen_of(3), (1500, 4, 128), BF)
+    cu = ints([0, 1500])
+    whole = rnn.attn_prompt(x, x, x, cu)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], [], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(rnn.attn_decode_shared(*args[i]))
+        with torch.cuda.stream(streams[2]):
+            got[2].append(rnn.attn_prompt(x, x, x, cu))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+    assert all(torch.equal(y, whole) for y in got[2])
