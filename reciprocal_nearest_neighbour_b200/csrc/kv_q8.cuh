@@ -137,28 +137,30 @@ __device__ __forceinline__ int64_t times(int x, int stride) {
   return static_cast<int64_t>(x) * stride;
 }
 
-// A lane's channels of a row: two vectors of 8 (cb < 0: one).  Where channels i and
-// pairs + i of an axis form a pair and 8 divides the pairs (kVec = 8), a lane of the
-// rotated channels has 8 pairs; else they are 16 neighbours.
+// A lane's channels of a row: two vectors of 8 (cb < 0: one; ca = d: none), so that
+// neighbouring lanes have neighbouring vectors.  Where channels i and pairs + i of an axis
+// form a pair and 8 divides the pairs (kVec = 8), a lane of the rotated channels has 8
+// pairs.  (With 16 neighbouring channels a lane, a warp's access would take half of each
+// sector: 25825 prompt tokens with pairs side by side 146 us.)
 struct Q8Place {
   int ca, cb, turn;  // turn: the first pair, < 0 behind the rotated channels
 };
 template <int kVec>
 __device__ __forceinline__ Q8Place q8_place(int unit, const AppendQ8Params& p) {
-  Q8Place at{unit * 16, unit * 16 + 8, -1};
+  int first = 0;  // channel where the vectors start that have no partner
   if (kVec == 8) {
     const int per_axis = p.pairs >> 3, rot = p.axes * per_axis;
     if (unit < rot) {
       const int axis = unit >= per_axis ? 1 : 0, i0 = (unit - axis * per_axis) * 8;
-      at.ca = 2 * axis * p.pairs + i0;
-      at.cb = at.ca + p.pairs;
-      at.turn = axis * p.pairs + i0;
-      return at;
+      const int ca = 2 * axis * p.pairs + i0;
+      return Q8Place{ca, ca + p.pairs, axis * p.pairs + i0};
     }
-    at.ca = 2 * p.axes * p.pairs + (unit - rot) * 16;
-    at.cb = at.ca + 8;
+    first = 2 * p.axes * p.pairs;
+    unit -= rot;
   }
-  if (at.cb >= p.d) at.cb = -1;
+  const int units = (p.d - first + 15) >> 4;
+  Q8Place at{unit < units ? first + unit * 8 : p.d, first + (unit + units) * 8, -1};
+  if (at.ca >= p.d || at.cb >= p.d) at.cb = -1;
   return at;
 }
 
@@ -185,11 +187,13 @@ kv_append_q8_kernel(const AppendQ8Params p) {
   uint8_t* const ring = app_smem + warp * (kQ8Ring * kQ8PassBytes);
   float2* const turn = reinterpret_cast<float2*>(app_smem + kQ8Warps * kQ8Ring * kQ8PassBytes) +
                        warp * ((angles + 7) & ~7);
-  // Lanes with 8 pairs each read them two at a time: those of all lanes lie side by side,
-  // the first two, the next two and so on, so that eight lanes meet no bank twice.
-  const int eights = (angles + 7) >> 3;
+  // Lanes with 8 pairs (or 4 side by side in a vector) read them two at a time: those of
+  // all lanes lie side by side, the first two, the next two and so on, so that eight lanes
+  // meet no bank twice (25825 prompt tokens 95 us, 109 with the pairs in order).
+  constexpr int kOf = kVec == kNeighbours ? 4 : 8;
+  const int groups = (angles + kOf - 1) / kOf;
   auto turn_at = [&](int a) {
-    return kVec >= 8 ? ((((a & 7) >> 1) * eights + (a >> 3)) << 1) + (a & 1) : a;
+    return kVec >= 8 ? (((a % kOf >> 1) * groups + a / kOf) << 1) + (a & 1) : a;
   };
   const int sub = lane >> p.row_lanes;                   // row of the pass
   const int unit = lane & ((1 << p.row_lanes) - 1);
@@ -294,15 +298,15 @@ kv_append_q8_kernel(const AppendQ8Params p) {
       }
       if (!is_v && here) {
         if constexpr (kVec == kNeighbours) {
-          const float4* cs = reinterpret_cast<const float4*>(turn) + (at.ca >> 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (at.ca + 4 * e >= rotated) break;
-            const float4 z = cs[e * eights];
+            const int c = (e < 2 ? at.ca : at.cb) + 4 * (e & 1);
+            if (c >= rotated || (e >= 2 && !both)) continue;
+            const float4 z = reinterpret_cast<const float4*>(turn)[(e & 1) * groups + (c >> 3)];
             const float a0 = f[4 * e], b0 = f[4 * e + 1], a1 = f[4 * e + 2], b1 = f[4 * e + 3];
             f[4 * e] = a0 * z.x - b0 * z.y;
             f[4 * e + 1] = b0 * z.x + a0 * z.y;
-            if (at.ca + 4 * e + 2 < rotated) {
+            if (c + 2 < rotated) {
               f[4 * e + 2] = a1 * z.z - b1 * z.w;
               f[4 * e + 3] = b1 * z.z + a1 * z.w;
             }
@@ -312,7 +316,7 @@ kv_append_q8_kernel(const AppendQ8Params p) {
             const float4* cs = reinterpret_cast<const float4*>(turn) + (at.turn >> 3);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float4 z = cs[e * eights];
+              const float4 z = cs[e * groups];
               const float a0 = f[2 * e], a1 = f[2 * e + 1], b0 = f[8 + 2 * e], b1 = f[9 + 2 * e];
               f[2 * e] = a0 * z.x - b0 * z.y;
               f[2 * e + 1] = a1 * z.z - b1 * z.w;
@@ -322,18 +326,20 @@ kv_append_q8_kernel(const AppendQ8Params p) {
           }
         } else {
           const uint8_t* row = from + (sub << p.row_lanes) * 16;
+          const int units = (p.d + 15) >> 4;  // first vectors, and so lanes, of a row
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < 8 / kPiece; ++s) {
-              const int c = at.ca + 8 * h + s * kPiece;
-              if (c >= rotated) break;
+              const int c = (h ? at.cb : at.ca) + s * kPiece;
+              if (c >= rotated || (h && !both)) break;
               const int axis = c >= 2 * p.pairs ? 1 : 0, in_axis = c - 2 * axis * p.pairs;
               const bool second = in_axis >= p.pairs;
               const int o = second ? c - p.pairs : c + p.pairs;  // the partners
               union { V v; uint16_t e[kPiece]; } g;
-              g.v = *reinterpret_cast<const V*>(row + ((o >> 3) & 1) * 512 + (o >> 4) * 16 +
-                                                (o & 7) * 2);
+              const int vec = o >> 3, second_vec = vec >= units;
+              g.v = *reinterpret_cast<const V*>(row + second_vec * 512 +
+                                                (vec - second_vec * units) * 16 + (o & 7) * 2);
               const float2* cs = turn + axis * p.pairs + (second ? in_axis - p.pairs : in_axis);
 #pragma unroll
               for (int e = 0; e < kPiece; ++e) {
