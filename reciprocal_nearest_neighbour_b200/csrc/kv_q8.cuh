@@ -187,13 +187,13 @@ kv_append_q8_kernel(const AppendQ8Params p) {
   uint8_t* const ring = app_smem + warp * (kQ8Ring * kQ8PassBytes);
   float2* const turn = reinterpret_cast<float2*>(app_smem + kQ8Warps * kQ8Ring * kQ8PassBytes) +
                        warp * ((angles + 7) & ~7);
-  // Lanes with 8 pairs (or 4 side by side in a vector) read them two at a time: those of
+  // Lanes with 8 pairs (or 4, in pieces and side by side) read them two at a time: those of
   // all lanes lie side by side, the first two, the next two and so on, so that eight lanes
   // meet no bank twice (25825 prompt tokens 95 us, 109 with the pairs in order).
-  constexpr int kOf = kVec == kNeighbours ? 4 : 8;
+  constexpr int kOf = kVec == 8 ? 8 : kVec >= 4 ? 4 : 2;
   const int groups = (angles + kOf - 1) / kOf;
   auto turn_at = [&](int a) {
-    return kVec >= 8 ? (((a % kOf >> 1) * groups + a / kOf) << 1) + (a & 1) : a;
+    return kVec >= 4 ? (((a % kOf >> 1) * groups + a / kOf) << 1) + (a & 1) : a;
   };
   const int sub = lane >> p.row_lanes;                   // row of the pass
   const int unit = lane & ((1 << p.row_lanes) - 1);
@@ -336,16 +336,24 @@ kv_append_q8_kernel(const AppendQ8Params p) {
               const int axis = c >= 2 * p.pairs ? 1 : 0, in_axis = c - 2 * axis * p.pairs;
               const bool second = in_axis >= p.pairs;
               const int o = second ? c - p.pairs : c + p.pairs;  // the partners
-              union { V v; uint16_t e[kPiece]; } g;
+              union { V v; uint16_t e[kPiece]; uint32_t w[(kPiece + 1) / 2]; } g;
               const int vec = o >> 3, second_vec = vec >= units;
               g.v = *reinterpret_cast<const V*>(row + second_vec * 512 +
                                                 (vec - second_vec * units) * 16 + (o & 7) * 2);
-              const float2* cs = turn + axis * p.pairs + (second ? in_axis - p.pairs : in_axis);
+              const int a = axis * p.pairs + (second ? in_axis - p.pairs : in_axis);
+              float* y = f + 8 * h + s * kPiece;
+              if constexpr (kPiece == 1) {
+                const float2 z = turn[a];
+                y[0] = y[0] * z.x + app_float<kBf16>(g.e[0]) * (second ? z.y : -z.y);
+              } else {
+                const float4* cs = reinterpret_cast<const float4*>(turn) + a / kOf;
 #pragma unroll
-              for (int e = 0; e < kPiece; ++e) {
-                const float2 z = cs[e];
-                float& y = f[8 * h + s * kPiece + e];
-                y = y * z.x + app_float<kBf16>(g.e[e]) * (second ? z.y : -z.y);
+                for (int e = 0; e < kPiece / 2; ++e) {
+                  const float4 z = cs[e * groups];
+                  const float2 u = unpack2<kBf16>(g.w[e]);
+                  y[2 * e] = y[2 * e] * z.x + u.x * (second ? z.y : -z.y);
+                  y[2 * e + 1] = y[2 * e + 1] * z.z + u.y * (second ? z.w : -z.w);
+                }
               }
             }
         }
