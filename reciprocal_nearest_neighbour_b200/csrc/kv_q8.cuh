@@ -12,8 +12,11 @@
 // infinity gets a NaN for its scale and reads back as NaN.
 //
 // Bound by memory: a 16-bit channel is read, a code and d-th of a scale written (append),
-// or the other way round (read).  What it takes is enough reads under way: an append's
-// warp has three passes over its rows on their way to shared memory.
+// or the other way round (read).  What an append takes is enough reads under way (a warp has
+// three passes over its rows on their way to shared memory), few instructions a pass, and
+// whole sectors.  Measured, in a CUDA graph: 11 prompt chunks, 25825 tokens of 32/8 heads of
+// 128, bf16 to e4m3, 583 MB, 94 us (6.2 TB/s, 0.95 of a copy's rate); with rows of 72
+// channels, whose pairs come in pieces of 2, 122 us for 328 MB (2.7 TB/s).  One token 3.4 us.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -204,8 +207,8 @@ kv_append_q8_kernel(const AppendQ8Params p) {
   const int q_passes = (p.Hq + fill) >> rows_log, k_passes = (p.Hkv + fill) >> rows_log;
   const int passes = q_passes + 2 * k_passes, step = 1 << p.share;
   // The next pass to fetch, its kind's end, this lane's row of it, and where that is.
-  // (One walk per kind with pointers that move on: with every pass's kind looked at and
-  // its addresses made anew, 80 more instructions a pass, 122 us in place of 99.)
+  // (Pointers move on along a kind: with every pass's kind looked at and its addresses made
+  // anew, 80 instructions a pass more, 25825 prompt tokens took 122 us where they then took 114.)
   int f_pass = part, f_end = 0, f_row = 0, f_rows = 0;
   const uint16_t* f_src = nullptr;
   int64_t f_step = 0;
