@@ -146,7 +146,8 @@ attn_decode_q8_kernel(const DecodeParams p) {
     if (p.page16) {
       // pages are whole 16-key groups: one base per group, no shuffles per row
       const bool all = p.wide && valid == 0xffffffffu && kChunks * 16 == p.d;
-      const int64_t k_step = int64_t{kRowsPer * 8} * p.k_s8[1], v_step = int64_t{kRowsPer * 8} * p.v_s8[1];
+      const int64_t k_step = int64_t{kRowsPer * 8} * p.k_s8[1];
+      const int64_t v_step = int64_t{kRowsPer * 8} * p.v_s8[1];
 #pragma unroll
       for (int g = 0; g < kMT; ++g) {
         const int page = max(0, __shfl_sync(0xffffffffu, id, g * 16));

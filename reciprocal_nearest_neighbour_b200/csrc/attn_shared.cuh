@@ -20,8 +20,9 @@
 //                   them as the 16-bit A operand of the second product; in the end the
 //                   rows' parts
 //   warps 8, 9      issue S = Q K^T and O += P V of tile 0 and 1
-//   warps 12-15     fetch K tiles (two warps) and V tiles (two) into a ring each, by 16-byte asynchronous copies: pages of any size and stride
-//                   lie in shared memory as the tensor cores' 128-byte swizzle wants them
+//   warps 12-15     fetch K tiles (two warps) and V tiles (two) into a ring each, by 16-byte
+//                   asynchronous copies: pages of any size and stride lie in shared memory
+//                   as the tensor cores' 128-byte swizzle wants them
 // Tensor memory: two score tiles of 128 columns, two output tiles of kDP.
 //
 // Measured, in a CUDA graph, all three kernels: 144 streams of 5 to 700 tokens behind 30 011,
@@ -330,6 +331,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         if (k + 1 == n_of[i]) umma_commit_warp(last_bar + 8 * i);
         __syncwarp();
       }
+      // (the last arrival at this barrier too is made before the CTA exits)
+      if (n_of[i] > 0) wait_mma(o_bar + 8 * i, (n_of[i] - 1) & 1);
       if (aborted() && any) {
         // let every product issued finish before tensor memory is released
         umma_commit_warp(drain_bar + 8 * i);
@@ -497,7 +500,8 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
         for (int e = 0; e < 8; ++e) {
           const int x = e * 4 + (lane >> 3), row = (warp & 3) * 32 + x;
           if (row < mine)
-            *reinterpret_cast<uint4*>(to + row * kDP + c) = lds_v4(stage + x * 128 + ((ch ^ (x & 7)) << 4));
+            *reinterpret_cast<uint4*>(to + row * kDP + c) =
+                lds_v4(stage + x * 128 + ((ch ^ (x & 7)) << 4));
         }
         __syncwarp();
       }
@@ -532,13 +536,14 @@ attn_shared_join_kernel(const DecodeParams p, const __grid_constant__ PrefixPara
   const int member = warp % kTeam;
   const int64_t at_row = static_cast<int64_t>(blockIdx.x) * (4 / kTeam) + warp / kTeam;
   if (at_row >= static_cast<int64_t>(p.B) * p.Hq) return;  // (never with a team of 4)
-  const int b = static_cast<int>(at_row / p.Hq), head = static_cast<int>(at_row - static_cast<int64_t>(b) * p.Hq);
+  const int b = static_cast<int>(at_row / p.Hq);
+  const int head = static_cast<int>(at_row - static_cast<int64_t>(b) * p.Hq);
   const int hk = head / p.group, in = head - hk * p.group;
   const int hb = in / kDecRows, dec_row = in - hb * kDecRows;
   const int row = b * p.group + in, unit = row / kPreUnit, at = row - unit * kPreUnit;
   const bool wide = unit < pre.wide;
-  const int64_t pre0 = static_cast<int64_t>(pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0)) * kAttnM +
-                       (wide ? at % kAttnM : at);
+  const int64_t pre_slot = pre_slot0(pre, hk, unit) + (wide ? at / kAttnM : 0);
+  const int64_t pre0 = pre_slot * kAttnM + (wide ? at % kAttnM : at);
   const int n_pre = wide ? pre.wide_splits : 2 * pre.narrow_splits;
   const int pre_step = (wide ? 2 : 1) * kAttnM;
   const bool own = dec_len(p, b) > 0;

@@ -16,7 +16,7 @@
 // three passes over its rows on their way to shared memory), few instructions a pass, and
 // whole sectors.  Measured, in a CUDA graph: 11 prompt chunks, 25825 tokens of 32/8 heads of
 // 128, bf16 to e4m3, 583 MB, 94 us (6.2 TB/s, 0.95 of a copy's rate); with rows of 72
-// channels, whose pairs come in pieces of 2, 122 us for 328 MB (2.7 TB/s).  One token 3.4 us.
+// channels, whose 36 pairs come in pieces of 4, 122 us for 328 MB (2.7 TB/s).  One token 3.4 us.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -271,8 +271,9 @@ kv_append_q8_kernel(const AppendQ8Params p) {
     uint16_t* out = is_q ? p.q_out + 8 * (times(t, p.qo_ts) + times(r, p.qo_hs))
                          : p.k_out + 8 * (times(t, p.ko_ts) + times(r, p.ko_hs));
     const bool with_out = is_q || (!is_v && p.k_out);
-    uint8_t* codes = is_v ? p.vc + 8 * (times(to.page, p.vc_ps) + times(to.row, p.vc_ts) + times(r, p.vc_hs))
-                          : p.kc + 8 * (times(to.page, p.kc_ps) + times(to.row, p.kc_ts) + times(r, p.kc_hs));
+    const int ps = is_v ? p.vc_ps : p.kc_ps, ts = is_v ? p.vc_ts : p.kc_ts;
+    uint8_t* codes = (is_v ? p.vc : p.kc) +
+                     8 * (times(to.page, ps) + times(to.row, ts) + times(r, is_v ? p.vc_hs : p.kc_hs));
     float2* scales = p.scales + (times(to.page, p.s_ps) + to.row + times(r, p.s_hs));
     out += at.ca;
     codes += at.ca;
