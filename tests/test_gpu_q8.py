@@ -686,3 +686,31 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+def test_refusals_reach_the_caller():
+    """Through the extension module as through Python."""
+    g = gen_of(3)
+    kc, vc, scales, _, _ = filled(g, "int8", 3, 16, 2, 64)
+    q = normal(g, (1, 4, 64), HF)
+    tab, lens = ints([[0, 1]]), ints([20])
+    with pytest.raises(TypeError):
+        rnn.attn_decode_q8(q, kc.view(CODES["e4m3"]), vc, scales, tab, lens)
+    with pytest.raises(ValueError):
+        rnn.attn_decode_q8(q, kc, vc, scales[:2], tab, lens)
+    with pytest.raises(ValueError):
+        rnn.attn_decode_q8(q, kc, vc, scales, tab, lens, scale=-1.0)
+    with pytest.raises(rnn.RNNError) as e:
+        rnn.attn_decode_q8(q, kc, vc, scales, tab, lens, workspace=torch.empty(
+            256, dtype=torch.uint8, device="cuda"))
+    assert e.value.name == "RNN_EWORKSPACE"
+    two = torch.zeros(2, 4, 64, dtype=HF, device="cuda")
+    with pytest.raises(rnn.RNNError) as e:          # rows of the output that overlap
+        rnn.attn_decode_q8(two, kc, vc, scales, ints([[0, 1]] * 2), ints([20, 3]),
+                           out=two.new_zeros(1024).as_strided((2, 4, 64), (64, 64, 1)))
+    assert e.value.name == "RNN_EINVAL"
+    k = normal(g, (5, 2, 64), HF)
+    with pytest.raises(rnn.RNNError):               # the same output twice
+        rnn.kv_read_q8(kc, vc, scales, tab, ints([0, 5]), 5, HF, k_out=k, v_out=k)
+    with pytest.raises(ValueError):
+        rnn.kv_append_q8(k, k, kc, vc, scales, tab, ints([0]), ints([0, 5]), q=k)

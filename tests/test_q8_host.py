@@ -212,3 +212,19 @@ def test_binding_refuses_cpu_tensors():
         rnn.kv_append_q8(x, x, c, c, s, torch.zeros((1, 2), dtype=torch.int32), i[:1], i)
     with pytest.raises(ValueError):
         rnn.kv_read_q8(c, c, s, torch.zeros((1, 2), dtype=torch.int32), i, 4)
+
+
+def test_extension_module_serves_no_unusual_call(lib):
+    """What is not as expected comes back as None, for the Python form to look at."""
+    fast = _lib.load_fast()
+    assert fast.__name__.endswith("_fast")
+    for name, n in (("attn_decode_q8", 10), ("attn_decode_shared", 11), ("kv_read_q8", 10),
+                    ("kv_append_q8", 15)):
+        call = getattr(fast, name)
+        assert call() is None and call(*[None] * n) is None and call(*[1.5] * n) is None
+        assert call(*[torch.zeros(2, 2, 64, dtype=torch.float16)] * n) is None
+        assert call(*[OnGpu(2, 2, 64)] * n) is None
+    with pytest.raises(TypeError):
+        fast.bind(1, 2)
+    with pytest.raises(ValueError):
+        fast.bind(0, 0, 0, 0, 0, 0)
