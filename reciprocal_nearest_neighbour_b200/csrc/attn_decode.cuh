@@ -100,10 +100,10 @@ __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
   return static_cast<int>(n < 0 ? 0 : (n < room ? n : room));
 }
 // places of a sequence's pairs in the list: per pair its cost, then its tiles
-template <int kTile>
+template <int kTile, int kCost>
 __device__ __forceinline__ int64_t dec_places(const DecodeParams& p, int b) {
   const int n = dec_len(p, b);
-  return n > 0 ? (n + kTile - 1) / kTile + kDecPairCost : 0;
+  return n > 0 ? (n + kTile - 1) / kTile + kCost : 0;
 }
 __device__ __forceinline__ int64_t dec_share(int64_t c, int64_t total, int64_t grid) {
   return c * total / grid;
@@ -124,7 +124,7 @@ struct DecCursor {
 
 // This CTA's share of the list: its first tile and the place behind its last; all
 // places, and the CTAs with a share.  False where there is none.  By the whole block.
-template <int kTile>
+template <int kTile, int kCost = kDecPairCost>
 __device__ __forceinline__ bool dec_begin(const DecodeParams& p, int warp, int lane, DecCursor& ld,
                                           int64_t& hi, int64_t& total, int64_t& grid) {
   const int Hv = p.Hkv * p.hblocks;
@@ -134,7 +134,7 @@ __device__ __forceinline__ bool dec_begin(const DecodeParams& p, int warp, int l
   const int per = (p.B + kDecWarps * 32 - 1) / (kDecWarps * 32);
   const int b_lo = min(p.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.B, b_lo + per);
   int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += dec_places<kTile>(p, b);
+  for (int b = b_lo; b < b_hi; ++b) mine += dec_places<kTile, kCost>(p, b);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool dec_begin(const DecodeParams& p, int warp, int l
   if (lo >= before * Hv && lo < (before + mine) * Hv) {
     int64_t at = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t n = dec_places<kTile>(p, b);
+      const int64_t n = dec_places<kTile, kCost>(p, b);
       if (lo < (at + n) * Hv) {
         sh_b = b;
         sh_before = at;
@@ -172,18 +172,18 @@ __device__ __forceinline__ bool dec_begin(const DecodeParams& p, int warp, int l
   ld.len = dec_len(p, ld.b);
   ld.n = (ld.len + kTile - 1) / kTile;
   // the share's first place is a tile, or stands for its pair's cost
-  const int64_t r = lo - sh_before * Hv, per_pair = ld.n + kDecPairCost;
+  const int64_t r = lo - sh_before * Hv, per_pair = ld.n + kCost;
   ld.h = static_cast<int>(r / per_pair);
-  ld.j = max(0, static_cast<int>(r - ld.h * per_pair) - kDecPairCost);
-  ld.at = sh_before * Hv + ld.h * per_pair + kDecPairCost + ld.j;
+  ld.j = max(0, static_cast<int>(r - ld.h * per_pair) - kCost);
+  ld.at = sh_before * Hv + ld.h * per_pair + kCost + ld.j;
   return true;
 }
-template <int kTile>
+template <int kTile, int kCost = kDecPairCost>
 __device__ __forceinline__ void dec_advance(const DecodeParams& p, int Hv, DecCursor& k) {
   ++k.at;
   if (++k.j < k.n) return;
   k.j = 0;
-  k.at += kDecPairCost;
+  k.at += kCost;
   if (++k.h < Hv) return;
   k.h = 0;
   do {

@@ -15,8 +15,8 @@
 // also transposes them.
 //
 // Measured, in a CUDA graph with the join: 90 streams of 50 to 9000 keys, 32/8 heads of 128,
-// e4m3, pages of 16, 0.32 GB, 66 us (4.8 TB/s; attn_decode takes 1.6 times as long over twice
-// the bytes); 4 streams of 80 001 to 131 000 keys, 32/4 heads, int8, 0.44 GB, 80 us (5.4 TB/s, 0.83
+// e4m3, pages of 16, 0.32 GB, 65 us (4.9 TB/s; attn_decode takes 1.6 times as long over twice
+// the bytes; 62 us with a head's rows of a page side by side); 4 streams of 80 001 to 131 000 keys, 32/4 heads, int8, 0.44 GB, 80 us (5.4 TB/s, 0.83
 // of a copy's rate).  It is latency and issue that are left: about 720 instructions (e4m3, 830
 // int8) a warp and tile, of which the conversions are 200 at half rate, with three warps a
 // scheduler in 168 registers.  (Two CTAs per SM with three tiles a warp: 83 and 100 us, when
@@ -38,6 +38,10 @@
 namespace rnn {
 
 constexpr int kQ8Keys = 32;  // keys per warp and tile, the lanes of a warp
+// What a pair costs beside its tiles, in tiles.  90 streams of 50 to 9000 keys, 8 key
+// heads: of 128 channels 86 us without it, 65 at 1, 66 at 2, 68 at 4; of 96 channels 91, 74,
+// 78 and 82.
+constexpr int kQ8PairCost = 1;
 // Three CTAs per SM for up to 8 query heads a key head, with two tiles each a warp.
 template <int kDP>
 struct DecQ8Shape {
@@ -97,9 +101,9 @@ attn_decode_q8_kernel(const DecodeParams p) {
   const int Hv = p.Hkv * p.hblocks;
   DecCursor ld, cur;
   int64_t hi, total, grid;
-  if (!dec_begin<S::kTile>(p, warp, lane, ld, hi, total, grid)) return;
+  if (!dec_begin<S::kTile, kQ8PairCost>(p, warp, lane, ld, hi, total, grid)) return;
   cur = ld;
-  auto advance = [&](DecCursor& k) { dec_advance<S::kTile>(p, Hv, k); };
+  auto advance = [&](DecCursor& k) { dec_advance<S::kTile, kQ8PairCost>(p, Hv, k); };
   // Page of key `lane` of a tile, -1 where there is none.
   auto page_of = [&](const DecCursor& k) -> int {
     const int t = k.j * S::kTile + warp * kQ8Keys + lane;
