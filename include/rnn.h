@@ -690,8 +690,9 @@ rnn_status rnn_kv_read_q8(const rnn_kv_read_q8_args *args, rnn_stream_t stream);
  * scale, with a power of two for each query head) is rounded to fp16 once.
  * Queries are held as fp16 times a power of two for each head: what is 2^-39 of
  * a row's largest channel and less may be lost.  Values beyond about 2^100 may
- * lose their small weights.  Strides are at most 2^34 codes (2^32 scales), in
- * the other two calls too (larger ones: RNN_EUNSUPPORTED).  2 kernel launches.
+ * lose their small weights; small ones keep theirs, down to an append's least
+ * scale.  Strides are at most 2^34 codes (2^32 scales), in the other two calls
+ * too (larger ones: RNN_EUNSUPPORTED).  2 kernel launches.
  */
 typedef struct rnn_attn_decode_q8_args {
   rnn_rows q, out;

@@ -28,7 +28,12 @@
 // reference z of a head is that of score + log2 vs, not of the score: with p_t =
 // 2^(score - z) the largest weight is put at 2^6 when z is chosen, and z is chosen again,
 // the sums following, when a weight passes 2^15.  The totals sum p_t in fp32, which z
-// keeps below 2^100, and whose least 2^-126 a value beyond about 2^100 would come near.
+// keeps below 2^100, and whose least 2^-126 a value beyond about 2^100 would come near:
+// z is no less than the largest score - 60.  Where that leaves the weights below 2^6
+// (scales below 2^-54) they take a further factor 2^lift on their way into the product,
+// which brings the largest to 2^5 at least; a pair's end, or what is held, takes it out
+// again.  A power of two up to 2^72 (an append's scales are 2^-126 and more), it is exact
+// in fp32 both ways.
 #pragma once
 #include <cstdint>
 #include "attn_decode.cuh"
@@ -54,6 +59,11 @@ struct DecQ8Shape {
   static constexpr size_t kSmem = size_t(kDecWarps) * kStages * kStageBytes +
                                   kDecWarps * kDecRows * 8;
 };
+
+// 1 / x of a power of two between 2^-126 and 2^126.
+__device__ __forceinline__ float inverse_pow2(float x) {
+  return __uint_as_float(0x7F000000u - __float_as_uint(x));
+}
 
 // 8 bytes to shared memory; with `live` false they are zeroed and nothing is read.
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
@@ -91,7 +101,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
   constexpr int kRowsPer = 32 / kChunks; // rows moved by one warp-wide copy
   constexpr int kLaneCh = kDP / 8;       // a lane's channels of a value row
   constexpr float kWeightTop = 32768.f, kTotalTop = 1.2676506e30f;  // 2^15, 2^100
-  constexpr float kAim = 6.f, kTotalAim = 60.f;                      // log2
+  constexpr float kAim = 6.f, kTotalAim = 60.f, kMostLift = 80.f;    // log2
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* const tiles = dec_smem + warp * kStages * S::kStageBytes;
@@ -218,6 +228,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
   float o[kNT][kSteps][4];   // channel kLaneCh g + 2 c (+ 1 in 2, 3), head 8 n + 2 q (+ 1 in 1, 3)
   float ch_scale[kNT][2];    // of those heads: scale * log2(e) / the queries' factor
   float z[kNT][2], l[kNT][2];
+  float lift[kNT][2];        // the factor 2^lift of those heads' weights and sums
   constexpr int kSums = kNT * kSteps * 4, kHoldTiles = kDecHoldKeys / kQ8Keys;
   volatile float held[kSums + 4 * kNT];  // sums taken out, their totals and references
   bool any_held = false;
@@ -230,14 +241,15 @@ attn_decode_q8_kernel(const DecodeParams p) {
         const float ref = held[kSums + 2 * kNT + 2 * n + e];
         const float a = ref == kNegInf ? 0.f : exp2_approx(ref - z[n][e]);
         l[n][e] = fmaf(held[kSums + 2 * n + e], a, l[n][e]);
+        const float up = a * lift[n][e];
 #pragma unroll
         for (int c = 0; c < kSteps; ++c)
 #pragma unroll
           for (int h = e; h < 4; h += 2)
-            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], a, o[n][c][h]);
+            o[n][c][h] = fmaf(held[(n * kSteps + c) * 4 + h], up, o[n][c][h]);
       }
   };
-  bool fresh = true;
+  bool fresh = true, lifted = false;  // lifted: one of the warp's factors is not 1
   bool whole = cur.j == 0;   // the pair started in this share
 #pragma unroll 1
   while (cur.at < hi) {
@@ -282,7 +294,9 @@ attn_decode_q8_kernel(const DecodeParams p) {
           ch_scale[n][e] = __shfl_sync(0xffffffffu, back, (q2 + e) * 4) * p.c;
           z[n][e] = kNegInf;
           l[n][e] = 0.f;
+          lift[n][e] = 1.f;
         }
+        lifted = false;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -342,7 +356,8 @@ attn_decode_q8_kernel(const DecodeParams p) {
 #pragma unroll
               for (int n = 0; n < kNT; ++n) s[t][n][e] = kNegInf;
       }
-      // ---- p = 2^(score - z), and the weights p vs
+      // ---- p = 2^(score - z), and the weights p vs 2^lift (in this order: vs 2^lift may
+      // be infinite where p is 0)
       float pr[kMT][kNT][4], w[kMT][kNT][4];
       auto weigh = [&](int n, int e) {
         const float zz = z[n][e] == kNegInf ? 0.f : z[n][e];
@@ -353,6 +368,12 @@ attn_decode_q8_kernel(const DecodeParams p) {
             pr[t][n][e + 2 * h] = exp2_approx(s[t][n][e + 2 * h] - zz);
             w[t][n][e + 2 * h] = pr[t][n][e + 2 * h] * vscale[t][h];
           }
+        if (lifted) {
+#pragma unroll
+          for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[t][n][e + 2 * h] *= lift[n][e];
+        }
       };
       bool over = false;
 #pragma unroll
@@ -370,31 +391,47 @@ attn_decode_q8_kernel(const DecodeParams p) {
         }
       // ---- the reference
       if (__any_sync(0xffffffffu, over)) {
+        bool any = false;
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y = z[n][e];
+            // the reference, and where the largest weight so far and here would be at 2^6
+            const int had = static_cast<int>(__float_as_uint(lift[n][e]) >> 23) - 127;
+            float put = z[n][e] - had, y = z[n][e];
 #pragma unroll
             for (int t = 0; t < kMT; ++t)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float x = s[t][n][e + 2 * h];
-                y = fmax3(y, x + (log2f(vscale[t][h]) - kAim), x - kTotalAim);
+                put = fmaxf(put, x + (log2f(vscale[t][h]) - kAim));
+                y = fmaxf(y, x - kTotalAim);
               }
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+#pragma unroll
+            for (int h = 4; h < 32; h *= 2) {
+              put = fmaxf(put, __shfl_xor_sync(0xffffffffu, put, h));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, h));
+            }
+            y = fmaxf(y, put);
             const float a = z[n][e] == kNegInf ? 0.f : exp2_approx(z[n][e] - y);
+            // (all scales so far 0: the most; no score so far: 2^0)
+            const int up = y == kNegInf ? 0 : static_cast<int>(fminf(floorf(y - put), kMostLift));
+            const float b = a * __uint_as_float(static_cast<uint32_t>(127 + up - had) << 23);
+            lift[n][e] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            any = any || up > 0;
             z[n][e] = y;
             l[n][e] *= a;
 #pragma unroll
             for (int c = 0; c < kSteps; ++c) {
-              o[n][c][e] *= a;
-              o[n][c][e + 2] *= a;
+              o[n][c][e] *= b;
+              o[n][c][e + 2] *= b;
             }
-            weigh(n, e);
           }
+        lifted = __any_sync(0xffffffffu, any);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) weigh(n, e);
       }
       uint32_t pf[kMT][kNT][2];
 #pragma unroll
@@ -450,11 +487,12 @@ attn_decode_q8_kernel(const DecodeParams p) {
           held[kSums + 2 * n + e] = l[n][e];
           held[kSums + 2 * kNT + 2 * n + e] = z[n][e];
           l[n][e] = 0.f;
+          const float down = inverse_pow2(lift[n][e]);
 #pragma unroll
           for (int c = 0; c < kSteps; ++c)
 #pragma unroll
             for (int h = e; h < 4; h += 2) {
-              held[(n * kSteps + c) * 4 + h] = o[n][c][h];
+              held[(n * kSteps + c) * 4 + h] = o[n][c][h] * down;
               o[n][c][h] = 0.f;
             }
         }
@@ -493,7 +531,7 @@ attn_decode_q8_kernel(const DecodeParams p) {
           float M = kNegInf;
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * kDecRows + n * 8 + q2 + e].x);
-          r[e] = z[n][e] == kNegInf ? 0.f : exp2_approx(z[n][e] - M);
+          r[e] = z[n][e] == kNegInf ? 0.f : exp2_approx(z[n][e] - M) * inverse_pow2(lift[n][e]);
         }
 #pragma unroll
         for (int c = 0; c < kSteps; ++c)
