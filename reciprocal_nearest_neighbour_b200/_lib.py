@@ -180,7 +180,8 @@ class _Python:
 
 
 # The extension module ``_fast`` once it is loaded.  Its functions serve the usual calls
-# of their namesakes, or return None.
+# of their namesakes, or return None without having called the library; a status that the
+# library gave comes back as an int.
 fast = None
 
 
@@ -279,6 +280,13 @@ def load():
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def served(result, where: str):
+    """What the extension module returned, or the error that it stands for."""
+    if type(result) is int:
+        check(result, where)
+    return result
 
 
 def check(code: int, where: str) -> None:

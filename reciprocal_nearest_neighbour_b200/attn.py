@@ -406,7 +406,7 @@ def attn_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         q, k_cache, v_cache, prefix_pages, prefix_len, page_table, lens, scale, with_lse, out,
         workspace)
     if done is not None:
-        return done
+        return _lib.served(done, "rnn_attn_decode_shared")
     kind = _value_dtype(q, "q")
     dev = q.device
     _all(kind, dev, 3, q, "q")

@@ -79,7 +79,7 @@ def kv_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         k, v, k_cache, v_cache, scales, page_table, start, cu, q, inv_freq, positions, paired,
         with_k, q_out, k_out)
     if done is not None:
-        return done
+        return _lib.served(done, "rnn_kv_append_q8")
     kind, dev, T, hq, hkv, d = _new_rows(k, v, q, q_out, inv_freq)
     codes, _, num_pages, size, scale_at = _coded(k_cache, v_cache, scales, dev, hkv, d)
     B = _cu(cu, "cu", dev)
@@ -115,7 +115,7 @@ def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tenso
     done = (_lib.fast or _lib.load_fast()).kv_read_q8(
         k_cache, v_cache, scales, page_table, cu, tokens, dtype is torch.bfloat16, start, k_out, v_out)
     if done is not None:
-        return done
+        return _lib.served(done, "rnn_kv_read_q8")
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, heads, d] tensor")
     dev, d, tokens = k_cache.device, k_cache.shape[3], int(tokens)
@@ -157,7 +157,7 @@ def attn_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     done = (_lib.fast or _lib.load_fast()).attn_decode_q8(
         q, k_cache, v_cache, scales, page_table, lens, scale, with_lse, out, workspace)
     if done is not None:
-        return done
+        return _lib.served(done, "rnn_attn_decode_q8")
     kind = _value_dtype(q, "q")
     dev = q.device
     _all(kind, dev, 3, q, "q")

@@ -6,6 +6,9 @@
 // position, and returns what that returns, or None where anything is not as
 // expected: the Python form then checks step by step and raises what there is to raise,
 // or serves the rare case (another current device, a stride of a dimension of size 1).
+// None means that the library was not called.  Once it was, its status is the answer, an
+// int if it is not 0: the call may have done its work all the same (the runtime reports
+// an earlier error to whoever asks next), and rows rotated in place must not be again.
 #include <Python.h>
 
 #include <cmath>
@@ -29,8 +32,8 @@ decltype(&rnn_attn_decode_shared_workspace_size) f_shared_need = nullptr;
 
 // The tensors of a call, all on one device.
 struct Call {
-  bool ok = true;
-  int device = -1;
+  bool ok = true, made = false;  // made: the library was called, with this status
+  int device = -1, status = 0;
   const at::Tensor* tensor(PyObject* o, int64_t ndim, at::ScalarType type) {
     if (!ok || !THPVariable_CheckExact(o)) return fail();
     const at::Tensor& t = THPVariable_Unpack(o);
@@ -86,28 +89,32 @@ struct Call {
   rnn_stream_t stream() const {
     return reinterpret_cast<rnn_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
   }
+  at::Tensor bytes(size_t n) const { return empty({static_cast<int64_t>(n)}, at::kByte); }
   at::Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
     return at::empty(size, at::TensorOptions().dtype(type).device(at::kCUDA, device));
   }
-  // the caller's tensor of this shape, or a new one
+  // the caller's tensor of this shape; none yet where a new one is to be made
   at::Tensor out(PyObject* o, at::IntArrayRef size, at::ScalarType type) {
-    if (o == Py_None) return empty(size, type);
+    if (o == Py_None) return {};
     const at::Tensor* t = tensor(o, static_cast<int64_t>(size.size()), type);
     if (!t || !want(t->sizes() == size)) return {};
     return *t;
   }
-  // address and size of the workspace; a new one is kept in `hold` until the call is made
-  void* scratch(PyObject* o, size_t need, at::Tensor* hold, uint64_t* bytes) {
-    if (o == Py_None) {
-      *hold = empty({static_cast<int64_t>(need)}, at::kByte);
-    } else {
-      const at::Tensor* t = tensor(o, 1, at::kByte);
-      if (!t || !want(t->is_contiguous())) return nullptr;
-      *hold = *t;
-    }
-    *bytes = static_cast<uint64_t>(hold->numel());
-    return hold->data_ptr();
+  // the caller's workspace, or none yet
+  at::Tensor scratch(PyObject* o) {
+    if (o == Py_None) return {};
+    const at::Tensor* t = tensor(o, 1, at::kByte);
+    if (!t || !want(t->is_contiguous())) return {};
+    return *t;
   }
+  // the library's call
+  template <typename Args>
+  void call(rnn_status (*f)(const Args*, rnn_stream_t), const Args& p) {
+    if (!ok) return;
+    made = true;
+    status = f(&p, stream());
+  }
+  bool done() const { return made && status == RNN_OK; }
   float scale(PyObject* o, int64_t d) {
     if (o == Py_None) return static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
     if (!want(PyFloat_CheckExact(o))) return 0.f;
@@ -167,8 +174,7 @@ bool heads(int64_t hq, int64_t hkv) {
 }
 
 // (q, k_cache, v_cache, scales, page_table, lens, scale, with_lse, out, workspace)
-PyObject* decode_q8(PyObject* const* a) {
-  Call c;
+PyObject* decode_q8(Call& c, PyObject* const* a) {
   at::ScalarType type;
   rnn_attn_decode_q8_args p;
   std::memset(&p, 0, sizeof(p));
@@ -187,24 +193,26 @@ PyObject* decode_q8(PyObject* const* a) {
   p.scale = c.scale(a[6], d);
   const bool with_lse = c.flag(a[7]);
   if (!c.ok) return nullptr;
-  const at::Tensor out = c.out(a[8], q->sizes(), type);
+  at::Tensor out = c.out(a[8], q->sizes(), type), scratch = c.scratch(a[9]), lse;
   if (!c.ok) return nullptr;
-  p.out = c.rows(out, d);
-  at::Tensor hold, lse;
-  p.workspace = c.scratch(a[9], f_decode_need(B, hq, cache.heads, d), &hold, &p.ws_bytes);
-  if (!c.ok) return nullptr;
-  if (with_lse) lse = c.empty({B, hq}, at::kFloat), p.lse = lse.data_ptr<float>();
   p.num_pages = cache.pages;
   p.page_size = static_cast<int32_t>(cache.size);
   p.B = static_cast<int32_t>(B), p.Hq = static_cast<int32_t>(hq);
   p.Hkv = static_cast<int32_t>(cache.heads), p.d = static_cast<int32_t>(d);
   p.codes = cache.codes;
-  return f_decode(&p, c.stream()) ? nullptr : give(out, lse);
+  {
+    if (!out.defined()) out = c.empty({B, hq, d}, type);
+    if (!scratch.defined()) scratch = c.bytes(f_decode_need(p.B, p.Hq, p.Hkv, p.d));
+    if (with_lse) lse = c.empty({B, hq}, at::kFloat), p.lse = lse.data_ptr<float>();
+    p.out = c.rows(out, d);
+    p.workspace = scratch.data_ptr(), p.ws_bytes = static_cast<uint64_t>(scratch.numel());
+    c.call(f_decode, p);
+  }
+  return c.done() ? give(out, lse) : nullptr;
 }
 
 // (q, k_cache, v_cache, prefix_pages, prefix_len, page_table, lens, scale, with_lse, out, workspace)
-PyObject* shared(PyObject* const* a) {
-  Call c;
+PyObject* shared(Call& c, PyObject* const* a) {
   at::ScalarType type;
   rnn_attn_decode_shared_args p;
   std::memset(&p, 0, sizeof(p));
@@ -230,25 +238,27 @@ PyObject* shared(PyObject* const* a) {
   p.scale = c.scale(a[7], d);
   const bool with_lse = c.flag(a[8]);
   if (!c.ok) return nullptr;
-  const at::Tensor out = c.out(a[9], q->sizes(), type);
+  at::Tensor out = c.out(a[9], q->sizes(), type), scratch = c.scratch(a[10]), lse;
   if (!c.ok) return nullptr;
-  p.out = c.rows(out, d);
-  at::Tensor hold, lse;
-  p.workspace =
-      c.scratch(a[10], f_shared_need(B, hq, hkv, d, count * k->size(1)), &hold, &p.ws_bytes);
-  if (!c.ok) return nullptr;
-  if (with_lse) lse = c.empty({B, hq}, at::kFloat), p.lse = lse.data_ptr<float>();
   p.num_pages = k->size(0);
   p.page_size = static_cast<int32_t>(k->size(1));
   p.prefix_pages_count = static_cast<int32_t>(count);
   p.B = static_cast<int32_t>(B), p.Hq = static_cast<int32_t>(hq);
   p.Hkv = static_cast<int32_t>(hkv), p.d = static_cast<int32_t>(d);
-  return f_shared(&p, c.stream()) ? nullptr : give(out, lse);
+  {
+    if (!out.defined()) out = c.empty({B, hq, d}, type);
+    if (!scratch.defined())
+      scratch = c.bytes(f_shared_need(p.B, p.Hq, p.Hkv, p.d, count * p.page_size));
+    if (with_lse) lse = c.empty({B, hq}, at::kFloat), p.lse = lse.data_ptr<float>();
+    p.out = c.rows(out, d);
+    p.workspace = scratch.data_ptr(), p.ws_bytes = static_cast<uint64_t>(scratch.numel());
+    c.call(f_shared, p);
+  }
+  return c.done() ? give(out, lse) : nullptr;
 }
 
 // (k_cache, v_cache, scales, page_table, cu, tokens, bf16, start, k_out, v_out)
-PyObject* read_q8(PyObject* const* a) {
-  Call c;
+PyObject* read_q8(Call& c, PyObject* const* a) {
   rnn_kv_read_q8_args p;
   std::memset(&p, 0, sizeof(p));
   const Coded cache = coded(c, a[0], a[1], a[2]);
@@ -268,10 +278,8 @@ PyObject* read_q8(PyObject* const* a) {
   p.page_table = c.table(a[3], B, &p.table_stride, &p.max_pages);
   if (!c.ok) return nullptr;
   const at::ScalarType type = a[6] == Py_True ? at::kBFloat16 : at::kHalf;
-  const at::Tensor k = c.out(a[8], {T, cache.heads, cache.d}, type);
-  const at::Tensor v = c.ok ? c.out(a[9], {T, cache.heads, cache.d}, type) : at::Tensor();
-  if (!c.ok) return nullptr;
-  p.k = c.rows(k, cache.d), p.v = c.rows(v, cache.d);
+  at::Tensor k = c.out(a[8], {T, cache.heads, cache.d}, type);
+  at::Tensor v = c.out(a[9], {T, cache.heads, cache.d}, type);
   if (!c.ok) return nullptr;
   p.k_cache = cache.k, p.v_cache = cache.v, p.scales = cache.scales;
   p.T = T, p.num_pages = cache.pages;
@@ -279,13 +287,18 @@ PyObject* read_q8(PyObject* const* a) {
   p.dtype = type == at::kBFloat16 ? RNN_BF16 : RNN_F16;
   p.codes = cache.codes, p.page_size = static_cast<int32_t>(cache.size);
   p.B = static_cast<int32_t>(B);
-  return f_read(&p, c.stream()) ? nullptr : give(k, v);
+  {
+    for (at::Tensor* t : {&k, &v})
+      if (!t->defined()) *t = c.empty({T, cache.heads, cache.d}, type);
+    p.k = c.rows(k, cache.d), p.v = c.rows(v, cache.d);
+    c.call(f_read, p);
+  }
+  return c.done() ? give(k, v) : nullptr;
 }
 
 // (k, v, k_cache, v_cache, scales, page_table, start, cu, q, inv_freq, positions, paired, with_k,
 //  q_out, k_out)
-PyObject* append_q8(PyObject* const* a) {
-  Call c;
+PyObject* append_q8(Call& c, PyObject* const* a) {
   at::ScalarType type;
   rnn_kv_append_q8_args p;
   std::memset(&p, 0, sizeof(p));
@@ -342,24 +355,22 @@ PyObject* append_q8(PyObject* const* a) {
   p.paired = c.flag(a[11]);
   const bool with_k = c.flag(a[12]);
   if (!c.ok) return nullptr;
-  at::Tensor q_out, k_out;
-  if (q) {
-    q_out = c.out(a[13], q->sizes(), type);
-    if (!c.ok) return nullptr;
-    p.q_out = c.rows(q_out, d);
-  }
-  if (with_k || a[14] != Py_None) {
-    k_out = c.out(a[14], k->sizes(), type);
-    if (!c.ok) return nullptr;
-    p.k_out = c.rows(k_out, d);
-  }
+  at::Tensor q_out, k_out = c.out(a[14], k->sizes(), type);
+  if (q) q_out = c.out(a[13], q->sizes(), type);
   if (!c.ok) return nullptr;
   p.k_cache = cache.k, p.v_cache = cache.v, p.scales = cache.scales;
   p.T = T, p.num_pages = cache.pages;
   p.Hkv = static_cast<int32_t>(hkv), p.d = static_cast<int32_t>(d);
   p.codes = cache.codes, p.page_size = static_cast<int32_t>(cache.size);
   p.B = static_cast<int32_t>(B);
-  if (f_append(&p, c.stream())) return nullptr;
+  {
+    if (q && !q_out.defined()) q_out = c.empty({T, p.Hq, d}, type);
+    if (with_k && !k_out.defined()) k_out = c.empty({T, hkv, d}, type);
+    if (q) p.q_out = c.rows(q_out, d);
+    if (k_out.defined()) p.k_out = c.rows(k_out, d);
+    c.call(f_append, p);
+  }
+  if (!c.done()) return nullptr;
   PyObject* qo = q ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
   PyObject* ko = k_out.defined() ? THPVariable_Wrap(k_out) : Py_NewRef(Py_None);
   PyObject* both = PyTuple_Pack(2, qo, ko);
@@ -369,12 +380,19 @@ PyObject* append_q8(PyObject* const* a) {
 }
 
 // A call that could not be served here, by an error of torch's allocator too, is None.
-template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
+template <PyObject* (*kCall)(Call&, PyObject* const*), Py_ssize_t kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != kArgs || !f_append) Py_RETURN_NONE;
+  Call c;
   try {
-    if (PyObject* r = kCall(args)) return r;
-  } catch (const std::exception&) {
+    if (PyObject* r = kCall(c, args)) return r;
+  } catch (const std::exception& e) {
+    if (c.made && !PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  if (c.made) {
+    if (c.status == RNN_OK) return nullptr;  // its results could not be handed over
+    PyErr_Clear();
+    return PyLong_FromLong(c.status);
   }
   if (PyErr_Occurred()) PyErr_Clear();
   Py_RETURN_NONE;

@@ -1,0 +1,91 @@
+"""What the calls through the extension module do when the library's call fails
+(needs a B200)."""
+import ctypes
+
+import pytest
+import torch
+
+import reciprocal_nearest_neighbour_b200 as rnn
+from test_gpu_q8 import filled, gen_of, ints, normal
+
+pytestmark = pytest.mark.gpu
+
+HF = torch.float16
+NAMES = ("rnn_kv_read_q8", "rnn_attn_decode_q8", "rnn_attn_decode_q8_workspace_size",
+         "rnn_attn_decode_shared", "rnn_attn_decode_shared_workspace_size", "rnn_kv_append_q8")
+
+
+def address(f):
+    return ctypes.cast(f, ctypes.c_void_p).value
+
+
+@pytest.fixture
+def entry():
+    """Puts a function in the place of the library's calls, until the test's end."""
+    lib, fast = rnn._lib.load(), rnn._lib.load_fast()
+
+    def put(f):
+        fast.bind(*(address(getattr(lib, n) if f is None or n.endswith("_size") else f)
+                    for n in NAMES))
+
+    yield put
+    put(None)
+
+
+def calls():
+    """The four calls, on small inputs, and the tensors that they write."""
+    g = gen_of(3)
+    kc, vc, scales, _, _ = filled(g, "int8", 3, 16, 2, 64)
+    k16, v16 = (normal(g, (3, 16, 2, 64), HF) for _ in range(2))
+    q, k, v = (normal(g, (5, h, 64), HF) for h in (4, 2, 2))
+    one = normal(g, (1, 4, 64), HF)
+    inv = torch.ones(32, dtype=torch.float64, device="cuda")
+    tab = ints([[0, 1]])
+    outs = [torch.full((1, 4, 64), 7.0, dtype=HF, device="cuda") for _ in range(2)]
+    read = [torch.full((5, 2, 64), 7.0, dtype=HF, device="cuda") for _ in range(2)]
+    todo = {
+        "kv_append_q8": lambda m, n: m(k, v, kc, vc, scales, tab, ints([0]), ints([0, 5]),
+                                       **n(q=q, inv_freq=inv, positions=None, paired=False,
+                                           with_k=False, q_out=q, k_out=k)),
+        "kv_read_q8": lambda m, n: m(kc, vc, scales, tab, ints([0, 5]), 5, n.dtype,
+                                     **n(start=None, k_out=read[0], v_out=read[1])),
+        "attn_decode_q8": lambda m, n: m(one, kc, vc, scales, tab, ints([20]),
+                                         **n(scale=0.25, with_lse=False, out=outs[0], workspace=None)),
+        "attn_decode_shared": lambda m, n: m(one, k16, v16, ints([2]), ints([9]), tab, ints([20]),
+                                             **n(scale=0.25, with_lse=False, out=outs[1],
+                                                 workspace=None)),
+    }
+    return todo, [q, k, kc, vc, scales, *outs, *read]
+
+
+class Named:
+    """Keyword arguments of the package's function."""
+    dtype = HF
+
+    def __call__(self, **kw):
+        return kw
+
+
+@pytest.mark.parametrize("name", ["kv_append_q8", "kv_read_q8", "attn_decode_q8", "attn_decode_shared"])
+@pytest.mark.parametrize("code", [4, 6])
+def test_a_failed_call_is_not_made_again(entry, name, code):
+    """A status of the library reaches the caller; nothing runs a second time (rows rotated
+    in place would be turned twice)."""
+    todo, written = calls()
+    before = [t.clone() for t in written]
+    made = []
+
+    @ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
+    def fails(args, stream):
+        made.append(args)
+        return code
+
+    entry(fails)
+    with pytest.raises(rnn.RNNError) as e:
+        todo[name](getattr(rnn, name), Named())
+    assert e.value.name == rnn._lib.STATUS[code] and len(made) == 1
+    torch.cuda.synchronize()
+    for t, was in zip(written, before):
+        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
+    entry(None)
+    assert todo[name](getattr(rnn, name), Named()) is not None
