@@ -9,6 +9,7 @@
 // None means that the library was not called.  Once it was, its status is the answer, an
 // int if it is not 0: the call may have done its work all the same (the runtime reports
 // an earlier error to whoever asks next), and rows rotated in place must not be again.
+// The interpreter's lock is released over allocations and the library's call.
 #include <Python.h>
 
 #include <cmath>
@@ -29,6 +30,12 @@ decltype(&rnn_attn_decode_q8) f_decode = nullptr;
 decltype(&rnn_attn_decode_q8_workspace_size) f_decode_need = nullptr;
 decltype(&rnn_attn_decode_shared) f_shared = nullptr;
 decltype(&rnn_attn_decode_shared_workspace_size) f_shared_need = nullptr;
+
+// Other Python threads run while this lives.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // The tensors of a call, all on one device.
 struct Call {
@@ -201,6 +208,7 @@ PyObject* decode_q8(Call& c, PyObject* const* a) {
   p.Hkv = static_cast<int32_t>(cache.heads), p.d = static_cast<int32_t>(d);
   p.codes = cache.codes;
   {
+    Unlocked unlocked;
     if (!out.defined()) out = c.empty({B, hq, d}, type);
     if (!scratch.defined()) scratch = c.bytes(f_decode_need(p.B, p.Hq, p.Hkv, p.d));
     if (with_lse) lse = c.empty({B, hq}, at::kFloat), p.lse = lse.data_ptr<float>();
@@ -246,6 +254,7 @@ PyObject* shared(Call& c, PyObject* const* a) {
   p.B = static_cast<int32_t>(B), p.Hq = static_cast<int32_t>(hq);
   p.Hkv = static_cast<int32_t>(hkv), p.d = static_cast<int32_t>(d);
   {
+    Unlocked unlocked;
     if (!out.defined()) out = c.empty({B, hq, d}, type);
     if (!scratch.defined())
       scratch = c.bytes(f_shared_need(p.B, p.Hq, p.Hkv, p.d, count * p.page_size));
@@ -288,6 +297,7 @@ PyObject* read_q8(Call& c, PyObject* const* a) {
   p.codes = cache.codes, p.page_size = static_cast<int32_t>(cache.size);
   p.B = static_cast<int32_t>(B);
   {
+    Unlocked unlocked;
     for (at::Tensor* t : {&k, &v})
       if (!t->defined()) *t = c.empty({T, cache.heads, cache.d}, type);
     p.k = c.rows(k, cache.d), p.v = c.rows(v, cache.d);
@@ -364,6 +374,7 @@ PyObject* append_q8(Call& c, PyObject* const* a) {
   p.codes = cache.codes, p.page_size = static_cast<int32_t>(cache.size);
   p.B = static_cast<int32_t>(B);
   {
+    Unlocked unlocked;
     if (q && !q_out.defined()) q_out = c.empty({T, p.Hq, d}, type);
     if (with_k && !k_out.defined()) k_out = c.empty({T, hkv, d}, type);
     if (q) p.q_out = c.rows(q_out, d);

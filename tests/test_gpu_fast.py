@@ -1,5 +1,5 @@
-"""What the calls through the extension module do when the library's call fails
-(needs a B200)."""
+"""What the calls through the extension module do when the library's call fails, and that
+other threads run beside it (needs a B200)."""
 import ctypes
 
 import pytest
@@ -89,3 +89,25 @@ def test_a_failed_call_is_not_made_again(entry, name, code):
         assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
     entry(None)
     assert todo[name](getattr(rnn, name), Named()) is not None
+
+
+@pytest.mark.parametrize("name", ["kv_append_q8", "kv_read_q8", "attn_decode_q8", "attn_decode_shared"])
+def test_the_interpreter_is_free_during_the_call(entry, name):
+    """In the library's place a function that says whether its thread holds the lock."""
+    todo, _ = calls()
+    fast = rnn._lib.load_fast()
+    entry(ctypes.pythonapi.PyGILState_Check)
+    seen = []
+
+    def positional(*args, **kw):
+        order = {"kv_append_q8": ("q", "inv_freq", "positions", "paired", "with_k", "q_out", "k_out"),
+                 "kv_read_q8": ("start", "k_out", "v_out")}.get(
+                     name, ("scale", "with_lse", "out", "workspace"))
+        args = list(args)
+        if name == "kv_read_q8":
+            args[-1] = False                 # bf16 or not
+        seen.append(getattr(fast, name)(*args, *(kw[x] for x in order)))
+
+    todo[name](positional, Named())
+    # 0, and so the call's result; 1 is a status
+    assert seen[0] is not None and not isinstance(seen[0], int)
