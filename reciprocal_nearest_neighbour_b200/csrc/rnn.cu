@@ -69,9 +69,16 @@ struct DeviceInfo {
 static std::mutex g_mu;
 static DeviceInfo g_dev[64];
 
+// A call of the runtime failed.  The runtime keeps the error for whoever asks next, and
+// launched() asks: it is taken from there, so that no later call reports it again.
+static rnn_status cuda_failed() {
+  cudaGetLastError();
+  return RNN_ECUDA;
+}
+
 static rnn_status device_info(DeviceInfo** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RNN_ECUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cuda_failed();
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceInfo& di = g_dev[dev];
   if (di.sms == 0) {
@@ -79,7 +86,7 @@ static rnn_status device_info(DeviceInfo** out) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return RNN_ECUDA;
+      return cuda_failed();
     di.sm100 = (major == 10 && minor == 0);
     di.sms = sms;
   }
@@ -188,7 +195,7 @@ static uint32_t make_idesc(rnn_dtype dt, int block_n) {
 static rnn_status make_map(CUtensorMap* m, const void* base, int d, int64_t rows, int nbatch,
                            int64_t bstride, const Geometry& g, int box_rows = 0) {
   auto fn = encode_fn();
-  if (!fn) return RNN_ECUDA;
+  if (!fn) return cuda_failed();
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(nbatch)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(bstride) * 2};
@@ -262,14 +269,14 @@ static rnn_status timer_begin(cudaStream_t s, int* slot) {
   const int k = (*g_timer_count)++;
   if (k >= g_timer_cap) return RNN_OK;
   if (cudaEventRecord(static_cast<cudaEvent_t>(g_timer_start[k]), s) != cudaSuccess)
-    return RNN_ECUDA;
+    return cuda_failed();
   *slot = k;
   return RNN_OK;
 }
 
 static rnn_status timer_end(cudaStream_t s, int slot) {
   if (slot >= 0 && cudaEventRecord(static_cast<cudaEvent_t>(g_timer_stop[slot]), s) != cudaSuccess)
-    return RNN_ECUDA;
+    return cuda_failed();
   return RNN_OK;
 }
 
@@ -304,7 +311,7 @@ static rnn_status launch_nn(const NNParams& p_in, const CUtensorMap& m0, const C
               cudaSuccess ||
           cudaFuncSetAttribute(nn_argmax_kernel<8, 4, 4, false, true>, attr, sm) != cudaSuccess ||
           cudaFuncSetAttribute(nn_argmax_kernel<16, 2, 2, true, true>, attr, sm) != cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
       di->smem_set = true;
     }
   }
@@ -1610,7 +1617,7 @@ static rnn_status frm_run(int B, const void* D1, int64_t bs1, const void* D2, in
   if (!body_stream) {
     int dev = 0;
     cudaStreamCaptureStatus cst = cudaStreamCaptureStatusNone;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RNN_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cuda_failed();
     if (cudaStreamIsCapturing(s, &cst) != cudaSuccess) {
       cudaGetLastError();
       cst = cudaStreamCaptureStatusNone;
@@ -1650,10 +1657,10 @@ static rnn_status frm_run(int B, const void* D1, int64_t bs1, const void* D2, in
   const int mode = copies_for(d, metric);
   if (k == 0) {
     // no seeds: every count is zero (the basin, if asked for, untouched pixels)
-    if (cudaMemsetAsync(count_out, 0, sizeof(int32_t) * B, s) != cudaSuccess) return RNN_ECUDA;
-    if (cudaMemsetAsync(st.err, 0, sizeof(int), s) != cudaSuccess) return RNN_ECUDA;
+    if (cudaMemsetAsync(count_out, 0, sizeof(int32_t) * B, s) != cudaSuccess) return cuda_failed();
+    if (cudaMemsetAsync(st.err, 0, sizeof(int), s) != cudaSuccess) return cuda_failed();
     if (basin && cudaMemsetAsync(basin, 0xFF, sizeof(int32_t) * B * (N1 + 1), s) != cudaSuccess)
-      return RNN_ECUDA;
+      return cuda_failed();
     return RNN_OK;
   }
   if (mode == kCopiesNone) {
@@ -1731,19 +1738,19 @@ static rnn_status frm_run(int B, const void* D1, int64_t bs1, const void* D2, in
     cudaGraph_t cg = nullptr;
     if (cudaStreamGetCaptureInfo(s, &cst, nullptr, &cg, nullptr, nullptr) != cudaSuccess ||
         cst != cudaStreamCaptureStatusActive || !cg)
-      return RNN_ECUDA;
+      return cuda_failed();
     // condition handles of iterations 2..max_iter (0 unless enabled this launch)
     cudaGraphConditionalHandle hnd[kMaxGraphIters + 1] = {};
     for (int it = 2; it <= max_iter; ++it)
       if (cudaGraphConditionalHandleCreate(&hnd[it], cg, 0, cudaGraphCondAssignDefault) !=
           cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
     if ((r = iteration(1, s, max_iter > 1 ? hnd[2] : 0)) != RNN_OK) return r;
     for (int it = 2; it <= max_iter; ++it) {
       const cudaGraphNode_t* deps = nullptr;
       size_t ndeps = 0;
       if (cudaStreamGetCaptureInfo(s, &cst, nullptr, nullptr, &deps, &ndeps) != cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
       // the params union has no default constructor: zeroed storage instead
       alignas(cudaGraphNodeParams) unsigned char cp_raw[sizeof(cudaGraphNodeParams)] = {};
       cudaGraphNodeParams& cp = *reinterpret_cast<cudaGraphNodeParams*>(cp_raw);
@@ -1752,19 +1759,19 @@ static rnn_status frm_run(int B, const void* D1, int64_t bs1, const void* D2, in
       cp.conditional.type = cudaGraphCondTypeIf;
       cp.conditional.size = 1;
       cudaGraphNode_t node;
-      if (cudaGraphAddNode(&node, cg, deps, ndeps, &cp) != cudaSuccess) return RNN_ECUDA;
+      if (cudaGraphAddNode(&node, cg, deps, ndeps, &cp) != cudaSuccess) return cuda_failed();
       if (cudaStreamUpdateCaptureDependencies(s, &node, 1, cudaStreamSetCaptureDependencies) !=
           cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
       if (cudaStreamBeginCaptureToGraph(body_stream, cp.conditional.phGraph_out[0], nullptr,
                                         nullptr, 0, cudaStreamCaptureModeThreadLocal) !=
           cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
       r = iteration(it, body_stream, it < max_iter ? hnd[it + 1] : 0);
       cudaGraph_t body;
       const cudaError_t ce = cudaStreamEndCapture(body_stream, &body);
       if (r != RNN_OK) return r;
-      if (ce != cudaSuccess) return RNN_ECUDA;
+      if (ce != cudaSuccess) return cuda_failed();
     }
   }
   return frm_merge(st, W1, pairs, cap, count_out, seed_state, s, pdl);
@@ -1916,10 +1923,10 @@ static rnn_status frm_run_pts(int B, const float* P1, int64_t bs1, const float* 
   st.pixel_tol = pixel_tol;
   st.starts = init ? 1 : 0;
   if (k == 0) {
-    if (cudaMemsetAsync(count_out, 0, sizeof(int32_t) * B, s) != cudaSuccess) return RNN_ECUDA;
-    if (cudaMemsetAsync(st.err, 0, sizeof(int), s) != cudaSuccess) return RNN_ECUDA;
+    if (cudaMemsetAsync(count_out, 0, sizeof(int32_t) * B, s) != cudaSuccess) return cuda_failed();
+    if (cudaMemsetAsync(st.err, 0, sizeof(int), s) != cudaSuccess) return cuda_failed();
     if (basin && cudaMemsetAsync(basin, 0xFF, sizeof(int32_t) * B * (N1 + 1), s) != cudaSuccess)
-      return RNN_ECUDA;
+      return cuda_failed();
     return RNN_OK;
   }
   if ((r = frm_seed(st, init, n_init, W1, S, di, s)) != RNN_OK) return r;
@@ -1982,8 +1989,8 @@ rnn_status rnn_workspace_status(const void* workspace, rnn_stream_t stream) {
   int err = 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemcpyAsync(&err, workspace, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return RNN_ECUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return RNN_ECUDA;
+    return cuda_failed();
+  if (cudaStreamSynchronize(s) != cudaSuccess) return cuda_failed();
   return err ? RNN_ETIMEOUT : RNN_OK;
 }
 
@@ -2218,7 +2225,7 @@ static rnn_status mnn_onepass(const uint16_t* X1, int64_t n1, const uint16_t* X2
                                227 * 1024) != cudaSuccess ||
           loc_resolve_attr<false>(kLocSmem) != cudaSuccess ||
           loc_resolve_attr<true>(kLocSmem) != cudaSuccess)
-        return RNN_ECUDA;
+        return cuda_failed();
       di->op_smem_set = true;
     }
   }
@@ -2511,10 +2518,10 @@ rnn_status rnn_frm_graph_create(int B, const void* D1, int64_t d1_batch_stride, 
   rnn_status r = device_info(&di);  // device queries stay outside the capture
   if (r != RNN_OK) return r;
   cudaStream_t s = nullptr, body = nullptr;
-  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return RNN_ECUDA;
+  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return cuda_failed();
   if (cudaStreamCreateWithFlags(&body, cudaStreamNonBlocking) != cudaSuccess) {
     cudaStreamDestroy(s);
-    return RNN_ECUDA;
+    return cuda_failed();
   }
   cudaGraph_t graph = nullptr;
   cudaGraphExec_t exec = nullptr;
@@ -2552,7 +2559,7 @@ rnn_status rnn_frm_graph_launch(rnn_frm_graph_t graph, rnn_stream_t stream) {
   if (!graph) return RNN_EINVAL;
   NvtxRange nvtx_range("rnn_frm_graph_launch");
   if (cudaGraphLaunch(graph->exec, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return RNN_ECUDA;
+    return cuda_failed();
   return RNN_OK;
 }
 
@@ -2586,7 +2593,7 @@ rnn_status rnn_mnn_mutual(const int32_t* rowarg, int64_t n1, const int32_t* cola
   Carve c(workspace);
   int* err = c.take<int>(64);
   int* counts = c.take<int>(n1 / kMnnChunk + 2);
-  if (cudaMemsetAsync(err, 0, sizeof(int), s) != cudaSuccess) return RNN_ECUDA;
+  if (cudaMemsetAsync(err, 0, sizeof(int), s) != cudaSuccess) return cuda_failed();
   const int nblk = static_cast<int>((n1 + kMnnChunk - 1) / kMnnChunk);
   mutual_count_kernel<<<nblk, kSmallThreads, 0, s>>>(rowarg, n1, colarg, n2, counts);
   if ((r = launched()) != RNN_OK) return r;
@@ -2920,14 +2927,14 @@ static void* g_noalloc_ptr[64];
 // (none yet: RNN_ECUDA).
 static rnn_status noalloc_scratch(cudaStream_t s, void** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return RNN_ECUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cuda_failed();
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return RNN_ECUDA;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return cuda_failed();
   std::lock_guard<std::mutex> lk(g_noalloc_mu);
   if (cs == cudaStreamCaptureStatusNone) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr)
-      return RNN_ECUDA;
+      return cuda_failed();
     g_noalloc_ptr[dev] = p;
   }
   if (!g_noalloc_ptr[dev]) return RNN_ECUDA;
@@ -2963,8 +2970,8 @@ extern "C" rnn_status rnn_nn_argmax_noalloc_status(rnn_stream_t stream) {
   if (r != RNN_OK) return r;
   int err = 0;
   if (cudaMemcpyAsync(&err, scratch, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return RNN_ECUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return RNN_ECUDA;
+    return cuda_failed();
+  if (cudaStreamSynchronize(s) != cudaSuccess) return cuda_failed();
   return err ? RNN_ETIMEOUT : RNN_OK;
 }
 
@@ -3041,7 +3048,7 @@ static rnn_status attn_setup(DeviceInfo* di) {
       !set(AttnShape<128>::kSmem, attn_prompt_kernel<true, 128, false>,
            attn_prompt_kernel<false, 128, false>, attn_prompt_kernel<true, 128, true>,
            attn_prompt_kernel<false, 128, true>))
-    return RNN_ECUDA;
+    return cuda_failed();
   di->attn_smem_set = true;
   return RNN_OK;
 }
@@ -3049,7 +3056,7 @@ static rnn_status attn_setup(DeviceInfo* di) {
 // [tokens][heads][d] rows in boxes of 64 channels x 1 head x 128 tokens.
 static rnn_status make_rows_map(CUtensorMap* m, const rnn_rows& r, int64_t tokens, int heads, int d) {
   auto fn = encode_fn();
-  if (!fn) return RNN_ECUDA;
+  if (!fn) return cuda_failed();
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
                         static_cast<cuuint64_t>(tokens)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(r.head_stride) * 2,
@@ -3525,7 +3532,7 @@ static bool decode_q8_smem() {
 static rnn_status decode_q8_setup(DeviceInfo* di) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (di->attn_q8_smem_set) return RNN_OK;
-  if (!decode_q8_smem<64>() || !decode_q8_smem<128>()) return RNN_ECUDA;
+  if (!decode_q8_smem<64>() || !decode_q8_smem<128>()) return cuda_failed();
   di->attn_q8_smem_set = true;
   return RNN_OK;
 }
@@ -3877,7 +3884,7 @@ static rnn_status shared_setup(DeviceInfo* di) {
   if (di->attn_shared_smem_set) return RNN_OK;
   if (!shared_smem<true, 64>() || !shared_smem<false, 64>() || !shared_smem<true, 128>() ||
       !shared_smem<false, 128>())
-    return RNN_ECUDA;
+    return cuda_failed();
   di->attn_shared_smem_set = true;
   return RNN_OK;
 }

@@ -1,6 +1,9 @@
 """What the calls through the extension module do when the library's call fails, and that
 other threads run beside it (needs a B200)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -11,6 +14,7 @@ from test_gpu_q8 import filled, gen_of, ints, normal
 pytestmark = pytest.mark.gpu
 
 HF = torch.float16
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 NAMES = ("rnn_kv_read_q8", "rnn_attn_decode_q8", "rnn_attn_decode_q8_workspace_size",
          "rnn_attn_decode_shared", "rnn_attn_decode_shared_workspace_size", "rnn_kv_append_q8")
 
@@ -111,3 +115,39 @@ def test_the_interpreter_is_free_during_the_call(entry, name):
     todo[name](positional, Named())
     # 0, and so the call's result; 1 is a status
     assert seen[0] is not None and not isinstance(seen[0], int)
+
+
+LEFT_BEHIND = """
+import torch, reciprocal_nearest_neighbour_b200 as rnn
+x = torch.ones(4, 2, 64, device="cuda").half()
+cache = torch.zeros(2, 16, 2, 64, device="cuda").half()
+i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+args = (x, x, cache, cache.clone(), i(0, 1)[None], i(0), i(0, 4))
+rnn.kv_append(*args)
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+failed = False
+try:
+    with torch.cuda.stream(s):
+        g.capture_begin(capture_error_mode="thread_local")
+        try:
+            rnn.workspace_status(ws)         # waits for its stream, which a capture cannot
+        except rnn.RNNError as e:
+            failed = e.name == "RNN_ECUDA"
+        finally:
+            g.capture_end()
+except RuntimeError:
+    pass                                     # the capture is lost
+assert failed
+rnn.kv_append(*args)
+torch.cuda.synchronize()
+print("the next call is fine")
+"""
+
+
+def test_a_failed_call_leaves_nothing_for_the_next():
+    """An error of the runtime that one call reported is not reported again by another."""
+    r = subprocess.run([sys.executable, "-c", LEFT_BEHIND], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "the next call is fine" in r.stdout, r.stdout + r.stderr
