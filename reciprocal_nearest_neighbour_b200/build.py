@@ -6,7 +6,8 @@ file.  The CUDA runtime is linked statically and the driver's tensor-map
 encoder is looked up at run time, so the library loads on a machine without
 a GPU (its entry points then fail with RNN_ECUDA).  ``csrc/fast.cpp`` becomes
 the extension module ``_fast.so`` (g++, against torch's headers): the short way
-from tensors to some of the library's calls.
+from tensors to some of the library's calls.  The library needs neither, and is
+built also where the module cannot be: its calls then take their Python forms.
 """
 from __future__ import annotations
 
@@ -51,9 +52,13 @@ def _older(path: str, deps) -> bool:
         any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
 
 
+def _fast_stale() -> bool:
+    return _older(FAST, [FAST_SOURCE, os.path.join(INCLUDE, "rnn.h")])
+
+
 def build_fast(force: bool = False) -> str:
     """The extension module of csrc/fast.cpp."""
-    if not force and not _older(FAST, [FAST_SOURCE, os.path.join(INCLUDE, "rnn.h")]):
+    if not force and not _fast_stale():
         return FAST
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
@@ -70,8 +75,8 @@ def build_fast(force: bool = False) -> str:
     return FAST
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_fast(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """The CUDA library."""
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -82,6 +87,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, and the extension module where it can be built."""
+    build_library(force, verbose)
+    try:
+        build_fast(force)
+    except (OSError, subprocess.CalledProcessError) as e:
+        if _fast_stale() and os.path.exists(FAST):
+            os.remove(FAST)     # of other sources: it may not fit the library
+        print(f"{LIB}: without the extension module ({e})", file=sys.stderr)
     return LIB
 
 
