@@ -7,6 +7,8 @@ raises ``RNNLibraryError``.  Build it with
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librnn.so")
@@ -186,12 +188,18 @@ fast = None
 
 
 def load_fast():
-    """Load the library and the extension module beside it (not built: the Python forms)."""
+    """Load the library and the extension module beside it, if there is one for this Python
+    and this torch (else the Python forms)."""
     global fast
     if fast is None:
+        from .build import fast_path
+
         lib = load()
+        loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._fast", fast_path())
         try:
-            from . import _fast as module
+            module = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader(loader.name, loader))
+            loader.exec_module(module)
         except ImportError:
             fast = _Python
             return fast

@@ -1,10 +1,11 @@
-"""Building the extension module (no GPU)."""
+"""Building and choosing the extension module (no GPU)."""
 import os
 import subprocess
 
 import pytest
+import torch
 
-from reciprocal_nearest_neighbour_b200 import build as rnn_build
+from reciprocal_nearest_neighbour_b200 import _lib, build as rnn_build
 
 
 @pytest.fixture
@@ -24,7 +25,6 @@ def compilers(monkeypatch, tmp_path):
     monkeypatch.setattr(rnn_build, "PKG", str(tmp_path))
     monkeypatch.setattr(rnn_build, "LIB", str(tmp_path / "librnn.so"))
     monkeypatch.setattr(rnn_build.subprocess, "check_call", check_call)
-    monkeypatch.setattr(rnn_build, "FAST", str(tmp_path / "_fast.so"))
     return ran, broken
 
 
@@ -62,3 +62,30 @@ def test_a_module_of_other_sources_does_not_stay(compilers):
     broken.add("module")
     rnn_build.build(force=True)          # of these sources: it stays
     assert os.path.exists(new)
+
+
+def test_another_torch_needs_another_module(compilers, monkeypatch):
+    """The file's name says what it was built for, so one for another torch or Python is
+    neither kept nor loaded."""
+    ran, _ = compilers
+    first = rnn_build.build_fast()
+    assert ran == ["module"] and rnn_build.build_fast() == first and ran == ["module"]
+    monkeypatch.setattr(torch, "__version__", "9.9.0+cu999")
+    second = rnn_build.build_fast()
+    assert second != first and ran == ["module", "module"]
+    assert os.path.exists(first) and os.path.exists(second)
+
+
+def test_no_module_for_this_torch_means_the_python_forms(monkeypatch):
+    monkeypatch.setattr(_lib, "fast", None)
+    monkeypatch.setattr(torch, "__version__", "9.9.0+cu999")
+    assert _lib.load_fast() is _lib._Python
+
+
+def test_the_module_of_this_torch_is_loaded(monkeypatch):
+    rnn_build.build()
+    rnn_build.build_fast()
+    monkeypatch.setattr(_lib, "fast", None)
+    module = _lib.load_fast()
+    assert module.__name__.endswith("_fast") and module.__file__ == rnn_build.fast_path()
+    assert _lib.load_fast() is module
