@@ -602,6 +602,8 @@ rnn_status rnn_attn_decode(const rnn_attn_decode_args *args, rnn_stream_t stream
  *                 0, values beyond prefix_pages_count * page_size as that).
  *   page_table, lens  each sequence's own tokens, the new one included, which
  *                 start on a page of their own (0: it sees the prefix only).
+ * It is the faster call from about four sequences on, where B times the prefix
+ * is above 32000 tokens; for less rnn_attn_decode over longer page tables is.
  * The rest is as in rnn_attn_decode: keys whose page is outside [0, num_pages)
  * count as absent, a row without a key gets zeros and -infinity.  Where keys
  * stand in the sequence (for a rotation) was settled when they were appended.

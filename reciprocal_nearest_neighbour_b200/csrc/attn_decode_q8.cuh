@@ -16,8 +16,9 @@
 //
 // Measured, in a CUDA graph with the join: 90 streams of 50 to 9000 keys, 32/8 heads of 128,
 // e4m3, pages of 16, 0.32 GB, 65 us (4.9 TB/s; attn_decode takes 1.6 times as long over twice
-// the bytes; 62 us with a head's rows of a page side by side); 4 streams of 80 001 to 131 000 keys, 32/4 heads, int8, 0.44 GB, 80 us (5.4 TB/s, 0.83
-// of a copy's rate).  It is latency and issue that are left: about 720 instructions (e4m3, 830
+// the bytes; 62 us with a head's rows of a page side by side); 4 streams of 80 001 to 131 000
+// keys, 32/4 heads, int8, 0.44 GB, 80 us (5.4 TB/s, 0.83 of a copy's rate); the 90 streams
+// with 32/2 heads (kNT = 2) 40 us (2.0 TB/s).  It is latency and issue that are left: about 720 instructions (e4m3, 830
 // int8) a warp and tile, of which the conversions are 200 at half rate, with three warps a
 // scheduler in 168 registers.  (Two CTAs per SM with three tiles a warp: 83 and 100 us, when
 // the others took 71 and 97.)

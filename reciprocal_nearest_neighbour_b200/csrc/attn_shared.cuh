@@ -118,7 +118,6 @@ attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
   const int unit = wide ? x % units : p.wide;
   x /= units;
   const int split = x % splits, hk = x / splits;
-  const int rows = min(kPreUnit, p.rows - unit * kPreUnit);
   const int64_t room = static_cast<int64_t>(p.max_pages) * p.page.div;
   const int64_t given = __ldg(p.len);
   const int keys = static_cast<int>(

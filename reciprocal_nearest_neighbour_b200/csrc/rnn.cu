@@ -3781,7 +3781,7 @@ static PrefixPlan make_prefix_plan(int64_t rows, int Hkv, int64_t room) {
   // The time of a wave, in the time of a row tile's products with 128 keys: 2 for a wide
   // unit's key tile, 1.3 for a narrow one's (its loads), 6 to begin and to end, and 1/16000
   // for each row's part, which the join reads.
-  constexpr int kSms = 148;
+  constexpr int kSms = 148;  // (not the device's: the workspace's size is asked without one)
   double least = 0;
   // (from what one accumulator takes; a narrow unit has two)
   const int64_t from = (tiles + kPreMostTiles - 1) / kPreMostTiles;
