@@ -151,3 +151,85 @@ def test_a_failed_call_leaves_nothing_for_the_next():
     r = subprocess.run([sys.executable, "-c", LEFT_BEHIND], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "the next call is fine" in r.stdout, r.stdout + r.stderr
+
+
+def good_calls():
+    """Arguments by position, of calls that are served."""
+    g = gen_of(3)
+    kc, vc, scales, _, _ = filled(g, "int8", 3, 16, 2, 64)
+    k16, v16 = (normal(g, (3, 16, 2, 64), HF) for _ in range(2))
+    q, k, v = (normal(g, (5, h, 64), HF) for h in (4, 2, 2))
+    inv = torch.ones(16, dtype=torch.float64, device="cuda")
+    at = ints([[1, 2]] * 5)
+    tab, cu, two, one = ints([[0, 1], [2, 2]]), ints([0, 2, 5]), ints([3, 4]), ints([9])
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    return {
+        "kv_append_q8": [k, v, kc, vc, scales, tab, two, cu, q, inv, at, False, True,
+                         torch.empty_like(q), torch.empty_like(k)],
+        "kv_read_q8": [kc, vc, scales, tab, cu, 5, False, two, torch.empty_like(k),
+                       torch.empty_like(k)],
+        "attn_decode_q8": [q[:2], kc, vc, scales, tab, two, 0.25, True, torch.empty_like(q[:2]), ws],
+        "attn_decode_shared": [q[:2], k16, v16, one, one, tab, two, 0.25, True,
+                               torch.empty_like(q[:2]), ws],
+    }
+
+
+def worse(x):
+    """Forms of an argument that its call cannot take as it is."""
+    if isinstance(x, bool):
+        return {"an int": 1, "none": None}
+    if isinstance(x, float):
+        return {"negative": -1.0, "nan": float("nan"), "too large": 1e39, "zero": 0.0, "text": "1"}
+    if isinstance(x, int):
+        return {"negative": -1, "a float": 5.0, "more": 6, "beyond 64 bits": 1 << 70}
+    bad = {"no tensor": 3, "a list": [1], "on the host": x.cpu(), "of another type": x.to(torch.complex64),
+           "a dimension more": x[None], "a dimension less": x[0], "nothing": x[:0]}
+    if x.dim() > 1 or x.dtype != torch.uint8:
+        bad["one less"] = x[:-1]
+        if x.numel() > 1:
+            bad["not contiguous"] = torch.stack([x, x], -1)[..., 0]
+    if x.dim() >= 2:
+        bad["one wider"] = torch.cat([x, x[..., :1]], -1)
+        bad["a row less"] = x[:, :-1]
+    if x.dim() >= 3 and x.dtype != torch.float32:
+        room = torch.zeros(x.numel() + 64, dtype=x.dtype, device="cuda")
+        bad["off its boundary"] = room[1:1 + x.numel()].view(x.shape)
+        bad["strides of 4"] = torch.zeros(*x.shape[:-1], x.shape[-1] + 4, dtype=x.dtype,
+                                          device="cuda")[..., :x.shape[-1]]
+    return bad
+
+
+# What a call takes after all: longer or shorter rows of the page table, fewer pairs to rotate,
+# one column of positions; a workspace whose size the library refuses itself.
+ALLOWED = {
+    "kv_append_q8": {(5, "one wider"), (5, "a row less"), (9, "one less"), (10, "a row less")},
+    "kv_read_q8": {(3, "one wider"), (3, "a row less")},
+    "attn_decode_q8": {(4, "one wider"), (4, "a row less"), (9, "nothing")},
+    "attn_decode_shared": {(5, "one wider"), (5, "a row less"), (10, "nothing")},
+}
+
+
+@pytest.mark.parametrize("name", ["kv_append_q8", "kv_read_q8", "attn_decode_q8", "attn_decode_shared"])
+def test_unusual_arguments_do_not_reach_the_library(entry, name):
+    """Each argument in turn in a form that does not fit the others.  In the library's place a
+    function that launches nothing."""
+    fast, good = rnn._lib.load_fast(), good_calls()[name]
+    made = []
+
+    @ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
+    def counts(args, stream):
+        made.append(args)
+        return 0
+
+    entry(counts)
+    call = getattr(fast, name)
+    assert call(*good) is not None and len(made) == 1
+    served = []
+    for i, x in enumerate(good):
+        for what, bad in worse(x).items():
+            args = list(good)
+            args[i] = bad
+            before = len(made)
+            if call(*args) is not None or len(made) != before:
+                served.append((i, what))
+    assert set(served) == ALLOWED[name]
